@@ -404,6 +404,50 @@ dsa_status dsa_decode_run_noalloc(const dsa_decode_plan_t *plan, const void *q,
                                   void *out, float *lse, int32_t *device_status,
                                   dsa_stream_t stream);
 
+/* Element types of dense rows (dsa_cache_write, dsa_cache_read). */
+enum { DSA_TYPE_BF16 = 0, DSA_TYPE_F16 = 1, DSA_TYPE_F32 = 2 };
+
+/* Quantize rows of keys and store them at slots of a paged cache (the pages
+ * take the caches as given; they have no counterpart of this call).
+ * Row i, x = rows[i*row_stride + 0..d-1] (d = 512, or 576 for V32_656), goes
+ * to the record of slots[i]:
+ *   norm_weight != NULL: dims 0..511 become x * w / sqrt(mean(x^2) + eps),
+ *     norm_weight fp32 [512], 16-byte aligned, norm_eps finite and >= 0;
+ *   cos_sin != NULL (with positions; both NULL = no RoPE): the last 64 dims
+ *     are rotated by row positions[i] of the table [cos(32) | sin(32)],
+ *     pairs as rope_style says (DSA_ROPE_*, over those 64 dims);
+ *   then every block of the format takes its scale from its largest
+ *     magnitude a, and the codes are x / scale rounded to nearest even,
+ *     saturating: FP8_528 and V32_656 fp32(a / 448); FP8_528_UE8M0 and
+ *     MODEL1_584 the smallest power of two >= a / 448 (exponent in
+ *     [-127, 127]; 2^0 for a block of zeros); NVFP4_288 a / 6 rounded to
+ *     e4m3, at most 448. bf16 parts are rounded to nearest even.
+ * All of it is computed in fp32 from the row's values to the codes. A block
+ * that holds a NaN reads back as NaN throughout (for FP8_528 and V32_656 one
+ * that holds an infinity too; the other scales saturate).
+ * rows: row_type DSA_TYPE_*, 16-byte aligned, row_stride (elements) >= d and
+ * a multiple of 16 bytes. slots: int32 [num_rows]; a slot outside the cache
+ * (-1 for padding) writes nothing. The slots inside the cache must be
+ * distinct within a call: rows given the same slot race, and its record may
+ * mix them. The rest of the cache is untouched; rows must not overlap it.
+ * A row whose position lies outside the table is not written; with
+ * device_status != NULL (int32 device word, set to 0 by the caller) that
+ * sets it to DSA_ERR_INVALID_ARG. Asynchronous, one launch, no workspace. */
+dsa_status dsa_cache_write(const dsa_cache_desc *cache, const int32_t *slots, int64_t num_rows,
+                           const void *rows, int64_t row_stride, int32_t row_type,
+                           const float *norm_weight, float norm_eps, const int64_t *positions,
+                           const float *cos_sin, int64_t cos_sin_rows, int32_t rope_style,
+                           int32_t *device_status, dsa_stream_t stream);
+
+/* Read records back as dense rows (no counterpart on the pages): row i gets
+ * the d values (code * scale, one product in fp32, rounded once to row_type)
+ * of the record of slots[i], or zeros when that slot lies outside the cache.
+ * rows: as for dsa_cache_write (the columns past d of a wider stride are
+ * left as they are); it must not overlap the cache. A slot may be named any
+ * number of times. Asynchronous, one launch, no workspace. */
+dsa_status dsa_cache_read(const dsa_cache_desc *cache, const int32_t *slots, int64_t num_rows,
+                          void *rows, int64_t row_stride, int32_t row_type, dsa_stream_t stream);
+
 /* Static description of a status code (no counterpart on the pages). */
 const char *dsa_decode_status_string(dsa_status s);
 

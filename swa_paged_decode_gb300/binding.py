@@ -25,8 +25,10 @@ STATUS_NAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED
 EXPORTED = ("dsa_decode_plan", "dsa_decode_plan_qk", "dsa_decode_run", "dsa_decode_combine", "dsa_decode_selection",
             "dsa_decode_read_status", "dsa_decode_status_string", "dsa_decode_abi_version",
             "dsa_decode_run_noalloc", "dsa_decode_run_v41", "dsa_decode_combine_v41")
+EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
+ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # DSA_TYPE_*
 
 
 class DsaError(RuntimeError):
@@ -147,6 +149,11 @@ def _load_path(path: str):
     lib.dsa_decode_combine_v41.restype = ctypes.c_int
     lib.dsa_decode_combine_v41.argtypes = [ctypes.POINTER(Plan), vp, ctypes.c_size_t, vp, vp, vp,
                                            i64, i32, vp, ctypes.POINTER(MxOutDesc), vp, vp]
+    lib.dsa_cache_write.restype = ctypes.c_int
+    lib.dsa_cache_write.argtypes = [ctypes.POINTER(CacheDesc), vp, i64, vp, i64, i32, vp,
+                                    ctypes.c_float, vp, vp, i64, i32, vp, vp]
+    lib.dsa_cache_read.restype = ctypes.c_int
+    lib.dsa_cache_read.argtypes = [ctypes.POINTER(CacheDesc), vp, i64, vp, i64, i32, vp]
     lib.dsa_decode_status_string.restype = ctypes.c_char_p
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
@@ -305,6 +312,67 @@ def dsa_decode_run_noalloc(plan: Plan, q: torch.Tensor, swa_cache: W.PagedCache,
         out.data_ptr(), lse.data_ptr(), _ptr(device_status), _stream(stream))
     if check:
         _check("dsa_decode_run_noalloc", rc)
+    return rc
+
+
+def _require(fn: str, device, **tensors):
+    """The tensors' own properties, which pointers cannot carry: each is None
+    or (tensor, dtype(s), shape with None for any extent, contiguous) and has
+    to lie on ``device``, the current CUDA device. DSA_ERR_INVALID_ARG
+    otherwise, before the library is called."""
+    ok = device.type == "cuda" and (device.index or 0) == torch.cuda.current_device()
+    for v in tensors.values():
+        if v is None or v[0] is None:
+            continue
+        t, dtype, shape, contiguous = v
+        ok = (ok and t.device == device
+              and t.dtype in (dtype if isinstance(dtype, (tuple, dict)) else (dtype,))
+              and t.dim() == len(shape) and all(b is None or a == b for a, b in zip(t.shape, shape))
+              and (t.is_contiguous() if contiguous else t.dim() == 0 or t.numel() == 0 or t.stride(-1) == 1))
+    if not ok:
+        raise DsaError(fn, -1)
+
+
+def _cache_rows(fn: str, cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor, **more):
+    n, dims = slots.shape[0] if slots.dim() else 0, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM
+    _require(fn, cache.data.device, data=(cache.data, torch.uint8, (None, None), False),
+             slots=(slots, torch.int32, (n,), True), rows=(rows, ROW_TYPES, (n, dims), False), **more)
+    return (ctypes.byref(cache_desc(cache)), slots.data_ptr(), n, rows.data_ptr(),
+            rows.stride(0) if n > 1 else max(rows.stride(0), dims), ROW_TYPES[rows.dtype])
+
+
+def dsa_cache_write(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
+                    norm_weight: Optional[torch.Tensor] = None, norm_eps: float = 0.0,
+                    positions: Optional[torch.Tensor] = None,
+                    cos_sin: Optional[torch.Tensor] = None, rope_style: int = DSA_ROPE_NEOX,
+                    device_status: Optional[torch.Tensor] = None, stream=None,
+                    check: bool = True) -> int:
+    """Quantize rows [n, 512] (576 for V3.2 records; bf16, f16 or fp32, any
+    row stride) into the records of ``slots`` [n] int32 (-1: not written),
+    after an optional RMS norm (weight fp32 [512]) and RoPE of their last 64
+    dims (positions int64 [n], cos_sin fp32 [rows, 64])."""
+    fn = "dsa_cache_write"
+    n = slots.shape[0] if slots.dim() else 0
+    args = _cache_rows(fn, cache, slots, rows, norm=(norm_weight, torch.float32, (W.HEAD_DIM,), True),
+                       pos=(positions, torch.int64, (n,), True),
+                       table=(cos_sin, torch.float32, (None, 64), True),
+                       status=(device_status, torch.int32, (1,), True))
+    rc = load().dsa_cache_write(*args, _ptr(norm_weight), float(norm_eps), _ptr(positions),
+                                _ptr(cos_sin), 0 if cos_sin is None else cos_sin.shape[0],
+                                int(rope_style), _ptr(device_status), _stream(stream))
+    if check:
+        _check(fn, rc)
+    return rc
+
+
+def dsa_cache_read(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor, stream=None,
+                   check: bool = True) -> int:
+    """Fill rows [n, 512] (576 for V3.2 records; bf16, f16 or fp32, any row
+    stride) with the values of the records of ``slots`` [n] int32; a slot
+    outside the cache gives zeros."""
+    rc = load().dsa_cache_read(*_cache_rows("dsa_cache_read", cache, slots, rows), _stream(stream))
+    if check:
+        _check("dsa_cache_read", rc)
     return rc
 
 

@@ -11,11 +11,14 @@
 #include <cstring>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
+#include "dsa_host.cuh"
 
-#include "dsa_internal.cuh"
-
+using dsa::align_up;
+using dsa::aligned;
+using dsa::cuda_status;
+using dsa::NvtxRange;
 using dsa::Params;
+using dsa::record_bytes;
 
 namespace {
 constexpr int kCfgDevices = 64;
@@ -37,25 +40,8 @@ cudaError_t dsa::dsa_configure_once(int bit, cudaError_t (*f)(void *), void *arg
 
 namespace {
 
-// NVTX range over one entry point (host side: argument checks and launches),
-// so a profiler timeline shows each run / combine call.
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-
 constexpr int64_t kAlignWs = 256;
 constexpr int64_t kStatusBytes = 256;
-
-int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-int record_bytes(int32_t fmt) {
-  if (fmt == DSA_REC_FP8_528 || fmt == DSA_REC_FP8_528_UE8M0) return 528;
-  if (fmt == DSA_REC_MODEL1_584) return 584;
-  if (fmt == DSA_REC_V32_656) return 656;
-  return fmt == DSA_REC_NVFP4_288 ? 288 : -1;
-}
 
 bool heads_supported(int32_t H) {
   return H == 16 || H == 32 || H == 48 || H == 64 || H == 96 || H == 128;
@@ -64,39 +50,16 @@ bool heads_supported(int32_t H) {
 dsa_status fill_list(const dsa_cache_desc *c, const int32_t *idx, int64_t stride,
                      const int32_t *lens, int32_t width, dsa::ListArgs &L) {
   if (!c || !idx || !lens || !c->base) return DSA_ERR_INVALID_ARG;
-  const int rb = record_bytes(c->format);
-  if (rb < 0) return DSA_ERR_UNSUPPORTED;
-  if (c->num_pages < 1 || !pow2(c->page_size)) return DSA_ERR_INVALID_ARG;
-  if (c->page_stride_bytes < (int64_t)c->page_size * rb) return DSA_ERR_INVALID_ARG;
-  if (c->num_pages * (int64_t)c->page_size > (int64_t)INT32_MAX + 1) return DSA_ERR_UNSUPPORTED;
+  if (record_bytes(c->format) < 0) return DSA_ERR_UNSUPPORTED;
   if (stride < width) return DSA_ERR_INVALID_ARG;
-  if (!aligned(c->base, 16) || c->page_stride_bytes % 16 != 0) return DSA_ERR_ALIGNMENT;
+  const dsa_status s = dsa::fill_cache(c, L);
+  if (s != DSA_OK) return s;
   if (!aligned(idx, 4) || !aligned(lens, 4)) return DSA_ERR_ALIGNMENT;
-  L.base = static_cast<const uint8_t *>(c->base);
-  L.num_slots = c->num_pages * (int64_t)c->page_size;
-  L.page_stride = c->page_stride_bytes;
   L.ids = idx;
   L.lens = lens;
   L.idx_stride = stride;
-  int sh = 0;
-  while ((1 << sh) < c->page_size) ++sh;
-  L.page_shift = sh;
-  L.page_mask = c->page_size - 1;
-  L.fmt = c->format;
-  L.rec = rb;
   L.width = width;
   L.tiles = (width + dsa::kTile - 1) / dsa::kTile;
-  L.extent = c->num_pages * c->page_stride_bytes;
-#ifdef DSA_DEBUG
-  // Checking build only: a smaller extent for the record checks (a test
-  // knob: records past it are reported and skipped, never read).
-  if (const char *cap = std::getenv("DSA_DEBUG_CHECK_EXTENT")) {
-    const long long v = std::atoll(cap);
-    if (v > 0 && v < L.extent) L.extent = v;
-  }
-#endif
-  L.aligned32 = (aligned(c->base, 32) && c->page_stride_bytes % 32 == 0 && rb % 32 == 0) ? 1 : 0;
-  L.sectors32 = (aligned(c->base, 32) && c->page_stride_bytes % 32 == 0) ? 1 : 0;
   return DSA_OK;
 }
 
@@ -126,8 +89,6 @@ void fill_schedule(const dsa_decode_plan_t *plan, void *ws, Params &p) {
   p.merge = plan->merge_in_run != 0 ? 1 : 0;
   p.tok_cnt = reinterpret_cast<int32_t *>(w + plan->ws_count_offset);
 }
-
-dsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
 // Output options shared by run and combine: bf16 `out` or the MXFP8
 // descriptor, the RoPE pairing and the inverse-rotation rule.
