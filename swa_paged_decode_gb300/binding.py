@@ -172,8 +172,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream of the current device
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -315,30 +315,48 @@ def dsa_decode_run_noalloc(plan: Plan, q: torch.Tensor, swa_cache: W.PagedCache,
     return rc
 
 
-def _require(fn: str, device, **tensors):
-    """The tensors' own properties, which pointers cannot carry: each is None
-    or (tensor, dtype(s), shape with None for any extent, contiguous) and has
-    to lie on ``device``, the current CUDA device. DSA_ERR_INVALID_ARG
-    otherwise, before the library is called."""
-    ok = device.type == "cuda" and (device.index or 0) == torch.cuda.current_device()
-    for v in tensors.values():
-        if v is None or v[0] is None:
-            continue
-        t, dtype, shape, contiguous = v
-        ok = (ok and t.device == device
-              and t.dtype in (dtype if isinstance(dtype, (tuple, dict)) else (dtype,))
-              and t.dim() == len(shape) and all(b is None or a == b for a, b in zip(t.shape, shape))
-              and (t.is_contiguous() if contiguous else t.dim() == 0 or t.numel() == 0 or t.stride(-1) == 1))
-    if not ok:
+# A tensor's own properties, which its pointer cannot carry, are checked here
+# with as few calls as will do (a step of a small batch waits for the host):
+# device, dtype and extents; DSA_ERR_INVALID_ARG before the library is called.
+
+def _device(fn: str, t: torch.Tensor) -> int:
+    """The tensor's device, which has to be the current CUDA device."""
+    d = t.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
         raise DsaError(fn, -1)
+    return d
 
 
-def _cache_rows(fn: str, cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor, **more):
-    n, dims = slots.shape[0] if slots.dim() else 0, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM
-    _require(fn, cache.data.device, data=(cache.data, torch.uint8, (None, None), False),
-             slots=(slots, torch.int32, (n,), True), rows=(rows, ROW_TYPES, (n, dims), False), **more)
-    return (ctypes.byref(cache_desc(cache)), slots.data_ptr(), n, rows.data_ptr(),
-            rows.stride(0) if n > 1 else max(rows.stride(0), dims), ROW_TYPES[rows.dtype])
+def _vec(fn: str, t: Optional[torch.Tensor], d: int, dtype, shape) -> Optional[int]:
+    """Pointer of a contiguous tensor of this dtype and shape (None: none)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != d or not t.is_contiguous():
+        raise DsaError(fn, -1)
+    return t.data_ptr()
+
+
+def _table(fn: str, t: Optional[torch.Tensor], d: int):
+    """(pointer, rows) of a cos / sin table [rows, 64]."""
+    if t is None:
+        return None, 0
+    n = t.shape[0]
+    return _vec(fn, t, d, torch.float32, (n, 64)), n
+
+
+def _cache(fn: str, c: W.PagedCache, d: int) -> CacheDesc:
+    t = c.data
+    if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1 or t.get_device() != d:
+        raise DsaError(fn, -1)
+    return CacheDesc(t.data_ptr(), t.shape[0], t.stride(0), c.page_size, c.fmt)
+
+
+def _rows(fn: str, t: torch.Tensor, d: int, n: int, dims: int):
+    """(pointer, stride, DSA_TYPE_*) of dense rows [n, dims]."""
+    ty = ROW_TYPES.get(t.dtype)
+    if ty is None or t.shape != (n, dims) or t.get_device() != d or (t.stride(1) != 1 and n > 0):
+        raise DsaError(fn, -1)
+    return t.data_ptr(), t.stride(0) if n > 1 else dims, ty
 
 
 def dsa_cache_write(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
@@ -352,14 +370,15 @@ def dsa_cache_write(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor
     after an optional RMS norm (weight fp32 [512]) and RoPE of their last 64
     dims (positions int64 [n], cos_sin fp32 [rows, 64])."""
     fn = "dsa_cache_write"
-    n = slots.shape[0] if slots.dim() else 0
-    args = _cache_rows(fn, cache, slots, rows, norm=(norm_weight, torch.float32, (W.HEAD_DIM,), True),
-                       pos=(positions, torch.int64, (n,), True),
-                       table=(cos_sin, torch.float32, (None, 64), True),
-                       status=(device_status, torch.int32, (1,), True))
-    rc = load().dsa_cache_write(*args, _ptr(norm_weight), float(norm_eps), _ptr(positions),
-                                _ptr(cos_sin), 0 if cos_sin is None else cos_sin.shape[0],
-                                int(rope_style), _ptr(device_status), _stream(stream))
+    d, n = _device(fn, slots), slots.numel()
+    desc = _cache(fn, cache, d)
+    p_slots = _vec(fn, slots, d, torch.int32, (n,))
+    ptr, stride, ty = _rows(fn, rows, d, n, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM)
+    table, table_rows = _table(fn, cos_sin, d)
+    rc = load().dsa_cache_write(ctypes.byref(desc), p_slots, n, ptr, stride, ty,
+                                _vec(fn, norm_weight, d, torch.float32, (W.HEAD_DIM,)), norm_eps,
+                                _vec(fn, positions, d, torch.int64, (n,)), table, table_rows, rope_style,
+                                _vec(fn, device_status, d, torch.int32, (1,)), _stream(stream))
     if check:
         _check(fn, rc)
     return rc
@@ -370,9 +389,14 @@ def dsa_cache_read(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
     """Fill rows [n, 512] (576 for V3.2 records; bf16, f16 or fp32, any row
     stride) with the values of the records of ``slots`` [n] int32; a slot
     outside the cache gives zeros."""
-    rc = load().dsa_cache_read(*_cache_rows("dsa_cache_read", cache, slots, rows), _stream(stream))
+    fn = "dsa_cache_read"
+    d, n = _device(fn, slots), slots.numel()
+    desc = _cache(fn, cache, d)
+    p_slots = _vec(fn, slots, d, torch.int32, (n,))
+    ptr, stride, ty = _rows(fn, rows, d, n, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM)
+    rc = load().dsa_cache_read(ctypes.byref(desc), p_slots, n, ptr, stride, ty, _stream(stream))
     if check:
-        _check("dsa_cache_read", rc)
+        _check(fn, rc)
     return rc
 
 

@@ -166,22 +166,46 @@ __global__ void __launch_bounds__(32 * kCacheWarps) cache_write_kernel(CachePara
   load16<TY>(row + 16 * lane * kTypeBytes<TY>, v);
   if constexpr (kV32) load2<TY>(row + (kD + 2 * lane) * kTypeBytes<TY>, t0, t1);
   if (sid < 0 || (int64_t)sid >= p.L.num_slots) return;   // padding: nothing is written
-  // x * w / sqrt(mean x^2 + eps) over dims 0..511
+  // x * w / sqrt(mean x^2 + eps) over dims 0..511, each result its exact
+  // value rounded to fp32 (but for a few in a hundred off by one step): a
+  // relative error of 2^-23 in front of the quantization would move the codes
+  // of four elements in a million. The squares are summed as a tree and the
+  // lanes' sums with their rounding errors; the root's reciprocal carries a
+  // correction r1, and the products theirs. 90 instructions more for a row
+  // than the plain fp32 form.
   if (p.norm_w) {
-    float ss = 0.f;
+    float sq[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) ss = fmaf(v[k], v[k], ss);
+    for (int k = 0; k < 8; ++k) sq[k] = fmaf(v[2 * k], v[2 * k], v[2 * k + 1] * v[2 * k + 1]);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float r = 1.0f / sqrtf(ss * (1.0f / kD) + p.eps);
+    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < o; ++k) sq[k] += sq[k + o];
+    float ss = sq[0], sl = 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, ss, off), ol = __shfl_xor_sync(0xffffffffu, sl, off);
+      const float t = ss + o, z = t - ss;          // ss + o = t + the error of t
+      sl += ol + ((ss - (t - z)) + (o - z));
+      ss = t;
+    }
+    const float ms = ss * (1.0f / kD), me = ms + p.eps, mz = me - ms;
+    const float ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (p.eps - mz));
+    // 1 / sqrt(me + ml) = r0 + r1: one Newton step, its residual 1 - (me + ml) r0^2 by FMAs
+    const float r0 = 1.0f / sqrtf(me);
+    const float h = me * r0, hl = fmaf(me, r0, -h) + ml * r0;
+    const float r1 = 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f));
     const float4 *w4 = reinterpret_cast<const float4 *>(p.norm_w) + 4 * lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float4 w = __ldg(w4 + k);
-      v[4 * k] *= r * w.x;
-      v[4 * k + 1] *= r * w.y;
-      v[4 * k + 2] *= r * w.z;
-      v[4 * k + 3] *= r * w.w;
+      const float wk[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float &x = v[4 * k + e];
+        const float q = x * wk[e], ql = fmaf(x, wk[e], -q);
+        x = fmaf(q, r0, fmaf(q, r1, ql * r0));
+      }
     }
   }
   // (a, b) -> (a cos - b sin, b cos + a sin) on the last 64 dims
