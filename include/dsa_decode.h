@@ -448,6 +448,75 @@ dsa_status dsa_cache_write(const dsa_cache_desc *cache, const int32_t *slots, in
 dsa_status dsa_cache_read(const dsa_cache_desc *cache, const int32_t *slots, int64_t num_rows,
                           void *rows, int64_t row_stride, int32_t row_type, dsa_stream_t stream);
 
+/* Plan of a shared-prefix call (dsa_prefix_plan). Plain data: copy it freely;
+ * callers must not edit the fields. */
+typedef struct {
+  int32_t magic;
+  int32_t abi_version;
+  int32_t num_tokens;      /* T                                              */
+  int32_t num_heads;       /* H                                              */
+  int32_t width;           /* entries of the prefix list                     */
+  int32_t d_qk;            /* 512, or 576 for V3.2 records                   */
+  int32_t num_sms;
+  int32_t pairs;           /* CTA pairs that the work is cut for             */
+  int32_t row_tiles;       /* 128-row tiles of the T*H query rows            */
+  int32_t key_tiles;       /* 128-key tiles of the list                      */
+  int64_t ws_info_offset;  /* workspace byte offsets                         */
+  int64_t ws_key_e_offset;
+  int64_t ws_image_offset;
+  int64_t ws_part_lse_offset;
+  int64_t ws_part_o_offset;
+  int64_t workspace_bytes;
+  int64_t wait_budget_cycles; /* as in dsa_decode_plan_t                     */
+  int64_t reserved[5];
+} dsa_prefix_plan_t;
+
+/* Plan the attention of num_tokens tokens over ONE list of records that all
+ * of them share (the pages decode every token over its own lists; they have
+ * no counterpart of this call). num_tokens >= 0, any num_heads >= 1, width
+ * >= 1 entries of the list (its length is read on the device), d_qk 512 or
+ * 576 (V3.2 records). num_sms: SMs to spread the work over (0 = as many CTA
+ * pairs as the current device runs at a time). Fills *plan and
+ * *workspace_bytes. Host only; launches nothing. */
+dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width, int32_t num_sms,
+                           int32_t d_qk, dsa_prefix_plan_t *plan, size_t *workspace_bytes);
+
+/* Attention over a shared prefix (no counterpart on the pages): the formulas
+ * of dsa_decode_run with the one list (slots, length) for every token, each
+ * of its records gathered and dequantized once, and the state of the token's
+ * own list merged in:
+ *   lse_p, O_p  over the kept rows of the prefix list;
+ *   lse = log(e^lse_p + e^tail_lse),
+ *   out = (e^lse_p O_p + e^tail_lse tail_out) / (e^lse + e^sink).
+ * A decode step of a batch behind a common prompt is dsa_decode_run (and
+ * dsa_decode_combine) over each token's own list with sink = NULL, then this
+ * call with its out and lse as the tail and the sink given here.
+ *   q, cache, sink, positions, cos_sin, cos_sin_rows, rope_style, scale: as
+ *     for dsa_decode_run_v41 (any head count; V32_656 needs a plan with d_qk
+ *     = 576 and no table). q_stride_t >= (H - 1) q_stride_h + d_qk.
+ *   slots: int32 [width], entries outside the cache are ignored; length:
+ *     int32 [1] on the device; entries at positions >= clamp(length, 0,
+ *     width) are ignored.
+ *   tail_out bf16 [T, H, 512] contiguous, 16-byte aligned, and tail_lse fp32
+ *     [T, H], or both NULL. tail_lse = -inf: that row has no tail (tail_out
+ *     is not read). out may be tail_out and lse may be tail_lse.
+ *   out bf16 [T, H, 512], lse fp32 [T, H], contiguous; a row with nothing
+ *     kept gives zeros and -inf.
+ *   workspace: plan->workspace_bytes, 256-byte aligned; calls that share one
+ *     must be ordered. Its first word is the device status
+ *     (dsa_decode_read_status; a position outside the table sets
+ *     DSA_ERR_INVALID_ARG and uses row 0).
+ * Precision: as dsa_decode_run, f16 products with fp32 sums; keys whose
+ * largest magnitude lies in 2^-48 .. 2^48 keep f16 precision relative to it.
+ * Three launches on `stream`; allocates nothing, never synchronizes. */
+dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t workspace_bytes,
+                          const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                          const dsa_cache_desc *cache, const int32_t *slots, const int32_t *length,
+                          const float *sink, const int64_t *positions, const float *cos_sin,
+                          int64_t cos_sin_rows, int32_t rope_style, float scale,
+                          const void *tail_out, const float *tail_lse, void *out, float *lse,
+                          dsa_stream_t stream);
+
 /* Static description of a status code (no counterpart on the pages). */
 const char *dsa_decode_status_string(dsa_status s);
 

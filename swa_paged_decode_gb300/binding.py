@@ -26,6 +26,7 @@ EXPORTED = ("dsa_decode_plan", "dsa_decode_plan_qk", "dsa_decode_run", "dsa_deco
             "dsa_decode_read_status", "dsa_decode_status_string", "dsa_decode_abi_version",
             "dsa_decode_run_noalloc", "dsa_decode_run_v41", "dsa_decode_combine_v41")
 EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
+EXPORTED_PREFIX = ("dsa_prefix_plan", "dsa_prefix_run")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
 ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # DSA_TYPE_*
@@ -54,6 +55,16 @@ class Plan(ctypes.Structure):
             "ws_stage_offset", "workspace_bytes_mx", "wait_budget_cycles", "d_qk",
             "producer_q", "merge_in_run", "ws_count_offset")] + \
         [("reserved", ctypes.c_int64 * 7)]
+
+
+class PrefixPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "magic", "abi_version", "num_tokens", "num_heads", "width", "d_qk", "num_sms", "pairs",
+        "row_tiles", "key_tiles")] + \
+        [(n, ctypes.c_int64) for n in (
+            "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_part_lse_offset",
+            "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
+        [("reserved", ctypes.c_int64 * 5)]
 
 
 _lib = None
@@ -154,6 +165,13 @@ def _load_path(path: str):
                                     ctypes.c_float, vp, vp, i64, i32, vp, vp]
     lib.dsa_cache_read.restype = ctypes.c_int
     lib.dsa_cache_read.argtypes = [ctypes.POINTER(CacheDesc), vp, i64, vp, i64, i32, vp]
+    lib.dsa_prefix_plan.restype = ctypes.c_int
+    lib.dsa_prefix_plan.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(PrefixPlan),
+                                    ctypes.POINTER(ctypes.c_size_t)]
+    lib.dsa_prefix_run.restype = ctypes.c_int
+    lib.dsa_prefix_run.argtypes = [ctypes.POINTER(PrefixPlan), vp, ctypes.c_size_t, vp, i64, i64,
+                                   ctypes.POINTER(CacheDesc), vp, vp, vp, vp, vp, i64, i32,
+                                   ctypes.c_float, vp, vp, vp, vp, vp]
     lib.dsa_decode_status_string.restype = ctypes.c_char_p
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
@@ -398,6 +416,69 @@ def dsa_cache_read(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
     if check:
         _check(fn, rc)
     return rc
+
+
+def dsa_prefix_plan(num_tokens: int, num_heads: int, width: int, num_sms: int = 0,
+                    d_qk: int = 512):
+    """-> (PrefixPlan, workspace_bytes)."""
+    plan = PrefixPlan()
+    ws = ctypes.c_size_t(0)
+    _check("dsa_prefix_plan", load().dsa_prefix_plan(num_tokens, num_heads, width, num_sms, d_qk,
+                                                     ctypes.byref(plan), ctypes.byref(ws)))
+    return plan, int(ws.value)
+
+
+def dsa_prefix_run(plan: PrefixPlan, workspace: torch.Tensor, q: torch.Tensor, cache: W.PagedCache,
+                   slots: torch.Tensor, length: torch.Tensor, sink: Optional[torch.Tensor],
+                   positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                   rope_style: int, scale: float, tail_out: Optional[torch.Tensor],
+                   tail_lse: Optional[torch.Tensor], out: torch.Tensor, lse: torch.Tensor,
+                   stream=None, check: bool = True) -> int:
+    """Attention of every token over the shared list ``slots`` [width] int32
+    of ``length`` [1] int32 (on the device), merged with the tail state."""
+    fn = "dsa_prefix_run"
+    d = _device(fn, q)
+    T, H = plan.num_tokens, plan.num_heads
+    if q.dtype != torch.bfloat16 or q.shape != (T, H, plan.d_qk) or (q.stride(2) != 1 and T > 0):
+        raise DsaError(fn, -1)
+    desc = _cache(fn, cache, d)
+    table, table_rows = _table(fn, cos_sin, d)
+    head, full = (T, H), (T, H, W.HEAD_DIM)
+    rc = load().dsa_prefix_run(
+        ctypes.byref(plan), _vec(fn, workspace, d, torch.uint8, (workspace.numel(),)),
+        workspace.numel(), q.data_ptr(), q.stride(0) if T > 1 else max(q.stride(0), H * plan.d_qk),
+        q.stride(1) if H > 1 else plan.d_qk, ctypes.byref(desc),
+        _vec(fn, slots, d, torch.int32, (plan.width,)), _vec(fn, length, d, torch.int32, (1,)),
+        _vec(fn, sink, d, torch.float32, (H,)), _vec(fn, positions, d, torch.int64, (T,)), table,
+        table_rows, rope_style, scale, _vec(fn, tail_out, d, torch.bfloat16, full),
+        _vec(fn, tail_lse, d, torch.float32, head), _vec(fn, out, d, torch.bfloat16, full),
+        _vec(fn, lse, d, torch.float32, head), _stream(stream))
+    if check:
+        _check(fn, rc)
+    return rc
+
+
+class PrefixAttention:
+    """Plan + workspace for T tokens of H heads behind one shared list of up
+    to ``width`` records; ``__call__`` runs on the current stream and returns
+    (``self.out``, ``self.lse``). Behind each token's own list: a ``Decoder``
+    of a workload without a sink gives ``tail_out`` and ``tail_lse``, and the
+    sink goes here."""
+
+    def __init__(self, T: int, H: int, width: int, device, d_qk: int = 512, num_sms: int = 0):
+        self.plan, nbytes = dsa_prefix_plan(T, H, width, num_sms, d_qk)
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        self.out = torch.empty((T, H, W.HEAD_DIM), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((T, H), dtype=torch.float32, device=device)
+
+    def __call__(self, q: torch.Tensor, cache: W.PagedCache, slots: torch.Tensor,
+                 length: torch.Tensor, scale: float, sink: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+                 rope_style: int = DSA_ROPE_NEOX, tail_out: Optional[torch.Tensor] = None,
+                 tail_lse: Optional[torch.Tensor] = None, stream=None):
+        dsa_prefix_run(self.plan, self.workspace, q, cache, slots, length, sink, positions, cos_sin,
+                       rope_style, scale, tail_out, tail_lse, self.out, self.lse, stream)
+        return self.out, self.lse
 
 
 class Decoder:

@@ -1,0 +1,1003 @@
+// dsa_prefix.cu -- attention of a whole decode batch over one shared list of
+// records (dsa_prefix_plan / dsa_prefix_run): T tokens x H heads = `rows`
+// query rows against P keys, every key gathered and dequantized once.
+//
+//   s_rj = scale q_r . k_j,  lse_r = log sum_j e^{s_rj},
+//   O_r = sum_j e^{s_rj - lse_r} v_j     (v_j = dims 0..511 of k_j)
+//
+// and, with the state (O', lse') of the token's own list and the sink z,
+//   lse = log(e^{lse_r} + e^{lse'}),
+//   out = (e^{lse_r} O_r + e^{lse'} O') / (e^lse + e^z).
+//
+// Three launches, each the programmatic dependent of the one before it:
+//   gather  32 records per block -> f16 tile images in the workspace, each
+//           value times 2^-E, E the exponent of the 32 keys' largest value
+//           (one per key where their magnitudes differ by more than 2^5);
+//   attend  pairs of CTAs (tcgen05 cta_group::2) on 128 query rows, a range
+//           of (row tile, key tile) units per pair;
+//   merge   the rows whose key tiles were split over pairs, and the rows of
+//           an empty prefix.
+#include <cmath>
+#include <cstring>
+
+#include "dsa_host.cuh"
+#include "dsa_records.cuh"
+
+namespace dsa {
+
+constexpr int32_t kPrefixMagic = 0x50415344;   // "DSAP"
+constexpr int kPfGroup = 32;                   // keys that share an exponent
+constexpr int kPfSpread = 5;                   // log2 spread of their magnitudes up to which they do
+constexpr int kPfTop = 14;                     // the largest value's exponent in the f16 tile
+constexpr int kPfRange = 48;                   // exponents of the keys' magnitudes: -48..48
+constexpr int32_t kPfNoKey = INT32_MAX;        // exponent of a key that is not kept
+constexpr int32_t kPfMixed = INT32_MIN;        // group exponent: one per key instead
+
+struct PrefixParams {
+  ListArgs L;                  // the cache; ids: the prefix list, lens: its length, width
+  const __nv_bfloat16 *q;
+  int64_t q_st, q_sh;
+  const float *sink;
+  const int64_t *positions;
+  const float *cos_sin;
+  int64_t cs_rows;
+  int32_t gptj;
+  float scale_log2;
+  const __nv_bfloat16 *tail_out;   // [T, H, 512] state of the token's own list, or null
+  const float *tail_lse;
+  __nv_bfloat16 *out;
+  float *lse;
+  int32_t T, H, rows, R;       // query rows, 128-row tiles
+  int32_t C;                   // CTA pairs
+  long long wait_budget;
+  // workspace
+  int32_t *status;
+  int2 *info;                  // [groups] (exponent or kPfMixed, mask of kept keys)
+  int32_t *key_e;              // [keys] exponent of each key
+  uint8_t *image;              // [key tile][64-dim block][8-key group][1 KiB]
+  float *part_lse;             // [2C][128]
+  float *part_o;               // [2C][128][512]
+};
+
+// min(len, width) of the prefix list, and its 128-key tiles
+__device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &len) {
+  len = list_limit(p.L, 0);
+  return (len + 127) >> 7;
+}
+// Units are (row tile, key tile) pairs, row tile major; pair c owns
+// [pair_begin(c), pair_begin(c + 1)).
+__device__ __forceinline__ int64_t pair_begin(int64_t U, int32_t C, int32_t c) { return U * c / C; }
+
+// Weights of a row's prefix state (normalized, lse) and of its tail state in
+// the output, and the lse of both: M = the larger lse, den = e^{lse - M} +
+// e^{lse' - M} (+ e^{z - M}); a state with lse = -inf weighs nothing.
+struct RowWeights {
+  float o, tail, lse;
+};
+__device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int64_t gr, int32_t h, float lse) {
+  const float lt = p.tail_lse ? p.tail_lse[gr] : -INFINITY;
+  const float M = fmaxf(lse, lt);
+  RowWeights w = {0.f, 0.f, -INFINITY};
+  if (!(M > -INFINITY)) {
+    if (lse != lse || lt != lt) w.o = w.tail = w.lse = __uint_as_float(0x7FC00000u);
+    return w;
+  }
+  const float a = expf(lse - M), b = expf(lt - M), z = a + b;
+  w.lse = M + logf(z);
+  float den = z;
+  if (p.sink) {
+    const float sk = __ldg(p.sink + h);
+    den = sk == INFINITY ? INFINITY : z + expf(sk - M);
+  }
+  w.o = a / den;
+  w.tail = b / den;
+  return w;
+}
+// 16 dims of a row's output: o (weighted) + wt * tail, as bf16. A tail that
+// weighs nothing is not read.
+__device__ __forceinline__ void store_out16(const PrefixParams &p, int64_t gr, int d, float (&o)[16], float wt) {
+  const int64_t at = gr * kD + d;
+  if (p.tail_out && wt != 0.f) {
+    const uint4 *t = reinterpret_cast<const uint4 *>(p.tail_out + at);
+    const uint4 a = t[0], b = t[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[2 * i] = fmaf(wt, bf16_bits_to_f32(w[i] & 0xFFFFu), o[2 * i]);
+      o[2 * i + 1] = fmaf(wt, bf16_bits_to_f32(w[i] >> 16), o[2 * i + 1]);
+    }
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  uint4 *d4 = reinterpret_cast<uint4 *>(p.out + at);
+  d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// ------------------------------------------------------------ gather
+template <int FMT>
+__global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
+  constexpr bool kV32 = FMT == DSA_REC_V32_656;
+  constexpr int kDB = kV32 ? 9 : 8;   // 64-dim blocks of a key
+  __shared__ int32_t e_s[kPfGroup];
+  // (the checking build clears the word before this launch instead)
+  if (!kDebug && blockIdx.x == 0 && threadIdx.x == 0) *p.status = DSA_OK;
+  pdl_launch_dependents();
+  int32_t len;
+  const int32_t tiles = prefix_tiles(p, len);
+  const int32_t key0 = blockIdx.x * kPfGroup;
+  if (key0 >= tiles * 128) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float v[4][16], t[4][2];
+  // 4 keys per warp, their loads in flight together
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t r = key0 + 4 * warp + i;
+    const int32_t sid = r < len ? __ldg(p.L.ids + r) : -1;
+    bool ok = slot_valid(p.L, r, len, sid);
+    const uint8_t *rec = record_ptr(p.L, ok ? sid : 0);
+    if (ok) ok = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[i][k] = 0.f;
+    t[i][0] = t[i][1] = 0.f;
+    if (ok) decode_record<FMT>(rec, lane, v[i], t[i][0], t[i][1]);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[i][k]) & 0x7FFFFFFFu);
+    if constexpr (kV32) m = max(m, max(__float_as_uint(t[i][0]) & 0x7FFFFFFFu, __float_as_uint(t[i][1]) & 0x7FFFFFFFu));
+    m = __reduce_max_sync(0xffffffffu, m);
+    const int e = (int)(m >> 23) - 127;
+    if (lane == 0)
+      e_s[4 * warp + i] = !ok ? kPfNoKey : (e < -kPfRange ? -kPfRange : (e > kPfRange ? kPfRange : e));
+  }
+  __syncthreads();
+  const int my = e_s[lane];   // lane's key of the 32
+  const bool kept = my != kPfNoKey;
+  const int hi = __reduce_max_sync(0xffffffffu, kept ? my : -kPfRange);
+  const int lo = __reduce_min_sync(0xffffffffu, kept ? my : kPfRange);
+  const uint32_t mask = __ballot_sync(0xffffffffu, kept);
+  const bool mixed = mask != 0u && hi - lo > kPfSpread;
+  if (warp == 0) {
+    p.key_e[key0 + lane] = (kept ? (mixed ? my : hi) : hi) - kPfTop;
+    if (lane == 0) p.info[blockIdx.x] = make_int2(mixed ? kPfMixed : hi - kPfTop, (int)mask);
+  }
+  // image: key r of the tile in row r % 8 of 8-key group r / 8, 16-byte
+  // chunk c of its 128 bytes at c ^ (r % 8)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t r = key0 + 4 * warp + i;
+    const int es = e_s[4 * warp + i];
+    const int E = ((mixed && es != kPfNoKey) ? es : hi) - kPfTop;
+    const float down = __uint_as_float((uint32_t)(127 - E) << 23);
+    const int64_t tile = r >> 7;
+    const int g = (r & 127) >> 3, x = r & 7;
+    uint8_t *base = p.image + tile * (kDB * 16384) + g * 1024 + x * 128;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = tc::pack_f16x2(v[i][2 * k] * down, v[i][2 * k + 1] * down);
+    uint8_t *b = base + (lane >> 2) * 16384;
+    const int c0 = 2 * (lane & 3);
+    *reinterpret_cast<uint4 *>(b + ((c0 ^ x) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(b + (((c0 + 1) ^ x) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    if constexpr (kV32)
+      *reinterpret_cast<uint32_t *>(base + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) =
+          tc::pack_f16x2(t[i][0] * down, t[i][1] * down);
+  }
+}
+
+// ------------------------------------------------------------ attend
+// A pair of CTAs works on 128 query rows x 128 keys at a time:
+//   S[128, 128] = Q . K^T   M = 128 over the pair (64 query rows in each
+//       CTA), N = 128 keys (64 keys' rows of the operand in each CTA);
+//   O[128, 512] += P . V    two N = 256 halves, 128 dims of each in either
+//       CTA's shared memory; the accumulator takes 256 of the 512 TMEM
+//       columns, S twice 64.
+// One CTA alone cannot hold this: O for 128 rows fills all of its TMEM. In
+// the pair's layout lane l of CTA r holds row 64 r + l % 64, and the upper
+// half of each product's columns sits in lanes 64..127.
+//
+// K and V of a unit come as 16 KiB chunks of the tile images (K: 64 keys x
+// 128 dims; V: 32 keys x 256 dims, both contiguous runs of the same image, the
+// one read K-major, the other MN-major) through one ring in the order of their
+// use: QK of unit i + 1 is issued before PV of unit i, so the softmax of a
+// unit overlaps the products around it.
+//
+// Roles: warps 0-7 softmax (a row is held by 4 threads, 32 keys each), Q
+// staging and the epilogue; warp 8 copies; warp 9 issues the MMAs (leader
+// CTA) or tells the leader which chunks have landed here (the other CTA).
+// Every wait is bounded as in the decode kernel.
+constexpr int kPfThreads = 320;
+constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
+
+template <bool V32>
+struct PfCfg {
+  static constexpr int kDB = V32 ? 9 : 8;
+  static constexpr int kKChunks = V32 ? 5 : 4;               // the fifth holds 64 dims
+  static constexpr int kSlots = V32 ? 8 : 9;
+  static constexpr uint32_t kQ = 0;                          // [kDB][64 rows x 64 dims] f16
+  static constexpr uint32_t kP = kDB * 8192;                 // [2][64 rows x 64 keys] f16
+  static constexpr uint32_t kRing = kP + 16384;
+  static constexpr uint32_t kRed = kRing + kSlots * 16384;   // [4][64] f32
+  static constexpr uint32_t kHeadF = kRed + 1024;            // [64] f32: scale log2(e) 2^e of a row
+  static constexpr uint32_t kRowW = kHeadF + 256;            // [3][64] f32 epilogue weights
+  static constexpr uint32_t kMisc = kRowW + 768;
+  static constexpr uint32_t kBytes = kMisc + 512;
+  static constexpr uint32_t kSmem = kBytes + 1024 > 232448u ? 232448u : kBytes + 1024;
+  static constexpr uint32_t kIdQK = tc::idesc_f16(128, 128, false, false);
+  static constexpr uint32_t kIdPV = tc::idesc_f16(128, 256, false, true);
+  static constexpr uint32_t kColO = 0, kColS = 256;
+  // barriers (8 bytes each) in the misc area
+  static constexpr int kFull = 0, kPeer = kSlots, kEmpty = 2 * kSlots, kSFull = 3 * kSlots,
+                       kPFull = kSFull + 2, kPvDone = kPFull + 1, kQReady = kPvDone + 1,
+                       kDrain = kQReady + 1, kBars = kDrain + 1;
+  static constexpr uint32_t kAbort = 8 * kBars, kTmem = kAbort + 4;
+  static_assert(kTmem + 4 <= 512, "misc area");
+  static_assert(kBytes <= 232448u, "shared memory layout exceeds 227 KiB");
+};
+
+template <bool kV32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
+    prefix_attend_kernel(PrefixParams p) {
+  using Cfg = PfCfg<kV32>;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = tc::smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+  uint8_t *smem = smem_raw + pad;
+  const uint32_t sbase = raw_base + pad;
+  const uint32_t q_base = sbase + Cfg::kQ, p_base = sbase + Cfg::kP, ring = sbase + Cfg::kRing;
+  float *red_s = reinterpret_cast<float *>(smem + Cfg::kRed);
+  float *headf_s = reinterpret_cast<float *>(smem + Cfg::kHeadF);
+  float *roww_s = reinterpret_cast<float *>(smem + Cfg::kRowW);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kMisc);
+  volatile int32_t *abort_s = reinterpret_cast<volatile int32_t *>(smem + Cfg::kMisc + Cfg::kAbort);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kMisc + Cfg::kTmem);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair = blockIdx.x >> 1;
+  int32_t len;
+  const int32_t KT = prefix_tiles(p, len);
+  const int64_t U = (int64_t)p.R * KT;
+  const int64_t u0 = pair_begin(U, p.C, pair), u1 = pair_begin(U, p.C, pair + 1);
+  if (u0 >= u1 || pad + Cfg::kBytes > Cfg::kSmem) {   // both CTAs of a pair alike
+    if (u0 < u1 && tid == 0) report_status(p.status, DSA_ERR_UNSUPPORTED);
+    pdl_wait_primary();
+    return;
+  }
+  if (warp == 0) tc::tmem_alloc_pair(tmem_slot, 512);
+  if (tid == 0) {
+    for (int b = 0; b < Cfg::kBars; ++b)
+      tc::mbar_init(&bars[b], (b == Cfg::kPFull || b == Cfg::kQReady) ? 16u : 1u);
+    tc::fence_mbar_init();
+    *abort_s = 0;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](int b, uint32_t phase) {
+    if (!*abort_s) {
+      const long long budget = p.wait_budget > 0 ? p.wait_budget : kPfWait;
+      if (!tc::mbar_wait_cluster(&bars[b], phase, budget) && !*abort_s) {
+        *abort_s = 1;
+        report_status(p.status, DSA_ERR_TIMEOUT);
+      }
+    }
+  };
+  const uint32_t lead_pfull = tc::mapa(tc::smem_u32(&bars[Cfg::kPFull]), 0);
+  const uint32_t lead_qready = tc::mapa(tc::smem_u32(&bars[Cfg::kQReady]), 0);
+
+  if (warp == 8) {
+    // ======================================================== copies
+    if (lane == 0) {
+      pdl_wait_primary();   // the images are complete
+      uint32_t slot = 0, ph = 1;   // the first round finds every slot empty
+      uint32_t used = 0;           // slots filled so far (at most kSlots counted)
+      auto next = [&]() {
+        if (++slot == Cfg::kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      };
+      const uint8_t *img = p.image;
+      auto load_k = [&](int64_t kt) {   // this CTA's 64 keys, 128 dims a chunk
+        const uint8_t *t = img + kt * (Cfg::kDB * 16384) + rank * 8192;
+#pragma unroll 1
+        for (int c = 0; c < Cfg::kKChunks; ++c) {
+          wait(Cfg::kEmpty + slot, ph);
+          if (*abort_s) return;
+          const int nb = (kV32 && c == 4) ? 1 : 2;
+          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], nb * 8192u);
+          for (int b = 0; b < nb; ++b)
+            tc::bulk_load(ring + slot * 16384 + b * 8192, t + (2 * c + b) * 16384, 8192u, &bars[Cfg::kFull + slot]);
+          used = used < Cfg::kSlots ? used + 1 : used;
+          next();
+        }
+      };
+      auto load_v = [&](int64_t kt) {   // all keys, this CTA's 4 dim blocks, 32 keys a chunk
+        const uint8_t *t = img + kt * (Cfg::kDB * 16384) + (2 * rank) * 16384;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          wait(Cfg::kEmpty + slot, ph);
+          if (*abort_s) return;
+          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 16384u);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)   // dims 128 rank + 64 b of the first and the second half
+            tc::bulk_load(ring + slot * 16384 + b * 4096, t + ((b >> 1) * 4 + (b & 1)) * 16384 + s * 4096, 4096u,
+                          &bars[Cfg::kFull + slot]);
+          used = used < Cfg::kSlots ? used + 1 : used;
+          next();
+        }
+      };
+      for (int64_t u = u0; u < u1 && !*abort_s;) {
+        const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
+        load_k(u - qt * KT);
+        for (; u < end && !*abort_s; ++u) {
+          if (u + 1 < end) load_k(u + 1 - qt * KT);
+          if (!*abort_s) load_v(u - qt * KT);
+        }
+      }
+      // The slots' last releases have arrived: no commit of the leader
+      // reaches this CTA's barriers after its end. (A slot that was never
+      // filled passes at once.)
+      {
+        uint32_t sl = slot, pz = ph;
+        for (int k = 0; k < Cfg::kSlots && !*abort_s; ++k) {
+          wait(Cfg::kEmpty + sl, pz);
+          if (++sl == Cfg::kSlots) {
+            sl = 0;
+            pz ^= 1u;
+          }
+        }
+      }
+      // after a timeout: no copy may be in flight into shared memory when
+      // the CTA ends (the slots' latest fills, whatever their phase)
+      if (*abort_s)
+        for (uint32_t k = 0; k < used; ++k) {
+          const uint32_t s = (slot + Cfg::kSlots - 1 - k) % Cfg::kSlots;
+          const uint32_t fph = (s < slot ? ph : ph ^ 1u) ^ 1u;
+          tc::mbar_wait(&bars[Cfg::kFull + s], fph, kPfWait);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      uint32_t slot = 0, ph = 0;
+      auto next = [&]() {
+        if (++slot == Cfg::kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      };
+      if (rank == 1) {
+        // ==================================================== relay
+        const int64_t chunks = (u1 - u0) * (Cfg::kKChunks + 4);
+        for (int64_t k = 0; k < chunks && !*abort_s; ++k) {
+          wait(Cfg::kFull + slot, ph);
+          if (!*abort_s) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars[Cfg::kPeer + slot]), 0));
+          next();
+        }
+      } else {
+        // ==================================================== MMA issue
+        const uint64_t dq = tc::sdesc(q_base, 16, 1024, tc::kSwz128);
+        const uint64_t dp = tc::sdesc(p_base, 16, 1024, tc::kSwz128);
+        uint32_t ph_p = 0, ph_q = 0, nqk = 0;
+        bool issued = false;
+        auto chunk_wait = [&]() {
+          wait(Cfg::kFull + slot, ph);
+          wait(Cfg::kPeer + slot, ph);
+          tc::tc_fence_after();
+        };
+        auto qk = [&]() {
+          const uint32_t d = tmem + Cfg::kColS + (nqk & 1u) * 64u;
+#pragma unroll 1
+          for (int c = 0; c < Cfg::kKChunks; ++c) {
+            chunk_wait();
+            if (*abort_s) return;
+            const uint64_t dk = tc::sdesc(ring + slot * 16384, 16, 1024, tc::kSwz128);
+            const int nb = (kV32 && c == 4) ? 1 : 2;
+            for (int b = 0; b < nb; ++b)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc::mma_f16_pair(d, dq + (uint64_t)(((2 * c + b) * 8192 + ks * 32) >> 4),
+                                 dk + (uint64_t)((b * 8192 + ks * 32) >> 4), Cfg::kIdQK,
+                                 (c | b | ks) ? 1u : 0u);
+            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
+            next();
+          }
+          tc::mma_commit_pair(&bars[Cfg::kSFull + (nqk & 1u)]);
+          issued = true;
+          ++nqk;
+        };
+        auto pv = [&](bool first) {
+          wait(Cfg::kPFull, ph_p);
+          ph_p ^= 1u;
+#pragma unroll 1
+          for (int s = 0; s < 4; ++s) {
+            chunk_wait();
+            if (*abort_s) return;
+            const uint64_t dv = tc::sdesc(ring + slot * 16384, 4096, 1024, tc::kSwz128);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tc::mma_f16_pair(tmem + Cfg::kColO + 128 * j,
+                                 dp + (uint64_t)(((s >> 1) * 8192 + (s & 1) * 64 + ks * 32) >> 4),
+                                 dv + (uint64_t)((j * 8192 + ks * 2048) >> 4), Cfg::kIdPV,
+                                 (first && s == 0 && ks == 0) ? 0u : 1u);
+            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
+            next();
+          }
+          tc::mma_commit_pair(&bars[Cfg::kPvDone]);
+        };
+        for (int64_t u = u0; u < u1 && !*abort_s;) {
+          const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
+          wait(Cfg::kQReady, ph_q);
+          ph_q ^= 1u;
+          if (*abort_s) break;
+          tc::tc_fence_after();
+          qk();
+          const int64_t first = u;
+          for (; u < end && !*abort_s; ++u) {
+            if (u + 1 < end) qk();
+            if (!*abort_s) pv(u == first);
+          }
+        }
+        if (*abort_s && issued) {   // MMAs issued before a timeout end before TMEM is freed
+          tc::mma_commit_one(&bars[Cfg::kDrain]);
+          tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ======================================================== softmax
+    const int q4 = warp & 3, half = warp >> 2;
+    const int lr = 32 * q4 + lane;             // TMEM lane
+    const int row = lr & 63, kh = lr >> 6;     // query row of this CTA, half of the tile's keys
+    const int grp = 2 * kh + half;             // its 32-key group of the tile
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
+    auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
+    auto sm_bar_or = [&](bool x) {
+      int r;
+      asm volatile(
+          "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\t"
+          "barrier.red.or.pred b, 1, 256, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
+          : "=r"(r) : "r"((int)x) : "memory");
+      return r != 0;
+    };
+    bool bad_pos = false;   // reported once the gather, which clears the status word, is done
+    // Q rows of this CTA -> f16 K-major tile, RoPE in fp32, then a power of
+    // two per row so that its largest magnitude lies in [1, 2).
+    auto stage_q = [&](int64_t qt) {
+      const bool rl = lane >= 28;
+      const int ca = rl ? 56 + (lane - 28) : 2 * lane, cb = rl ? 60 + (lane - 28) : 2 * lane + 1;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        uint4 qa[4], qb[4], qc[4];
+        int32_t tok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t gr = qt * 128 + rank * 64 + 8 * warp + i0 + i;
+          qa[i] = qb[i] = qc[i] = make_uint4(0, 0, 0, 0);
+          tok[i] = -1;
+          if (gr < p.rows) {
+            const int32_t t = (int32_t)(gr / p.H), h = (int32_t)(gr - (int64_t)t * p.H);
+            tok[i] = t;
+            const uint4 *qh = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
+            qa[i] = __ldg(qh + ca);
+            qb[i] = __ldg(qh + cb);
+            if (kV32 && lane < 8) qc[i] = __ldg(qh + 64 + lane);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * warp + i0 + i;
+          const uint32_t w[8] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w, qb[i].x, qb[i].y, qb[i].z, qb[i].w};
+          float v[16], vc[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu);
+            v[2 * k + 1] = bf16_bits_to_f32(w[k] >> 16);
+          }
+          if (p.cos_sin && tok[i] >= 0 && rl) {
+            int64_t pos = __ldg(p.positions + tok[i]);
+            if (pos < 0 || pos >= p.cs_rows) {   // outside the table: flag, row 0
+              bad_pos = true;
+              pos = 0;
+            }
+            const float4 *cs = reinterpret_cast<const float4 *>(p.cos_sin + pos * 64);
+            const int f0 = p.gptj ? lane - 28 : 2 * (lane - 28), f1 = p.gptj ? lane - 24 : 2 * (lane - 28) + 1;
+            const float4 c0 = __ldg(cs + f0), c1 = __ldg(cs + f1), s0 = __ldg(cs + 8 + f0), s1 = __ldg(cs + 8 + f1);
+            const float c8[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const float s8[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {   // GPT-J (2k, 2k + 1); NeoX (k, 8 + k)
+              const float x1 = p.gptj ? v[2 * k] : v[k], x2 = p.gptj ? v[2 * k + 1] : v[8 + k];
+              const float y1 = fmaf(x1, c8[k], -(x2 * s8[k])), y2 = fmaf(x2, c8[k], x1 * s8[k]);
+              if (p.gptj) {
+                v[2 * k] = y1;
+                v[2 * k + 1] = y2;
+              } else {
+                v[k] = y1;
+                v[8 + k] = y2;
+              }
+            }
+          }
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(v[k]));
+          if constexpr (kV32) {
+            const uint32_t wc[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              vc[2 * k] = bf16_bits_to_f32(wc[k] & 0xFFFFu);
+              vc[2 * k + 1] = bf16_bits_to_f32(wc[k] >> 16);
+              mx = fmaxf(mx, fmaxf(fabsf(vc[2 * k]), fabsf(vc[2 * k + 1])));
+            }
+          }
+          const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+          int e = mb ? (int)((mb >> 23) & 0xFF) - 127 : 0;
+          e = e < -126 ? -126 : (e > 126 ? 126 : e);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (lane == 0) headf_s[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          uint32_t f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k] * down, v[2 * k + 1] * down);
+          const uint32_t ro = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
+          tc::st_shared_v4(q_base + (ca >> 3) * 8192 + ro + (((ca & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+          tc::st_shared_v4(q_base + (cb >> 3) * 8192 + ro + (((cb & 7) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+          if constexpr (kV32) {
+            if (lane < 8) {
+              uint32_t fc[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) fc[k] = tc::pack_f16x2(vc[2 * k] * down, vc[2 * k + 1] * down);
+              tc::st_shared_v4(q_base + 8 * 8192 + ro + ((lane ^ (r & 7)) << 4), fc[0], fc[1], fc[2], fc[3]);
+            }
+          }
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_remote(lead_qready);
+    };
+
+    uint32_t ph_s = 0, nqk = 0, ph_pv = 0;
+    const uint32_t prow = p_base + kh * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
+    bool waited = false;
+    for (int64_t u = u0; u < u1;) {
+      const int64_t qt = u / KT, first = u, end = min((qt + 1) * KT, u1);
+      stage_q(qt);
+      if (!waited) {
+        pdl_wait_primary();   // group records of the gather
+        waited = true;
+      }
+      if (bad_pos) report_status(p.status, DSA_ERR_INVALID_ARG);
+      sm_bar();   // headf_s
+      const float hf = headf_s[row];
+      float m = -1e30f, l = 0.f;
+      int2 inf = __ldcg(p.info + (u - qt * KT) * 4 + grp);
+      for (; u < end; ++u) {
+        const int64_t kt = u - qt * KT;
+        const int2 cur = inf;
+        if (u + 1 < end) inf = __ldcg(p.info + (kt + 1) * 4 + grp);
+        const uint32_t mask = (uint32_t)cur.y;
+        const bool mixed = cur.x == kPfMixed;
+        const int32_t *ke = p.key_e + kt * 128 + grp * 32;
+        const float er = mixed ? 0.f : (float)cur.x;
+        const float a = mixed ? 0.f : hf * __uint_as_float((uint32_t)(127 + cur.x) << 23);
+        float x[32];
+        auto load_y = [&]() {   // y = score in log2 units + exponent of the key
+          const uint32_t c = tl + Cfg::kColS + (nqk & 1u) * 64u + half * 32;
+          uint32_t ra[16], rb[16];
+          tc::tmem_ld16x2(c, c + 16, ra, rb);
+          if (!mixed) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              x[i] = fmaf(__uint_as_float(ra[i]), a, er);
+              x[16 + i] = fmaf(__uint_as_float(rb[i]), a, er);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = __ldcg(ke + i);
+              x[i] = fmaf(__uint_as_float(i < 16 ? ra[i & 15] : rb[i & 15]),
+                          hf * __uint_as_float((uint32_t)(127 + e) << 23), (float)e);
+            }
+          }
+          if (mask != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((mask >> i) & 1u)) x[i] = -INFINITY;
+          }
+        };
+        wait(Cfg::kSFull + (nqk & 1u), ph_s);
+        tc::tc_fence_after();
+        load_y();
+        bool need = u == first;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+        need |= top > m + 8.0f;
+        if (sm_bar_or(need)) {
+          red_s[(2 * kh + half) * 64 + row] = top;
+          sm_bar();
+          const float tm = fmaxf(fmaxf(red_s[row], red_s[64 + row]), fmaxf(red_s[128 + row], red_s[192 + row]));
+          const float mn = fmaxf(m, tm);
+          const float f = tc::ex2(m - mn);   // 0 before the first kept key
+          m = mn;
+          l *= f;
+          if (u > first) {
+            wait(Cfg::kPvDone, ph_pv);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int g = 0; g < 8; ++g) {
+              const uint32_t ta = tl + Cfg::kColO + half * 128 + 16 * g;
+              float o[16];
+              tc::tmem_ld<16>(ta, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tc::tmem_st<16>(ta, o);
+            }
+          }
+          sm_bar();   // red_s free again
+        } else {
+          wait(Cfg::kPvDone, ph_pv);   // (the segment's first unit always takes the other branch)
+        }
+        if (u > first) ph_pv ^= 1u;
+        // P = 2^(y - m); the sums take P 2^-E = 2^(x - m)
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = tc::ex2(x[i] - m);
+        if (!mixed) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s += x[i];
+          l = fmaf(s, __uint_as_float((uint32_t)(127 - cur.x) << 23), l);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) l = fmaf(x[i], __uint_as_float((uint32_t)(127 - __ldcg(ke + i)) << 23), l);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::st_shared_v4(prow + (((half * 4 + k) ^ (row & 7)) << 4), tc::pack_f16x2(x[8 * k], x[8 * k + 1]),
+                           tc::pack_f16x2(x[8 * k + 2], x[8 * k + 3]), tc::pack_f16x2(x[8 * k + 4], x[8 * k + 5]),
+                           tc::pack_f16x2(x[8 * k + 6], x[8 * k + 7]));
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(lead_pfull);
+        ++nqk;
+        if ((nqk & 1u) == 0) ph_s ^= 1u;
+      }
+      // ---- epilogue
+      red_s[(2 * kh + half) * 64 + row] = l;
+      const int64_t gr = qt * 128 + rank * 64 + row;
+      const bool live = gr < p.rows;
+      const bool whole = first == qt * KT && end == (qt + 1) * KT;
+      const int64_t ps = (2 * (int64_t)pair + (qt == u0 / KT ? 0 : 1)) * 128 + rank * 64 + row;
+      sm_bar();
+      if (tid < 64) {   // row tid: lane tid of the lower half holds it
+        const float lt = (red_s[row] + red_s[64 + row]) + (red_s[128 + row] + red_s[192 + row]);
+        // (a NaN among the scores or values stays one)
+        const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
+        float wo = lt == 0.f ? 0.f : 1.f / lt, wt = 0.f;
+        if (whole) {
+          if (live) {
+            const int32_t h = (int32_t)(gr % p.H);
+            const RowWeights w = row_weights(p, gr, h, lse);
+            wo *= w.o;
+            wt = w.tail;
+            p.lse[gr] = w.lse;
+          }
+        } else {
+          p.part_lse[ps] = lse;
+        }
+        roww_s[row] = wo;
+        roww_s[64 + row] = wt;
+      }
+      wait(Cfg::kPvDone, ph_pv);
+      ph_pv ^= 1u;
+      tc::tc_fence_after();
+      sm_bar();
+      const float wo = roww_s[row], wt = roww_s[64 + row];
+      const int d0 = half * 256 + kh * 128;   // this thread's 128 dims
+#pragma unroll 1
+      for (int g = 0; g < 8; ++g) {
+        float o[16];
+        tc::tmem_ld<16>(tl + Cfg::kColO + half * 128 + 16 * g, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] *= wo;
+        if (!whole) {
+          float4 *d = reinterpret_cast<float4 *>(p.part_o + ps * kD + d0 + 16 * g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) __stcg(d + i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+        } else if (live) {
+          store_out16(p, gr, d0 + 16 * g, o, wt);
+        }
+      }
+      tc::tc_fence_before();
+      sm_bar();   // headf_s, red_s and roww_s free; O read before the next product
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();   // no MMA, commit or arrive of the other CTA reaches this one any more
+  if (warp == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ merge
+// A warp per row: parts are the pairs whose ranges meet the row tile's units,
+// in order (bitwise reproducible); M = max_i lse_i, w_i = e^{lse_i - M}.
+__global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31;
+  const int64_t gr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (gr >= p.rows) return;
+  int32_t len;
+  const int32_t KT = prefix_tiles(p, len);
+  const int64_t U = (int64_t)p.R * KT, qt = gr >> 7, us = qt * KT, ue = us + KT;
+  int32_t c0 = 0, c1 = -1;   // no parts: an empty prefix
+  if (KT > 0) {
+    auto owner = [&](int64_t u) {
+      int32_t c = (int32_t)(u * p.C / U);
+      while (c + 1 < p.C && pair_begin(U, p.C, c + 1) <= u) ++c;
+      while (c > 0 && pair_begin(U, p.C, c) > u) --c;
+      return c;
+    };
+    c0 = owner(us);
+    c1 = owner(ue - 1);
+    if (c0 == c1) return;   // written by the pair itself
+  }
+  const int r = (int)(gr & 127);
+  auto slot = [&](int32_t c) {   // 2c when the tile is the pair's first, else 2c + 1
+    return (2 * (int64_t)c + (pair_begin(U, p.C, c) < us ? 1 : 0)) * 128 + r;
+  };
+  float M = -INFINITY;
+  bool nan = false;
+  for (int32_t c = c0 + lane; c <= c1; c += 32)
+    if (pair_begin(U, p.C, c) < pair_begin(U, p.C, c + 1)) {
+      const float x = __ldcg(p.part_lse + slot(c));
+      nan |= x != x;
+      M = fmaxf(M, x);
+    }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7FC00000u);
+  float acc[16], z = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  if (M != -INFINITY) {
+    for (int32_t c = c0; c <= c1; ++c) {
+      if (pair_begin(U, p.C, c) >= pair_begin(U, p.C, c + 1)) continue;   // a pair without units
+      const int64_t s = slot(c);
+      const float w = expf(__ldcg(p.part_lse + s) - M);
+      if (w == 0.f) continue;
+      z += w;
+      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + s * kD) + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = __ldcg(o + i);
+        acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+      }
+    }
+  }
+  const float lse = z == 0.f ? -INFINITY : M + logf(z);
+  const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
+  const float wo = z == 0.f ? 0.f : w.o / z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] *= wo;
+  __syncwarp();   // every lane has read the row's tail_lse, which lse may alias
+  if (lane == 0) p.lse[gr] = w.lse;
+  store_out16(p, gr, 16 * lane, acc, w.tail);
+}
+
+}  // namespace dsa
+
+namespace {
+
+using dsa::aligned;
+using dsa::PrefixParams;
+
+template <bool V32>
+cudaError_t attend_setup(void *) {
+  return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)dsa::PfCfg<V32>::kSmem);
+}
+template <bool V32>
+cudaError_t attend_ready() {
+  return dsa::dsa_configure_once(V32 ? 57 : 56, &attend_setup<V32>, nullptr);
+}
+
+cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t st) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  return c;
+}
+// As the programmatic dependent of the launch before it on the stream.
+template <typename K>
+cudaError_t launch_dependent(cudaLaunchConfig_t c, K kernel, const PrefixParams &p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, p);
+}
+
+// CTA pairs that run at the same time on the current device (the GPCs'
+// odd SMs take no pair), from the occupancy of the attend kernel.
+template <bool V32>
+cudaError_t resident_pairs(int *pairs) {
+  cudaError_t e = attend_ready<V32>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = config(2, dsa::kPfThreads, dsa::PfCfg<V32>::kSmem, nullptr);
+  return cudaOccupancyMaxActiveClusters(pairs, dsa::prefix_attend_kernel<V32>, &c);
+}
+
+bool prefix_plan_ok(const dsa_prefix_plan_t *plan) {
+  return plan && plan->magic == dsa::kPrefixMagic && plan->abi_version == DSA_DECODE_ABI_VERSION;
+}
+
+template <int FMT>
+cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
+  using namespace dsa;
+  constexpr bool kV32 = FMT == DSA_REC_V32_656;
+  cudaError_t e = attend_ready<kV32>();
+  if (e != cudaSuccess) return e;
+  const unsigned tiles = (unsigned)((p.L.width + 127) / 128);
+  prefix_gather_kernel<FMT><<<tiles * (128 / kPfGroup), 256, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(config((unsigned)((p.rows + 7) / 8), 256, 0, st), prefix_merge_kernel, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width, int32_t num_sms,
+                           int32_t d_qk, dsa_prefix_plan_t *plan, size_t *workspace_bytes) {
+  if (!plan || !workspace_bytes) return DSA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_heads < 1 || width < 1 || num_sms < 0) return DSA_ERR_INVALID_ARG;
+  if (d_qk != 512 && d_qk != 576) return DSA_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)num_tokens * num_heads;
+  if (rows > INT32_MAX - 128 || width > INT32_MAX - 128) return DSA_ERR_UNSUPPORTED;
+  int pairs = num_sms / 2;
+  if (num_sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        (d_qk == 576 ? resident_pairs<true>(&pairs) : resident_pairs<false>(&pairs)) != cudaSuccess)
+      return DSA_ERR_CUDA;
+  }
+  std::memset(plan, 0, sizeof(*plan));
+  plan->magic = dsa::kPrefixMagic;
+  plan->abi_version = DSA_DECODE_ABI_VERSION;
+  plan->num_tokens = num_tokens;
+  plan->num_heads = num_heads;
+  plan->width = width;
+  plan->d_qk = d_qk;
+  plan->num_sms = num_sms;
+  plan->row_tiles = (int32_t)((rows + 127) / 128);
+  plan->key_tiles = (width + 127) / 128;
+  // one pair per unit at most
+  const int64_t units = (int64_t)plan->row_tiles * plan->key_tiles;
+  pairs = pairs < 1 ? 1 : pairs;
+  plan->pairs = units < pairs ? (int32_t)(units < 1 ? 1 : units) : pairs;
+  // Workspace: status | group info | key exponents | images | part_lse | part_o
+  const int64_t keys = (int64_t)plan->key_tiles * 128, slots = 2 * (int64_t)plan->pairs * 128;
+  int64_t off = 256;
+  plan->ws_info_offset = off;
+  off = dsa::align_up(off + 8 * (keys / dsa::kPfGroup), 256);
+  plan->ws_key_e_offset = off;
+  off = dsa::align_up(off + 4 * keys, 256);
+  plan->ws_image_offset = off;
+  off += keys * d_qk * 2;
+  plan->ws_part_lse_offset = off;
+  off = dsa::align_up(off + 4 * slots, 256);
+  plan->ws_part_o_offset = off;
+  off += 4 * slots * dsa::kD;
+  plan->workspace_bytes = num_tokens == 0 ? 0 : off;
+  // Test knob, read only here, as in dsa_decode_plan.
+  if (const char *wb = std::getenv("DSA_DECODE_WAIT_BUDGET")) {
+    const long long v = std::atoll(wb);
+    if (v > 0) plan->wait_budget_cycles = v;
+  }
+  *workspace_bytes = (size_t)plan->workspace_bytes;
+  return DSA_OK;
+}
+
+dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t workspace_bytes,
+                          const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                          const dsa_cache_desc *cache, const int32_t *slots, const int32_t *length,
+                          const float *sink, const int64_t *positions, const float *cos_sin,
+                          int64_t cos_sin_rows, int32_t rope_style, float scale,
+                          const void *tail_out, const float *tail_lse, void *out, float *lse,
+                          dsa_stream_t stream) {
+  dsa::NvtxRange range("dsa_prefix_run");
+  if (!prefix_plan_ok(plan)) return DSA_ERR_PLAN;
+  if (plan->num_tokens == 0) return DSA_OK;
+  if (!q || !slots || !length || !out || !lse) return DSA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return DSA_ERR_INVALID_ARG;
+  if (rope_style != DSA_ROPE_NEOX && rope_style != DSA_ROPE_GPTJ) return DSA_ERR_INVALID_ARG;
+  if (q_stride_h < plan->d_qk || q_stride_t < (int64_t)(plan->num_heads - 1) * q_stride_h + plan->d_qk)
+    return DSA_ERR_INVALID_ARG;
+  if ((positions == nullptr) != (cos_sin == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (cos_sin && cos_sin_rows < 1) return DSA_ERR_INVALID_ARG;
+  if ((tail_out == nullptr) != (tail_lse == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || q_stride_t % 8 != 0 || q_stride_h % 8 != 0 || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(slots, 4) || !aligned(length, 4) || (sink && !aligned(sink, 4)) ||
+      (cos_sin && (!aligned(cos_sin, 16) || !aligned(positions, 8))) ||
+      (tail_out && (!aligned(tail_out, 16) || !aligned(tail_lse, 4))))
+    return DSA_ERR_ALIGNMENT;
+  if (!workspace || (int64_t)workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256))
+    return DSA_ERR_WORKSPACE;
+  PrefixParams p;
+  std::memset(&p, 0, sizeof(p));
+  const dsa_status s = dsa::fill_cache(cache, p.L);
+  if (s != DSA_OK) return s;
+  // V3.2 records go with 576-dim queries and no table, as in dsa_decode_run
+  if ((cache->format == DSA_REC_V32_656) != (plan->d_qk == 576)) return DSA_ERR_UNSUPPORTED;
+  if (plan->d_qk == 576 && cos_sin) return DSA_ERR_UNSUPPORTED;
+  p.L.ids = slots;
+  p.L.lens = length;
+  p.L.width = plan->width;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.q_st = q_stride_t;
+  p.q_sh = q_stride_h;
+  p.sink = sink;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.cs_rows = cos_sin_rows;
+  p.gptj = rope_style == DSA_ROPE_GPTJ ? 1 : 0;
+  p.scale_log2 = scale * dsa::kLog2e;
+  p.tail_out = static_cast<const __nv_bfloat16 *>(tail_out);
+  p.tail_lse = tail_lse;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.T = plan->num_tokens;
+  p.H = plan->num_heads;
+  p.rows = plan->num_tokens * plan->num_heads;
+  p.R = plan->row_tiles;
+  p.C = plan->pairs;
+  p.wait_budget = plan->wait_budget_cycles;
+  char *w = static_cast<char *>(workspace);
+  p.status = reinterpret_cast<int32_t *>(w);
+  p.info = reinterpret_cast<int2 *>(w + plan->ws_info_offset);
+  p.key_e = reinterpret_cast<int32_t *>(w + plan->ws_key_e_offset);
+  p.image = reinterpret_cast<uint8_t *>(w + plan->ws_image_offset);
+  p.part_lse = reinterpret_cast<float *>(w + plan->ws_part_lse_offset);
+  p.part_o = reinterpret_cast<float *>(w + plan->ws_part_o_offset);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dsa::kDebug && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return DSA_ERR_CUDA;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (cache->format) {
+    case DSA_REC_FP8_528: e = launch_prefix<DSA_REC_FP8_528>(p, st); break;
+    case DSA_REC_NVFP4_288: e = launch_prefix<DSA_REC_NVFP4_288>(p, st); break;
+    case DSA_REC_FP8_528_UE8M0: e = launch_prefix<DSA_REC_FP8_528_UE8M0>(p, st); break;
+    case DSA_REC_MODEL1_584: e = launch_prefix<DSA_REC_MODEL1_584>(p, st); break;
+    case DSA_REC_V32_656: e = launch_prefix<DSA_REC_V32_656>(p, st); break;
+  }
+  return dsa::cuda_status(e);
+}
+
+}  // extern "C"
