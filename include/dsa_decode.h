@@ -460,7 +460,7 @@ typedef struct {
   int32_t num_sms;
   int32_t pairs;           /* CTA pairs that the work is cut for             */
   int32_t row_tiles;       /* 128-row tiles of the T*H query rows            */
-  int32_t key_tiles;       /* 128-key tiles of the list                      */
+  int32_t key_tiles;       /* 256-key tiles of the list                      */
   int64_t ws_info_offset;  /* workspace byte offsets                         */
   int64_t ws_key_e_offset;
   int64_t ws_image_offset;

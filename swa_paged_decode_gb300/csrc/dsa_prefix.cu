@@ -26,6 +26,7 @@
 namespace dsa {
 
 constexpr int32_t kPrefixMagic = 0x50415344;   // "DSAP"
+constexpr int kPfTile = 256;                   // keys per tile
 constexpr int kPfGroup = 32;                   // keys that share an exponent
 constexpr int kPfSpread = 5;                   // log2 spread of their magnitudes up to which they do
 constexpr int kPfTop = 14;                     // the largest value's exponent in the f16 tile
@@ -54,15 +55,15 @@ struct PrefixParams {
   int32_t *status;
   int2 *info;                  // [groups] (exponent or kPfMixed, mask of kept keys)
   int32_t *key_e;              // [keys] exponent of each key
-  uint8_t *image;              // [key tile][64-dim block][8-key group][1 KiB]
+  uint8_t *image;              // [128 keys][64-dim block][8-key group][1 KiB]
   float *part_lse;             // [2C][128]
   float *part_o;               // [2C][128][512]
 };
 
-// min(len, width) of the prefix list, and its 128-key tiles
+// min(len, width) of the prefix list, and its key tiles
 __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &len) {
   len = list_limit(p.L, 0);
-  return (len + 127) >> 7;
+  return (len + kPfTile - 1) / kPfTile;
 }
 // Units are (row tile, key tile) pairs, row tile major; pair c owns
 // [pair_begin(c), pair_begin(c + 1)).
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   int32_t len;
   const int32_t tiles = prefix_tiles(p, len);
   const int32_t key0 = blockIdx.x * kPfGroup;
-  if (key0 >= tiles * 128) return;
+  if (key0 >= tiles * kPfTile) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float v[4][16], t[4][2];
   // 4 keys per warp, their loads in flight together
@@ -190,44 +191,48 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 }
 
 // ------------------------------------------------------------ attend
-// A pair of CTAs works on 128 query rows x 128 keys at a time:
-//   S[128, 128] = Q . K^T   M = 128 over the pair (64 query rows in each
-//       CTA), N = 128 keys (64 keys' rows of the operand in each CTA);
+// A pair of CTAs works on 128 query rows x 256 keys at a time:
+//   S[128, 256] = Q . K^T   M = 128 over the pair (64 query rows in each
+//       CTA), N = 256 keys (128 keys' rows of the operand in each CTA);
 //   O[128, 512] += P . V    two N = 256 halves, 128 dims of each in either
 //       CTA's shared memory; the accumulator takes 256 of the 512 TMEM
-//       columns, S twice 64.
+//       columns, S twice 128.
 // One CTA alone cannot hold this: O for 128 rows fills all of its TMEM. In
 // the pair's layout lane l of CTA r holds row 64 r + l % 64, and the upper
-// half of each product's columns sits in lanes 64..127.
+// half of each product's columns sits in lanes 64..127. (N = 128 for S, the
+// largest that a 128-key tile allows, runs at half the rate: measured 62
+// cycles per instruction of 128 x 128 x 16 against 71 for 128 x 256 x 16.)
 //
-// K and V of a unit come as 16 KiB chunks of the tile images (K: 64 keys x
-// 128 dims; V: 32 keys x 256 dims, both contiguous runs of the same image, the
-// one read K-major, the other MN-major) through one ring in the order of their
-// use: QK of unit i + 1 is issued before PV of unit i, so the softmax of a
-// unit overlaps the products around it.
+// K and V of a unit come as 16 KiB chunks of the tile images, 128 keys x 64
+// dims each (the same bytes read K-major as K and MN-major as V), one copy a
+// chunk, through one ring in the order of their use: QK of unit i + 1 is
+// issued before PV of unit i, so the softmax of a unit overlaps the products
+// around it. V goes by two chunks (the 128 dims of an N = 256 half).
 //
-// Roles: warps 0-7 softmax (a row is held by 4 threads, 32 keys each), Q
+// Roles: warps 0-7 softmax (a row is held by 4 threads, 64 keys each), Q
 // staging and the epilogue; warp 8 copies; warp 9 issues the MMAs (leader
 // CTA) or tells the leader which chunks have landed here (the other CTA).
-// Every wait is bounded as in the decode kernel.
+// Warp 9 runs its loop converged, one elected lane issuing: with uniform
+// operands an instruction goes out in fewer cycles than the tensor core
+// takes for it. Every wait is bounded as in the decode kernel.
 constexpr int kPfThreads = 320;
 constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
 
 template <bool V32>
 struct PfCfg {
   static constexpr int kDB = V32 ? 9 : 8;
-  static constexpr int kKChunks = V32 ? 5 : 4;               // the fifth holds 64 dims
-  static constexpr int kSlots = V32 ? 8 : 9;
+  static constexpr int kKChunks = V32 ? 10 : 8;   // V3.2: the tenth is empty, so that V starts on an even slot
+  static constexpr int kSlots = V32 ? 6 : 8;      // even: the two chunks of a V half lie side by side
   static constexpr uint32_t kQ = 0;                          // [kDB][64 rows x 64 dims] f16
-  static constexpr uint32_t kP = kDB * 8192;                 // [2][64 rows x 64 keys] f16
-  static constexpr uint32_t kRing = kP + 16384;
+  static constexpr uint32_t kP = kDB * 8192;                 // [4][64 rows x 64 keys] f16
+  static constexpr uint32_t kRing = kP + 32768;
   static constexpr uint32_t kRed = kRing + kSlots * 16384;   // [4][64] f32
   static constexpr uint32_t kHeadF = kRed + 1024;            // [64] f32: scale log2(e) 2^e of a row
   static constexpr uint32_t kRowW = kHeadF + 256;            // [3][64] f32 epilogue weights
   static constexpr uint32_t kMisc = kRowW + 768;
   static constexpr uint32_t kBytes = kMisc + 512;
   static constexpr uint32_t kSmem = kBytes + 1024 > 232448u ? 232448u : kBytes + 1024;
-  static constexpr uint32_t kIdQK = tc::idesc_f16(128, 128, false, false);
+  static constexpr uint32_t kIdQK = tc::idesc_f16(128, 256, false, false);
   static constexpr uint32_t kIdPV = tc::idesc_f16(128, 256, false, true);
   static constexpr uint32_t kColO = 0, kColS = 256;
   // barriers (8 bytes each) in the misc area
@@ -307,34 +312,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         }
       };
       const uint8_t *img = p.image;
-      auto load_k = [&](int64_t kt) {   // this CTA's 64 keys, 128 dims a chunk
-        const uint8_t *t = img + kt * (Cfg::kDB * 16384) + rank * 8192;
-#pragma unroll 1
-        for (int c = 0; c < Cfg::kKChunks; ++c) {
-          wait(Cfg::kEmpty + slot, ph);
-          if (*abort_s) return;
-          const int nb = (kV32 && c == 4) ? 1 : 2;
-          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], nb * 8192u);
-          for (int b = 0; b < nb; ++b)
-            tc::bulk_load(ring + slot * 16384 + b * 8192, t + (2 * c + b) * 16384, 8192u, &bars[Cfg::kFull + slot]);
-          used = used < Cfg::kSlots ? used + 1 : used;
-          next();
-        }
+      auto chunk = [&](const uint8_t *src, uint32_t bytes) {
+        wait(Cfg::kEmpty + slot, ph);
+        if (*abort_s) return;
+        tc::mbar_expect_tx(&bars[Cfg::kFull + slot], bytes);
+        if (bytes) tc::bulk_load(ring + slot * 16384, src, bytes, &bars[Cfg::kFull + slot]);
+        used = used < Cfg::kSlots ? used + 1 : used;
+        next();
       };
-      auto load_v = [&](int64_t kt) {   // all keys, this CTA's 4 dim blocks, 32 keys a chunk
-        const uint8_t *t = img + kt * (Cfg::kDB * 16384) + (2 * rank) * 16384;
+      constexpr int64_t kHalf = Cfg::kDB * 16384;   // bytes of 128 keys
+      auto load_k = [&](int64_t kt) {   // this CTA's 128 keys, 64 dims a chunk
+        const uint8_t *t = img + (2 * kt + rank) * kHalf;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
-          wait(Cfg::kEmpty + slot, ph);
-          if (*abort_s) return;
-          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 16384u);
-#pragma unroll
-          for (int b = 0; b < 4; ++b)   // dims 128 rank + 64 b of the first and the second half
-            tc::bulk_load(ring + slot * 16384 + b * 4096, t + ((b >> 1) * 4 + (b & 1)) * 16384 + s * 4096, 4096u,
-                          &bars[Cfg::kFull + slot]);
-          used = used < Cfg::kSlots ? used + 1 : used;
-          next();
-        }
+        for (int c = 0; c < Cfg::kKChunks && !*abort_s; ++c) chunk(t + c * 16384, c < Cfg::kDB ? 16384u : 0u);
+      };
+      auto load_v = [&](int64_t kt) {   // 128 keys, then the others; dims 128 rank .. of either half
+        const uint8_t *t = img + 2 * kt * kHalf + 2 * rank * 16384;
+#pragma unroll 1
+        for (int c = 0; c < 8 && !*abort_s; ++c)
+          chunk(t + (c >> 2) * kHalf + ((c >> 1) & 1) * 65536 + (c & 1) * 16384, 16384u);
       };
       for (int64_t u = u0; u < u1 && !*abort_s;) {
         const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
@@ -368,92 +364,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0) {
-      uint32_t slot = 0, ph = 0;
-      auto next = [&]() {
-        if (++slot == Cfg::kSlots) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      };
-      if (rank == 1) {
-        // ==================================================== relay
-        const int64_t chunks = (u1 - u0) * (Cfg::kKChunks + 4);
+    uint32_t slot = 0, ph = 0;
+    auto next = [&]() {
+      if (++slot == Cfg::kSlots) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    };
+    if (rank == 1) {
+      // ====================================================== relay
+      if (lane == 0) {
+        const int64_t chunks = (u1 - u0) * (Cfg::kKChunks + 8);
         for (int64_t k = 0; k < chunks && !*abort_s; ++k) {
           wait(Cfg::kFull + slot, ph);
           if (!*abort_s) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars[Cfg::kPeer + slot]), 0));
           next();
         }
-      } else {
-        // ==================================================== MMA issue
-        const uint64_t dq = tc::sdesc(q_base, 16, 1024, tc::kSwz128);
-        const uint64_t dp = tc::sdesc(p_base, 16, 1024, tc::kSwz128);
-        uint32_t ph_p = 0, ph_q = 0, nqk = 0;
-        bool issued = false;
-        auto chunk_wait = [&]() {
-          wait(Cfg::kFull + slot, ph);
-          wait(Cfg::kPeer + slot, ph);
+      }
+    } else {
+      // ====================================================== MMA issue
+      constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
+      const uint32_t dq = tc::sdesc_lo(q_base, 16), dp = tc::sdesc_lo(p_base, 16);
+      const uint32_t dk0 = tc::sdesc_lo(ring, 16), dv0 = tc::sdesc_lo(ring, 16384);
+      uint32_t ph_p = 0, ph_q = 0, nqk = 0;
+      bool issued = false;
+      auto landed = [&](uint32_t sl) {   // in both CTAs
+        wait(Cfg::kFull + sl, ph);
+        wait(Cfg::kPeer + sl, ph);
+      };
+      auto qk = [&]() {
+        const uint32_t d = tmem + Cfg::kColS + (nqk & 1u) * 128u;
+#pragma unroll
+        for (int c = 0; c < Cfg::kKChunks; ++c) {
+          landed(slot);
+          if (__any_sync(0xffffffffu, *abort_s)) return;
           tc::tc_fence_after();
-        };
-        auto qk = [&]() {
-          const uint32_t d = tmem + Cfg::kColS + (nqk & 1u) * 64u;
-#pragma unroll 1
-          for (int c = 0; c < Cfg::kKChunks; ++c) {
-            chunk_wait();
-            if (*abort_s) return;
-            const uint64_t dk = tc::sdesc(ring + slot * 16384, 16, 1024, tc::kSwz128);
-            const int nb = (kV32 && c == 4) ? 1 : 2;
-            for (int b = 0; b < nb; ++b)
+          if (tc::elect_one()) {
+            const uint32_t dk = dk0 + slot * 1024u;
+            if (c < Cfg::kDB) {
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                tc::mma_f16_pair(d, dq + (uint64_t)(((2 * c + b) * 8192 + ks * 32) >> 4),
-                                 dk + (uint64_t)((b * 8192 + ks * 32) >> 4), Cfg::kIdQK,
-                                 (c | b | ks) ? 1u : 0u);
+                tc::mma_f16_pair(d, dq + ((c * 8192 + ks * 32) >> 4), dk + ((ks * 32) >> 4), kHi, Cfg::kIdQK,
+                                 (c | ks) ? 1u : 0u);
+            }
             tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
-            next();
+            if (c == Cfg::kKChunks - 1) tc::mma_commit_pair(&bars[Cfg::kSFull + (nqk & 1u)]);
           }
-          tc::mma_commit_pair(&bars[Cfg::kSFull + (nqk & 1u)]);
-          issued = true;
-          ++nqk;
-        };
-        auto pv = [&](bool first) {
-          wait(Cfg::kPFull, ph_p);
-          ph_p ^= 1u;
-#pragma unroll 1
-          for (int s = 0; s < 4; ++s) {
-            chunk_wait();
-            if (*abort_s) return;
-            const uint64_t dv = tc::sdesc(ring + slot * 16384, 4096, 1024, tc::kSwz128);
+          __syncwarp();
+          next();
+        }
+        issued = true;
+        ++nqk;
+      };
+      auto pv = [&](bool first) {
+        wait(Cfg::kPFull, ph_p);
+        ph_p ^= 1u;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                tc::mma_f16_pair(tmem + Cfg::kColO + 128 * j,
-                                 dp + (uint64_t)(((s >> 1) * 8192 + (s & 1) * 64 + ks * 32) >> 4),
-                                 dv + (uint64_t)((j * 8192 + ks * 2048) >> 4), Cfg::kIdPV,
-                                 (first && s == 0 && ks == 0) ? 0u : 1u);
-            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
-            next();
-          }
-          tc::mma_commit_pair(&bars[Cfg::kPvDone]);
-        };
-        for (int64_t u = u0; u < u1 && !*abort_s;) {
-          const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
-          wait(Cfg::kQReady, ph_q);
-          ph_q ^= 1u;
-          if (*abort_s) break;
+        for (int c = 0; c < 4; ++c) {    // (128 keys, half of the dims)
+          landed(slot);
+          landed(slot + 1);
+          if (__any_sync(0xffffffffu, *abort_s)) return;
           tc::tc_fence_after();
-          qk();
-          const int64_t first = u;
-          for (; u < end && !*abort_s; ++u) {
-            if (u + 1 < end) qk();
-            if (!*abort_s) pv(u == first);
+          if (tc::elect_one()) {
+            const uint32_t dv = dv0 + slot * 1024u, d = tmem + Cfg::kColO + 128 * (c & 1);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc::mma_f16_pair(d, dp + (((c >> 1) * 16384 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
+                               dv + ((ks * 2048) >> 4), kHi, Cfg::kIdPV, (c >> 1) | ks ? 1u : (first ? 0u : 1u));
+            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
+            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot + 1]);
+            if (c == 3) tc::mma_commit_pair(&bars[Cfg::kPvDone]);
           }
+          __syncwarp();
+          next();
+          next();
         }
-        if (*abort_s && issued) {   // MMAs issued before a timeout end before TMEM is freed
-          tc::mma_commit_one(&bars[Cfg::kDrain]);
-          tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
+      };
+      for (int64_t u = u0; u < u1;) {
+        const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
+        wait(Cfg::kQReady, ph_q);
+        ph_q ^= 1u;
+        if (__any_sync(0xffffffffu, *abort_s)) break;
+        qk();
+        const int64_t first = u;
+        for (; u < end; ++u) {
+          if (u + 1 < end) qk();
+          if (__any_sync(0xffffffffu, *abort_s)) break;
+          pv(u == first);
         }
+        if (__any_sync(0xffffffffu, *abort_s)) break;
+      }
+      // MMAs issued before a timeout end before TMEM is freed
+      if (issued && __any_sync(0xffffffffu, *abort_s) && tc::elect_one()) {
+        tc::mma_commit_one(&bars[Cfg::kDrain]);
+        tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
       }
     }
     __syncwarp();
@@ -462,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     const int q4 = warp & 3, half = warp >> 2;
     const int lr = 32 * q4 + lane;             // TMEM lane
     const int row = lr & 63, kh = lr >> 6;     // query row of this CTA, half of the tile's keys
-    const int grp = 2 * kh + half;             // its 32-key group of the tile
+    const int part = 2 * kh + half;            // this thread's 64 keys of the tile: two 32-key groups
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
     auto sm_bar_or = [&](bool x) {
@@ -570,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     };
 
     uint32_t ph_s = 0, nqk = 0, ph_pv = 0;
-    const uint32_t prow = p_base + kh * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
+    const uint32_t prow = p_base + part * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
     bool waited = false;
     for (int64_t u = u0; u < u1;) {
       const int64_t qt = u / KT, first = u, end = min((qt + 1) * KT, u1);
@@ -583,59 +587,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       sm_bar();   // headf_s
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
-      int2 inf = __ldcg(p.info + (u - qt * KT) * 4 + grp);
+      const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
+      int4 inf = __ldcg(info + (u - qt * KT) * 4);
       for (; u < end; ++u) {
         const int64_t kt = u - qt * KT;
-        const int2 cur = inf;
-        if (u + 1 < end) inf = __ldcg(p.info + (kt + 1) * 4 + grp);
-        const uint32_t mask = (uint32_t)cur.y;
-        const bool mixed = cur.x == kPfMixed;
-        const int32_t *ke = p.key_e + kt * 128 + grp * 32;
-        const float er = mixed ? 0.f : (float)cur.x;
-        const float a = mixed ? 0.f : hf * __uint_as_float((uint32_t)(127 + cur.x) << 23);
-        float x[32];
-        auto load_y = [&]() {   // y = score in log2 units + exponent of the key
-          const uint32_t c = tl + Cfg::kColS + (nqk & 1u) * 64u + half * 32;
-          uint32_t ra[16], rb[16];
-          tc::tmem_ld16x2(c, c + 16, ra, rb);
-          if (!mixed) {
+        const int4 cur = inf;
+        if (u + 1 < end) inf = __ldcg(info + (kt + 1) * 4);
+        const bool mixed = cur.x == kPfMixed || cur.z == kPfMixed;   // one exponent per key
+        const bool full = ((uint32_t)cur.y & (uint32_t)cur.w) == 0xFFFFFFFFu;
+        const int32_t *ke = p.key_e + kt * kPfTile + part * 64;
+        float x[64];
+        // x = score in log2 units + exponent of the key - mm (-inf: not kept)
+        auto load_t = [&](float mm) {
+          const uint32_t c = tl + Cfg::kColS + (nqk & 1u) * 128u + half * 64;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i] = fmaf(__uint_as_float(ra[i]), a, er);
-              x[16 + i] = fmaf(__uint_as_float(rb[i]), a, er);
+          for (int g = 0; g < 2; ++g) {
+            uint32_t ra[16], rb[16];
+            tc::tmem_ld16x2(c + 32 * g, c + 32 * g + 16, ra, rb);
+            const int e = g ? cur.z : cur.x;
+            if (!mixed) {
+              const float a = hf * __uint_as_float((uint32_t)(127 + e) << 23), b = (float)e - mm;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                x[32 * g + i] = fmaf(__uint_as_float(ra[i]), a, b);
+                x[32 * g + 16 + i] = fmaf(__uint_as_float(rb[i]), a, b);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int ei = __ldcg(ke + 32 * g + i);
+                x[32 * g + i] = fmaf(__uint_as_float(i < 16 ? ra[i & 15] : rb[i & 15]),
+                                     hf * __uint_as_float((uint32_t)(127 + ei) << 23), (float)ei - mm);
+              }
             }
-          } else {
+            if (!full) {
+              const uint32_t mask = (uint32_t)(g ? cur.w : cur.y);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int e = __ldcg(ke + i);
-              x[i] = fmaf(__uint_as_float(i < 16 ? ra[i & 15] : rb[i & 15]),
-                          hf * __uint_as_float((uint32_t)(127 + e) << 23), (float)e);
+              for (int i = 0; i < 32; ++i)
+                if (!((mask >> i) & 1u)) x[32 * g + i] = -INFINITY;
             }
-          }
-          if (mask != 0xFFFFFFFFu) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((mask >> i) & 1u)) x[i] = -INFINITY;
           }
         };
         wait(Cfg::kSFull + (nqk & 1u), ph_s);
         tc::tc_fence_after();
-        load_y();
-        bool need = u == first;
-        float top = -INFINITY;
+        // (a row that has kept no key yet has no maximum: its scores stand alone)
+        const bool unset = m < -1e29f;
+        const float mm = unset ? 0.f : m;
+        load_t(mm);
+        float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
-        need |= top > m + 8.0f;
-        if (sm_bar_or(need)) {
-          red_s[(2 * kh + half) * 64 + row] = top;
+        for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        bool rescaled = false;
+        if (sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f))) {
+          // The running max moves to the tile's; O and the sums follow.
+          red_s[part * 64 + row] = top[0];
           sm_bar();
           const float tm = fmaxf(fmaxf(red_s[row], red_s[64 + row]), fmaxf(red_s[128 + row], red_s[192 + row]));
-          const float mn = fmaxf(m, tm);
-          const float f = tc::ex2(m - mn);   // 0 before the first kept key
+          const float mn = fmaxf(m, mm + tm);
+          const float f = tc::ex2(m - mn);   // 0 with the first kept key
           m = mn;
           l *= f;
-          if (u > first) {
+          if (u > first) {   // (zero on a row without a key: 0 * 0)
             wait(Cfg::kPvDone, ph_pv);
+            rescaled = true;
             tc::tc_fence_after();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
@@ -647,28 +662,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
               tc::tmem_st<16>(ta, o);
             }
           }
+          load_t(m);
           sm_bar();   // red_s free again
-        } else {
-          wait(Cfg::kPvDone, ph_pv);   // (the segment's first unit always takes the other branch)
         }
-        if (u > first) ph_pv ^= 1u;
-        // P = 2^(y - m); the sums take P 2^-E = 2^(x - m)
-        float s = 0.f;
+        // P = 2^x; the sums take P 2^-E = 2^(score - m)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = tc::ex2(x[i] - m);
+        for (int i = 0; i < 64; ++i) x[i] = tc::ex2(x[i]);
         if (!mixed) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s += x[i];
-          l = fmaf(s, __uint_as_float((uint32_t)(127 - cur.x) << 23), l);
+          for (int g = 0; g < 2; ++g) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i & 3] += x[32 * g + i];
+            l = fmaf((s[0] + s[1]) + (s[2] + s[3]), __uint_as_float((uint32_t)(127 - (g ? cur.z : cur.x)) << 23), l);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) l = fmaf(x[i], __uint_as_float((uint32_t)(127 - __ldcg(ke + i)) << 23), l);
+          for (int i = 0; i < 64; ++i) l = fmaf(x[i], __uint_as_float((uint32_t)(127 - __ldcg(ke + i)) << 23), l);
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = tc::pack_f16x2(x[2 * i], x[2 * i + 1]);
+        // P of the unit before has been read (a segment's first unit follows
+        // an epilogue, which waited for that)
+        if (u > first) {
+          if (!rescaled) wait(Cfg::kPvDone, ph_pv);
+          ph_pv ^= 1u;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::st_shared_v4(prow + (((half * 4 + k) ^ (row & 7)) << 4), tc::pack_f16x2(x[8 * k], x[8 * k + 1]),
-                           tc::pack_f16x2(x[8 * k + 2], x[8 * k + 3]), tc::pack_f16x2(x[8 * k + 4], x[8 * k + 5]),
-                           tc::pack_f16x2(x[8 * k + 6], x[8 * k + 7]));
+        for (int k = 0; k < 8; ++k)
+          tc::st_shared_v4(prow + ((k ^ (row & 7)) << 4), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         tc::fence_async_smem();
         tc::tc_fence_before();
         __syncwarp();
@@ -677,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if ((nqk & 1u) == 0) ph_s ^= 1u;
       }
       // ---- epilogue
-      red_s[(2 * kh + half) * 64 + row] = l;
+      red_s[part * 64 + row] = l;
       const int64_t gr = qt * 128 + rank * 64 + row;
       const bool live = gr < p.rows;
       const bool whole = first == qt * KT && end == (qt + 1) * KT;
@@ -861,8 +884,8 @@ cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
   cudaError_t e = attend_ready<kV32>();
   if (e != cudaSuccess) return e;
-  const unsigned tiles = (unsigned)((p.L.width + 127) / 128);
-  prefix_gather_kernel<FMT><<<tiles * (128 / kPfGroup), 256, 0, st>>>(p);
+  const unsigned tiles = (unsigned)((p.L.width + kPfTile - 1) / kPfTile);
+  prefix_gather_kernel<FMT><<<tiles * (kPfTile / kPfGroup), 256, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p);
@@ -880,7 +903,7 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   if (num_tokens < 0 || num_heads < 1 || width < 1 || num_sms < 0) return DSA_ERR_INVALID_ARG;
   if (d_qk != 512 && d_qk != 576) return DSA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)num_tokens * num_heads;
-  if (rows > INT32_MAX - 128 || width > INT32_MAX - 128) return DSA_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX - 128 || width > INT32_MAX - 256) return DSA_ERR_UNSUPPORTED;
   int pairs = num_sms / 2;
   if (num_sms == 0) {
     int dev = 0;
@@ -898,13 +921,13 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   plan->d_qk = d_qk;
   plan->num_sms = num_sms;
   plan->row_tiles = (int32_t)((rows + 127) / 128);
-  plan->key_tiles = (width + 127) / 128;
+  plan->key_tiles = (width + dsa::kPfTile - 1) / dsa::kPfTile;
   // one pair per unit at most
   const int64_t units = (int64_t)plan->row_tiles * plan->key_tiles;
   pairs = pairs < 1 ? 1 : pairs;
   plan->pairs = units < pairs ? (int32_t)(units < 1 ? 1 : units) : pairs;
   // Workspace: status | group info | key exponents | images | part_lse | part_o
-  const int64_t keys = (int64_t)plan->key_tiles * 128, slots = 2 * (int64_t)plan->pairs * 128;
+  const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->pairs * 128;
   int64_t off = 256;
   plan->ws_info_offset = off;
   off = dsa::align_up(off + 8 * (keys / dsa::kPfGroup), 256);

@@ -156,7 +156,7 @@ def test_splits(sms, tail):
     """Row tiles whole in a pair, shared by two, cut into many."""
     c = Case(20, 32, 1100, W.FMT_NVFP4_288, seed=sms, sink=True, tail=tail)
     out, lse, attn = c.run(num_sms=sms)
-    assert attn.plan.row_tiles == 5 and attn.plan.key_tiles == 9 and attn.plan.pairs == min(45, sms // 2)
+    assert attn.plan.row_tiles == 5 and attn.plan.key_tiles == 5 and attn.plan.pairs == min(25, sms // 2)
     c.check(out, lse)
 
 
