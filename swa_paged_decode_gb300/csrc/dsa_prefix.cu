@@ -760,13 +760,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 }
 
 // ------------------------------------------------------------ merge
-// A warp per row: parts are the pairs whose ranges meet the row tile's units,
-// in order (bitwise reproducible); M = max_i lse_i, w_i = e^{lse_i - M}.
-__global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
+// A block per row, a thread per 4 dims: parts are the pairs whose ranges meet
+// the row tile's units, in order (bitwise reproducible); M = max_i lse_i, w_i
+// = e^{lse_i - M}. The weights are found with a thread per part, then 8
+// parts' values are in flight together: a row in 76 parts takes two round
+// trips to L2 and ten groups of loads (a warp per row, one part after the
+// other, took 150 us at 256 rows in 38 parts).
+constexpr int kPfMergeThreads = 128;
+
+__global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixParams p) {
+  __shared__ float w_s[kPfMergeThreads];
+  __shared__ float red_s[8];
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31;
-  const int64_t gr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (gr >= p.rows) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t gr = blockIdx.x;
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
   const int64_t U = (int64_t)p.R * KT, qt = gr >> 7, us = qt * KT, ue = us + KT;
@@ -782,50 +789,78 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixParams p) {
     c1 = owner(ue - 1);
     if (c0 == c1) return;   // written by the pair itself
   }
-  const int r = (int)(gr & 127);
-  auto slot = [&](int32_t c) {   // 2c when the tile is the pair's first, else 2c + 1
-    return (2 * (int64_t)c + (pair_begin(U, p.C, c) < us ? 1 : 0)) * 128 + r;
+  // Partial of pair c: slot 2c when the tile is the pair's first, else 2c + 1
+  // (only c0 can have begun before it).
+  const int64_t row = gr & 127, late = pair_begin(U, p.C, c0) < us ? 128 : 0;
+  auto slot = [&](int32_t c) { return (int64_t)c * 256 + (c == c0 ? late : 0) + row; };
+  auto part_lse = [&](int32_t c) {   // -inf for a pair without units
+    const bool has = c <= c1 && (U >= p.C || pair_begin(U, p.C, c) < pair_begin(U, p.C, c + 1));
+    return has ? __ldcg(p.part_lse + slot(c)) : -INFINITY;
   };
-  float M = -INFINITY;
-  bool nan = false;
-  for (int32_t c = c0 + lane; c <= c1; c += 32)
-    if (pair_begin(U, p.C, c) < pair_begin(U, p.C, c + 1)) {
-      const float x = __ldcg(p.part_lse + slot(c));
-      nan |= x != x;
-      M = fmaxf(M, x);
-    }
+  const float first = part_lse(c0 + tid);
+  float M = first;
+  bool nan = first != first;
+  for (int32_t c = c0 + tid + kPfMergeThreads; c <= c1; c += kPfMergeThreads) {
+    const float x = part_lse(c);
+    nan |= x != x;
+    M = fmaxf(M, x);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7FC00000u);
-  float acc[16], z = 0.f;
+  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7FC00000u);   // a NaN stays one
+  if (lane == 0) red_s[warp] = M;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kPfMergeThreads / 32; ++i) {
+    const float x = red_s[i];
+    M = (x != x || M != M) ? __uint_as_float(0x7FC00000u) : fmaxf(M, x);
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
   if (M != -INFINITY) {
-    for (int32_t c = c0; c <= c1; ++c) {
-      if (pair_begin(U, p.C, c) >= pair_begin(U, p.C, c + 1)) continue;   // a pair without units
-      const int64_t s = slot(c);
-      const float w = expf(__ldcg(p.part_lse + s) - M);
-      if (w == 0.f) continue;
-      z += w;
-      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + s * kD) + 4 * lane;
+    for (int32_t cb = c0; cb <= c1; cb += kPfMergeThreads) {
+      const float x = cb == c0 ? first : part_lse(cb + tid);
+      __syncthreads();
+      w_s[tid] = x == -INFINITY ? 0.f : expf(x - M);
+      __syncthreads();
+      const int n = min(kPfMergeThreads, c1 - cb + 1);
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 o[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 x = __ldcg(o + i);
-        acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
-        acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
-        acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
-        acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+        for (int i = 0; i < 8; ++i) {
+          o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + i < n && w_s[i0 + i] != 0.f)
+            o[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(cb + i0 + i) * kD) + tid);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float w = i0 + i < n ? w_s[i0 + i] : 0.f;
+          z += w;
+          acc.x = fmaf(w, o[i].x, acc.x);
+          acc.y = fmaf(w, o[i].y, acc.y);
+          acc.z = fmaf(w, o[i].z, acc.z);
+          acc.w = fmaf(w, o[i].w, acc.w);
+        }
       }
     }
   }
   const float lse = z == 0.f ? -INFINITY : M + logf(z);
   const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
   const float wo = z == 0.f ? 0.f : w.o / z;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] *= wo;
-  __syncwarp();   // every lane has read the row's tail_lse, which lse may alias
-  if (lane == 0) p.lse[gr] = w.lse;
-  store_out16(p, gr, 16 * lane, acc, w.tail);
+  float o[4] = {acc.x * wo, acc.y * wo, acc.z * wo, acc.w * wo};
+  const int64_t at = gr * kD + 4 * tid;
+  if (p.tail_out && w.tail != 0.f) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(p.tail_out + at);
+    o[0] = fmaf(w.tail, bf16_bits_to_f32(t.x & 0xFFFFu), o[0]);
+    o[1] = fmaf(w.tail, bf16_bits_to_f32(t.x >> 16), o[1]);
+    o[2] = fmaf(w.tail, bf16_bits_to_f32(t.y & 0xFFFFu), o[2]);
+    o[3] = fmaf(w.tail, bf16_bits_to_f32(t.y >> 16), o[3]);
+  }
+  __syncthreads();   // every thread has read the row's tail_lse, which lse may alias
+  if (tid == 0) p.lse[gr] = w.lse;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+  *reinterpret_cast<uint2 *>(p.out + at) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 }  // namespace dsa
@@ -890,7 +925,7 @@ cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(config((unsigned)((p.rows + 7) / 8), 256, 0, st), prefix_merge_kernel, p);
+  return launch_dependent(config((unsigned)p.rows, kPfMergeThreads, 0, st), prefix_merge_kernel, p);
 }
 
 }  // namespace
