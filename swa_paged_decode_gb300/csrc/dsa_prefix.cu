@@ -48,16 +48,18 @@ struct PrefixParams {
   const float *tail_lse;
   __nv_bfloat16 *out;
   float *lse;
-  int32_t T, H, rows, R;       // query rows, 128-row tiles
-  int32_t C;                   // CTA pairs
+  int32_t T, H, rows;          // query rows
+  int32_t G;                   // CTA pairs per cluster: 128 G rows to a row tile
+  int32_t R;                   // row tiles
+  int32_t C;                   // clusters
   long long wait_budget;
   // workspace
   int32_t *status;
   int2 *info;                  // [groups] (exponent or kPfMixed, mask of kept keys)
   int32_t *key_e;              // [keys] exponent of each key
   uint8_t *image;              // [128 keys][64-dim block][8-key group][1 KiB]
-  float *part_lse;             // [2C][128]
-  float *part_o;               // [2C][128][512]
+  float *part_lse;             // [C][G][2][128]
+  float *part_o;               // [C][G][2][128][512]
 };
 
 // min(len, width) of the prefix list, and its key tiles
@@ -65,9 +67,9 @@ __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &
   len = list_limit(p.L, 0);
   return (len + kPfTile - 1) / kPfTile;
 }
-// Units are (row tile, key tile) pairs, row tile major; pair c owns
-// [pair_begin(c), pair_begin(c + 1)).
-__device__ __forceinline__ int64_t pair_begin(int64_t U, int32_t C, int32_t c) { return U * c / C; }
+// Units are (row tile, key tile) pairs, row tile major; cluster c owns
+// [range_begin(c), range_begin(c + 1)).
+__device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) { return U * c / C; }
 
 // Weights of a row's prefix state (normalized, lse) and of its tail state in
 // the output, and the lse of both: M = the larger lse, den = e^{lse - M} +
@@ -94,29 +96,20 @@ __device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int64_t
   w.tail = b / den;
   return w;
 }
-// 16 dims of a row's output: o (weighted) + wt * tail, as bf16. A tail that
+// 4 dims of a row's output: o (weighted) + wt * tail, as bf16. A tail that
 // weighs nothing is not read.
-__device__ __forceinline__ void store_out16(const PrefixParams &p, int64_t gr, int d, float (&o)[16], float wt) {
+__device__ __forceinline__ void store_out4(const PrefixParams &p, int64_t gr, int d, float4 o, float wt) {
   const int64_t at = gr * kD + d;
   if (p.tail_out && wt != 0.f) {
-    const uint4 *t = reinterpret_cast<const uint4 *>(p.tail_out + at);
-    const uint4 a = t[0], b = t[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o[2 * i] = fmaf(wt, bf16_bits_to_f32(w[i] & 0xFFFFu), o[2 * i]);
-      o[2 * i + 1] = fmaf(wt, bf16_bits_to_f32(w[i] >> 16), o[2 * i + 1]);
-    }
+    const uint2 t = *reinterpret_cast<const uint2 *>(p.tail_out + at);
+    o.x = fmaf(wt, bf16_bits_to_f32(t.x & 0xFFFFu), o.x);
+    o.y = fmaf(wt, bf16_bits_to_f32(t.x >> 16), o.y);
+    o.z = fmaf(wt, bf16_bits_to_f32(t.y & 0xFFFFu), o.z);
+    o.w = fmaf(wt, bf16_bits_to_f32(t.y >> 16), o.w);
   }
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  uint4 *d4 = reinterpret_cast<uint4 *>(p.out + at);
-  d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+  *reinterpret_cast<uint2 *>(p.out + at) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 // ------------------------------------------------------------ gather
@@ -210,13 +203,15 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 // around it. V goes by two chunks (the 128 dims of an N = 256 half).
 //
 // Roles: warps 0-7 softmax (a row is held by 4 threads, 64 keys each), Q
-// staging and the epilogue; warp 8 copies; warp 9 issues the MMAs (leader
-// CTA) or tells the leader which chunks have landed here (the other CTA).
-// Warp 9 runs its loop converged, one elected lane issuing: with uniform
+// staging and the epilogue; warp 8 issues the MMAs (leader CTA) or tells the
+// leader which chunks have landed here (the other CTA); warps 9-11 copy.
+// Warp 8 runs its loop converged, one elected lane issuing: with uniform
 // operands an instruction goes out in fewer cycles than the tensor core
 // takes for it. Every wait is bounded as in the decode kernel.
-constexpr int kPfThreads = 320;
+constexpr int kPfThreads = 384;
+constexpr int kPfCopyWarps = 3;
 constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
+constexpr long long kPfCopyWait = 20000000ll; // ~10 ms: copies in flight after a timeout
 
 template <bool V32>
 struct PfCfg {
@@ -236,7 +231,7 @@ struct PfCfg {
   static constexpr uint32_t kIdPV = tc::idesc_f16(128, 256, false, true);
   static constexpr uint32_t kColO = 0, kColS = 256;
   // barriers (8 bytes each) in the misc area
-  static constexpr int kFull = 0, kPeer = kSlots, kEmpty = 2 * kSlots, kSFull = 3 * kSlots,
+  static constexpr int kFull = 0, kEmpty = kSlots, kSFull = 2 * kSlots,
                        kPFull = kSFull + 2, kPvDone = kPFull + 1, kQReady = kPvDone + 1,
                        kDrain = kQReady + 1, kBars = kDrain + 1;
   static constexpr uint32_t kAbort = 8 * kBars, kTmem = kAbort + 4;
@@ -244,9 +239,8 @@ struct PfCfg {
   static_assert(kBytes <= 232448u, "shared memory layout exceeds 227 KiB");
 };
 
-template <bool kV32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
-    prefix_attend_kernel(PrefixParams p) {
+template <bool kV32, int G>
+__global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixParams p) {
   using Cfg = PfCfg<kV32>;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -264,12 +258,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc::cluster_rank();
-  const int pair = blockIdx.x >> 1;
+  const uint32_t side = rank & 1u, pr = rank >> 1;   // CTA of its pair (0 leads), pair of its cluster
+  const int cl = blockIdx.x / (2 * G);
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
   const int64_t U = (int64_t)p.R * KT;
-  const int64_t u0 = pair_begin(U, p.C, pair), u1 = pair_begin(U, p.C, pair + 1);
-  if (u0 >= u1 || pad + Cfg::kBytes > Cfg::kSmem) {   // both CTAs of a pair alike
+  const int64_t u0 = range_begin(U, p.C, cl), u1 = range_begin(U, p.C, cl + 1);
+  if (u0 >= u1 || pad + Cfg::kBytes > Cfg::kSmem) {   // all CTAs of a cluster alike
     if (u0 < u1 && tid == 0) report_status(p.status, DSA_ERR_UNSUPPORTED);
     pdl_wait_primary();
     return;
@@ -277,7 +272,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
   if (warp == 0) tc::tmem_alloc_pair(tmem_slot, 512);
   if (tid == 0) {
     for (int b = 0; b < Cfg::kBars; ++b)
-      tc::mbar_init(&bars[b], (b == Cfg::kPFull || b == Cfg::kQReady) ? 16u : 1u);
+      // a chunk counts as landed in the leader once it has in both CTAs
+      tc::mbar_init(&bars[b], (b == Cfg::kPFull || b == Cfg::kQReady)                 ? 16u
+                              : (b >= Cfg::kEmpty && b < Cfg::kEmpty + Cfg::kSlots) ? (uint32_t)G
+                              : (b < Cfg::kFull + Cfg::kSlots && side == 0)         ? 2u
+                                                                                    : 1u);
     tc::fence_mbar_init();
     *abort_s = 0;
   }
@@ -287,83 +286,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  auto wait = [&](int b, uint32_t phase) {
+  // Bounded wait on a phase, after any timeout of the CTA a mere test; false:
+  // given up. What is there already passes in one test: at a chunk every 270
+  // cycles the issuing and copying threads have no time for more.
+  auto wait = [&](int b, uint32_t phase) -> bool {
+    if (tc::mbar_test_wait(&bars[b], phase)) return true;
+    if (*abort_s) return false;
+    const long long budget = p.wait_budget > 0 ? p.wait_budget : kPfWait;
+    if (tc::mbar_wait(&bars[b], phase, budget)) return true;
     if (!*abort_s) {
-      const long long budget = p.wait_budget > 0 ? p.wait_budget : kPfWait;
-      if (!tc::mbar_wait_cluster(&bars[b], phase, budget) && !*abort_s) {
-        *abort_s = 1;
-        report_status(p.status, DSA_ERR_TIMEOUT);
-      }
+      *abort_s = 1;
+      report_status(p.status, DSA_ERR_TIMEOUT);
     }
+    return false;
   };
-  const uint32_t lead_pfull = tc::mapa(tc::smem_u32(&bars[Cfg::kPFull]), 0);
-  const uint32_t lead_qready = tc::mapa(tc::smem_u32(&bars[Cfg::kQReady]), 0);
+  const uint32_t lead_pfull = tc::mapa(tc::smem_u32(&bars[Cfg::kPFull]), rank & ~1u);
+  const uint32_t lead_qready = tc::mapa(tc::smem_u32(&bars[Cfg::kQReady]), rank & ~1u);
 
-  if (warp == 8) {
+  if (warp >= 9) {
     // ======================================================== copies
+    // The warps take turns, chunk by chunk: one thread issues a chunk in
+    // about 300 cycles, too slow for a chunk every 270.
     if (lane == 0) {
       pdl_wait_primary();   // the images are complete
       uint32_t slot = 0, ph = 1;   // the first round finds every slot empty
-      uint32_t used = 0;           // slots filled so far (at most kSlots counted)
-      auto next = [&]() {
+      int turn = warp - 9;         // 0: this warp's
+      bool ok = true;
+      uint32_t filled = 0, fill_ph = 0;   // slots this warp has filled, and the phase of their latest fill
+      constexpr int64_t kHalf = Cfg::kDB * 16384;   // bytes of 128 keys
+      const uint8_t *img = p.image;
+      auto chunk = [&](const uint8_t *src, uint32_t bytes) {
+        if (turn == 0) {
+          turn = kPfCopyWarps;
+          ok = wait(Cfg::kEmpty + slot, ph);
+          if (!ok) return;
+          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], bytes);
+          if (bytes) {
+            if constexpr (G == 1)
+              tc::bulk_load(ring + slot * 16384, src, bytes, &bars[Cfg::kFull + slot]);
+            else   // half of the chunk, to both CTAs that want it
+              tc::bulk_load_multicast(ring + slot * 16384 + pr * 8192, src + pr * 8192, 8192u,
+                                      &bars[Cfg::kFull + slot], (uint16_t)(5u << side));
+          }
+          filled |= 1u << slot;
+          fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+        }
+        --turn;
         if (++slot == Cfg::kSlots) {
           slot = 0;
           ph ^= 1u;
         }
       };
-      const uint8_t *img = p.image;
-      auto chunk = [&](const uint8_t *src, uint32_t bytes) {
-        wait(Cfg::kEmpty + slot, ph);
-        if (*abort_s) return;
-        tc::mbar_expect_tx(&bars[Cfg::kFull + slot], bytes);
-        if (bytes) tc::bulk_load(ring + slot * 16384, src, bytes, &bars[Cfg::kFull + slot]);
-        used = used < Cfg::kSlots ? used + 1 : used;
-        next();
-      };
-      constexpr int64_t kHalf = Cfg::kDB * 16384;   // bytes of 128 keys
       auto load_k = [&](int64_t kt) {   // this CTA's 128 keys, 64 dims a chunk
-        const uint8_t *t = img + (2 * kt + rank) * kHalf;
+        const uint8_t *t = img + (2 * kt + side) * kHalf;
 #pragma unroll 1
-        for (int c = 0; c < Cfg::kKChunks && !*abort_s; ++c) chunk(t + c * 16384, c < Cfg::kDB ? 16384u : 0u);
+        for (int c = 0; c < Cfg::kKChunks && ok; ++c) chunk(t + c * 16384, c < Cfg::kDB ? 16384u : 0u);
       };
-      auto load_v = [&](int64_t kt) {   // 128 keys, then the others; dims 128 rank .. of either half
-        const uint8_t *t = img + 2 * kt * kHalf + 2 * rank * 16384;
+      auto load_v = [&](int64_t kt) {   // 128 keys, then the others; dims 128 side .. of either half
+        const uint8_t *t = img + 2 * kt * kHalf + 2 * side * 16384;
 #pragma unroll 1
-        for (int c = 0; c < 8 && !*abort_s; ++c)
+        for (int c = 0; c < 8 && ok; ++c)
           chunk(t + (c >> 2) * kHalf + ((c >> 1) & 1) * 65536 + (c & 1) * 16384, 16384u);
       };
-      for (int64_t u = u0; u < u1 && !*abort_s;) {
-        const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
-        load_k(u - qt * KT);
-        for (; u < end && !*abort_s; ++u) {
-          if (u + 1 < end) load_k(u + 1 - qt * KT);
-          if (!*abort_s) load_v(u - qt * KT);
+      for (int64_t u = u0; u < u1 && ok;) {
+        const int64_t st = u / KT, end = min((st + 1) * KT, u1);
+        load_k(u - st * KT);
+        for (; u < end && ok; ++u) {
+          if (u + 1 < end) load_k(u + 1 - st * KT);
+          if (ok) load_v(u - st * KT);
         }
       }
       // The slots' last releases have arrived: no commit of the leader
       // reaches this CTA's barriers after its end. (A slot that was never
       // filled passes at once.)
-      {
-        uint32_t sl = slot, pz = ph;
-        for (int k = 0; k < Cfg::kSlots && !*abort_s; ++k) {
-          wait(Cfg::kEmpty + sl, pz);
-          if (++sl == Cfg::kSlots) {
-            sl = 0;
-            pz ^= 1u;
-          }
+      for (int k = 0; k < Cfg::kSlots && ok; ++k) {
+        ok = wait(Cfg::kEmpty + slot, ph);
+        if (++slot == Cfg::kSlots) {
+          slot = 0;
+          ph ^= 1u;
         }
       }
-      // after a timeout: no copy may be in flight into shared memory when
-      // the CTA ends (the slots' latest fills, whatever their phase)
-      if (*abort_s)
-        for (uint32_t k = 0; k < used; ++k) {
-          const uint32_t s = (slot + Cfg::kSlots - 1 - k) % Cfg::kSlots;
-          const uint32_t fph = (s < slot ? ph : ph ^ 1u) ^ 1u;
-          tc::mbar_wait(&bars[Cfg::kFull + s], fph, kPfWait);
-        }
+      // After a timeout: no copy may be in flight into shared memory when
+      // the CTA ends (each slot's latest fill; a copy that the other pair did
+      // not issue any more never comes).
+      if (!ok)
+        for (int k = 0; k < Cfg::kSlots; ++k)
+          if ((filled >> k) & 1u) tc::mbar_wait(&bars[Cfg::kFull + k], (fill_ph >> k) & 1u, kPfCopyWait);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 8) {
     uint32_t slot = 0, ph = 0;
     auto next = [&]() {
       if (++slot == Cfg::kSlots) {
@@ -371,33 +382,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         ph ^= 1u;
       }
     };
-    if (rank == 1) {
+    if (side == 1) {
       // ====================================================== relay
       if (lane == 0) {
         const int64_t chunks = (u1 - u0) * (Cfg::kKChunks + 8);
-        for (int64_t k = 0; k < chunks && !*abort_s; ++k) {
-          wait(Cfg::kFull + slot, ph);
-          if (!*abort_s) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars[Cfg::kPeer + slot]), 0));
+        const uint32_t lead_full = tc::mapa(tc::smem_u32(&bars[Cfg::kFull]), rank & ~1u);
+        for (int64_t k = 0; k < chunks && wait(Cfg::kFull + slot, ph); ++k) {
+          tc::mbar_arrive_remote(lead_full + 8 * slot);
           next();
         }
       }
     } else {
       // ====================================================== MMA issue
+      // a slot is free once both pairs have read it (they fill each other's)
+      constexpr uint16_t kAll = G == 1 ? 3 : 15;
+      const uint16_t both = (uint16_t)(3u << (2 * pr));
       constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
       const uint32_t dq = tc::sdesc_lo(q_base, 16), dp = tc::sdesc_lo(p_base, 16);
       const uint32_t dk0 = tc::sdesc_lo(ring, 16), dv0 = tc::sdesc_lo(ring, 16384);
       uint32_t ph_p = 0, ph_q = 0, nqk = 0;
       bool issued = false;
-      auto landed = [&](uint32_t sl) {   // in both CTAs
-        wait(Cfg::kFull + sl, ph);
-        wait(Cfg::kPeer + sl, ph);
-      };
-      auto qk = [&]() {
+      auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
+      auto qk = [&]() -> bool {
         const uint32_t d = tmem + Cfg::kColS + (nqk & 1u) * 128u;
 #pragma unroll
         for (int c = 0; c < Cfg::kKChunks; ++c) {
-          landed(slot);
-          if (__any_sync(0xffffffffu, *abort_s)) return;
+          if (!here(wait(Cfg::kFull + slot, ph))) return false;
           tc::tc_fence_after();
           if (tc::elect_one()) {
             const uint32_t dk = dk0 + slot * 1024u;
@@ -407,23 +417,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 tc::mma_f16_pair(d, dq + ((c * 8192 + ks * 32) >> 4), dk + ((ks * 32) >> 4), kHi, Cfg::kIdQK,
                                  (c | ks) ? 1u : 0u);
             }
-            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
-            if (c == Cfg::kKChunks - 1) tc::mma_commit_pair(&bars[Cfg::kSFull + (nqk & 1u)]);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kAll);
+            if (c == Cfg::kKChunks - 1) tc::mma_commit_to(&bars[Cfg::kSFull + (nqk & 1u)], both);
           }
           __syncwarp();
           next();
         }
-        issued = true;
         ++nqk;
+        return true;
       };
-      auto pv = [&](bool first) {
-        wait(Cfg::kPFull, ph_p);
+      auto pv = [&](bool first) -> bool {
+        if (!here(wait(Cfg::kPFull, ph_p))) return false;
         ph_p ^= 1u;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {    // (128 keys, half of the dims)
-          landed(slot);
-          landed(slot + 1);
-          if (__any_sync(0xffffffffu, *abort_s)) return;
+          if (!here(wait(Cfg::kFull + slot, ph) && wait(Cfg::kFull + slot + 1, ph))) return false;
           tc::tc_fence_after();
           if (tc::elect_one()) {
             const uint32_t dv = dv0 + slot * 1024u, d = tmem + Cfg::kColO + 128 * (c & 1);
@@ -431,31 +439,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             for (int ks = 0; ks < 8; ++ks)
               tc::mma_f16_pair(d, dp + (((c >> 1) * 16384 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
                                dv + ((ks * 2048) >> 4), kHi, Cfg::kIdPV, (c >> 1) | ks ? 1u : (first ? 0u : 1u));
-            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot]);
-            tc::mma_commit_pair(&bars[Cfg::kEmpty + slot + 1]);
-            if (c == 3) tc::mma_commit_pair(&bars[Cfg::kPvDone]);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kAll);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot + 1], kAll);
+            if (c == 3) tc::mma_commit_to(&bars[Cfg::kPvDone], both);
           }
           __syncwarp();
           next();
           next();
         }
+        return true;
       };
-      for (int64_t u = u0; u < u1;) {
-        const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
-        wait(Cfg::kQReady, ph_q);
+      bool ok = true;
+      for (int64_t u = u0; u < u1 && ok;) {
+        const int64_t end = min((u / KT + 1) * KT, u1), first = u;
+        ok = here(wait(Cfg::kQReady, ph_q));
         ph_q ^= 1u;
-        if (__any_sync(0xffffffffu, *abort_s)) break;
-        qk();
-        const int64_t first = u;
-        for (; u < end; ++u) {
-          if (u + 1 < end) qk();
-          if (__any_sync(0xffffffffu, *abort_s)) break;
-          pv(u == first);
+        if (ok) {
+          issued = true;   // (qk may give up after some of its products)
+          ok = qk();
         }
-        if (__any_sync(0xffffffffu, *abort_s)) break;
+        for (; u < end && ok; ++u) {
+          if (u + 1 < end) ok = qk();
+          if (ok) ok = pv(u == first);
+        }
       }
       // MMAs issued before a timeout end before TMEM is freed
-      if (issued && __any_sync(0xffffffffu, *abort_s) && tc::elect_one()) {
+      if (issued && !ok && tc::elect_one()) {
         tc::mma_commit_one(&bars[Cfg::kDrain]);
         tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
       }
@@ -478,83 +487,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       return r != 0;
     };
     bool bad_pos = false;   // reported once the gather, which clears the status word, is done
-    // Q rows of this CTA -> f16 K-major tile, RoPE in fp32, then a power of
-    // two per row so that its largest magnitude lies in [1, 2).
+    // Q rows of this CTA -> f16 K-major tile: RoPE in fp32, times a power of
+    // two per row so that its largest unrotated magnitude lies in [1, 2) (a
+    // rotation adds half a bit at most). A warp takes 8 rows, all their loads
+    // in flight together; of the table's only those of 2 rows.
     auto stage_q = [&](int64_t qt) {
       const bool rl = lane >= 28;
       const int ca = rl ? 56 + (lane - 28) : 2 * lane, cb = rl ? 60 + (lane - 28) : 2 * lane + 1;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 8; i0 += 4) {
-        uint4 qa[4], qb[4], qc[4];
-        int32_t tok[4];
+      const int64_t g0 = qt * 128 + side * 64 + 8 * warp;   // the warp's first row
+      const int64_t gl = g0 + (lane & 7);
+      int64_t pos = 0;                                       // of row lane & 7
+      if (p.cos_sin && gl < p.rows) {
+        pos = __ldg(p.positions + gl / p.H);
+        if (pos < 0 || pos >= p.cs_rows) {   // outside the table: flag, row 0
+          bad_pos = true;
+          pos = 0;
+        }
+      }
+      const int32_t t0 = (int32_t)(g0 / p.H), h0 = (int32_t)(g0 - (int64_t)t0 * p.H);
+      uint4 qa[8], qb[8];
+      auto q_row = [&](int i) {   // row g0 + i (a warp's rows may cross several tokens)
+        int32_t t = t0, h = h0 + i;
+        if (h >= p.H) {
+          t += h / p.H;
+          h = h % p.H;
+        }
+        return reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
+      };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t gr = qt * 128 + rank * 64 + 8 * warp + i0 + i;
-          qa[i] = qb[i] = qc[i] = make_uint4(0, 0, 0, 0);
-          tok[i] = -1;
-          if (gr < p.rows) {
-            const int32_t t = (int32_t)(gr / p.H), h = (int32_t)(gr - (int64_t)t * p.H);
-            tok[i] = t;
-            const uint4 *qh = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
-            qa[i] = __ldg(qh + ca);
-            qb[i] = __ldg(qh + cb);
-            if (kV32 && lane < 8) qc[i] = __ldg(qh + 64 + lane);
+      for (int i = 0; i < 8; ++i) {
+        qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
+        if (g0 + i < p.rows) {
+          qa[i] = __ldg(q_row(i) + ca);
+          qb[i] = __ldg(q_row(i) + cb);
+        }
+      }
+      const int f0 = p.gptj ? lane - 28 : 2 * (lane - 28), f1 = p.gptj ? lane - 24 : 2 * (lane - 28) + 1;
+#pragma unroll
+      for (int i0 = 0; i0 < 8; i0 += 2) {
+        uint4 qc[2];   // V3.2: lanes 0..7, dims 512 + 8 lane ..
+        if constexpr (kV32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qc[i] = (g0 + i0 + i < p.rows && lane < 8) ? __ldg(q_row(i0 + i) + 64 + lane) : make_uint4(0, 0, 0, 0);
+        }
+        float4 cs[2][4];
+        if (p.cos_sin) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int64_t ps = __shfl_sync(0xffffffffu, pos, i0 + i);
+            const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + ps * 64);
+            if (rl) {
+              cs[i][0] = __ldg(row + f0);
+              cs[i][1] = __ldg(row + f1);
+              cs[i][2] = __ldg(row + 8 + f0);
+              cs[i][3] = __ldg(row + 8 + f1);
+            }
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const int r = 8 * warp + i0 + i;
-          const uint32_t w[8] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w, qb[i].x, qb[i].y, qb[i].z, qb[i].w};
-          float v[16], vc[8];
+          const uint4 a4 = qa[i0 + i], b4 = qb[i0 + i];
+          const uint32_t w[8] = {a4.x, a4.y, a4.z, a4.w, b4.x, b4.y, b4.z, b4.w};
+          // largest magnitude, from the bf16 bits
+          uint32_t mb = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu);
-            v[2 * k + 1] = bf16_bits_to_f32(w[k] >> 16);
-          }
-          if (p.cos_sin && tok[i] >= 0 && rl) {
-            int64_t pos = __ldg(p.positions + tok[i]);
-            if (pos < 0 || pos >= p.cs_rows) {   // outside the table: flag, row 0
-              bad_pos = true;
-              pos = 0;
-            }
-            const float4 *cs = reinterpret_cast<const float4 *>(p.cos_sin + pos * 64);
-            const int f0 = p.gptj ? lane - 28 : 2 * (lane - 28), f1 = p.gptj ? lane - 24 : 2 * (lane - 28) + 1;
-            const float4 c0 = __ldg(cs + f0), c1 = __ldg(cs + f1), s0 = __ldg(cs + 8 + f0), s1 = __ldg(cs + 8 + f1);
-            const float c8[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float s8[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {   // GPT-J (2k, 2k + 1); NeoX (k, 8 + k)
-              const float x1 = p.gptj ? v[2 * k] : v[k], x2 = p.gptj ? v[2 * k + 1] : v[8 + k];
-              const float y1 = fmaf(x1, c8[k], -(x2 * s8[k])), y2 = fmaf(x2, c8[k], x1 * s8[k]);
-              if (p.gptj) {
-                v[2 * k] = y1;
-                v[2 * k + 1] = y2;
-              } else {
-                v[k] = y1;
-                v[8 + k] = y2;
-              }
-            }
-          }
-          float mx = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(v[k]));
+          for (int k = 0; k < 8; ++k) mb = __vmaxu2(mb, w[k] & 0x7FFF7FFFu);
+          uint32_t wc[4] = {0, 0, 0, 0};
           if constexpr (kV32) {
-            const uint32_t wc[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
+            wc[0] = qc[i].x;
+            wc[1] = qc[i].y;
+            wc[2] = qc[i].z;
+            wc[3] = qc[i].w;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              vc[2 * k] = bf16_bits_to_f32(wc[k] & 0xFFFFu);
-              vc[2 * k + 1] = bf16_bits_to_f32(wc[k] >> 16);
-              mx = fmaxf(mx, fmaxf(fabsf(vc[2 * k]), fabsf(vc[2 * k + 1])));
-            }
+            for (int k = 0; k < 4; ++k) mb = __vmaxu2(mb, wc[k] & 0x7FFF7FFFu);
           }
-          const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-          int e = mb ? (int)((mb >> 23) & 0xFF) - 127 : 0;
+          mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
+          int e = mb ? (int)(mb >> 7) - 127 : 0;
           e = e < -126 ? -126 : (e > 126 ? 126 : e);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
           if (lane == 0) headf_s[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu) * down;
+            v[2 * k + 1] = bf16_bits_to_f32(w[k] >> 16) * down;
+          }
+          if (p.cos_sin && rl) {
+            const float c8[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w,
+                                 cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
+            const float s8[8] = {cs[i][2].x, cs[i][2].y, cs[i][2].z, cs[i][2].w,
+                                 cs[i][3].x, cs[i][3].y, cs[i][3].z, cs[i][3].w};
+            if (p.gptj) {   // pairs (2k, 2k + 1)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float x1 = v[2 * k], x2 = v[2 * k + 1];
+                v[2 * k] = fmaf(x1, c8[k], -(x2 * s8[k]));
+                v[2 * k + 1] = fmaf(x2, c8[k], x1 * s8[k]);
+              }
+            } else {        // pairs (k, 8 + k)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float x1 = v[k], x2 = v[8 + k];
+                v[k] = fmaf(x1, c8[k], -(x2 * s8[k]));
+                v[8 + k] = fmaf(x2, c8[k], x1 * s8[k]);
+              }
+            }
+          }
           uint32_t f[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k] * down, v[2 * k + 1] * down);
+          for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
           const uint32_t ro = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
           tc::st_shared_v4(q_base + (ca >> 3) * 8192 + ro + (((ca & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
           tc::st_shared_v4(q_base + (cb >> 3) * 8192 + ro + (((cb & 7) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
@@ -562,7 +605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             if (lane < 8) {
               uint32_t fc[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) fc[k] = tc::pack_f16x2(vc[2 * k] * down, vc[2 * k + 1] * down);
+              for (int k = 0; k < 4; ++k)
+                fc[k] = tc::pack_f16x2(bf16_bits_to_f32(wc[k] & 0xFFFFu) * down, bf16_bits_to_f32(wc[k] >> 16) * down);
               tc::st_shared_v4(q_base + 8 * 8192 + ro + ((lane ^ (r & 7)) << 4), fc[0], fc[1], fc[2], fc[3]);
             }
           }
@@ -577,7 +621,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     const uint32_t prow = p_base + part * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
     bool waited = false;
     for (int64_t u = u0; u < u1;) {
-      const int64_t qt = u / KT, first = u, end = min((qt + 1) * KT, u1);
+      const int64_t st = u / KT, first = u, end = min((st + 1) * KT, u1);
+      const int64_t qt = st * G + pr;   // the pair's 128 rows
       stage_q(qt);
       if (!waited) {
         pdl_wait_primary();   // group records of the gather
@@ -588,9 +633,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
       const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
-      int4 inf = __ldcg(info + (u - qt * KT) * 4);
+      int4 inf = __ldcg(info + (u - st * KT) * 4);
       for (; u < end; ++u) {
-        const int64_t kt = u - qt * KT;
+        const int64_t kt = u - st * KT;
         const int4 cur = inf;
         if (u + 1 < end) inf = __ldcg(info + (kt + 1) * 4);
         const bool mixed = cur.x == kPfMixed || cur.z == kPfMixed;   // one exponent per key
@@ -600,10 +645,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         // x = score in log2 units + exponent of the key - mm (-inf: not kept)
         auto load_t = [&](float mm) {
           const uint32_t c = tl + Cfg::kColS + (nqk & 1u) * 128u + half * 64;
+          uint32_t r4[4][16];
+          DSA_TMEM_LD16_NOWAIT(c, r4[0]);
+          DSA_TMEM_LD16_NOWAIT(c + 16, r4[1]);
+          DSA_TMEM_LD16_NOWAIT(c + 32, r4[2]);
+          DSA_TMEM_LD16_NOWAIT(c + 48, r4[3]);
+          DSA_TMEM_WAIT32(r4[0], r4[1]);
+          DSA_TMEM_WAIT32(r4[2], r4[3]);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            uint32_t ra[16], rb[16];
-            tc::tmem_ld16x2(c + 32 * g, c + 32 * g + 16, ra, rb);
+            const uint32_t(&ra)[16] = r4[2 * g], (&rb)[16] = r4[2 * g + 1];
             const int e = g ? cur.z : cur.x;
             if (!mixed) {
               const float a = hf * __uint_as_float((uint32_t)(127 + e) << 23), b = (float)e - mm;
@@ -701,26 +752,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       }
       // ---- epilogue
       red_s[part * 64 + row] = l;
-      const int64_t gr = qt * 128 + rank * 64 + row;
-      const bool live = gr < p.rows;
-      const bool whole = first == qt * KT && end == (qt + 1) * KT;
-      const int64_t ps = (2 * (int64_t)pair + (qt == u0 / KT ? 0 : 1)) * 128 + rank * 64 + row;
+      const int64_t g0 = qt * 128 + side * 64;   // this CTA's first row
+      const bool whole = first == st * KT && end == (st + 1) * KT;
+      const int64_t ps = (((int64_t)cl * G + pr) * 2 + (st == u0 / KT ? 0 : 1)) * 128 + side * 64;
       sm_bar();
       if (tid < 64) {   // row tid: lane tid of the lower half holds it
+        const int64_t gr = g0 + row;
         const float lt = (red_s[row] + red_s[64 + row]) + (red_s[128 + row] + red_s[192 + row]);
         // (a NaN among the scores or values stays one)
         const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
         float wo = lt == 0.f ? 0.f : 1.f / lt, wt = 0.f;
-        if (whole) {
-          if (live) {
-            const int32_t h = (int32_t)(gr % p.H);
-            const RowWeights w = row_weights(p, gr, h, lse);
+        if (gr < p.rows) {
+          if (whole) {
+            const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
             wo *= w.o;
             wt = w.tail;
             p.lse[gr] = w.lse;
+          } else {
+            p.part_lse[ps + row] = lse;
           }
-        } else {
-          p.part_lse[ps] = lse;
         }
         roww_s[row] = wo;
         roww_s[64 + row] = wt;
@@ -729,24 +779,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       ph_pv ^= 1u;
       tc::tc_fence_after();
       sm_bar();
-      const float wo = roww_s[row], wt = roww_s[64 + row];
-      const int d0 = half * 256 + kh * 128;   // this thread's 128 dims
+      // O leaves in two passes of 256 dims (64 of each thread's 128) through
+      // the Q tile, whose products are done: rows of 1 KiB, 16-byte piece i
+      // at i ^ (row % 8); then a warp stores whole runs of 8 rows. (Straight
+      // from the threads, 16 bytes to a row at a time, an epilogue took 11000
+      // cycles.)
+      const float wo = roww_s[row];
 #pragma unroll 1
-      for (int g = 0; g < 8; ++g) {
-        float o[16];
-        tc::tmem_ld<16>(tl + Cfg::kColO + half * 128 + 16 * g, o);
+      for (int pass = 0; pass < 2; ++pass) {
+        const uint32_t dst = q_base + row * 1024;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= wo;
-        if (!whole) {
-          float4 *d = reinterpret_cast<float4 *>(p.part_o + ps * kD + d0 + 16 * g);
+        for (int g = 0; g < 4; ++g) {
+          float o[16];
+          tc::tmem_ld<16>(tl + Cfg::kColO + half * 128 + pass * 64 + 16 * g, o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) __stcg(d + i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
-        } else if (live) {
-          store_out16(p, gr, d0 + 16 * g, o, wt);
+          for (int i = 0; i < 4; ++i)
+            tc::st_shared_v4(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4),
+                             __float_as_uint(o[4 * i] * wo), __float_as_uint(o[4 * i + 1] * wo),
+                             __float_as_uint(o[4 * i + 2] * wo), __float_as_uint(o[4 * i + 3] * wo));
         }
+        sm_bar();
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          const int r = 8 * warp + i;
+          const int64_t gr = g0 + r;
+          if (gr >= p.rows) break;
+          const float wt = roww_s[64 + r];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int pc = lane + 32 * k, d = (pc >> 4) * 128 + pass * 64 + (pc & 15) * 4;
+            const float4 o = *reinterpret_cast<const float4 *>(smem + Cfg::kQ + r * 1024 + ((pc ^ (r & 7)) << 4));
+            if (whole) store_out4(p, gr, d, o, wt);
+            else __stcg(reinterpret_cast<float4 *>(p.part_o + (ps + r) * kD + d), o);
+          }
+        }
+        sm_bar();   // the tile is free again
       }
-      tc::tc_fence_before();
-      sm_bar();   // headf_s, red_s and roww_s free; O read before the next product
+      tc::tc_fence_before();   // O read before the next product
     }
   }
 
@@ -760,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 }
 
 // ------------------------------------------------------------ merge
-// A block per row, a thread per 4 dims: parts are the pairs whose ranges meet
+// A block per row, a thread per 4 dims: parts are the clusters whose ranges meet
 // the row tile's units, in order (bitwise reproducible); M = max_i lse_i, w_i
 // = e^{lse_i - M}. The weights are found with a thread per part, then 8
 // parts' values are in flight together: a row in 76 parts takes two round
@@ -776,25 +845,26 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
   const int64_t gr = blockIdx.x;
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
-  const int64_t U = (int64_t)p.R * KT, qt = gr >> 7, us = qt * KT, ue = us + KT;
+  const int64_t U = (int64_t)p.R * KT, qt = gr >> 7, st = qt / p.G, pr = qt - st * p.G;
+  const int64_t us = st * KT, ue = us + KT;
   int32_t c0 = 0, c1 = -1;   // no parts: an empty prefix
   if (KT > 0) {
     auto owner = [&](int64_t u) {
       int32_t c = (int32_t)(u * p.C / U);
-      while (c + 1 < p.C && pair_begin(U, p.C, c + 1) <= u) ++c;
-      while (c > 0 && pair_begin(U, p.C, c) > u) --c;
+      while (c + 1 < p.C && range_begin(U, p.C, c + 1) <= u) ++c;
+      while (c > 0 && range_begin(U, p.C, c) > u) --c;
       return c;
     };
     c0 = owner(us);
     c1 = owner(ue - 1);
-    if (c0 == c1) return;   // written by the pair itself
+    if (c0 == c1) return;   // written by its pair
   }
-  // Partial of pair c: slot 2c when the tile is the pair's first, else 2c + 1
-  // (only c0 can have begun before it).
-  const int64_t row = gr & 127, late = pair_begin(U, p.C, c0) < us ? 128 : 0;
-  auto slot = [&](int32_t c) { return (int64_t)c * 256 + (c == c0 ? late : 0) + row; };
-  auto part_lse = [&](int32_t c) {   // -inf for a pair without units
-    const bool has = c <= c1 && (U >= p.C || pair_begin(U, p.C, c) < pair_begin(U, p.C, c + 1));
+  // Partial of cluster c: its first slot when the tile is its first, else its
+  // second (only c0 can have begun before the tile).
+  const int64_t row = gr & 127, late = range_begin(U, p.C, c0) < us ? 128 : 0;
+  auto slot = [&](int32_t c) { return ((int64_t)c * p.G + pr) * 256 + (c == c0 ? late : 0) + row; };
+  auto part_lse = [&](int32_t c) {   // -inf for a cluster without units
+    const bool has = c <= c1 && (U >= p.C || range_begin(U, p.C, c) < range_begin(U, p.C, c + 1));
     return has ? __ldcg(p.part_lse + slot(c)) : -INFINITY;
   };
   const float first = part_lse(c0 + tid);
@@ -847,20 +917,9 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
   const float lse = z == 0.f ? -INFINITY : M + logf(z);
   const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
   const float wo = z == 0.f ? 0.f : w.o / z;
-  float o[4] = {acc.x * wo, acc.y * wo, acc.z * wo, acc.w * wo};
-  const int64_t at = gr * kD + 4 * tid;
-  if (p.tail_out && w.tail != 0.f) {
-    const uint2 t = *reinterpret_cast<const uint2 *>(p.tail_out + at);
-    o[0] = fmaf(w.tail, bf16_bits_to_f32(t.x & 0xFFFFu), o[0]);
-    o[1] = fmaf(w.tail, bf16_bits_to_f32(t.x >> 16), o[1]);
-    o[2] = fmaf(w.tail, bf16_bits_to_f32(t.y & 0xFFFFu), o[2]);
-    o[3] = fmaf(w.tail, bf16_bits_to_f32(t.y >> 16), o[3]);
-  }
   __syncthreads();   // every thread has read the row's tail_lse, which lse may alias
   if (tid == 0) p.lse[gr] = w.lse;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
-  *reinterpret_cast<uint2 *>(p.out + at) =
-      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+  store_out4(p, gr, 4 * tid, make_float4(acc.x * wo, acc.y * wo, acc.z * wo, acc.w * wo), w.tail);
 }
 
 }  // namespace dsa
@@ -870,14 +929,14 @@ namespace {
 using dsa::aligned;
 using dsa::PrefixParams;
 
-template <bool V32>
+template <bool V32, int G>
 cudaError_t attend_setup(void *) {
-  return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)dsa::PfCfg<V32>::kSmem);
 }
-template <bool V32>
+template <bool V32, int G>
 cudaError_t attend_ready() {
-  return dsa::dsa_configure_once(V32 ? 57 : 56, &attend_setup<V32>, nullptr);
+  return dsa::dsa_configure_once(54 + 2 * G + (V32 ? 1 : 0), &attend_setup<V32, G>, nullptr);
 }
 
 cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t st) {
@@ -888,25 +947,35 @@ cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream
   c.stream = st;
   return c;
 }
-// As the programmatic dependent of the launch before it on the stream.
+// As the programmatic dependent of the launch before it on the stream, in
+// clusters of `cluster` CTAs.
 template <typename K>
-cudaError_t launch_dependent(cudaLaunchConfig_t c, K kernel, const PrefixParams &p) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch_dependent(cudaLaunchConfig_t c, K kernel, const PrefixParams &p, unsigned cluster = 1) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   c.attrs = attr;
-  c.numAttrs = 1;
+  c.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&c, kernel, p);
 }
 
-// CTA pairs that run at the same time on the current device (the GPCs'
-// odd SMs take no pair), from the occupancy of the attend kernel.
-template <bool V32>
-cudaError_t resident_pairs(int *pairs) {
-  cudaError_t e = attend_ready<V32>();
+// Clusters of G pairs that run at the same time on the current device (a
+// GPC's SMs past a multiple of 2 G take none), from the kernel's occupancy.
+template <bool V32, int G>
+cudaError_t resident_clusters(int *clusters) {
+  cudaError_t e = attend_ready<V32, G>();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = config(2, dsa::kPfThreads, dsa::PfCfg<V32>::kSmem, nullptr);
-  return cudaOccupancyMaxActiveClusters(pairs, dsa::prefix_attend_kernel<V32>, &c);
+  cudaLaunchConfig_t c = config(2 * G, dsa::kPfThreads, dsa::PfCfg<V32>::kSmem, nullptr);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * G;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(clusters, dsa::prefix_attend_kernel<V32, G>, &c);
 }
 
 bool prefix_plan_ok(const dsa_prefix_plan_t *plan) {
@@ -917,13 +986,15 @@ template <int FMT>
 cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   using namespace dsa;
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
-  cudaError_t e = attend_ready<kV32>();
+  cudaError_t e = p.G == 2 ? attend_ready<kV32, 2>() : attend_ready<kV32, 1>();
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.L.width + kPfTile - 1) / kPfTile);
   prefix_gather_kernel<FMT><<<tiles * (kPfTile / kPfGroup), 256, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p);
+  const cudaLaunchConfig_t c = config(2u * p.G * p.C, kPfThreads, PfCfg<kV32>::kSmem, st);
+  e = p.G == 2 ? launch_dependent(c, prefix_attend_kernel<kV32, 2>, p, 4)
+               : launch_dependent(c, prefix_attend_kernel<kV32, 1>, p, 2);
   if (e != cudaSuccess) return e;
   return launch_dependent(config((unsigned)p.rows, kPfMergeThreads, 0, st), prefix_merge_kernel, p);
 }
@@ -939,13 +1010,20 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   if (d_qk != 512 && d_qk != 576) return DSA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)num_tokens * num_heads;
   if (rows > INT32_MAX - 128 || width > INT32_MAX - 256) return DSA_ERR_UNSUPPORTED;
-  int pairs = num_sms / 2;
+  // Two pairs to a cluster from 129 rows on: they read the same keys, each
+  // fetching half of a chunk for both, so half as many bytes leave L2.
+  const int group = rows > 128 ? 2 : 1;
+  int clusters = num_sms / (2 * group);
   if (num_sms == 0) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        (d_qk == 576 ? resident_pairs<true>(&pairs) : resident_pairs<false>(&pairs)) != cudaSuccess)
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return DSA_ERR_CUDA;
+    const cudaError_t e = d_qk == 576 ? (group == 2 ? resident_clusters<true, 2>(&clusters)
+                                                    : resident_clusters<true, 1>(&clusters))
+                                      : (group == 2 ? resident_clusters<false, 2>(&clusters)
+                                                    : resident_clusters<false, 1>(&clusters));
+    if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
   std::memset(plan, 0, sizeof(*plan));
   plan->magic = dsa::kPrefixMagic;
@@ -955,14 +1033,15 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   plan->width = width;
   plan->d_qk = d_qk;
   plan->num_sms = num_sms;
-  plan->row_tiles = (int32_t)((rows + 127) / 128);
+  plan->pair_group = group;
+  plan->row_tiles = (int32_t)((rows + 128 * group - 1) / (128 * group));
   plan->key_tiles = (width + dsa::kPfTile - 1) / dsa::kPfTile;
-  // one pair per unit at most
+  // one cluster per unit at most
   const int64_t units = (int64_t)plan->row_tiles * plan->key_tiles;
-  pairs = pairs < 1 ? 1 : pairs;
-  plan->pairs = units < pairs ? (int32_t)(units < 1 ? 1 : units) : pairs;
+  clusters = clusters < 1 ? 1 : clusters;
+  plan->clusters = units < clusters ? (int32_t)(units < 1 ? 1 : units) : clusters;
   // Workspace: status | group info | key exponents | images | part_lse | part_o
-  const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->pairs * 128;
+  const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->clusters * group * 128;
   int64_t off = 256;
   plan->ws_info_offset = off;
   off = dsa::align_up(off + 8 * (keys / dsa::kPfGroup), 256);
@@ -1036,7 +1115,8 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
   p.H = plan->num_heads;
   p.rows = plan->num_tokens * plan->num_heads;
   p.R = plan->row_tiles;
-  p.C = plan->pairs;
+  p.C = plan->clusters;
+  p.G = plan->pair_group;
   p.wait_budget = plan->wait_budget_cycles;
   char *w = static_cast<char *>(workspace);
   p.status = reinterpret_cast<int32_t *>(w);

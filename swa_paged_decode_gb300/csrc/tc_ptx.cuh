@@ -264,31 +264,22 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
                : "memory");
 }
-// Bounded wait on a phase that the other CTA's arrivals may complete.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long budget) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait_cluster(bar, parity))
-    if (clock64() - t0 > budget) return false;
-  return true;
-}
 // `bytes` contiguous bytes (a multiple of 16, both ends 16-byte aligned) into
 // this CTA's shared memory; completes on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// The same into every CTA of `mask` (cluster ranks), at this CTA's offsets of
+// dst and bar in each.
+__device__ __forceinline__ void bulk_load_multicast(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                                    uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], "
+      "%4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
@@ -327,14 +318,14 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint32_t a_lo, uin
       "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
 }
-// Arrive on the barrier at this address in both CTAs once every tcgen05 op
-// that this thread issued so far completed; or in this CTA alone.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
-  const uint16_t both = 3;
+// Arrive on the barrier at this address in the CTAs of `mask` (cluster ranks)
+// once every tcgen05 op that this thread issued so far completed; or in this
+// CTA alone.
+__device__ __forceinline__ void mma_commit_to(uint64_t *bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(both)
+      "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit_one(uint64_t *bar) {
