@@ -69,7 +69,10 @@ __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &
 }
 // Units are (row tile, key tile) pairs, row tile major; cluster c owns
 // [range_begin(c), range_begin(c + 1)).
-__device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) { return U * c / C; }
+__device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) {
+  const int64_t x = U * c;
+  return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)C) : x / C;   // (32-bit where it does)
+}
 
 // Weights of a row's prefix state (normalized, lse) and of its tail state in
 // the output, and the lse of both: M = the larger lse, den = e^{lse - M} +
@@ -77,8 +80,7 @@ __device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) 
 struct RowWeights {
   float o, tail, lse;
 };
-__device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int64_t gr, int32_t h, float lse) {
-  const float lt = p.tail_lse ? p.tail_lse[gr] : -INFINITY;
+__device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int32_t h, float lse, float lt) {
   const float M = fmaxf(lse, lt);
   RowWeights w = {0.f, 0.f, -INFINITY};
   if (!(M > -INFINITY)) {
@@ -126,27 +128,24 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   const int32_t key0 = blockIdx.x * kPfGroup;
   if (key0 >= tiles * kPfTile) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float v[4][16], t[4][2];
-  // 4 keys per warp, their loads in flight together
+  // 4 keys per warp, their loads in flight together and kept as loaded until
+  // the 32 keys' exponent is known
+  RawRecord raw[4];
+  bool ok[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int32_t r = key0 + 4 * warp + i;
     const int32_t sid = r < len ? __ldg(p.L.ids + r) : -1;
-    bool ok = slot_valid(p.L, r, len, sid);
-    const uint8_t *rec = record_ptr(p.L, ok ? sid : 0);
-    if (ok) ok = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
+    ok[i] = slot_valid(p.L, r, len, sid);
+    const uint8_t *rec = record_ptr(p.L, ok[i] ? sid : 0);
+    if (ok[i]) ok[i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
+    if (ok[i]) load_record<FMT>(rec, lane, raw[i]);
+  }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[i][k] = 0.f;
-    t[i][0] = t[i][1] = 0.f;
-    if (ok) decode_record<FMT>(rec, lane, v[i], t[i][0], t[i][1]);
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[i][k]) & 0x7FFFFFFFu);
-    if constexpr (kV32) m = max(m, max(__float_as_uint(t[i][0]) & 0x7FFFFFFFu, __float_as_uint(t[i][1]) & 0x7FFFFFFFu));
-    m = __reduce_max_sync(0xffffffffu, m);
-    const int e = (int)(m >> 23) - 127;
+  for (int i = 0; i < 4; ++i) {
+    const int e = __reduce_max_sync(0xffffffffu, ok[i] ? record_exponent<FMT>(raw[i], lane) : 0);
     if (lane == 0)
-      e_s[4 * warp + i] = !ok ? kPfNoKey : (e < -kPfRange ? -kPfRange : (e > kPfRange ? kPfRange : e));
+      e_s[4 * warp + i] = !ok[i] ? kPfNoKey : (e < -kPfRange ? -kPfRange : (e > kPfRange ? kPfRange : e));
   }
   __syncthreads();
   const int my = e_s[lane];   // lane's key of the 32
@@ -170,16 +169,20 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
     const int64_t tile = r >> 7;
     const int g = (r & 127) >> 3, x = r & 7;
     uint8_t *base = p.image + tile * (kDB * 16384) + g * 1024 + x * 128;
+    float v[16], t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+    if (ok[i]) expand_record<FMT>(raw[i], lane, v, t0, t1);
     uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = tc::pack_f16x2(v[i][2 * k] * down, v[i][2 * k + 1] * down);
+    for (int k = 0; k < 8; ++k) w[k] = tc::pack_f16x2(v[2 * k] * down, v[2 * k + 1] * down);
     uint8_t *b = base + (lane >> 2) * 16384;
     const int c0 = 2 * (lane & 3);
     *reinterpret_cast<uint4 *>(b + ((c0 ^ x) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(b + (((c0 + 1) ^ x) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
     if constexpr (kV32)
       *reinterpret_cast<uint32_t *>(base + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) =
-          tc::pack_f16x2(t[i][0] * down, t[i][1] * down);
+          tc::pack_f16x2(t0 * down, t1 * down);
   }
 }
 
@@ -764,7 +767,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
         float wo = lt == 0.f ? 0.f : 1.f / lt, wt = 0.f;
         if (gr < p.rows) {
           if (whole) {
-            const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
+            const RowWeights w =
+                row_weights(p, (int32_t)(gr % p.H), lse, p.tail_lse ? p.tail_lse[gr] : -INFINITY);
             wo *= w.o;
             wt = w.tail;
             p.lse[gr] = w.lse;
@@ -829,28 +833,40 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
 }
 
 // ------------------------------------------------------------ merge
-// A block per row, a thread per 4 dims: parts are the clusters whose ranges meet
-// the row tile's units, in order (bitwise reproducible); M = max_i lse_i, w_i
-// = e^{lse_i - M}. The weights are found with a thread per part, then 8
-// parts' values are in flight together: a row in 76 parts takes two round
-// trips to L2 and ten groups of loads (a warp per row, one part after the
-// other, took 150 us at 256 rows in 38 parts).
+// kTh threads per row, 512 / kTh dims each. Parts of a row are the clusters
+// whose ranges meet the row tile's units, in order (bitwise reproducible); M =
+// max_i lse_i, w_i = e^{lse_i - M}: the weights with a thread per part, then
+// the values of several parts in flight together. A row in few parts takes a
+// warp (16384 rows in 2 or 3 parts: four times the rows in flight of a block
+// per row), a row in many a block (256 rows in 38 parts: 11 us; with a warp
+// per row, one part after the other, 150 us).
 constexpr int kPfMergeThreads = 128;
 
+template <int kTh>
 __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixParams p) {
-  __shared__ float w_s[kPfMergeThreads];
-  __shared__ float red_s[8];
+  constexpr int kQ = kD / 4 / kTh;               // float4 per thread: q = t + kTh i
+  constexpr int kIn = 8 / kQ;                    // parts in flight
+  __shared__ float w_sh[kPfMergeThreads];
+  __shared__ float red_s[kPfMergeThreads / 32];
   pdl_wait_primary();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t gr = blockIdx.x;
+  const int t = threadIdx.x % kTh, lane = threadIdx.x & 31;
+  float *w_s = w_sh + (threadIdx.x - t);
+  auto row_sync = [&]() {
+    if constexpr (kTh == 32) __syncwarp();
+    else __syncthreads();
+  };
+  const int64_t gr = (int64_t)blockIdx.x * (kPfMergeThreads / kTh) + threadIdx.x / kTh;
+  if (gr >= p.rows) return;                      // (whole warps; a block has one row where it syncs)
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
-  const int64_t U = (int64_t)p.R * KT, qt = gr >> 7, st = qt / p.G, pr = qt - st * p.G;
-  const int64_t us = st * KT, ue = us + KT;
+  const int64_t U = (int64_t)p.R * KT;
+  const int32_t qt = (int32_t)(gr >> 7), st = p.G == 2 ? qt >> 1 : qt, pr = qt - st * p.G;
+  const int64_t us = (int64_t)st * KT, ue = us + KT;
   int32_t c0 = 0, c1 = -1;   // no parts: an empty prefix
   if (KT > 0) {
     auto owner = [&](int64_t u) {
-      int32_t c = (int32_t)(u * p.C / U);
+      const int64_t x = u * p.C;
+      int32_t c = (x >> 32) == 0 && U < (1ll << 32) ? (int32_t)((uint32_t)x / (uint32_t)U) : (int32_t)(x / U);
       while (c + 1 < p.C && range_begin(U, p.C, c + 1) <= u) ++c;
       while (c > 0 && range_begin(U, p.C, c) > u) --c;
       return c;
@@ -867,10 +883,11 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
     const bool has = c <= c1 && (U >= p.C || range_begin(U, p.C, c) < range_begin(U, p.C, c + 1));
     return has ? __ldcg(p.part_lse + slot(c)) : -INFINITY;
   };
-  const float first = part_lse(c0 + tid);
+  const float first = part_lse(c0 + t);
+  const float lt = p.tail_lse ? p.tail_lse[gr] : -INFINITY;
   float M = first;
   bool nan = first != first;
-  for (int32_t c = c0 + tid + kPfMergeThreads; c <= c1; c += kPfMergeThreads) {
+  for (int32_t c = c0 + t + kTh; c <= c1; c += kTh) {
     const float x = part_lse(c);
     nan |= x != x;
     M = fmaxf(M, x);
@@ -878,48 +895,60 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7FC00000u);   // a NaN stays one
-  if (lane == 0) red_s[warp] = M;
-  __syncthreads();
+  if constexpr (kTh > 32) {
+    if (lane == 0) red_s[threadIdx.x >> 5] = M;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPfMergeThreads / 32; ++i) {
-    const float x = red_s[i];
-    M = (x != x || M != M) ? __uint_as_float(0x7FC00000u) : fmaxf(M, x);
+    for (int i = 0; i < kTh / 32; ++i) {
+      const float x = red_s[i];
+      M = (x != x || M != M) ? __uint_as_float(0x7FC00000u) : fmaxf(M, x);
+    }
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   if (M != -INFINITY) {
-    for (int32_t cb = c0; cb <= c1; cb += kPfMergeThreads) {
-      const float x = cb == c0 ? first : part_lse(cb + tid);
-      __syncthreads();
-      w_s[tid] = x == -INFINITY ? 0.f : expf(x - M);
-      __syncthreads();
-      const int n = min(kPfMergeThreads, c1 - cb + 1);
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        float4 o[8];
+    for (int32_t cb = c0; cb <= c1; cb += kTh) {
+      const float x = cb == c0 ? first : part_lse(cb + t);
+      row_sync();
+      w_s[t] = x == -INFINITY ? 0.f : expf(x - M);
+      row_sync();
+      const int n = min(kTh, c1 - cb + 1);
+      for (int i0 = 0; i0 < n; i0 += kIn) {
+        float4 o[kIn][kQ];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i0 + i < n && w_s[i0 + i] != 0.f)
-            o[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(cb + i0 + i) * kD) + tid);
+        for (int i = 0; i < kIn; ++i) {
+          const int j = min(i0 + i, n - 1);   // (loaded without a branch, used if it counts)
+          const float4 *src = reinterpret_cast<const float4 *>(p.part_o + slot(cb + j) * kD) + t;
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) o[i][q] = __ldcg(src + kTh * q);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kIn; ++i) {
           const float w = i0 + i < n ? w_s[i0 + i] : 0.f;
+          if (w == 0.f) continue;   // (a cluster without units left its slot as it was)
           z += w;
-          acc.x = fmaf(w, o[i].x, acc.x);
-          acc.y = fmaf(w, o[i].y, acc.y);
-          acc.z = fmaf(w, o[i].z, acc.z);
-          acc.w = fmaf(w, o[i].w, acc.w);
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            acc[q].x = fmaf(w, o[i][q].x, acc[q].x);
+            acc[q].y = fmaf(w, o[i][q].y, acc[q].y);
+            acc[q].z = fmaf(w, o[i][q].z, acc[q].z);
+            acc[q].w = fmaf(w, o[i][q].w, acc[q].w);
+          }
         }
       }
     }
   }
   const float lse = z == 0.f ? -INFINITY : M + logf(z);
-  const RowWeights w = row_weights(p, gr, (int32_t)(gr % p.H), lse);
+  const RowWeights w = row_weights(p, (int32_t)(gr % p.H), lse, lt);
   const float wo = z == 0.f ? 0.f : w.o / z;
-  __syncthreads();   // every thread has read the row's tail_lse, which lse may alias
-  if (tid == 0) p.lse[gr] = w.lse;
-  store_out4(p, gr, 4 * tid, make_float4(acc.x * wo, acc.y * wo, acc.z * wo, acc.w * wo), w.tail);
+  row_sync();   // every thread has read the row's tail_lse, which lse may alias
+  if (t == 0) p.lse[gr] = w.lse;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q)
+    store_out4(p, gr, 4 * (t + kTh * q), make_float4(acc[q].x * wo, acc[q].y * wo, acc[q].z * wo, acc[q].w * wo),
+               w.tail);
 }
 
 }  // namespace dsa
@@ -996,7 +1025,10 @@ cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   e = p.G == 2 ? launch_dependent(c, prefix_attend_kernel<kV32, 2>, p, 4)
                : launch_dependent(c, prefix_attend_kernel<kV32, 1>, p, 2);
   if (e != cudaSuccess) return e;
-  return launch_dependent(config((unsigned)p.rows, kPfMergeThreads, 0, st), prefix_merge_kernel, p);
+  // about C / R + 1 parts to a row
+  if (p.C < 4 * p.R)
+    return launch_dependent(config((unsigned)((p.rows + 3) / 4), kPfMergeThreads, 0, st), prefix_merge_kernel<32>, p);
+  return launch_dependent(config((unsigned)p.rows, kPfMergeThreads, 0, st), prefix_merge_kernel<kPfMergeThreads>, p);
 }
 
 }  // namespace
