@@ -458,11 +458,9 @@ typedef struct {
   int32_t width;           /* entries of the prefix list                     */
   int32_t d_qk;            /* 512, or 576 for V3.2 records                   */
   int32_t num_sms;
-  int32_t pair_group;      /* CTA pairs per cluster, 1 or 2: they share keys */
-  int32_t clusters;        /* clusters that the work is cut for              */
-  int32_t row_tiles;       /* tiles of 128 * pair_group of the T*H rows      */
+  int32_t pairs;           /* CTA pairs that the work is cut for             */
+  int32_t row_tiles;       /* 128-row tiles of the T*H query rows            */
   int32_t key_tiles;       /* 256-key tiles of the list                      */
-  int32_t reserved0;
   int64_t ws_info_offset;  /* workspace byte offsets                         */
   int64_t ws_key_e_offset;
   int64_t ws_image_offset;
@@ -476,7 +474,7 @@ typedef struct {
 /* Plan the attention of num_tokens tokens over ONE list of records that all
  * of them share (the pages decode every token over its own lists; they have
  * no counterpart of this call). num_tokens >= 0, any num_heads >= 1, width
- * >= 1 entries of the list (its length is read on the device), d_qk 512 or
+ * in [1, 2^29] entries of the list (its length is read on the device), d_qk 512 or
  * 576 (V3.2 records). num_sms: SMs to spread the work over (0 = as many CTA
  * pairs as the current device runs at a time). Fills *plan and
  * *workspace_bytes. Host only; launches nothing. */

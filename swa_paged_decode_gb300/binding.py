@@ -60,7 +60,7 @@ class Plan(ctypes.Structure):
 class PrefixPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "magic", "abi_version", "num_tokens", "num_heads", "width", "d_qk", "num_sms",
-        "pair_group", "clusters", "row_tiles", "key_tiles", "reserved0")] + \
+        "pairs", "row_tiles", "key_tiles")] + \
         [(n, ctypes.c_int64) for n in (
             "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_part_lse_offset",
             "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \

@@ -17,6 +17,8 @@
 //           of (row tile, key tile) units per pair;
 //   merge   the rows whose key tiles were split over pairs, and the rows of
 //           an empty prefix.
+#include <cuda.h>
+
 #include <cmath>
 #include <cstring>
 
@@ -49,17 +51,16 @@ struct PrefixParams {
   __nv_bfloat16 *out;
   float *lse;
   int32_t T, H, rows;          // query rows
-  int32_t G;                   // CTA pairs per cluster: 128 G rows to a row tile
-  int32_t R;                   // row tiles
-  int32_t C;                   // clusters
+  int32_t R;                   // 128-row tiles
+  int32_t C;                   // CTA pairs
   long long wait_budget;
   // workspace
   int32_t *status;
   int2 *info;                  // [groups] (exponent or kPfMixed, mask of kept keys)
   int32_t *key_e;              // [keys] exponent of each key
   uint8_t *image;              // [128 keys][64-dim block][8-key group][1 KiB]
-  float *part_lse;             // [C][G][2][128]
-  float *part_o;               // [C][G][2][128][512]
+  float *part_lse;             // [C][2][128]
+  float *part_o;               // [C][2][128][512]
 };
 
 // min(len, width) of the prefix list, and its key tiles
@@ -67,7 +68,7 @@ __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &
   len = list_limit(p.L, 0);
   return (len + kPfTile - 1) / kPfTile;
 }
-// Units are (row tile, key tile) pairs, row tile major; cluster c owns
+// Units are (row tile, key tile) pairs, row tile major; pair c owns
 // [range_begin(c), range_begin(c + 1)).
 __device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) {
   const int64_t x = U * c;
@@ -242,8 +243,9 @@ struct PfCfg {
   static_assert(kBytes <= 232448u, "shared memory layout exceeds 227 KiB");
 };
 
-template <bool kV32, int G>
-__global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixParams p) {
+template <bool kV32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
+    prefix_attend_kernel(PrefixParams p, const __grid_constant__ CUtensorMap image) {
   using Cfg = PfCfg<kV32>;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -260,29 +262,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kMisc + Cfg::kTmem);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = tc::cluster_rank();
-  const uint32_t side = rank & 1u, pr = rank >> 1;   // CTA of its pair (0 leads), pair of its cluster
-  const int cl = blockIdx.x / (2 * G);
-  int32_t len;
-  const int32_t KT = prefix_tiles(p, len);
-  const int64_t U = (int64_t)p.R * KT;
-  const int64_t u0 = range_begin(U, p.C, cl), u1 = range_begin(U, p.C, cl + 1);
-  if (u0 >= u1 || pad + Cfg::kBytes > Cfg::kSmem) {   // all CTAs of a cluster alike
-    if (u0 < u1 && tid == 0) report_status(p.status, DSA_ERR_UNSUPPORTED);
-    pdl_wait_primary();
+  const uint32_t side = tc::cluster_rank();   // CTA of its pair; 0 leads
+  const int pair = blockIdx.x >> 1;
+  if (pad + Cfg::kBytes > Cfg::kSmem) {       // every CTA alike
+    if (tid == 0) report_status(p.status, DSA_ERR_UNSUPPORTED);
     return;
   }
   if (warp == 0) tc::tmem_alloc_pair(tmem_slot, 512);
-  if (tid == 0) {
+  if (tid == 32) {
     for (int b = 0; b < Cfg::kBars; ++b)
-      // a chunk counts as landed in the leader once it has in both CTAs
-      tc::mbar_init(&bars[b], (b == Cfg::kPFull || b == Cfg::kQReady)                 ? 16u
-                              : (b >= Cfg::kEmpty && b < Cfg::kEmpty + Cfg::kSlots) ? (uint32_t)G
-                              : (b < Cfg::kFull + Cfg::kSlots && side == 0)         ? 2u
-                                                                                    : 1u);
+      tc::mbar_init(&bars[b], (b == Cfg::kPFull || b == Cfg::kQReady) ? 16u : 1u);
     tc::fence_mbar_init();
     *abort_s = 0;
   }
+  int32_t len;
+  const int32_t KT = prefix_tiles(p, len);
+  const int64_t U = (int64_t)p.R * KT;
+  const int64_t u0 = range_begin(U, p.C, pair);
+  const int64_t u1 = range_begin(U, p.C, pair + 1);   // (a pair may have no units)
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();
@@ -303,36 +300,33 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
     }
     return false;
   };
-  const uint32_t lead_pfull = tc::mapa(tc::smem_u32(&bars[Cfg::kPFull]), rank & ~1u);
-  const uint32_t lead_qready = tc::mapa(tc::smem_u32(&bars[Cfg::kQReady]), rank & ~1u);
+  const uint32_t lead_pfull = tc::mapa(tc::smem_u32(&bars[Cfg::kPFull]), 0);
+  const uint32_t lead_qready = tc::mapa(tc::smem_u32(&bars[Cfg::kQReady]), 0);
 
   if (warp >= 9) {
     // ======================================================== copies
     // The warps take turns, chunk by chunk: one thread issues a chunk in
-    // about 300 cycles, too slow for a chunk every 270.
+    // about 300 cycles, too slow for a chunk every 270. The bytes of both
+    // CTAs complete on the leader's barrier, which its own warps arm.
     if (lane == 0) {
       pdl_wait_primary();   // the images are complete
       uint32_t slot = 0, ph = 1;   // the first round finds every slot empty
       int turn = warp - 9;         // 0: this warp's
       bool ok = true;
       uint32_t filled = 0, fill_ph = 0;   // slots this warp has filled, and the phase of their latest fill
-      constexpr int64_t kHalf = Cfg::kDB * 16384;   // bytes of 128 keys
-      const uint8_t *img = p.image;
-      auto chunk = [&](const uint8_t *src, uint32_t bytes) {
+      const uint32_t full0 = tc::mapa(tc::smem_u32(&bars[Cfg::kFull]), 0);
+      constexpr int32_t kHalf = Cfg::kDB * 32;   // map rows (512 bytes) of 128 keys; a chunk has 32
+      auto chunk = [&](int32_t y, bool some) {
         if (turn == 0) {
           turn = kPfCopyWarps;
           ok = wait(Cfg::kEmpty + slot, ph);
           if (!ok) return;
-          tc::mbar_expect_tx(&bars[Cfg::kFull + slot], bytes);
-          if (bytes) {
-            if constexpr (G == 1)
-              tc::bulk_load(ring + slot * 16384, src, bytes, &bars[Cfg::kFull + slot]);
-            else   // half of the chunk, to both CTAs that want it
-              tc::bulk_load_multicast(ring + slot * 16384 + pr * 8192, src + pr * 8192, 8192u,
-                                      &bars[Cfg::kFull + slot], (uint16_t)(5u << side));
+          if (side == 0) {
+            tc::mbar_expect_tx(&bars[Cfg::kFull + slot], some ? 32768u : 0u);
+            filled |= 1u << slot;
+            fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
           }
-          filled |= 1u << slot;
-          fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+          if (some) tc::tma_load_pair(ring + slot * 16384, &image, 0, y, full0 + 8 * slot);
         }
         --turn;
         if (++slot == Cfg::kSlots) {
@@ -341,22 +335,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
         }
       };
       auto load_k = [&](int64_t kt) {   // this CTA's 128 keys, 64 dims a chunk
-        const uint8_t *t = img + (2 * kt + side) * kHalf;
+        const int32_t y = (int32_t)(2 * kt + side) * kHalf;
 #pragma unroll 1
-        for (int c = 0; c < Cfg::kKChunks && ok; ++c) chunk(t + c * 16384, c < Cfg::kDB ? 16384u : 0u);
+        for (int c = 0; c < Cfg::kKChunks && ok; ++c) chunk(y + c * 32, c < Cfg::kDB);
       };
       auto load_v = [&](int64_t kt) {   // 128 keys, then the others; dims 128 side .. of either half
-        const uint8_t *t = img + 2 * kt * kHalf + 2 * side * 16384;
+        const int32_t y = (int32_t)(2 * kt) * kHalf + 64 * side;
 #pragma unroll 1
-        for (int c = 0; c < 8 && ok; ++c)
-          chunk(t + (c >> 2) * kHalf + ((c >> 1) & 1) * 65536 + (c & 1) * 16384, 16384u);
+        for (int c = 0; c < 8 && ok; ++c) chunk(y + (c >> 2) * kHalf + ((c >> 1) & 1) * 128 + (c & 1) * 32, true);
       };
       for (int64_t u = u0; u < u1 && ok;) {
-        const int64_t st = u / KT, end = min((st + 1) * KT, u1);
-        load_k(u - st * KT);
+        const int64_t qt = u / KT, end = min((qt + 1) * KT, u1);
+        load_k(u - qt * KT);
         for (; u < end && ok; ++u) {
-          if (u + 1 < end) load_k(u + 1 - st * KT);
-          if (ok) load_v(u - st * KT);
+          if (u + 1 < end) load_k(u + 1 - qt * KT);
+          if (ok) load_v(u - qt * KT);
         }
       }
       // The slots' last releases have arrived: no commit of the leader
@@ -369,12 +362,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
           ph ^= 1u;
         }
       }
-      // After a timeout: no copy may be in flight into shared memory when
-      // the CTA ends (each slot's latest fill; a copy that the other pair did
-      // not issue any more never comes).
-      if (!ok)
+      // After a timeout no copy may be in flight into shared memory when the
+      // pair ends: the leader waits for the chunks it has armed (both CTAs'
+      // bytes, unless the other gave up before); then either thread lets a
+      // thousand times the latency of a copy pass.
+      if (!ok) {
         for (int k = 0; k < Cfg::kSlots; ++k)
           if ((filled >> k) & 1u) tc::mbar_wait(&bars[Cfg::kFull + k], (fill_ph >> k) & 1u, kPfCopyWait);
+        const long long t0 = clock64();
+        while (clock64() - t0 < kPfCopyWait / 10) __nanosleep(1000);
+      }
     }
     __syncwarp();
   } else if (warp == 8) {
@@ -385,21 +382,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
         ph ^= 1u;
       }
     };
-    if (side == 1) {
-      // ====================================================== relay
-      if (lane == 0) {
-        const int64_t chunks = (u1 - u0) * (Cfg::kKChunks + 8);
-        const uint32_t lead_full = tc::mapa(tc::smem_u32(&bars[Cfg::kFull]), rank & ~1u);
-        for (int64_t k = 0; k < chunks && wait(Cfg::kFull + slot, ph); ++k) {
-          tc::mbar_arrive_remote(lead_full + 8 * slot);
-          next();
-        }
-      }
-    } else {
+    if (side == 0) {
       // ====================================================== MMA issue
-      // a slot is free once both pairs have read it (they fill each other's)
-      constexpr uint16_t kAll = G == 1 ? 3 : 15;
-      const uint16_t both = (uint16_t)(3u << (2 * pr));
+      constexpr uint16_t kBoth = 3;
       constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
       const uint32_t dq = tc::sdesc_lo(q_base, 16), dp = tc::sdesc_lo(p_base, 16);
       const uint32_t dk0 = tc::sdesc_lo(ring, 16), dv0 = tc::sdesc_lo(ring, 16384);
@@ -420,8 +405,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
                 tc::mma_f16_pair(d, dq + ((c * 8192 + ks * 32) >> 4), dk + ((ks * 32) >> 4), kHi, Cfg::kIdQK,
                                  (c | ks) ? 1u : 0u);
             }
-            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kAll);
-            if (c == Cfg::kKChunks - 1) tc::mma_commit_to(&bars[Cfg::kSFull + (nqk & 1u)], both);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+            if (c == Cfg::kKChunks - 1) tc::mma_commit_to(&bars[Cfg::kSFull + (nqk & 1u)], kBoth);
           }
           __syncwarp();
           next();
@@ -442,9 +427,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
             for (int ks = 0; ks < 8; ++ks)
               tc::mma_f16_pair(d, dp + (((c >> 1) * 16384 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
                                dv + ((ks * 2048) >> 4), kHi, Cfg::kIdPV, (c >> 1) | ks ? 1u : (first ? 0u : 1u));
-            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kAll);
-            tc::mma_commit_to(&bars[Cfg::kEmpty + slot + 1], kAll);
-            if (c == 3) tc::mma_commit_to(&bars[Cfg::kPvDone], both);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+            tc::mma_commit_to(&bars[Cfg::kEmpty + slot + 1], kBoth);
+            if (c == 3) tc::mma_commit_to(&bars[Cfg::kPvDone], kBoth);
           }
           __syncwarp();
           next();
@@ -624,8 +609,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
     const uint32_t prow = p_base + part * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
     bool waited = false;
     for (int64_t u = u0; u < u1;) {
-      const int64_t st = u / KT, first = u, end = min((st + 1) * KT, u1);
-      const int64_t qt = st * G + pr;   // the pair's 128 rows
+      const int64_t qt = u / KT, first = u, end = min((qt + 1) * KT, u1);
       stage_q(qt);
       if (!waited) {
         pdl_wait_primary();   // group records of the gather
@@ -636,9 +620,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
       const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
-      int4 inf = __ldcg(info + (u - st * KT) * 4);
+      int4 inf = __ldcg(info + (u - qt * KT) * 4);
       for (; u < end; ++u) {
-        const int64_t kt = u - st * KT;
+        const int64_t kt = u - qt * KT;
         const int4 cur = inf;
         if (u + 1 < end) inf = __ldcg(info + (kt + 1) * 4);
         const bool mixed = cur.x == kPfMixed || cur.z == kPfMixed;   // one exponent per key
@@ -684,27 +668,29 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
         };
         wait(Cfg::kSFull + (nqk & 1u), ph_s);
         tc::tc_fence_after();
-        // (a row that has kept no key yet has no maximum: its scores stand alone)
-        const bool unset = m < -1e29f;
-        const float mm = unset ? 0.f : m;
-        load_t(mm);
-        float top[4] = {x[0], x[1], x[2], x[3]};
+        // Scores against the running max; where a row's exceed it by 2^8 (or
+        // it has none yet: its scores stand alone) the maxima, O and the sums
+        // of the whole CTA move, and the scores are taken again.
+        bool moved = false, unset = m < -1e29f;
+        float mm = unset ? 0.f : m;
+#pragma unroll 1
+        while (true) {
+          load_t(mm);
+          if (moved) break;
+          float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
-        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        bool rescaled = false;
-        if (sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f))) {
-          // The running max moves to the tile's; O and the sums follow.
+          for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+          top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (!sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f))) break;
           red_s[part * 64 + row] = top[0];
           sm_bar();
           const float tm = fmaxf(fmaxf(red_s[row], red_s[64 + row]), fmaxf(red_s[128 + row], red_s[192 + row]));
           const float mn = fmaxf(m, mm + tm);
           const float f = tc::ex2(m - mn);   // 0 with the first kept key
-          m = mn;
+          m = mm = mn;
           l *= f;
           if (u > first) {   // (zero on a row without a key: 0 * 0)
             wait(Cfg::kPvDone, ph_pv);
-            rescaled = true;
             tc::tc_fence_after();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
@@ -716,8 +702,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
               tc::tmem_st<16>(ta, o);
             }
           }
-          load_t(m);
           sm_bar();   // red_s free again
+          moved = true;
         }
         // P = 2^x; the sums take P 2^-E = 2^(score - m)
 #pragma unroll
@@ -740,7 +726,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
         // P of the unit before has been read (a segment's first unit follows
         // an epilogue, which waited for that)
         if (u > first) {
-          if (!rescaled) wait(Cfg::kPvDone, ph_pv);
+          if (!moved) wait(Cfg::kPvDone, ph_pv);
           ph_pv ^= 1u;
         }
 #pragma unroll
@@ -756,8 +742,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
       // ---- epilogue
       red_s[part * 64 + row] = l;
       const int64_t g0 = qt * 128 + side * 64;   // this CTA's first row
-      const bool whole = first == st * KT && end == (st + 1) * KT;
-      const int64_t ps = (((int64_t)cl * G + pr) * 2 + (st == u0 / KT ? 0 : 1)) * 128 + side * 64;
+      const bool whole = first == qt * KT && end == (qt + 1) * KT;
+      const int64_t ps = (2 * (int64_t)pair + (qt == u0 / KT ? 0 : 1)) * 128 + side * 64;
       sm_bar();
       if (tid < 64) {   // row tid: lane tid of the lower half holds it
         const int64_t gr = g0 + row;
@@ -791,17 +777,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
       const float wo = roww_s[row];
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        const uint32_t dst = q_base + row * 1024;
+        const uint32_t dst = q_base + row * 1024, c = tl + Cfg::kColO + half * 128 + pass * 64;
+        uint32_t o[4][16];
+        DSA_TMEM_LD16_NOWAIT(c, o[0]);
+        DSA_TMEM_LD16_NOWAIT(c + 16, o[1]);
+        DSA_TMEM_LD16_NOWAIT(c + 32, o[2]);
+        DSA_TMEM_LD16_NOWAIT(c + 48, o[3]);
+        DSA_TMEM_WAIT32(o[0], o[1]);
+        DSA_TMEM_WAIT32(o[2], o[3]);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float o[16];
-          tc::tmem_ld<16>(tl + Cfg::kColO + half * 128 + pass * 64 + 16 * g, o);
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc::st_shared_v4(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4),
-                             __float_as_uint(o[4 * i] * wo), __float_as_uint(o[4 * i + 1] * wo),
-                             __float_as_uint(o[4 * i + 2] * wo), __float_as_uint(o[4 * i + 3] * wo));
-        }
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(o[g][4 * i + k]) * wo);
+            tc::st_shared_v4(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+          }
         sm_bar();
 #pragma unroll 4
         for (int i = 0; i < 8; ++i) {
@@ -833,7 +825,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_attend_kernel(PrefixPara
 }
 
 // ------------------------------------------------------------ merge
-// kTh threads per row, 512 / kTh dims each. Parts of a row are the clusters
+// kTh threads per row, 512 / kTh dims each. Parts of a row are the pairs
 // whose ranges meet the row tile's units, in order (bitwise reproducible); M =
 // max_i lse_i, w_i = e^{lse_i - M}: the weights with a thread per part, then
 // the values of several parts in flight together. A row in few parts takes a
@@ -860,8 +852,7 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
   const int64_t U = (int64_t)p.R * KT;
-  const int32_t qt = (int32_t)(gr >> 7), st = p.G == 2 ? qt >> 1 : qt, pr = qt - st * p.G;
-  const int64_t us = (int64_t)st * KT, ue = us + KT;
+  const int64_t us = (gr >> 7) * KT, ue = us + KT;
   int32_t c0 = 0, c1 = -1;   // no parts: an empty prefix
   if (KT > 0) {
     auto owner = [&](int64_t u) {
@@ -875,11 +866,11 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
     c1 = owner(ue - 1);
     if (c0 == c1) return;   // written by its pair
   }
-  // Partial of cluster c: its first slot when the tile is its first, else its
+  // Partial of pair c: its first slot when the tile is its first, else its
   // second (only c0 can have begun before the tile).
   const int64_t row = gr & 127, late = range_begin(U, p.C, c0) < us ? 128 : 0;
-  auto slot = [&](int32_t c) { return ((int64_t)c * p.G + pr) * 256 + (c == c0 ? late : 0) + row; };
-  auto part_lse = [&](int32_t c) {   // -inf for a cluster without units
+  auto slot = [&](int32_t c) { return (int64_t)c * 256 + (c == c0 ? late : 0) + row; };
+  auto part_lse = [&](int32_t c) {   // -inf for a pair without units
     const bool has = c <= c1 && (U >= p.C || range_begin(U, p.C, c) < range_begin(U, p.C, c + 1));
     return has ? __ldcg(p.part_lse + slot(c)) : -INFINITY;
   };
@@ -927,7 +918,7 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
 #pragma unroll
         for (int i = 0; i < kIn; ++i) {
           const float w = i0 + i < n ? w_s[i0 + i] : 0.f;
-          if (w == 0.f) continue;   // (a cluster without units left its slot as it was)
+          if (w == 0.f) continue;   // (a pair without units left its slot as it was)
           z += w;
 #pragma unroll
           for (int q = 0; q < kQ; ++q) {
@@ -958,14 +949,14 @@ namespace {
 using dsa::aligned;
 using dsa::PrefixParams;
 
-template <bool V32, int G>
+template <bool V32>
 cudaError_t attend_setup(void *) {
-  return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)dsa::PfCfg<V32>::kSmem);
 }
-template <bool V32, int G>
+template <bool V32>
 cudaError_t attend_ready() {
-  return dsa::dsa_configure_once(54 + 2 * G + (V32 ? 1 : 0), &attend_setup<V32, G>, nullptr);
+  return dsa::dsa_configure_once(V32 ? 57 : 56, &attend_setup<V32>, nullptr);
 }
 
 cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t st) {
@@ -976,35 +967,53 @@ cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream
   c.stream = st;
   return c;
 }
-// As the programmatic dependent of the launch before it on the stream, in
-// clusters of `cluster` CTAs.
-template <typename K>
-cudaError_t launch_dependent(cudaLaunchConfig_t c, K kernel, const PrefixParams &p, unsigned cluster = 1) {
-  cudaLaunchAttribute attr[2];
+// As the programmatic dependent of the launch before it on the stream.
+template <typename... K, typename... A>
+cudaError_t launch_dependent(cudaLaunchConfig_t c, void (*kernel)(K...), const A &...args) {
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  c.attrs = attr;
-  c.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&c, kernel, p);
-}
-
-// Clusters of G pairs that run at the same time on the current device (a
-// GPC's SMs past a multiple of 2 G take none), from the kernel's occupancy.
-template <bool V32, int G>
-cudaError_t resident_clusters(int *clusters) {
-  cudaError_t e = attend_ready<V32, G>();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = config(2 * G, dsa::kPfThreads, dsa::PfCfg<V32>::kSmem, nullptr);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * G;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   c.attrs = attr;
   c.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(clusters, dsa::prefix_attend_kernel<V32, G>, &c);
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// CTA pairs that run at the same time on the current device (a GPC's odd SM
+// takes none), from the kernel's occupancy.
+template <bool V32>
+cudaError_t resident_pairs(int *pairs) {
+  cudaError_t e = attend_ready<V32>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = config(2, dsa::kPfThreads, dsa::PfCfg<V32>::kSmem, nullptr);
+  return cudaOccupancyMaxActiveClusters(pairs, dsa::prefix_attend_kernel<V32>, &c);
+}
+
+// The driver's tensor map encoder, looked up once (no link to libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+EncodeTiled tensor_map_encoder() {
+  static const EncodeTiled f = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return f;
+}
+// The images as rows of 512 bytes, 32 of them (a 16 KiB chunk, contiguous) to
+// a box.
+bool image_map(void *image, int64_t bytes, CUtensorMap *map) {
+  const EncodeTiled encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {256, (cuuint64_t)(bytes / 512)}, strides[1] = {512};
+  const cuuint32_t box[2] = {256, 32}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, image, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool prefix_plan_ok(const dsa_prefix_plan_t *plan) {
@@ -1015,15 +1024,15 @@ template <int FMT>
 cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   using namespace dsa;
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
-  cudaError_t e = p.G == 2 ? attend_ready<kV32, 2>() : attend_ready<kV32, 1>();
+  cudaError_t e = attend_ready<kV32>();
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.L.width + kPfTile - 1) / kPfTile);
+  CUtensorMap map;
+  if (!image_map(p.image, (int64_t)tiles * kPfTile * (kV32 ? 1152 : 1024), &map)) return cudaErrorNotSupported;
   prefix_gather_kernel<FMT><<<tiles * (kPfTile / kPfGroup), 256, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const cudaLaunchConfig_t c = config(2u * p.G * p.C, kPfThreads, PfCfg<kV32>::kSmem, st);
-  e = p.G == 2 ? launch_dependent(c, prefix_attend_kernel<kV32, 2>, p, 4)
-               : launch_dependent(c, prefix_attend_kernel<kV32, 1>, p, 2);
+  e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p, map);
   if (e != cudaSuccess) return e;
   // about C / R + 1 parts to a row
   if (p.C < 4 * p.R)
@@ -1041,21 +1050,15 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   if (num_tokens < 0 || num_heads < 1 || width < 1 || num_sms < 0) return DSA_ERR_INVALID_ARG;
   if (d_qk != 512 && d_qk != 576) return DSA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)num_tokens * num_heads;
-  if (rows > INT32_MAX - 128 || width > INT32_MAX - 256) return DSA_ERR_UNSUPPORTED;
-  // Two pairs to a cluster from 129 rows on: they read the same keys, each
-  // fetching half of a chunk for both, so half as many bytes leave L2.
-  const int group = rows > 128 ? 2 : 1;
-  int clusters = num_sms / (2 * group);
+  // (the images' map counts 512-byte rows in 31 bits)
+  if (rows > INT32_MAX - 128 || width > (1 << 29)) return DSA_ERR_UNSUPPORTED;
+  int pairs = num_sms / 2;
   if (num_sms == 0) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        (d_qk == 576 ? resident_pairs<true>(&pairs) : resident_pairs<false>(&pairs)) != cudaSuccess)
       return DSA_ERR_CUDA;
-    const cudaError_t e = d_qk == 576 ? (group == 2 ? resident_clusters<true, 2>(&clusters)
-                                                    : resident_clusters<true, 1>(&clusters))
-                                      : (group == 2 ? resident_clusters<false, 2>(&clusters)
-                                                    : resident_clusters<false, 1>(&clusters));
-    if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
   std::memset(plan, 0, sizeof(*plan));
   plan->magic = dsa::kPrefixMagic;
@@ -1065,15 +1068,14 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   plan->width = width;
   plan->d_qk = d_qk;
   plan->num_sms = num_sms;
-  plan->pair_group = group;
-  plan->row_tiles = (int32_t)((rows + 128 * group - 1) / (128 * group));
+  plan->row_tiles = (int32_t)((rows + 127) / 128);
   plan->key_tiles = (width + dsa::kPfTile - 1) / dsa::kPfTile;
-  // one cluster per unit at most
+  // one pair per unit at most
   const int64_t units = (int64_t)plan->row_tiles * plan->key_tiles;
-  clusters = clusters < 1 ? 1 : clusters;
-  plan->clusters = units < clusters ? (int32_t)(units < 1 ? 1 : units) : clusters;
+  pairs = pairs < 1 ? 1 : pairs;
+  plan->pairs = units < pairs ? (int32_t)(units < 1 ? 1 : units) : pairs;
   // Workspace: status | group info | key exponents | images | part_lse | part_o
-  const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->clusters * group * 128;
+  const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->pairs * 128;
   int64_t off = 256;
   plan->ws_info_offset = off;
   off = dsa::align_up(off + 8 * (keys / dsa::kPfGroup), 256);
@@ -1147,8 +1149,7 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
   p.H = plan->num_heads;
   p.rows = plan->num_tokens * plan->num_heads;
   p.R = plan->row_tiles;
-  p.C = plan->clusters;
-  p.G = plan->pair_group;
+  p.C = plan->pairs;
   p.wait_budget = plan->wait_budget_cycles;
   char *w = static_cast<char *>(workspace);
   p.status = reinterpret_cast<int32_t *>(w);

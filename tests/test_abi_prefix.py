@@ -50,11 +50,9 @@ def test_plan_needs_somewhere_to_put_it(lib):
                                              (128, 128, 16384, 148, 512), (3, 16, 300, 1, 512)])
 def test_plan_layout(lib, T, H, width, sms, d):
     p, nbytes = B.dsa_prefix_plan(T, H, width, sms, d)
-    G = p.pair_group
-    assert G == (2 if T * H > 128 else 1)
-    assert p.row_tiles == -(-T * H // (128 * G)) and p.key_tiles == -(-width // 256)
-    assert 1 <= p.clusters <= max(1, sms // (2 * G)) and p.clusters <= p.row_tiles * p.key_tiles
-    keys, parts = 256 * p.key_tiles, 2 * p.clusters * G * 128
+    assert p.row_tiles == -(-T * H // 128) and p.key_tiles == -(-width // 256)
+    assert 1 <= p.pairs <= max(1, sms // 2) and p.pairs <= p.row_tiles * p.key_tiles
+    keys, parts = 256 * p.key_tiles, 2 * p.pairs * 128
     spans = [(0, 256), (p.ws_info_offset, 8 * keys // 32), (p.ws_key_e_offset, 4 * keys),
              (p.ws_image_offset, 2 * d * keys), (p.ws_part_lse_offset, 4 * parts), (p.ws_part_o_offset, 2048 * parts)]
     for (a, n), (b, _) in zip(spans, spans[1:] + [(nbytes, 0)]):

@@ -154,13 +154,12 @@ def test_everything_on(fmt, T, H, width, length):
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("T", [4, 20])
 def test_splits(sms, tail, T):
-    """Row tiles whole in a cluster, shared by two, cut into many; clusters of
-    one pair (128 rows) and of two (640 rows: the last pair has none)."""
+    """Row tiles whole in a pair, shared by two, cut into many."""
     c = Case(T, 32, 1100, W.FMT_NVFP4_288, seed=sms, sink=True, tail=tail)
     out, lse, attn = c.run(num_sms=sms)
     p = attn.plan
-    assert (p.pair_group, p.row_tiles, p.key_tiles) == ((1, 1, 5) if T == 4 else (2, 3, 5))
-    assert p.clusters == max(1, min(p.row_tiles * 5, sms // (2 * p.pair_group)))
+    assert (p.row_tiles, p.key_tiles) == (1 if T == 4 else 5, 5)
+    assert p.pairs == min(p.row_tiles * 5, sms // 2)
     c.check(out, lse)
 
 
