@@ -477,77 +477,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     bool bad_pos = false;   // reported once the gather, which clears the status word, is done
     // Q rows of this CTA -> f16 K-major tile: RoPE in fp32, times a power of
     // two per row so that its largest unrotated magnitude lies in [1, 2) (a
-    // rotation adds half a bit at most). A warp takes 8 rows, all their loads
-    // in flight together; of the table's only those of 2 rows.
+    // rotation adds half a bit at most). A warp takes 8 rows, 2 at a time
+    // with the next 2 in flight; the loop stays rolled and a row's address is
+    // found once, by a lane of its own: this code runs once per 128 rows, so
+    // its size is its time (8 rows unrolled took 9700 cycles, 700 a row).
     auto stage_q = [&](int64_t qt) {
-      const bool rl = lane >= 28;
+      const bool rl = lane >= 28, rope = p.cos_sin != nullptr;
       const int ca = rl ? 56 + (lane - 28) : 2 * lane, cb = rl ? 60 + (lane - 28) : 2 * lane + 1;
-      const int64_t g0 = qt * 128 + side * 64 + 8 * warp;   // the warp's first row
-      const int64_t gl = g0 + (lane & 7);
-      int64_t pos = 0;                                       // of row lane & 7
-      if (p.cos_sin && gl < p.rows) {
-        pos = __ldg(p.positions + gl / p.H);
-        if (pos < 0 || pos >= p.cs_rows) {   // outside the table: flag, row 0
-          bad_pos = true;
-          pos = 0;
-        }
-      }
-      const int32_t t0 = (int32_t)(g0 / p.H), h0 = (int32_t)(g0 - (int64_t)t0 * p.H);
-      uint4 qa[8], qb[8];
-      auto q_row = [&](int i) {   // row g0 + i (a warp's rows may cross several tokens)
-        int32_t t = t0, h = h0 + i;
-        if (h >= p.H) {
-          t += h / p.H;
-          h = h % p.H;
-        }
-        return reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
-      };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
-        if (g0 + i < p.rows) {
-          qa[i] = __ldg(q_row(i) + ca);
-          qb[i] = __ldg(q_row(i) + cb);
-        }
-      }
       const int f0 = p.gptj ? lane - 28 : 2 * (lane - 28), f1 = p.gptj ? lane - 24 : 2 * (lane - 28) + 1;
-#pragma unroll
-      for (int i0 = 0; i0 < 8; i0 += 2) {
-        uint4 qc[2];   // V3.2: lanes 0..7, dims 512 + 8 lane ..
-        if constexpr (kV32) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qc[i] = (g0 + i0 + i < p.rows && lane < 8) ? __ldg(q_row(i0 + i) + 64 + lane) : make_uint4(0, 0, 0, 0);
+      // row lane % 8 of the warp's: its queries, its table row
+      const uint32_t gl = (uint32_t)qt * 128u + side * 64u + 8u * warp + (lane & 7);
+      const __nv_bfloat16 *qp = nullptr;
+      const float *cp = p.cos_sin;
+      if (gl < (uint32_t)p.rows) {
+        const uint32_t t = gl / (uint32_t)p.H, h = gl - t * (uint32_t)p.H;
+        qp = p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh;
+        if (rope) {
+          const int64_t pos = __ldg(p.positions + t);
+          if (pos >= 0 && pos < p.cs_rows) cp += pos * 64;
+          else bad_pos = true;   // outside the table: flag, row 0
         }
-        float4 cs[2][4];
-        if (p.cos_sin) {
+      }
+      uint4 na[2], nb[2], nc[2];
+      float4 ns[2][4];
+      auto fetch = [&](int i0) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int64_t ps = __shfl_sync(0xffffffffu, pos, i0 + i);
-            const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + ps * 64);
+        for (int i = 0; i < 2; ++i) {
+          const uint4 *r = reinterpret_cast<const uint4 *>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(qp), i0 + i));
+          na[i] = nb[i] = nc[i] = make_uint4(0, 0, 0, 0);
+          if (r) {
+            na[i] = __ldg(r + ca);
+            nb[i] = __ldg(r + cb);
+            if constexpr (kV32)
+              if (lane < 8) nc[i] = __ldg(r + 64 + lane);   // dims 512 + 8 lane ..
+          }
+          if (rope) {
+            const float4 *c = reinterpret_cast<const float4 *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cp), i0 + i));
             if (rl) {
-              cs[i][0] = __ldg(row + f0);
-              cs[i][1] = __ldg(row + f1);
-              cs[i][2] = __ldg(row + 8 + f0);
-              cs[i][3] = __ldg(row + 8 + f1);
+              ns[i][0] = __ldg(c + f0);
+              ns[i][1] = __ldg(c + f1);
+              ns[i][2] = __ldg(c + 8 + f0);
+              ns[i][3] = __ldg(c + 8 + f1);
             }
           }
         }
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += 2) {
+        uint4 qa[2], qb[2], qc[2];
+        float4 cs[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qa[i] = na[i];
+          qb[i] = nb[i];
+          qc[i] = nc[i];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) cs[i][k] = ns[i][k];
+        }
+        if (i0 < 6) fetch(i0 + 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = 8 * warp + i0 + i;
-          const uint4 a4 = qa[i0 + i], b4 = qb[i0 + i];
-          const uint32_t w[8] = {a4.x, a4.y, a4.z, a4.w, b4.x, b4.y, b4.z, b4.w};
+          const uint32_t w[8] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w, qb[i].x, qb[i].y, qb[i].z, qb[i].w};
+          const uint32_t wc[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
           // largest magnitude, from the bf16 bits
           uint32_t mb = 0;
 #pragma unroll
           for (int k = 0; k < 8; ++k) mb = __vmaxu2(mb, w[k] & 0x7FFF7FFFu);
-          uint32_t wc[4] = {0, 0, 0, 0};
           if constexpr (kV32) {
-            wc[0] = qc[i].x;
-            wc[1] = qc[i].y;
-            wc[2] = qc[i].z;
-            wc[3] = qc[i].w;
 #pragma unroll
             for (int k = 0; k < 4; ++k) mb = __vmaxu2(mb, wc[k] & 0x7FFF7FFFu);
           }
@@ -562,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu) * down;
             v[2 * k + 1] = bf16_bits_to_f32(w[k] >> 16) * down;
           }
-          if (p.cos_sin && rl) {
+          if (rope && rl) {
             const float c8[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w,
                                  cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
             const float s8[8] = {cs[i][2].x, cs[i][2].y, cs[i][2].z, cs[i][2].w,
@@ -670,25 +670,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         tc::tc_fence_after();
         // Scores against the running max; where a row's exceed it by 2^8 (or
         // it has none yet: its scores stand alone) the maxima, O and the sums
-        // of the whole CTA move, and the scores are taken again.
-        bool moved = false, unset = m < -1e29f;
-        float mm = unset ? 0.f : m;
-#pragma unroll 1
-        while (true) {
-          load_t(mm);
-          if (moved) break;
-          float top[4] = {x[0], x[1], x[2], x[3]};
+        // of the whole CTA move.
+        const bool unset = m < -1e29f;
+        const float mm = unset ? 0.f : m;
+        load_t(mm);
+        float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
-          top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (!sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f))) break;
+        for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool moved = sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f));
+        if (moved) {
           red_s[part * 64 + row] = top[0];
           sm_bar();
           const float tm = fmaxf(fmaxf(red_s[row], red_s[64 + row]), fmaxf(red_s[128 + row], red_s[192 + row]));
           const float mn = fmaxf(m, mm + tm);
           const float f = tc::ex2(m - mn);   // 0 with the first kept key
-          m = mm = mn;
+          const float d = mn - mm;
+          m = mn;
           l *= f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] -= d;
           if (u > first) {   // (zero on a row without a key: 0 * 0)
             wait(Cfg::kPvDone, ph_pv);
             tc::tc_fence_after();
@@ -703,7 +704,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             }
           }
           sm_bar();   // red_s free again
-          moved = true;
         }
         // P = 2^x; the sums take P 2^-E = 2^(score - m)
 #pragma unroll
