@@ -464,11 +464,12 @@ typedef struct {
   int64_t ws_info_offset;  /* workspace byte offsets                         */
   int64_t ws_key_e_offset;
   int64_t ws_image_offset;
+  int64_t ws_tile_offset;
   int64_t ws_part_lse_offset;
   int64_t ws_part_o_offset;
   int64_t workspace_bytes;
   int64_t wait_budget_cycles; /* as in dsa_decode_plan_t                     */
-  int64_t reserved[5];
+  int64_t reserved[4];
 } dsa_prefix_plan_t;
 
 /* Plan the attention of num_tokens tokens over ONE list of records that all

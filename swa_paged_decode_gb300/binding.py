@@ -62,9 +62,9 @@ class PrefixPlan(ctypes.Structure):
         "magic", "abi_version", "num_tokens", "num_heads", "width", "d_qk", "num_sms",
         "pairs", "row_tiles", "key_tiles")] + \
         [(n, ctypes.c_int64) for n in (
-            "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_part_lse_offset",
-            "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
-        [("reserved", ctypes.c_int64 * 5)]
+            "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_tile_offset",
+            "ws_part_lse_offset", "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
+        [("reserved", ctypes.c_int64 * 4)]
 
 
 _lib = None

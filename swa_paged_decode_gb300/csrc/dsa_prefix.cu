@@ -59,6 +59,7 @@ struct PrefixParams {
   int2 *info;                  // [groups] (exponent or kPfMixed, mask of kept keys)
   int32_t *key_e;              // [keys] exponent of each key
   uint8_t *image;              // [128 keys][64-dim block][8-key group][1 KiB]
+  int2 *tile;                  // [R] (pair of the tile's first units, * 2, + 1 if not its first tile; of its last)
   float *part_lse;             // [C][2][128]
   float *part_o;               // [C][2][128][512]
 };
@@ -68,11 +69,29 @@ __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &
   len = list_limit(p.L, 0);
   return (len + kPfTile - 1) / kPfTile;
 }
-// Units are (row tile, key tile) pairs, row tile major; pair c owns
-// [range_begin(c), range_begin(c + 1)).
-__device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) {
-  const int64_t x = U * c;
-  return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)C) : x / C;   // (32-bit where it does)
+// Units are (row tile, key tile) pairs, row tile major, R x KT of them. Pair c
+// owns [begin(c), begin(c + 1)): equal shares of the cost, a unit's 1 and, for
+// a row tile that starts within the range, tile_cost = 2 for its Q staging, first
+// scores and epilogue (a range that starts within a tile pays these too, but
+// so does every range). With fewer than 2 units to a pair a whole unit more or
+// less counts for more than that, and a tile's start costs nothing. A pair may
+// own nothing.
+struct Schedule {
+  int32_t R, KT, C, tile_cost;
+  __device__ __forceinline__ int64_t units() const { return (int64_t)R * KT; }
+  __device__ __forceinline__ int64_t total() const { return (int64_t)R * (KT + tile_cost); }
+  // a / b for a, b >= 0, in 32 bits where they do
+  static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  }
+  __device__ __forceinline__ int64_t begin(int32_t c) const {
+    const int64_t x = div(total() * c, C), t = div(x, KT + tile_cost), w = x - t * (KT + tile_cost) - tile_cost;
+    return t * KT + (w > 0 ? w : 0);
+  }
+};
+
+__device__ __forceinline__ Schedule make_schedule(int32_t R, int32_t KT, int32_t C) {
+  return {R, KT, C, (int64_t)R * KT >= 2 * (int64_t)C ? 2 : 0};
 }
 
 // Weights of a row's prefix state (normalized, lse) and of its tail state in
@@ -81,7 +100,7 @@ __device__ __forceinline__ int64_t range_begin(int64_t U, int32_t C, int32_t c) 
 struct RowWeights {
   float o, tail, lse;
 };
-__device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int32_t h, float lse, float lt) {
+__device__ __forceinline__ RowWeights row_weights(float lse, float lt, bool sink, float sk) {
   const float M = fmaxf(lse, lt);
   RowWeights w = {0.f, 0.f, -INFINITY};
   if (!(M > -INFINITY)) {
@@ -91,27 +110,22 @@ __device__ __forceinline__ RowWeights row_weights(const PrefixParams &p, int32_t
   const float a = expf(lse - M), b = expf(lt - M), z = a + b;
   w.lse = M + logf(z);
   float den = z;
-  if (p.sink) {
-    const float sk = __ldg(p.sink + h);
-    den = sk == INFINITY ? INFINITY : z + expf(sk - M);
-  }
+  if (sink) den = sk == INFINITY ? INFINITY : z + expf(sk - M);
   w.o = a / den;
   w.tail = b / den;
   return w;
 }
-// 4 dims of a row's output: o (weighted) + wt * tail, as bf16. A tail that
-// weighs nothing is not read.
-__device__ __forceinline__ void store_out4(const PrefixParams &p, int64_t gr, int d, float4 o, float wt) {
-  const int64_t at = gr * kD + d;
-  if (p.tail_out && wt != 0.f) {
-    const uint2 t = *reinterpret_cast<const uint2 *>(p.tail_out + at);
+// 4 dims of a row's output: o (weighted) + wt * tail (4 bf16 values), as bf16.
+// A tail that weighs nothing does not count, whatever it holds.
+__device__ __forceinline__ void store_out4(const PrefixParams &p, int64_t gr, int d, float4 o, float wt, uint2 t) {
+  if (wt != 0.f) {
     o.x = fmaf(wt, bf16_bits_to_f32(t.x & 0xFFFFu), o.x);
     o.y = fmaf(wt, bf16_bits_to_f32(t.x >> 16), o.y);
     o.z = fmaf(wt, bf16_bits_to_f32(t.y & 0xFFFFu), o.z);
     o.w = fmaf(wt, bf16_bits_to_f32(t.y >> 16), o.w);
   }
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-  *reinterpret_cast<uint2 *>(p.out + at) =
+  *reinterpret_cast<uint2 *>(p.out + gr * kD + d) =
       make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
@@ -127,8 +141,11 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   int32_t len;
   const int32_t tiles = prefix_tiles(p, len);
   const int32_t key0 = blockIdx.x * kPfGroup;
-  if (key0 >= tiles * kPfTile) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp's 4 slots, in lanes 0..3, loaded along with the length
+  int32_t slot = -1;
+  if (lane < 4 && key0 + 4 * warp + lane < p.L.width) slot = __ldg(p.L.ids + key0 + 4 * warp + lane);
+  if (key0 >= tiles * kPfTile) return;
   // 4 keys per warp, their loads in flight together and kept as loaded until
   // the 32 keys' exponent is known
   RawRecord raw[4];
@@ -136,7 +153,7 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int32_t r = key0 + 4 * warp + i;
-    const int32_t sid = r < len ? __ldg(p.L.ids + r) : -1;
+    const int32_t sid = __shfl_sync(0xffffffffu, slot, i);
     ok[i] = slot_valid(p.L, r, len, sid);
     const uint8_t *rec = record_ptr(p.L, ok[i] ? sid : 0);
     if (ok[i]) ok[i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
@@ -277,9 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
   }
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
-  const int64_t U = (int64_t)p.R * KT;
-  const int64_t u0 = range_begin(U, p.C, pair);
-  const int64_t u1 = range_begin(U, p.C, pair + 1);   // (a pair may have no units)
+  const Schedule sched = make_schedule(p.R, KT, p.C);
+  const int64_t u0 = sched.begin(pair), u1 = sched.begin(pair + 1);   // (a pair may have no units)
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();
@@ -605,6 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       if (lane == 0) tc::mbar_arrive_remote(lead_qready);
     };
 
+    if (u0 >= u1 && tid < 64) p.part_lse[(int64_t)pair * 256 + side * 64 + tid] = -INFINITY;
     uint32_t ph_s = 0, nqk = 0, ph_pv = 0;
     const uint32_t prow = p_base + part * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
     bool waited = false;
@@ -743,7 +760,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       red_s[part * 64 + row] = l;
       const int64_t g0 = qt * 128 + side * 64;   // this CTA's first row
       const bool whole = first == qt * KT && end == (qt + 1) * KT;
-      const int64_t ps = (2 * (int64_t)pair + (qt == u0 / KT ? 0 : 1)) * 128 + side * 64;
+      const int late = qt == u0 / KT ? 0 : 1;
+      const int64_t ps = (2 * (int64_t)pair + late) * 128 + side * 64;
+      if (side == 0 && tid == 0) {   // which pairs the merge finds this tile in
+        if (first == qt * KT) p.tile[qt].x = 2 * pair + late;
+        if (end == (qt + 1) * KT) p.tile[qt].y = pair;
+      }
       sm_bar();
       if (tid < 64) {   // row tid: lane tid of the lower half holds it
         const int64_t gr = g0 + row;
@@ -754,7 +776,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (gr < p.rows) {
           if (whole) {
             const RowWeights w =
-                row_weights(p, (int32_t)(gr % p.H), lse, p.tail_lse ? p.tail_lse[gr] : -INFINITY);
+                row_weights(lse, p.tail_lse ? p.tail_lse[gr] : -INFINITY, p.sink != nullptr,
+                            p.sink ? __ldg(p.sink + (uint32_t)gr % (uint32_t)p.H) : 0.f);
             wo *= w.o;
             wt = w.tail;
             p.lse[gr] = w.lse;
@@ -805,7 +828,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
           for (int k = 0; k < 2; ++k) {
             const int pc = lane + 32 * k, d = (pc >> 4) * 128 + pass * 64 + (pc & 15) * 4;
             const float4 o = *reinterpret_cast<const float4 *>(smem + Cfg::kQ + r * 1024 + ((pc ^ (r & 7)) << 4));
-            if (whole) store_out4(p, gr, d, o, wt);
+            if (whole)
+              store_out4(p, gr, d, o, wt,
+                         p.tail_out && wt != 0.f ? *reinterpret_cast<const uint2 *>(p.tail_out + gr * kD + d)
+                                                 : make_uint2(0, 0));
             else __stcg(reinterpret_cast<float4 *>(p.part_o + (ps + r) * kD + d), o);
           }
         }
@@ -825,72 +851,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 }
 
 // ------------------------------------------------------------ merge
-// kTh threads per row, 512 / kTh dims each. Parts of a row are the pairs
-// whose ranges meet the row tile's units, in order (bitwise reproducible); M =
-// max_i lse_i, w_i = e^{lse_i - M}: the weights with a thread per part, then
-// the values of several parts in flight together. A row in few parts takes a
-// warp (16384 rows in 2 or 3 parts: four times the rows in flight of a block
-// per row), a row in many a block (256 rows in 38 parts: 11 us; with a warp
-// per row, one part after the other, 150 us).
-constexpr int kPfMergeThreads = 128;
+// Parts of a row are the pairs whose ranges meet the row tile's units; M =
+// max_i lse_i, w_i = e^{lse_i - M}. kGroups groups of kTh threads per row:
+// group g takes parts g, g + kGroups, ... (thread t of it dims 4 (t + kTh q)
+// ..), the groups' sums are added in their order, so the result does not
+// depend on who finishes first. The attend kernel leaves each tile's pairs in
+// `tile` (found anew by every thread they took longer than all the rest: 64-bit
+// divisions), and the first values are loaded along with the lse.
+// A row in few parts takes a warp (<32, 1>), a row in many a block of 4 groups
+// (<128, 4>), so that 32 parts are one round trip to L2.
 
-template <int kTh>
-__global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixParams p) {
-  constexpr int kQ = kD / 4 / kTh;               // float4 per thread: q = t + kTh i
-  constexpr int kIn = 8 / kQ;                    // parts in flight
-  __shared__ float w_sh[kPfMergeThreads];
-  __shared__ float red_s[kPfMergeThreads / 32];
-  pdl_wait_primary();
-  const int t = threadIdx.x % kTh, lane = threadIdx.x & 31;
-  float *w_s = w_sh + (threadIdx.x - t);
+template <int kTh, int kGroups>
+__global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
+    prefix_merge_kernel(PrefixParams p) {
+  constexpr int kBlock = kTh * kGroups < 128 ? 128 : kTh * kGroups;
+  constexpr int kRow = kTh * kGroups;            // threads of a row
+  constexpr int kQ = kD / 4 / kTh;               // float4 per thread and part
+  constexpr int kIn = kTh == 32 ? 2 : 8;         // parts of a group in flight
+  constexpr int kW = kRow;                       // parts whose weights are held at a time
+  __shared__ float w_sh[kBlock / kRow][kW];
+  __shared__ float red_s[kBlock / 32];
+  __shared__ float4 sum_s[kGroups > 1 ? (kGroups - 1) * kTh : 1];
+  const int rt = threadIdx.x % kRow, t = rt % kTh, g = rt / kTh, lane = threadIdx.x & 31;
+  float *w_s = w_sh[threadIdx.x / kRow];
   auto row_sync = [&]() {
-    if constexpr (kTh == 32) __syncwarp();
+    if constexpr (kRow == 32) __syncwarp();
     else __syncthreads();
   };
-  const int64_t gr = (int64_t)blockIdx.x * (kPfMergeThreads / kTh) + threadIdx.x / kTh;
-  if (gr >= p.rows) return;                      // (whole warps; a block has one row where it syncs)
+  const int64_t gr = (int64_t)blockIdx.x * (kBlock / kRow) + threadIdx.x / kRow;
+  const bool live = gr < p.rows;                 // (whole warps; a block has one row where it syncs)
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
-  const int64_t U = (int64_t)p.R * KT;
-  const int64_t us = (gr >> 7) * KT, ue = us + KT;
-  int32_t c0 = 0, c1 = -1;   // no parts: an empty prefix
+  pdl_wait_primary();
+  if (gr >= p.rows) return;                      // (whole warps; a block has one row where it syncs)
+  int32_t c0 = 0, c1 = -1;                       // no parts: an empty prefix
+  int64_t late = 0;
   if (KT > 0) {
-    auto owner = [&](int64_t u) {
-      const int64_t x = u * p.C;
-      int32_t c = (x >> 32) == 0 && U < (1ll << 32) ? (int32_t)((uint32_t)x / (uint32_t)U) : (int32_t)(x / U);
-      while (c + 1 < p.C && range_begin(U, p.C, c + 1) <= u) ++c;
-      while (c > 0 && range_begin(U, p.C, c) > u) --c;
-      return c;
-    };
-    c0 = owner(us);
-    c1 = owner(ue - 1);
-    if (c0 == c1) return;   // written by its pair
+    const int2 tl = __ldcg(p.tile + (gr >> 7));
+    c0 = tl.x >> 1;
+    c1 = tl.y;
+    late = (tl.x & 1) * 128;
+    if (c0 == c1) return;                        // written by its pair
   }
+  float lt = -INFINITY, sk = 0.f;
+  uint2 tail[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) tail[q] = make_uint2(0, 0);
+  if (p.tail_lse) {
+    lt = p.tail_lse[gr];
+    if (g == 0) {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        tail[q] = reinterpret_cast<const uint2 *>(p.tail_out + gr * kD)[t + kTh * q];
+    }
+  }
+  if (p.sink) sk = __ldg(p.sink + (uint32_t)gr % (uint32_t)p.H);
   // Partial of pair c: its first slot when the tile is its first, else its
-  // second (only c0 can have begun before the tile).
-  const int64_t row = gr & 127, late = range_begin(U, p.C, c0) < us ? 128 : 0;
+  // second (only c0 can have begun before the tile). A pair without units has
+  // left -inf in its first slot.
+  const int64_t row = gr & 127;
   auto slot = [&](int32_t c) { return (int64_t)c * 256 + (c == c0 ? late : 0) + row; };
-  auto part_lse = [&](int32_t c) {   // -inf for a pair without units
-    const bool has = c <= c1 && (U >= p.C || range_begin(U, p.C, c) < range_begin(U, p.C, c + 1));
-    return has ? __ldcg(p.part_lse + slot(c)) : -INFINITY;
+  const int n_all = c1 - c0 + 1;
+  auto part_lse = [&](int i) { return i < n_all ? __ldcg(p.part_lse + slot(c0 + i)) : -INFINITY; };
+  float4 o[kIn][kQ];
+  auto fetch = [&](int i0) {         // the group's parts i0, i0 + kGroups, .. (the last one again past the end)
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const float4 *src =
+          reinterpret_cast<const float4 *>(p.part_o + slot(c0 + min(i0 + kGroups * i, n_all - 1)) * kD) + t;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) o[i][q] = __ldcg(src + kTh * q);
+    }
   };
-  const float first = part_lse(c0 + t);
-  const float lt = p.tail_lse ? p.tail_lse[gr] : -INFINITY;
+  const float first = part_lse(rt);
+  fetch(g);
   float M = first;
   bool nan = first != first;
-  for (int32_t c = c0 + t + kTh; c <= c1; c += kTh) {
-    const float x = part_lse(c);
+#pragma unroll 1
+  for (int i = rt + kRow; i < n_all; i += kRow) {
+    const float x = part_lse(i);
     nan |= x != x;
     M = fmaxf(M, x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7FC00000u);   // a NaN stays one
-  if constexpr (kTh > 32) {
+  if constexpr (kRow > 32) {
     if (lane == 0) red_s[threadIdx.x >> 5] = M;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kTh / 32; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < kRow / 32; ++i) {
       const float x = red_s[i];
       M = (x != x || M != M) ? __uint_as_float(0x7FC00000u) : fmaxf(M, x);
     }
@@ -898,48 +948,60 @@ __global__ void __launch_bounds__(kPfMergeThreads) prefix_merge_kernel(PrefixPar
   float4 acc[kQ];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f;
-  if (M != -INFINITY) {
-    for (int32_t cb = c0; cb <= c1; cb += kTh) {
-      const float x = cb == c0 ? first : part_lse(cb + t);
-      row_sync();
-      w_s[t] = x == -INFINITY ? 0.f : expf(x - M);
-      row_sync();
-      const int n = min(kTh, c1 - cb + 1);
-      for (int i0 = 0; i0 < n; i0 += kIn) {
-        float4 o[kIn][kQ];
+  float z = 0.f;                                 // (every thread adds all weights: no exchange)
+#pragma unroll 1
+  for (int cb = 0; cb < n_all && M != -INFINITY; cb += kW) {   // (M: a row without a kept key)
+    const int n = min(kW, n_all - cb);
+    row_sync();
+    if (rt < n) {
+      const float x = cb == 0 ? first : part_lse(cb + rt);
+      w_s[rt] = x == -INFINITY ? 0.f : expf(x - M);
+    }
+    row_sync();
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) z += w_s[i];
+#pragma unroll 1
+    for (int i0 = g; i0 < n; i0 += kGroups * kIn) {
+      if (cb + i0 > g) fetch(cb + i0);
 #pragma unroll
-        for (int i = 0; i < kIn; ++i) {
-          const int j = min(i0 + i, n - 1);   // (loaded without a branch, used if it counts)
-          const float4 *src = reinterpret_cast<const float4 *>(p.part_o + slot(cb + j) * kD) + t;
+      for (int i = 0; i < kIn; ++i) {
+        const int j = i0 + kGroups * i;
+        const float w = j < n ? w_s[j] : 0.f;
+        if (w == 0.f) continue;                  // (a pair without units left its slot as it was)
 #pragma unroll
-          for (int q = 0; q < kQ; ++q) o[i][q] = __ldcg(src + kTh * q);
-        }
-#pragma unroll
-        for (int i = 0; i < kIn; ++i) {
-          const float w = i0 + i < n ? w_s[i0 + i] : 0.f;
-          if (w == 0.f) continue;   // (a pair without units left its slot as it was)
-          z += w;
-#pragma unroll
-          for (int q = 0; q < kQ; ++q) {
-            acc[q].x = fmaf(w, o[i][q].x, acc[q].x);
-            acc[q].y = fmaf(w, o[i][q].y, acc[q].y);
-            acc[q].z = fmaf(w, o[i][q].z, acc[q].z);
-            acc[q].w = fmaf(w, o[i][q].w, acc[q].w);
-          }
+        for (int q = 0; q < kQ; ++q) {
+          acc[q].x = fmaf(w, o[i][q].x, acc[q].x);
+          acc[q].y = fmaf(w, o[i][q].y, acc[q].y);
+          acc[q].z = fmaf(w, o[i][q].z, acc[q].z);
+          acc[q].w = fmaf(w, o[i][q].w, acc[q].w);
         }
       }
     }
   }
+  if constexpr (kGroups > 1) {
+    if (g > 0) sum_s[(g - 1) * kTh + t] = acc[0];
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float4 x = sum_s[k * kTh + t];
+      acc[0].x += x.x;
+      acc[0].y += x.y;
+      acc[0].z += x.z;
+      acc[0].w += x.w;
+    }
+  }
   const float lse = z == 0.f ? -INFINITY : M + logf(z);
-  const RowWeights w = row_weights(p, (int32_t)(gr % p.H), lse, lt);
+  const RowWeights w = row_weights(lse, lt, p.sink != nullptr, sk);
   const float wo = z == 0.f ? 0.f : w.o / z;
-  row_sync();   // every thread has read the row's tail_lse, which lse may alias
-  if (t == 0) p.lse[gr] = w.lse;
+  // (out may alias the tail, which its own thread has read; lse too, which
+  // every thread of the row has read before a barrier above or this one)
+  if constexpr (kRow == 32) __syncwarp();
+  if (rt == 0) p.lse[gr] = w.lse;
 #pragma unroll
   for (int q = 0; q < kQ; ++q)
     store_out4(p, gr, 4 * (t + kTh * q), make_float4(acc[q].x * wo, acc[q].y * wo, acc[q].z * wo, acc[q].w * wo),
-               w.tail);
+               w.tail, tail[q]);
 }
 
 }  // namespace dsa
@@ -1034,10 +1096,10 @@ cudaError_t launch_prefix(const PrefixParams &p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32>, p, map);
   if (e != cudaSuccess) return e;
-  // about C / R + 1 parts to a row
-  if (p.C < 4 * p.R)
-    return launch_dependent(config((unsigned)((p.rows + 3) / 4), kPfMergeThreads, 0, st), prefix_merge_kernel<32>, p);
-  return launch_dependent(config((unsigned)p.rows, kPfMergeThreads, 0, st), prefix_merge_kernel<kPfMergeThreads>, p);
+  // about C / R + 1 parts to a row: up to 9 by a warp, more by a block
+  if (p.C < 8 * p.R)
+    return launch_dependent(config((unsigned)((p.rows + 3) / 4), 128, 0, st), prefix_merge_kernel<32, 1>, p);
+  return launch_dependent(config((unsigned)p.rows, 256, 0, st), prefix_merge_kernel<128, 2>, p);
 }
 
 }  // namespace
@@ -1074,7 +1136,7 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   const int64_t units = (int64_t)plan->row_tiles * plan->key_tiles;
   pairs = pairs < 1 ? 1 : pairs;
   plan->pairs = units < pairs ? (int32_t)(units < 1 ? 1 : units) : pairs;
-  // Workspace: status | group info | key exponents | images | part_lse | part_o
+  // Workspace: status | group info | key exponents | images | tile | part_lse | part_o
   const int64_t keys = (int64_t)plan->key_tiles * dsa::kPfTile, slots = 2 * (int64_t)plan->pairs * 128;
   int64_t off = 256;
   plan->ws_info_offset = off;
@@ -1083,6 +1145,8 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
   off = dsa::align_up(off + 4 * keys, 256);
   plan->ws_image_offset = off;
   off += keys * d_qk * 2;
+  plan->ws_tile_offset = off;
+  off = dsa::align_up(off + 8 * (int64_t)plan->row_tiles, 256);
   plan->ws_part_lse_offset = off;
   off = dsa::align_up(off + 4 * slots, 256);
   plan->ws_part_o_offset = off;
@@ -1156,6 +1220,7 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
   p.info = reinterpret_cast<int2 *>(w + plan->ws_info_offset);
   p.key_e = reinterpret_cast<int32_t *>(w + plan->ws_key_e_offset);
   p.image = reinterpret_cast<uint8_t *>(w + plan->ws_image_offset);
+  p.tile = reinterpret_cast<int2 *>(w + plan->ws_tile_offset);
   p.part_lse = reinterpret_cast<float *>(w + plan->ws_part_lse_offset);
   p.part_o = reinterpret_cast<float *>(w + plan->ws_part_o_offset);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

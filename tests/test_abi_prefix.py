@@ -54,7 +54,7 @@ def test_plan_layout(lib, T, H, width, sms, d):
     assert 1 <= p.pairs <= max(1, sms // 2) and p.pairs <= p.row_tiles * p.key_tiles
     keys, parts = 256 * p.key_tiles, 2 * p.pairs * 128
     spans = [(0, 256), (p.ws_info_offset, 8 * keys // 32), (p.ws_key_e_offset, 4 * keys),
-             (p.ws_image_offset, 2 * d * keys), (p.ws_part_lse_offset, 4 * parts), (p.ws_part_o_offset, 2048 * parts)]
+             (p.ws_image_offset, 2 * d * keys), (p.ws_tile_offset, 8 * p.row_tiles), (p.ws_part_lse_offset, 4 * parts), (p.ws_part_o_offset, 2048 * parts)]
     for (a, n), (b, _) in zip(spans, spans[1:] + [(nbytes, 0)]):
         assert a % 256 == 0 and a + n <= b
     assert p.workspace_bytes == nbytes and p.wait_budget_cycles == 0
