@@ -32,51 +32,94 @@ struct CacheParams {
   int32_t *status;           // optional status word
 };
 
-constexpr int kCacheWarps = 4;   // rows per block (a row has no shared state)
+constexpr int kCacheWarps = 4;      // warps per block (a row has no shared state)
+constexpr int kCacheBlocks = 760;   // 5 per SM of 152, all resident: more rows than that make the warps loop
 
-// Type TY's 16 values at p (16-byte aligned) -> fp32.
+// ------------------------------------------------------------ packed fp32
+// Two fp32 values in a register pair: one instruction for both (each result
+// rounded as the scalar instruction rounds it).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// ------------------------------------------------------------ rows
 template <int TY>
-__device__ __forceinline__ void load16(const void *p, float (&v)[16]) {
-  if constexpr (TY == DSA_TYPE_F32) {
+constexpr int kTypeBytes = TY == DSA_TYPE_F32 ? 4 : 2;
+
+// A lane's 16 values of a row as loaded: 32 or 64 bytes, in 32-byte loads where
+// the rows allow it (`wide`: they start on 32 bytes), else 16-byte ones.
+template <int TY>
+struct RowRaw {
+  uint4 q[TY == DSA_TYPE_F32 ? 4 : 2];
+  uint32_t t[TY == DSA_TYPE_F32 ? 2 : 1];   // V3.2: dims 512 + 2 lane, + 1
+};
+template <int TY, bool kV32>
+__device__ __forceinline__ void load_row(const char *row, int lane, bool wide, RowRaw<TY> &r) {
+  constexpr int kN = TY == DSA_TYPE_F32 ? 4 : 2;
+  const char *p = row + 16 * lane * kTypeBytes<TY>;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 w = ld_row(static_cast<const uint4 *>(p) + i);
-      v[4 * i] = __uint_as_float(w.x);
-      v[4 * i + 1] = __uint_as_float(w.y);
-      v[4 * i + 2] = __uint_as_float(w.z);
-      v[4 * i + 3] = __uint_as_float(w.w);
+  for (int i = 0; i < kN; i += 2) {
+    if (wide) {
+      tc::ldg_nc_v8(p + 16 * i, r.q[i], r.q[i + 1]);
+    } else {
+      r.q[i] = ld_row(p + 16 * i);
+      r.q[i + 1] = ld_row(p + 16 * i + 16);
     }
-  } else {
-    const uint4 a = ld_row(p), b = ld_row(static_cast<const uint4 *>(p) + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+  if constexpr (kV32) {
+    const uint32_t *p2 = reinterpret_cast<const uint32_t *>(row + (kD + 2 * lane) * kTypeBytes<TY>);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (TY == DSA_TYPE_BF16) {
-        v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-        v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-    }
+    for (int i = 0; i < kTypeBytes<TY> / 2; ++i) r.t[i] = __ldg(p2 + i);
   }
 }
 template <int TY>
-__device__ __forceinline__ void load2(const void *p, float &a, float &b) {
-  if constexpr (TY == DSA_TYPE_F32) {
-    const float2 f = __ldg(static_cast<const float2 *>(p));
-    a = f.x;
-    b = f.y;
-  } else {
-    const uint32_t w = __ldg(static_cast<const uint32_t *>(p));
-    if constexpr (TY == DSA_TYPE_BF16) {
-      a = bf16_bits_to_f32(w & 0xFFFFu);
-      b = bf16_bits_to_f32(w >> 16);
+__device__ __forceinline__ F2 unpack2(uint32_t w) {
+  if constexpr (TY == DSA_TYPE_BF16) return f2(bf16_bits_to_f32(w & 0xFFFFu), __uint_as_float(w & 0xFFFF0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return f2(f.x, f.y);
+}
+template <int TY, bool kV32>
+__device__ __forceinline__ void unpack_row(const RowRaw<TY> &r, F2 (&v)[8], float &t0, float &t1) {
+#pragma unroll
+  for (int i = 0; i < (TY == DSA_TYPE_F32 ? 4 : 2); ++i) {
+    const uint32_t w[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+    if constexpr (TY == DSA_TYPE_F32) {
+      v[2 * i] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      v[2 * i + 1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
     } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-      a = f.x;
-      b = f.y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * i + k] = unpack2<TY>(w[k]);
+    }
+  }
+  if constexpr (kV32) {
+    if constexpr (TY == DSA_TYPE_F32) {
+      t0 = __uint_as_float(r.t[0]);
+      t1 = __uint_as_float(r.t[1]);
+    } else {
+      f2_get(unpack2<TY>(r.t[0]), t0, t1);
     }
   }
 }
@@ -89,20 +132,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (TY == DSA_TYPE_BF16) return bf16x2_bits(lo, hi);
   else return tc::pack_f16x2(lo, hi);
 }
-template <int TY>
-constexpr int kTypeBytes = TY == DSA_TYPE_F32 ? 4 : 2;
 
-// Largest magnitude of 16 values as bits: magnitudes order as their bits, a
-// NaN above every number, so a NaN among the values is not lost.
-__device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+// ------------------------------------------------------------ blocks
+// The larger magnitude; a NaN stays one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-// ... over the block's neighbouring lanes.
+// Largest magnitude of a block: this lane's 16 values, then the block's
+// neighbouring lanes. As bits: magnitudes order as their bits, a NaN above
+// every number.
 template <int LANES>
-__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+__device__ __forceinline__ uint32_t block_amax(const float (&v)[16]) {
+  float a = max_nan(fabsf(v[0]), fabsf(v[1])), b = max_nan(fabsf(v[2]), fabsf(v[3]));
+#pragma unroll
+  for (int i = 4; i < 16; i += 2) {
+    a = max_nan(a, fabsf(v[i]));
+    b = max_nan(b, fabsf(v[i + 1]));
+  }
+  uint32_t m = __float_as_uint(max_nan(a, b));
 #pragma unroll
   for (int off = 1; off < LANES; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
   return m;
@@ -122,14 +171,46 @@ __device__ __forceinline__ float ue8m0_down(uint32_t byte) {
   if (byte == 255u) return __uint_as_float(0x7FC00000u);
   return __uint_as_float(byte == 254u ? 0x00400000u : (254u - byte) << 23);
 }
-// 16 values times a power of two -> e4m3 codes.
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float down) {
+// y = x / s for 16 values, each rounded to nearest. With inv = 1 / s rounded
+// to nearest, q = x inv and its exact remainder x - q s, q + inv (x - q s)
+// rounds to the quotient (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000", 1990): 3 packed instructions for two values.
+// The remainder is exact while it stays clear of the subnormals, which a
+// scale in 2^-60 .. 2^60 sees to wherever the quotient matters (below 2^-10
+// every code is 0); other scales, and blocks with an infinity, divide.
+__device__ __forceinline__ void divide16(const F2 (&x)[8], float s, bool finite, float (&y)[16]) {
+  if (finite && s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f) {
+    const float inv = __frcp_rn(s);
+    const F2 i2 = f2(inv, inv), ns = f2(-s, -s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const F2 q = f2_mul(x[k], i2);
+      f2_get(f2_fma(f2_fma(q, ns, x[k]), i2, q), y[2 * k], y[2 * k + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float a, b;
+      f2_get(x[k], a, b);
+      y[2 * k] = __fdiv_rn(a, s);
+      y[2 * k + 1] = __fdiv_rn(b, s);
+    }
+  }
+}
+// 16 values -> e4m3 codes.
+__device__ __forceinline__ uint4 codes16(const float (&y)[16]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = e4m3x2_rn_sat(v[4 * i] * down, v[4 * i + 1] * down) |
-           (e4m3x2_rn_sat(v[4 * i + 2] * down, v[4 * i + 3] * down) << 16);
+    w[i] = e4m3x2_rn_sat(y[4 * i], y[4 * i + 1]) | (e4m3x2_rn_sat(y[4 * i + 2], y[4 * i + 3]) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 codes16_scaled(const F2 (&x)[8], float down) {
+  const F2 d2 = f2(down, down);
+  float y[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f2_get(f2_mul(x[k], d2), y[2 * k], y[2 * k + 1]);
+  return codes16(y);
 }
 // Eight fp32 values -> e2m1 codes (nearest even, saturating at 6), element i
 // in nibble i; a zero code has no sign.
@@ -148,179 +229,230 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int o) {
   return w & (nz * 15u);
 }
 
+// ------------------------------------------------------------ norm
+// x * w / sqrt(mean x^2 + eps) over dims 0..511, each result its exact value
+// rounded to fp32 (but for a few in a hundred off by one step): a relative
+// error of 2^-23 in front of the quantization would move the codes of four
+// elements in a million. The squares are summed as a tree and the lanes' sums
+// with their rounding errors; the root's reciprocal carries a correction r1,
+// and the products theirs.
+__device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps) {
+  F2 sq[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sq[k] = f2_fma(v[2 * k], v[2 * k], f2_mul(v[2 * k + 1], v[2 * k + 1]));
+  float s0, s1;
+  f2_get(f2_add(f2_add(sq[0], sq[1]), f2_add(sq[2], sq[3])), s0, s1);
+  float ss = s0 + s1, sl = 0.f;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float o = __shfl_xor_sync(0xffffffffu, ss, off), ol = __shfl_xor_sync(0xffffffffu, sl, off);
+    const float t = ss + o, z = t - ss;          // ss + o = t + the error of t
+    sl += ol + ((ss - (t - z)) + (o - z));
+    ss = t;
+  }
+  const float ms = ss * (1.0f / kD), me = ms + eps, mz = me - ms;
+  const float ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (eps - mz));
+  // 1 / sqrt(me + ml) = r0 + r1: one Newton step, its residual 1 - (me + ml) r0^2 by FMAs
+  const float r0 = 1.0f / sqrtf(me);
+  const float h = me * r0, hl = fmaf(me, r0, -h) + ml * r0;
+  const float r1 = 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f));
+  const F2 a = f2(r0, r0), b = f2(r1, r1), minus = f2(-1.f, -1.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {   // x w = q + ql
+    const F2 q = f2_mul(v[k], w[k]), ql = f2_fma(v[k], w[k], f2_mul(q, minus));
+    v[k] = f2_fma(q, a, f2_fma(ql, a, f2_mul(q, b)));
+  }
+}
+
 // ------------------------------------------------------------ write
 // x -> (norm) -> (rotation) -> codes and scales, all in fp32 from the loaded
-// values to the codes: nothing is rounded to 16 bits in between.
+// values to the codes: nothing is rounded to 16 bits in between. A warp's next
+// row is loaded before its present one is worked on.
 template <int FMT, int TY>
-__global__ void __launch_bounds__(32 * kCacheWarps) cache_write_kernel(CacheParams p) {
+__global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheParams p) {
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
-  if (i >= p.n) return;   // whole warps
-  const int32_t sid = __ldg(p.L.ids + i);
-  const char *row = static_cast<const char *>(p.src) + i * p.stride * kTypeBytes<TY>;
-  float v[16], t0 = 0.f, t1 = 0.f;
-  load16<TY>(row + 16 * lane * kTypeBytes<TY>, v);
-  if constexpr (kV32) load2<TY>(row + (kD + 2 * lane) * kTypeBytes<TY>, t0, t1);
-  if (sid < 0 || (int64_t)sid >= p.L.num_slots) return;   // padding: nothing is written
-  // x * w / sqrt(mean x^2 + eps) over dims 0..511, each result its exact
-  // value rounded to fp32 (but for a few in a hundred off by one step): a
-  // relative error of 2^-23 in front of the quantization would move the codes
-  // of four elements in a million. The squares are summed as a tree and the
-  // lanes' sums with their rounding errors; the root's reciprocal carries a
-  // correction r1, and the products theirs. 90 instructions more for a row
-  // than the plain fp32 form.
+  const int64_t step = (int64_t)gridDim.x * kCacheWarps;
+  const char *src = static_cast<const char *>(p.src);
+  const int64_t stride = p.stride * kTypeBytes<TY>;
+  const bool wide = ((reinterpret_cast<uintptr_t>(src) | (uintptr_t)stride) & 31u) == 0;
+  F2 w[8];
   if (p.norm_w) {
-    float sq[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sq[k] = fmaf(v[2 * k], v[2 * k], v[2 * k + 1] * v[2 * k + 1]);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < o; ++k) sq[k] += sq[k + o];
-    float ss = sq[0], sl = 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float o = __shfl_xor_sync(0xffffffffu, ss, off), ol = __shfl_xor_sync(0xffffffffu, sl, off);
-      const float t = ss + o, z = t - ss;          // ss + o = t + the error of t
-      sl += ol + ((ss - (t - z)) + (o - z));
-      ss = t;
-    }
-    const float ms = ss * (1.0f / kD), me = ms + p.eps, mz = me - ms;
-    const float ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (p.eps - mz));
-    // 1 / sqrt(me + ml) = r0 + r1: one Newton step, its residual 1 - (me + ml) r0^2 by FMAs
-    const float r0 = 1.0f / sqrtf(me);
-    const float h = me * r0, hl = fmaf(me, r0, -h) + ml * r0;
-    const float r1 = 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f));
     const float4 *w4 = reinterpret_cast<const float4 *>(p.norm_w) + 4 * lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 w = __ldg(w4 + k);
-      const float wk[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float &x = v[4 * k + e];
-        const float q = x * wk[e], ql = fmaf(x, wk[e], -q);
-        x = fmaf(q, r0, fmaf(q, r1, ql * r0));
-      }
+      const float4 x = __ldg(w4 + k);
+      w[2 * k] = f2(x.x, x.y);
+      w[2 * k + 1] = f2(x.z, x.w);
     }
   }
-  // (a, b) -> (a cos - b sin, b cos + a sin) on the last 64 dims
-  if (p.cos_sin) {
-    const int64_t pos = __ldg(p.positions + i);
-    if (pos < 0 || pos >= p.cs_rows) {   // outside the table: the row is not written
-      if (p.status && lane == 0) report_status(p.status, DSA_ERR_INVALID_ARG);
-      return;
-    }
-    const float *cs = p.cos_sin + pos * 64;
-    if constexpr (kV32) {   // dims 512 + 2 lane, + 1
-      if (p.gptj) {         // one pair
-        const float c = __ldg(cs + lane), s = __ldg(cs + 32 + lane);
-        const float a = t0, b = t1;
-        t0 = fmaf(a, c, -(b * s));
-        t1 = fmaf(b, c, a * s);
-      } else {              // the partners of two pairs sit 16 lanes away
-        const float2 c = __ldg(reinterpret_cast<const float2 *>(cs) + (lane & 15));
-        const float2 s = __ldg(reinterpret_cast<const float2 *>(cs) + 16 + (lane & 15));
-        const float o0 = __shfl_xor_sync(0xffffffffu, t0, 16), o1 = __shfl_xor_sync(0xffffffffu, t1, 16);
-        const float sg = lane < 16 ? -1.f : 1.f;
-        t0 = fmaf(t0, c.x, sg * (o0 * s.x));
-        t1 = fmaf(t1, c.y, sg * (o1 * s.y));
+  RowRaw<TY> next;
+  int32_t next_sid = -1;
+  int64_t next_pos = 0;
+  auto fetch = [&](int64_t i) {
+    if (i >= p.n) return;
+    next_sid = __ldg(p.L.ids + i);
+    if (p.cos_sin) next_pos = __ldg(p.positions + i);
+    load_row<TY, kV32>(src + i * stride, lane, wide, next);
+  };
+  int64_t i = (int64_t)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
+  fetch(i);
+#pragma unroll 1
+  for (; i < p.n; i += step) {   // whole warps
+    const RowRaw<TY> raw = next;
+    const int32_t sid = next_sid;
+    const int64_t pos = next_pos;
+    fetch(i + step);
+    if (sid < 0 || (int64_t)sid >= p.L.num_slots) continue;   // padding: nothing is written
+    const float4 *cs = nullptr;
+    float4 c4[2][2];             // lanes 28..31: cos, sin of the lane's pairs (NeoX: of its 16 dims, loaded below)
+    if (p.cos_sin) {
+      if (pos < 0 || pos >= p.cs_rows) {   // outside the table: the row is not written
+        if (p.status && lane == 0) report_status(p.status, DSA_ERR_INVALID_ARG);
+        continue;
       }
-    } else {                // lanes 28..31
-      const int r = lane - 28;
-      if (p.gptj) {
-        if (r >= 0) {
+      cs = reinterpret_cast<const float4 *>(p.cos_sin + pos * 64);
+      if (!kV32 && p.gptj && lane >= 28) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          c4[0][k] = __ldg(cs + 2 * (lane - 28) + k);
+          c4[1][k] = __ldg(cs + 8 + 2 * (lane - 28) + k);
+        }
+      }
+    }
+    F2 v[8];
+    float t0 = 0.f, t1 = 0.f;
+    unpack_row<TY, kV32>(raw, v, t0, t1);
+    if (p.norm_w) norm_row(v, w, p.eps);
+    // (a, b) -> (a cos - b sin, b cos + a sin) on the last 64 dims
+    if (cs) {
+      const float *cf = reinterpret_cast<const float *>(cs);
+      if constexpr (kV32) {   // dims 512 + 2 lane, + 1
+        if (p.gptj) {         // one pair
+          const float c = __ldg(cf + lane), s = __ldg(cf + 32 + lane);
+          const float a = t0, b = t1;
+          t0 = fmaf(a, c, -(b * s));
+          t1 = fmaf(b, c, a * s);
+        } else {              // the partners of two pairs sit 16 lanes away
+          const float2 c = __ldg(reinterpret_cast<const float2 *>(cf) + (lane & 15));
+          const float2 s = __ldg(reinterpret_cast<const float2 *>(cf) + 16 + (lane & 15));
+          const float o0 = __shfl_xor_sync(0xffffffffu, t0, 16), o1 = __shfl_xor_sync(0xffffffffu, t1, 16);
+          const float sg = lane < 16 ? -1.f : 1.f;
+          t0 = fmaf(t0, c.x, sg * (o0 * s.x));
+          t1 = fmaf(t1, c.y, sg * (o1 * s.y));
+        }
+      } else if (p.gptj) {    // lanes 28..31, pairs within a lane
+        if (lane >= 28) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float c = __ldg(cs + 8 * r + k), s = __ldg(cs + 32 + 8 * r + k);
-            const float a = v[2 * k], b = v[2 * k + 1];
-            v[2 * k] = fmaf(a, c, -(b * s));
-            v[2 * k + 1] = fmaf(b, c, a * s);
+            const float4 c = c4[0][k >> 2], s4 = c4[1][k >> 2];
+            const float co = (k & 3) == 0 ? c.x : (k & 3) == 1 ? c.y : (k & 3) == 2 ? c.z : c.w;
+            const float si = (k & 3) == 0 ? s4.x : (k & 3) == 1 ? s4.y : (k & 3) == 2 ? s4.z : s4.w;
+            float a, b;
+            f2_get(v[k], a, b);
+            v[k] = f2(fmaf(a, co, -(b * si)), fmaf(b, co, a * si));
           }
         }
-      } else {              // partners two lanes away
-        const float sg = r < 2 ? -1.f : 1.f;
+      } else {                // partners two lanes away: (28, 30), (29, 31)
+        const float sg = lane < 30 ? -1.f : 1.f;
+        const int f = 4 * (lane & 1);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float o = __shfl_xor_sync(0xffffffffu, v[k], 2);
-          if (r >= 0) {
-            const float c = __ldg(cs + 16 * (r & 1) + k), s = __ldg(cs + 32 + 16 * (r & 1) + k);
-            v[k] = fmaf(v[k], c, sg * (o * s));
+        for (int k = 0; k < 4; ++k) {
+          float a, b, c, d;
+          f2_get(v[2 * k], a, b);
+          f2_get(v[2 * k + 1], c, d);
+          const float oa = __shfl_xor_sync(0xffffffffu, a, 2), ob = __shfl_xor_sync(0xffffffffu, b, 2);
+          const float oc = __shfl_xor_sync(0xffffffffu, c, 2), od = __shfl_xor_sync(0xffffffffu, d, 2);
+          if (lane >= 28) {
+            const float4 co = __ldg(cs + f + k), si = __ldg(cs + 8 + f + k);
+            v[2 * k] = f2(fmaf(a, co.x, sg * (oa * si.x)), fmaf(b, co.y, sg * (ob * si.y)));
+            v[2 * k + 1] = f2(fmaf(c, co.z, sg * (oc * si.z)), fmaf(d, co.w, sg * (od * si.w)));
           }
         }
       }
     }
-  }
-  uint8_t *rec = const_cast<uint8_t *>(record_ptr(p.L, sid));
-  if (kDebug && (rec < p.L.base || rec + p.L.rec > p.L.base + p.L.extent)) {
-    if (p.status) report_status(p.status, DSA_ERR_BOUNDS);
-    return;
-  }
-  const uint32_t am = amax16(v);
-  if constexpr (FMT == DSA_REC_FP8_528 || kV32) {
-    const uint32_t m = block_max<8>(am);
-    const float s = __fdiv_rn(__uint_as_float(m), 448.0f);
-    const float d = s > 0.f || !(s == s) ? s : 1.0f;   // zero blocks divide by one
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = e4m3x2_rn_sat(__fdiv_rn(v[4 * k], d), __fdiv_rn(v[4 * k + 1], d)) |
-             (e4m3x2_rn_sat(__fdiv_rn(v[4 * k + 2], d), __fdiv_rn(v[4 * k + 3], d)) << 16);
-    *reinterpret_cast<uint4 *>(rec + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
-    if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + 512 + (lane >> 1)) = s;
-    if constexpr (kV32) *reinterpret_cast<uint32_t *>(rec + 528 + 4 * lane) = bf16x2_bits(t0, t1);
-  } else if constexpr (FMT == DSA_REC_FP8_528_UE8M0) {
-    const uint32_t e = ue8m0_of(block_max<2>(am));
-    *reinterpret_cast<uint4 *>(rec + 16 * lane) = codes16(v, ue8m0_down(e));
-    if ((lane & 1) == 0) rec[512 + (lane >> 1)] = (uint8_t)e;
-  } else if constexpr (FMT == DSA_REC_MODEL1_584) {
-    const uint32_t e = ue8m0_of(block_max<4>(am));
-    if (lane < 28) {         // 8-byte aligned records
-      const uint4 w = codes16(v, ue8m0_down(e));
-      uint2 *d = reinterpret_cast<uint2 *>(rec + 16 * lane);
-      d[0] = make_uint2(w.x, w.y);
-      d[1] = make_uint2(w.z, w.w);
-      if ((lane & 3) == 0) rec[576 + (lane >> 2)] = (uint8_t)e;
-    } else {                 // the bf16 part, and the unused byte
-      uint2 *d = reinterpret_cast<uint2 *>(rec + 448 + 32 * (lane - 28));
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        d[k] = make_uint2(bf16x2_bits(v[4 * k], v[4 * k + 1]), bf16x2_bits(v[4 * k + 2], v[4 * k + 3]));
-      if (lane == 28) rec[583] = 0;
+    uint8_t *rec = const_cast<uint8_t *>(record_ptr(p.L, sid));
+    if (kDebug && (rec < p.L.base || rec + p.L.rec > p.L.base + p.L.extent)) {
+      if (p.status) report_status(p.status, DSA_ERR_BOUNDS);
+      continue;
     }
-  } else {                   // NVFP4: a block is one lane's 16 dims
-    const float a6 = fminf(__fdiv_rn(__uint_as_float(am), 6.0f), 448.0f);
-    const uint32_t sb = am > 0x7F800000u ? 0x7Fu : (e4m3x2_rn_sat(a6, 0.f) & 0xFFu);
-    const float s = e4m3_to_f32(sb);
-    uint2 w = make_uint2(0u, 0u);
-    if (sb != 0u && sb != 0x7Fu) {
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f2_get(v[k], x[2 * k], x[2 * k + 1]);
+    if constexpr (FMT == DSA_REC_FP8_528 || kV32) {
+      const uint32_t m = block_amax<8>(x);
+      const float s = __fdiv_rn(__uint_as_float(m), 448.0f);
       float y[16];
+      divide16(v, s > 0.f || s != s ? s : 1.0f, true, y);   // zero blocks divide by one
+      *reinterpret_cast<uint4 *>(rec + 16 * lane) = codes16(y);
+      if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + 512 + (lane >> 1)) = s;
+      if constexpr (kV32) *reinterpret_cast<uint32_t *>(rec + 528 + 4 * lane) = bf16x2_bits(t0, t1);
+    } else if constexpr (FMT == DSA_REC_FP8_528_UE8M0) {
+      const uint32_t e = ue8m0_of(block_amax<2>(x));
+      *reinterpret_cast<uint4 *>(rec + 16 * lane) = codes16_scaled(v, ue8m0_down(e));
+      if ((lane & 1) == 0) rec[512 + (lane >> 1)] = (uint8_t)e;
+    } else if constexpr (FMT == DSA_REC_MODEL1_584) {
+      const uint32_t e = ue8m0_of(block_amax<4>(x));
+      if (lane < 28) {         // 8-byte aligned records
+        const uint4 c = codes16_scaled(v, ue8m0_down(e));
+        uint2 *d = reinterpret_cast<uint2 *>(rec + 16 * lane);
+        d[0] = make_uint2(c.x, c.y);
+        d[1] = make_uint2(c.z, c.w);
+        if ((lane & 3) == 0) rec[576 + (lane >> 2)] = (uint8_t)e;
+      } else {                 // the bf16 part, and the unused byte
+        uint2 *d = reinterpret_cast<uint2 *>(rec + 448 + 32 * (lane - 28));
 #pragma unroll
-      for (int k = 0; k < 16; ++k) y[k] = __fdiv_rn(v[k], s);
-      w = make_uint2(e2m1x8(y, 0), e2m1x8(y, 8));
+        for (int k = 0; k < 4; ++k)
+          d[k] = make_uint2(bf16x2_bits(x[4 * k], x[4 * k + 1]), bf16x2_bits(x[4 * k + 2], x[4 * k + 3]));
+        if (lane == 28) rec[583] = 0;
+      }
+    } else {                   // NVFP4: a block is one lane's 16 dims
+      const uint32_t m = block_amax<1>(x);
+      const float a6 = fminf(__fdiv_rn(__uint_as_float(m), 6.0f), 448.0f);
+      const uint32_t sb = m > 0x7F800000u ? 0x7Fu : (e4m3x2_rn_sat(a6, 0.f) & 0xFFu);
+      uint2 c = make_uint2(0u, 0u);
+      if (sb != 0u && sb != 0x7Fu) {
+        float y[16];
+        divide16(v, e4m3_to_f32(sb), m < 0x7F800000u, y);
+        c = make_uint2(e2m1x8(y, 0), e2m1x8(y, 8));
+      }
+      *reinterpret_cast<uint2 *>(rec + 8 * lane) = c;
+      rec[256 + lane] = (uint8_t)sb;
     }
-    *reinterpret_cast<uint2 *>(rec + 8 * lane) = w;
-    rec[256 + lane] = (uint8_t)sb;
   }
 }
 
 // ------------------------------------------------------------ read
-template <int TY>
-__device__ __forceinline__ void store16(char *row, int lane, const float (&v)[16]) {
-  uint4 *d = reinterpret_cast<uint4 *>(row + 16 * lane * kTypeBytes<TY>);
-  if constexpr (TY == DSA_TYPE_F32) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      d[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
-                        __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+// 32 bytes in one store (p 32-byte aligned), or two of 16.
+__device__ __forceinline__ void store32(void *p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
   } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      d[k] = make_uint4(pack2<TY>(v[8 * k], v[8 * k + 1]), pack2<TY>(v[8 * k + 2], v[8 * k + 3]),
-                        pack2<TY>(v[8 * k + 4], v[8 * k + 5]), pack2<TY>(v[8 * k + 6], v[8 * k + 7]));
+    uint4 *d = static_cast<uint4 *>(p);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
+template <int TY>
+__device__ __forceinline__ void store16(char *row, int lane, bool wide, const float (&v)[16]) {
+  char *d = row + 16 * lane * kTypeBytes<TY>;
+  uint32_t w[8];
+  if constexpr (TY == DSA_TYPE_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * h + k]);
+      store32(d + 32 * h, wide, w);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack2<TY>(v[2 * k], v[2 * k + 1]);
+    store32(d, wide, w);
+  }
+}
+
 template <int FMT, int TY>
 __global__ void __launch_bounds__(32 * kCacheWarps) cache_read_kernel(CacheParams p) {
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
@@ -328,7 +460,9 @@ __global__ void __launch_bounds__(32 * kCacheWarps) cache_read_kernel(CacheParam
   const int64_t i = (int64_t)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
   if (i >= p.n) return;
   const int32_t sid = __ldg(p.L.ids + i);
-  char *row = static_cast<char *>(p.dst) + i * p.stride * kTypeBytes<TY>;
+  const int64_t stride = p.stride * kTypeBytes<TY>;
+  char *row = static_cast<char *>(p.dst) + i * stride;
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.dst) | (uintptr_t)stride) & 31u) == 0;
   float v[16], t0 = 0.f, t1 = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) v[k] = 0.f;
@@ -336,7 +470,7 @@ __global__ void __launch_bounds__(32 * kCacheWarps) cache_read_kernel(CacheParam
   if (sid >= 0 && (int64_t)sid < p.L.num_slots) rec = record_ptr(p.L, sid);
   if (kDebug && rec && rec + p.L.rec > p.L.base + p.L.extent) rec = nullptr;
   if (rec) decode_record<FMT>(rec, lane, v, t0, t1);   // a slot outside the cache: zeros
-  store16<TY>(row, lane, v);
+  store16<TY>(row, lane, wide, v);
   if constexpr (kV32) {
     char *d = row + (kD + 2 * lane) * kTypeBytes<TY>;
     if constexpr (TY == DSA_TYPE_F32) *reinterpret_cast<float2 *>(d) = make_float2(t0, t1);
@@ -354,7 +488,8 @@ using dsa::CacheParams;
 template <int FMT>
 cudaError_t launch(const CacheParams &p, int32_t type, bool write, cudaStream_t st) {
   using namespace dsa;
-  const unsigned grid = (unsigned)((p.n + kCacheWarps - 1) / kCacheWarps);
+  const int64_t blocks = (p.n + kCacheWarps - 1) / kCacheWarps;
+  const unsigned grid = (unsigned)(write && blocks > kCacheBlocks ? kCacheBlocks : blocks);
   constexpr int kT = 32 * kCacheWarps;
 #define DSA_CACHE_CASE(TY)                                        \
   case TY:                                                        \
