@@ -252,10 +252,11 @@ __device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps
   }
   const float ms = ss * (1.0f / kD), me = ms + eps, mz = me - ms;
   const float ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (eps - mz));
-  // 1 / sqrt(me + ml) = r0 + r1: one Newton step, its residual 1 - (me + ml) r0^2 by FMAs
-  const float r0 = 1.0f / sqrtf(me);
+  // 1 / sqrt(me + ml) = r0 + r1: an approximation and one Newton step, its
+  // residual 1 - (me + ml) r0^2 by FMAs (none where me is 0 or infinite)
+  const float r0 = rsqrtf(me);
   const float h = me * r0, hl = fmaf(me, r0, -h) + ml * r0;
-  const float r1 = 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f));
+  const float r1 = h == h ? 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f)) : 0.f;
   const F2 a = f2(r0, r0), b = f2(r1, r1), minus = f2(-1.f, -1.f);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {   // x w = q + ql

@@ -634,6 +634,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       }
       if (bad_pos) report_status(p.status, DSA_ERR_INVALID_ARG);
       sm_bar();   // headf_s
+      if (end < u1) {   // the next tile's queries on their way to L2
+        const int64_t nr = (qt + 1) * 128 + side * 64 + 8 * warp + (lane & 7);
+        if (nr < p.rows) {
+          const uint32_t t = (uint32_t)nr / (uint32_t)p.H, h = (uint32_t)nr - t * (uint32_t)p.H;
+          const char *qr = reinterpret_cast<const char *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
+          for (int b = 128 * (lane >> 3); b < Cfg::kDB * 128; b += 512)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(qr + b));
+        }
+      }
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
       const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
@@ -818,21 +827,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             tc::st_shared_v4(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
           }
         sm_bar();
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int r = 8 * warp + i;
-          const int64_t gr = g0 + r;
-          if (gr >= p.rows) break;
-          const float wt = roww_s[64 + r];
+        // lane's two 4-dim pieces of a row of the pass
+        const int d0 = (lane >> 4) * 128 + pass * 64 + (lane & 15) * 4, d1 = d0 + 256;
+        auto piece = [&](int r, int k) {
+          return *reinterpret_cast<const float4 *>(smem + Cfg::kQ + r * 1024 + (((lane + 32 * k) ^ (r & 7)) << 4));
+        };
+        const int n = (int)min((int64_t)8, (int64_t)p.rows - (g0 + 8 * warp));   // the warp's rows that exist
+        if (!whole) {
+#pragma unroll 2
+          for (int i = 0; i < n; ++i) {
+            const int r = 8 * warp + i;
+            float *dst = p.part_o + (ps + r) * kD;
+            __stcg(reinterpret_cast<float4 *>(dst + d0), piece(r, 0));
+            __stcg(reinterpret_cast<float4 *>(dst + d1), piece(r, 1));
+          }
+        } else {
+          // The tails of 4 rows are in flight before the first store, which
+          // might be to the same memory (with a load after each store, as the
+          // compiler must keep them, a pass took 16800 cycles).
+#pragma unroll 1
+          for (int i0 = 0; i0 < n; i0 += 4) {
+            uint2 tail[4][2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int pc = lane + 32 * k, d = (pc >> 4) * 128 + pass * 64 + (pc & 15) * 4;
-            const float4 o = *reinterpret_cast<const float4 *>(smem + Cfg::kQ + r * 1024 + ((pc ^ (r & 7)) << 4));
-            if (whole)
-              store_out4(p, gr, d, o, wt,
-                         p.tail_out && wt != 0.f ? *reinterpret_cast<const uint2 *>(p.tail_out + gr * kD + d)
-                                                 : make_uint2(0, 0));
-            else __stcg(reinterpret_cast<float4 *>(p.part_o + (ps + r) * kD + d), o);
+            for (int i = 0; i < 4; ++i) {
+              tail[i][0] = tail[i][1] = make_uint2(0, 0);
+              if (p.tail_out && i0 + i < n) {
+                const __nv_bfloat16 *src = p.tail_out + (g0 + 8 * warp + i0 + i) * kD;
+                tail[i][0] = *reinterpret_cast<const uint2 *>(src + d0);
+                tail[i][1] = *reinterpret_cast<const uint2 *>(src + d1);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * warp + i0 + i;
+              if (i0 + i < n) {   // (wt = 0 without a tail)
+                store_out4(p, g0 + r, d0, piece(r, 0), roww_s[64 + r], tail[i][0]);
+                store_out4(p, g0 + r, d1, piece(r, 1), roww_s[64 + r], tail[i][1]);
+              }
+            }
           }
         }
         sm_bar();   // the tile is free again
