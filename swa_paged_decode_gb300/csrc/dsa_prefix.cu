@@ -50,7 +50,7 @@ struct PrefixParams {
   const float *tail_lse;
   __nv_bfloat16 *out;
   float *lse;
-  int32_t T, H, rows;          // query rows
+  int32_t H, rows;             // heads; query rows T H
   int32_t R;                   // 128-row tiles
   int32_t C;                   // CTA pairs
   long long wait_budget;
@@ -71,14 +71,15 @@ __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &
 }
 // Units are (row tile, key tile) pairs, row tile major, R x KT of them. Pair c
 // owns [begin(c), begin(c + 1)): equal shares of the cost, a unit's 1 and, for
-// a row tile that starts within the range, tile_cost = 2 for its Q staging, first
-// scores and epilogue (a range that starts within a tile pays these too, but
-// so does every range). With fewer than 2 units to a pair a whole unit more or
-// less counts for more than that, and a tile's start costs nothing. A pair may
-// own nothing.
+// a row tile that starts within the range, tile_cost = 2 for its Q staging,
+// first scores and epilogue (a range that starts within a tile pays these too,
+// but so does every range). With 2048 rows x 4096 keys (3.4 units to a pair)
+// the attend kernel took 31 us without that and 24 us with it; 3, 4 or 6 gave
+// nothing more. With fewer than 2 units to a pair a whole unit more or less
+// counts for more, and a tile's start costs nothing (16.3 against 11.8 us at 2
+// units for 2 pairs). A pair may own nothing.
 struct Schedule {
   int32_t R, KT, C, tile_cost;
-  __device__ __forceinline__ int64_t units() const { return (int64_t)R * KT; }
   __device__ __forceinline__ int64_t total() const { return (int64_t)R * (KT + tile_cost); }
   // a / b for a, b >= 0, in 32 bits where they do
   static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
@@ -224,11 +225,23 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 // around it. V goes by two chunks (the 128 dims of an N = 256 half).
 //
 // Roles: warps 0-7 softmax (a row is held by 4 threads, 64 keys each), Q
-// staging and the epilogue; warp 8 issues the MMAs (leader CTA) or tells the
-// leader which chunks have landed here (the other CTA); warps 9-11 copy.
-// Warp 8 runs its loop converged, one elected lane issuing: with uniform
-// operands an instruction goes out in fewer cycles than the tensor core
-// takes for it. Every wait is bounded as in the decode kernel.
+// staging and the epilogue; warp 8 of the leader issues the MMAs; warps 9-11
+// copy. Warp 8 runs its loop converged, one elected lane issuing: with uniform
+// operands an instruction goes out in fewer cycles than the tensor core takes
+// for it. Every wait is bounded as in the decode kernel.
+//
+// What bounds it: the products' shared-memory operands and the issue of a
+// chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP): 348 us with
+// gather and merge, 1579 TFLOP/s of the 1872 that a library product of 8192^3
+// reaches in a burst (380 us, 1450 TFLOP/s, back to back under the power cap,
+// against its 1706); without the copies 313 us. The steps there: N = 128 tiles
+// with a relay of the chunks' arrival 1272; arrivals released at CTA scope 914;
+// N = 256, one copy a chunk, converged issue 561; three copying warps and
+// single-test waits 438; merge and gather 413; copies that complete on the
+// leader's barrier 380; Q staging, epilogue, merge and ranges 348. Two pairs
+// that share their key copies by multicast were no faster (L2 gives 11 TB/s)
+// and leave 4 of 76 pairs without a place. Few rows are latency: 32 rows x 512
+// keys take 15 us (gather 2.3, set-up and Q 4, a unit 5, epilogue 2, merge 2).
 constexpr int kPfThreads = 384;
 constexpr int kPfCopyWarps = 3;
 constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
@@ -244,8 +257,8 @@ struct PfCfg {
   static constexpr uint32_t kRing = kP + 32768;
   static constexpr uint32_t kRed = kRing + kSlots * 16384;   // [4][64] f32
   static constexpr uint32_t kHeadF = kRed + 1024;            // [64] f32: scale log2(e) 2^e of a row
-  static constexpr uint32_t kRowW = kHeadF + 256;            // [3][64] f32 epilogue weights
-  static constexpr uint32_t kMisc = kRowW + 768;
+  static constexpr uint32_t kRowW = kHeadF + 256;            // [2][64] f32 epilogue weights
+  static constexpr uint32_t kMisc = kRowW + 512;
   static constexpr uint32_t kBytes = kMisc + 512;
   static constexpr uint32_t kSmem = kBytes + 1024 > 232448u ? 232448u : kBytes + 1024;
   static constexpr uint32_t kIdQK = tc::idesc_f16(128, 256, false, false);
@@ -890,8 +903,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 // depend on who finishes first. The attend kernel leaves each tile's pairs in
 // `tile` (found anew by every thread they took longer than all the rest: 64-bit
 // divisions), and the first values are loaded along with the lse.
-// A row in few parts takes a warp (<32, 1>), a row in many a block of 4 groups
-// (<128, 4>), so that 32 parts are one round trip to L2.
+// A row in few parts takes a warp (<32, 1>: 2048 rows in 5 parts 5 us, with a
+// block of 512 threads per row 27), a row in many a block (<128, 2>: 512 rows
+// in 19 parts 6 us, with 512 threads 9, with 128 threads 8).
 
 template <int kTh, int kGroups>
 __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
@@ -1241,7 +1255,6 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
   p.tail_lse = tail_lse;
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-  p.T = plan->num_tokens;
   p.H = plan->num_heads;
   p.rows = plan->num_tokens * plan->num_heads;
   p.R = plan->row_tiles;
