@@ -656,6 +656,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(qr + b));
         }
       }
+      if (p.tail_out && first == qt * KT && end == (qt + 1) * KT) {   // and the tails that its epilogue adds
+        for (int b = tid; b < 512; b += 256) {
+          const int64_t gr = qt * 128 + side * 64 + (b >> 3);
+          if (gr < p.rows)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.tail_out + gr * kD + 64 * (b & 7)));
+        }
+      }
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
       const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
