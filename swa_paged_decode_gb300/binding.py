@@ -363,10 +363,13 @@ def _table(fn: str, t: Optional[torch.Tensor], d: int):
 
 
 def _cache(fn: str, c: W.PagedCache, d: int) -> CacheDesc:
-    t = c.data
-    if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1 or t.get_device() != d:
+    t, page = c.data, c.page_size
+    if t.dim() != 2 or t.dtype != torch.uint8 or t.get_device() != d:
         raise DsaError(fn, -1)
-    return CacheDesc(t.data_ptr(), t.shape[0], t.stride(0), c.page_size, c.fmt)
+    (pages, width), (stride, one) = t.shape, t.stride()
+    if one != 1 or width < page * W.RECORD_BYTES.get(c.fmt, 0):   # (the library knows the formats)
+        raise DsaError(fn, -1)
+    return CacheDesc(t.data_ptr(), pages, stride, page, c.fmt)
 
 
 def _rows(fn: str, t: torch.Tensor, d: int, n: int, dims: int):
@@ -444,10 +447,10 @@ def dsa_prefix_run(plan: PrefixPlan, workspace: torch.Tensor, q: torch.Tensor, c
     desc = _cache(fn, cache, d)
     table, table_rows = _table(fn, cos_sin, d)
     head, full = (T, H), (T, H, W.HEAD_DIM)
+    sh = q.stride(1) if H > 1 else plan.d_qk
     rc = load().dsa_prefix_run(
         ctypes.byref(plan), _vec(fn, workspace, d, torch.uint8, (workspace.numel(),)),
-        workspace.numel(), q.data_ptr(), q.stride(0) if T > 1 else max(q.stride(0), H * plan.d_qk),
-        q.stride(1) if H > 1 else plan.d_qk, ctypes.byref(desc),
+        workspace.numel(), q.data_ptr(), q.stride(0) if T > 1 else H * sh, sh, ctypes.byref(desc),
         _vec(fn, slots, d, torch.int32, (plan.width,)), _vec(fn, length, d, torch.int32, (1,)),
         _vec(fn, sink, d, torch.float32, (H,)), _vec(fn, positions, d, torch.int64, (T,)), table,
         table_rows, rope_style, scale, _vec(fn, tail_out, d, torch.bfloat16, full),

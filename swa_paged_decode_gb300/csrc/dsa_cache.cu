@@ -171,29 +171,30 @@ __device__ __forceinline__ float ue8m0_down(uint32_t byte) {
   if (byte == 255u) return __uint_as_float(0x7FC00000u);
   return __uint_as_float(byte == 254u ? 0x00400000u : (254u - byte) << 23);
 }
-// y = x / s for 16 values, each rounded to nearest. With inv = 1 / s rounded
-// to nearest, q = x inv and its exact remainder x - q s, q + inv (x - q s)
-// rounds to the quotient (Markstein, "Computation of elementary functions on
-// the IBM RISC System/6000", 1990): 3 packed instructions for two values.
-// The remainder is exact while it stays clear of the subnormals, which a
-// scale in 2^-60 .. 2^60 sees to wherever the quotient matters (below 2^-10
-// every code is 0); other scales, and blocks with an infinity, divide.
-__device__ __forceinline__ void divide16(const F2 (&x)[8], float s, bool finite, float (&y)[16]) {
+// y = -x / s for 16 values, each rounded to nearest (the codes' signs are
+// flipped back in packed form). With inv = 1 / s rounded to nearest, q = -x inv
+// and the exact remainder x + q s, q - inv (x + q s) rounds to the quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000", 1990): 3 packed instructions for two values, and a zero keeps
+// its sign. The remainder is exact while it stays clear of the subnormals,
+// which a scale in 2^-60 .. 2^60 sees to wherever the quotient matters (below
+// 2^-10 every code is 0); other scales, and blocks with an infinity, divide.
+__device__ __forceinline__ void divide16_neg(const F2 (&x)[8], float s, bool finite, float (&y)[16]) {
   if (finite && s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f) {
     const float inv = __frcp_rn(s);
-    const F2 i2 = f2(inv, inv), ns = f2(-s, -s);
+    const F2 ni = f2(-inv, -inv), s2 = f2(s, s);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const F2 q = f2_mul(x[k], i2);
-      f2_get(f2_fma(f2_fma(q, ns, x[k]), i2, q), y[2 * k], y[2 * k + 1]);
+      const F2 q = f2_mul(x[k], ni);
+      f2_get(f2_fma(f2_fma(q, s2, x[k]), ni, q), y[2 * k], y[2 * k + 1]);
     }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float a, b;
       f2_get(x[k], a, b);
-      y[2 * k] = __fdiv_rn(a, s);
-      y[2 * k + 1] = __fdiv_rn(b, s);
+      y[2 * k] = __fdiv_rn(a, -s);
+      y[2 * k + 1] = __fdiv_rn(b, -s);
     }
   }
 }
@@ -212,9 +213,9 @@ __device__ __forceinline__ uint4 codes16_scaled(const F2 (&x)[8], float down) {
   for (int k = 0; k < 8; ++k) f2_get(f2_mul(x[k], d2), y[2 * k], y[2 * k + 1]);
   return codes16(y);
 }
-// Eight fp32 values -> e2m1 codes (nearest even, saturating at 6), element i
-// in nibble i; a zero code has no sign.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int o) {
+// Eight negated fp32 values -> e2m1 codes (nearest even, saturating at 6),
+// element i in nibble i; a zero code has no sign.
+__device__ __forceinline__ uint32_t e2m1x8_neg(const float (&y)[16], int o) {
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -226,7 +227,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int o) {
       : "f"(y[o]), "f"(y[o + 1]), "f"(y[o + 2]), "f"(y[o + 3]), "f"(y[o + 4]), "f"(y[o + 5]),
         "f"(y[o + 6]), "f"(y[o + 7]));
   const uint32_t nz = (w | (w >> 1) | (w >> 2)) & 0x11111111u;
-  return w & (nz * 15u);
+  return (w ^ 0x88888888u) & (nz * 15u);
 }
 
 // ------------------------------------------------------------ norm
@@ -384,8 +385,10 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
       const uint32_t m = block_amax<8>(x);
       const float s = __fdiv_rn(__uint_as_float(m), 448.0f);
       float y[16];
-      divide16(v, s > 0.f || s != s ? s : 1.0f, true, y);   // zero blocks divide by one
-      *reinterpret_cast<uint4 *>(rec + 16 * lane) = codes16(y);
+      divide16_neg(v, s > 0.f || s != s ? s : 1.0f, true, y);   // zero blocks divide by one
+      const uint4 c = codes16(y);
+      *reinterpret_cast<uint4 *>(rec + 16 * lane) =
+          make_uint4(c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u);
       if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + 512 + (lane >> 1)) = s;
       if constexpr (kV32) *reinterpret_cast<uint32_t *>(rec + 528 + 4 * lane) = bf16x2_bits(t0, t1);
     } else if constexpr (FMT == DSA_REC_FP8_528_UE8M0) {
@@ -414,8 +417,8 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
       uint2 c = make_uint2(0u, 0u);
       if (sb != 0u && sb != 0x7Fu) {
         float y[16];
-        divide16(v, e4m3_to_f32(sb), m < 0x7F800000u, y);
-        c = make_uint2(e2m1x8(y, 0), e2m1x8(y, 8));
+        divide16_neg(v, e4m3_to_f32(sb), m < 0x7F800000u, y);
+        c = make_uint2(e2m1x8_neg(y, 0), e2m1x8_neg(y, 8));
       }
       *reinterpret_cast<uint2 *>(rec + 8 * lane) = c;
       rec[256 + lane] = (uint8_t)sb;

@@ -82,6 +82,40 @@ def test_write_matches_definition_bit_for_bit(fmt, dtype, n):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+def test_write_extreme_magnitudes_bit_for_bit(fmt):
+    """fp32 rows from the subnormals to the largest finite values, some of a
+    block's values far below its largest: records as defined, bit for bit."""
+    exps = list(range(-149, 128, 4)) + [-126, -127, 127]
+    n = len(exps)
+    g = torch.Generator().manual_seed(77)
+    x = torch.randn((n, dims(fmt)), generator=g, dtype=torch.float64).clamp(-1.9, 1.9)
+    x = x * torch.exp2(torch.tensor(exps, dtype=torch.float64))[:, None]
+    x[:, ::5] *= 2.0 ** -11                     # codes at the bottom of e4m3
+    x = x.float().clamp(-3.0e38, 3.0e38)
+    cache = empty_cache(fmt, 128, 64)
+    B.dsa_cache_write(cache, torch.arange(n, dtype=torch.int32, device="cuda"), x.cuda())
+    got, want = records(cache)[:n], ENC[fmt](x).numpy()
+    bad = np.argwhere(got != want)
+    assert bad.size == 0, [(exps[b[0]], int(b[1]), int(got[tuple(b)]), int(want[tuple(b)])) for b in bad[:6]]
+
+
+def test_write_quotients_at_ties():
+    """x / s on and next to the borders between codes, for scales of every mantissa."""
+    g = torch.Generator().manual_seed(78)
+    n = 512
+    s = (1 + torch.rand((n, 4, 1), generator=g)) * torch.exp2(torch.randint(-40, 40, (n, 4, 1), generator=g).float())
+    codes = torch.arange(128, dtype=torch.uint8)[:127].view(torch.float8_e4m3fn).float()
+    mids = (codes[1:] + codes[:-1]) / 2
+    y = torch.cat([torch.tensor([448.0]), mids, torch.tensor([-448.0])])          # 128 values
+    x = (y * s).reshape(n, 512)
+    step = torch.randint(-1, 2, x.shape, generator=g)
+    x = torch.where(step < 0, torch.nextafter(x, torch.zeros(())), torch.where(step > 0, torch.nextafter(x, 2 * x), x))
+    cache = empty_cache(W.FMT_FP8_528, n, 64)
+    B.dsa_cache_write(cache, torch.arange(n, dtype=torch.int32, device="cuda"), x.cuda())
+    assert np.array_equal(records(cache)[:n], ENC[W.FMT_FP8_528](x).numpy())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("norm,style", [(True, None), (False, W.ROPE_NEOX), (False, W.ROPE_GPTJ),
                                         (True, W.ROPE_NEOX), (True, W.ROPE_GPTJ)])
 @pytest.mark.parametrize("dtype", TYPES)
@@ -151,6 +185,8 @@ def test_write_wide_stride_and_offset():
     assert np.array_equal(records(cache)[:n], want)
     with pytest.raises(B.DsaError):      # a row that does not start on 16 bytes
         B.dsa_cache_write(cache, torch.arange(n, dtype=torch.int32, device="cuda"), big[:, 1025:1537])
+    with pytest.raises(B.DsaError):      # a cache view narrower than its pages
+        B.dsa_cache_write(W.PagedCache(cache.data[:, :-16], 64, fmt), torch.arange(n, dtype=torch.int32, device="cuda"), rows)
     with pytest.raises(B.DsaError):      # values that do not lie next to each other
         B.dsa_cache_write(cache, torch.arange(n, dtype=torch.int32, device="cuda"), big[:, ::4])
 

@@ -226,6 +226,51 @@ def test_strided_queries():
     c.check(out, lse)
 
 
+def test_one_token_of_any_stride():
+    c = Case(1, 16, 200, W.FMT_FP8_528, seed=30)
+    wide = torch.zeros((16, 1024), dtype=torch.bfloat16, device="cuda")
+    wide[:, 512:] = c.q[0]
+    c.q = wide[:, 512:].unsqueeze(0)
+    out, lse, _ = c.run()
+    c.check(out, lse)
+
+
+def test_nan_query_stays_in_its_row():
+    c = Case(3, 16, 300, W.FMT_FP8_528, seed=31)
+    c.q[1, 4, 7] = float("nan")
+    out, lse, _ = c.run()
+    assert bool(torch.isnan(out[1, 4]).all()) and bool(torch.isnan(lse[1, 4]))
+    ok = torch.ones((3, 16), dtype=torch.bool, device="cuda")
+    ok[1, 4] = False
+    assert not bool(torch.isnan(out[ok]).any()) and not bool(torch.isnan(lse[ok]).any())
+    c.q[1, 4] = 0
+    want, wlse, _ = c.run()
+    assert torch.equal(out[ok], want[ok]) and torch.equal(lse[ok], wlse[ok])
+
+
+@pytest.mark.parametrize("sink", [float("inf"), -float("inf"), 1e30, -1e30])
+def test_sinks_at_the_ends(sink):
+    c = Case(2, 16, 300, W.FMT_FP8_528, seed=32, sink=True, tail=True)
+    c.sink.fill_(sink)
+    out, lse, _ = c.run()
+    if sink > 0:
+        assert bool((out == 0).all())            # all weight on the sink
+        c.sink = None
+        assert torch.equal(c.run()[1], lse)      # which lse does not contain
+    else:
+        c.check(out, lse)
+
+
+def test_negative_and_zero_scale():
+    for scale in (-0.05, 0.0):
+        c = Case(2, 16, 300, W.FMT_NVFP4_288, seed=33)
+        c.scale = scale
+        out, lse, _ = c.run()
+        r_out, r_lse, tol, ltol = c.reference()
+        assert np.all(np.abs(lse.double().cpu().numpy().reshape(-1) - r_lse) <= 0.1 * abs(scale) + 1e-4)
+        assert np.abs(out.double().cpu().numpy().reshape(r_out.shape) - r_out).max() <= 2e-2
+
+
 def test_in_place_tail():
     c = Case(9, 64, 500, W.FMT_FP8_528, seed=16, sink=True, tail=True)
     want_out, want_lse, attn = c.run()
