@@ -29,6 +29,8 @@ EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
 EXPORTED_PREFIX = ("dsa_prefix_plan", "dsa_prefix_run")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # DSA_TYPE_*
 
 
@@ -191,7 +193,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:   # the current stream of the current device
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -340,7 +342,7 @@ def dsa_decode_run_noalloc(plan: Plan, q: torch.Tensor, swa_cache: W.PagedCache,
 def _device(fn: str, t: torch.Tensor) -> int:
     """The tensor's device, which has to be the current CUDA device."""
     d = t.get_device()
-    if d < 0 or d != torch._C._cuda_getDevice():
+    if d < 0 or d != _current_device():
         raise DsaError(fn, -1)
     return d
 

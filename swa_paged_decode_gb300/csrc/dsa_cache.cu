@@ -429,14 +429,12 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
 // ------------------------------------------------------------ read
 // 32 bytes in one store (p 32-byte aligned), or two of 16.
 __device__ __forceinline__ void store32(void *p, bool wide, const uint32_t (&w)[8]) {
+  const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
   if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+    tc::stg_v8(p, a, b);
   } else {
-    uint4 *d = static_cast<uint4 *>(p);
-    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    static_cast<uint4 *>(p)[0] = a;
+    static_cast<uint4 *>(p)[1] = b;
   }
 }
 template <int TY>

@@ -195,10 +195,11 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = tc::pack_f16x2(v[2 * k] * down, v[2 * k + 1] * down);
-    uint8_t *b = base + (lane >> 2) * 16384;
-    const int c0 = 2 * (lane & 3);
-    *reinterpret_cast<uint4 *>(b + ((c0 ^ x) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(b + (((c0 + 1) ^ x) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    // the lane's chunks c and c + 1 (c even) share a 32-byte sector, in either
+    // order: one store of it (65536 MODEL1 records: 21 us, 28 with two stores,
+    // each of half a sector)
+    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+    tc::stg_v8(base + (lane >> 2) * 16384 + (((2 * (lane & 3)) ^ (x & 6)) << 4), (x & 1) ? b : a, (x & 1) ? a : b);
     if constexpr (kV32)
       *reinterpret_cast<uint32_t *>(base + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) =
           tc::pack_f16x2(t0 * down, t1 * down);

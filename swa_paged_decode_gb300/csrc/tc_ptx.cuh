@@ -389,6 +389,13 @@ __device__ __forceinline__ void ldg_nc_v8(const void *p, uint4 &a, uint4 &b) {
                : "l"(p));
 }
 
+// 32-byte store, a whole sector; p 32-byte aligned.
+__device__ __forceinline__ void stg_v8(void *p, const uint4 &a, const uint4 &b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Bulk prefetch of `bytes` (multiple of 16, 16-byte aligned) into L2 by the
 // TMA engine: no registers, no L1 miss tracking.
 __device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes) {
