@@ -1,13 +1,16 @@
 """ctypes binding of libdsa_decode.so (include/dsa_decode.h).
 
 Argument marshalling only: torch tensors become device pointers, strides and
-sizes; every step of the decode runs in the library's CUDA kernels. The
-functions keep the C names. Loading fails loudly when the library is missing
+sizes; every step of the decode runs in the library's CUDA kernels. The cache
+and shared-prefix calls go through a small C extension (csrc/marshal.c) that
+also checks the tensors. The functions keep the C names. Loading fails loudly when the library is missing
 (there is no fallback path).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -17,6 +20,7 @@ from . import workloads as W
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libdsa_decode.so")
+MARSHAL_PATH = os.path.join(_HERE, "lib", "_marshal.so")
 
 DSA_OK = 0
 STATUS_NAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED",
@@ -31,7 +35,6 @@ DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
-ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # DSA_TYPE_*
 
 
 class DsaError(RuntimeError):
@@ -99,6 +102,24 @@ class MxOut:
     def scale_bytes(self) -> torch.Tensor:
         """[T, H/G, G*16] uint8 (byte ka of a group's scales, little-endian words)."""
         return self.scale.contiguous().view(torch.uint8)
+
+
+_marshal = None
+
+
+def _load_marshal():
+    """The marshalling extension of the cache and prefix calls (csrc/marshal.c)."""
+    global _marshal
+    if _marshal is None:
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"{MARSHAL_PATH} is missing: build it with `python -m swa_paged_decode_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(m)
+        m.setup(torch.uint8, torch.int32, torch.int64, torch.bfloat16, torch.float16, torch.float32,
+                _current_device, _raw_stream)
+        _marshal = m
+    return _marshal
 
 
 LIB_DEBUG_PATH = os.path.join(_HERE, "lib", "libdsa_decode_debug.so")
@@ -178,6 +199,9 @@ def _load_path(path: str):
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
     lib.dsa_decode_abi_version.argtypes = []
+    m = _load_marshal()
+    lib.marshal = {n: (getattr(m, n[4:]), ctypes.cast(getattr(lib, n), vp).value)
+                   for n in ("dsa_cache_write", "dsa_cache_read", "dsa_prefix_run")}
     _libs[path] = lib
     return lib
 
@@ -335,51 +359,17 @@ def dsa_decode_run_noalloc(plan: Plan, q: torch.Tensor, swa_cache: W.PagedCache,
     return rc
 
 
-# A tensor's own properties, which its pointer cannot carry, are checked here
-# with as few calls as will do (a step of a small batch waits for the host):
-# device, dtype and extents; DSA_ERR_INVALID_ARG before the library is called.
-
-def _device(fn: str, t: torch.Tensor) -> int:
-    """The tensor's device, which has to be the current CUDA device."""
-    d = t.get_device()
-    if d < 0 or d != _current_device():
+def _marshalled(fn: str, check: bool, *args) -> int:
+    """Call ``fn`` through the marshalling extension. A tensor of another
+    device than the current one, dtype, shape or layout than the call takes
+    raises DSA_ERR_INVALID_ARG before the library is called."""
+    f, address = load().marshal[fn]
+    rc = f(address, *args)
+    if rc == -1000:                      # BAD_TENSOR
         raise DsaError(fn, -1)
-    return d
-
-
-def _vec(fn: str, t: Optional[torch.Tensor], d: int, dtype, shape) -> Optional[int]:
-    """Pointer of a contiguous tensor of this dtype and shape (None: none)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or t.get_device() != d or not t.is_contiguous():
-        raise DsaError(fn, -1)
-    return t.data_ptr()
-
-
-def _table(fn: str, t: Optional[torch.Tensor], d: int):
-    """(pointer, rows) of a cos / sin table [rows, 64]."""
-    if t is None:
-        return None, 0
-    n = t.shape[0]
-    return _vec(fn, t, d, torch.float32, (n, 64)), n
-
-
-def _cache(fn: str, c: W.PagedCache, d: int) -> CacheDesc:
-    t, page = c.data, c.page_size
-    if t.dim() != 2 or t.dtype != torch.uint8 or t.get_device() != d:
-        raise DsaError(fn, -1)
-    (pages, width), (stride, one) = t.shape, t.stride()
-    if one != 1 or width < page * W.RECORD_BYTES.get(c.fmt, 0):   # (the library knows the formats)
-        raise DsaError(fn, -1)
-    return CacheDesc(t.data_ptr(), pages, stride, page, c.fmt)
-
-
-def _rows(fn: str, t: torch.Tensor, d: int, n: int, dims: int):
-    """(pointer, stride, DSA_TYPE_*) of dense rows [n, dims]."""
-    ty = ROW_TYPES.get(t.dtype)
-    if ty is None or t.shape != (n, dims) or t.get_device() != d or (t.stride(1) != 1 and n > 0):
-        raise DsaError(fn, -1)
-    return t.data_ptr(), t.stride(0) if n > 1 else dims, ty
+    if check and rc != DSA_OK:
+        raise DsaError(fn, rc)
+    return rc
 
 
 def dsa_cache_write(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
@@ -392,19 +382,9 @@ def dsa_cache_write(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor
     row stride) into the records of ``slots`` [n] int32 (-1: not written),
     after an optional RMS norm (weight fp32 [512]) and RoPE of their last 64
     dims (positions int64 [n], cos_sin fp32 [rows, 64])."""
-    fn = "dsa_cache_write"
-    d, n = _device(fn, slots), slots.numel()
-    desc = _cache(fn, cache, d)
-    p_slots = _vec(fn, slots, d, torch.int32, (n,))
-    ptr, stride, ty = _rows(fn, rows, d, n, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM)
-    table, table_rows = _table(fn, cos_sin, d)
-    rc = load().dsa_cache_write(ctypes.byref(desc), p_slots, n, ptr, stride, ty,
-                                _vec(fn, norm_weight, d, torch.float32, (W.HEAD_DIM,)), norm_eps,
-                                _vec(fn, positions, d, torch.int64, (n,)), table, table_rows, rope_style,
-                                _vec(fn, device_status, d, torch.int32, (1,)), _stream(stream))
-    if check:
-        _check(fn, rc)
-    return rc
+    return _marshalled("dsa_cache_write", check, cache.data, cache.page_size, cache.fmt, slots, rows,
+                       norm_weight, norm_eps, positions, cos_sin, rope_style, device_status,
+                       None if stream is None else _stream(stream))
 
 
 def dsa_cache_read(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor, stream=None,
@@ -412,15 +392,8 @@ def dsa_cache_read(cache: W.PagedCache, slots: torch.Tensor, rows: torch.Tensor,
     """Fill rows [n, 512] (576 for V3.2 records; bf16, f16 or fp32, any row
     stride) with the values of the records of ``slots`` [n] int32; a slot
     outside the cache gives zeros."""
-    fn = "dsa_cache_read"
-    d, n = _device(fn, slots), slots.numel()
-    desc = _cache(fn, cache, d)
-    p_slots = _vec(fn, slots, d, torch.int32, (n,))
-    ptr, stride, ty = _rows(fn, rows, d, n, W.KEY_DIMS_V32 if cache.fmt == W.FMT_V32_656 else W.HEAD_DIM)
-    rc = load().dsa_cache_read(ctypes.byref(desc), p_slots, n, ptr, stride, ty, _stream(stream))
-    if check:
-        _check(fn, rc)
-    return rc
+    return _marshalled("dsa_cache_read", check, cache.data, cache.page_size, cache.fmt, slots, rows,
+                       None if stream is None else _stream(stream))
 
 
 def dsa_prefix_plan(num_tokens: int, num_heads: int, width: int, num_sms: int = 0,
@@ -441,26 +414,9 @@ def dsa_prefix_run(plan: PrefixPlan, workspace: torch.Tensor, q: torch.Tensor, c
                    stream=None, check: bool = True) -> int:
     """Attention of every token over the shared list ``slots`` [width] int32
     of ``length`` [1] int32 (on the device), merged with the tail state."""
-    fn = "dsa_prefix_run"
-    d = _device(fn, q)
-    T, H = plan.num_tokens, plan.num_heads
-    if q.dtype != torch.bfloat16 or q.shape != (T, H, plan.d_qk) or (q.stride(2) != 1 and T > 0):
-        raise DsaError(fn, -1)
-    desc = _cache(fn, cache, d)
-    table, table_rows = _table(fn, cos_sin, d)
-    head, full = (T, H), (T, H, W.HEAD_DIM)
-    sh = q.stride(1) if H > 1 else plan.d_qk
-    rc = load().dsa_prefix_run(
-        ctypes.byref(plan), _vec(fn, workspace, d, torch.uint8, (workspace.numel(),)),
-        workspace.numel(), q.data_ptr(), q.stride(0) if T > 1 else H * sh, sh, ctypes.byref(desc),
-        _vec(fn, slots, d, torch.int32, (plan.width,)), _vec(fn, length, d, torch.int32, (1,)),
-        _vec(fn, sink, d, torch.float32, (H,)), _vec(fn, positions, d, torch.int64, (T,)), table,
-        table_rows, rope_style, scale, _vec(fn, tail_out, d, torch.bfloat16, full),
-        _vec(fn, tail_lse, d, torch.float32, head), _vec(fn, out, d, torch.bfloat16, full),
-        _vec(fn, lse, d, torch.float32, head), _stream(stream))
-    if check:
-        _check(fn, rc)
-    return rc
+    return _marshalled("dsa_prefix_run", check, ctypes.addressof(plan), workspace, q, cache.data,
+                       cache.page_size, cache.fmt, slots, length, sink, positions, cos_sin, rope_style,
+                       scale, tail_out, tail_lse, out, lse, None if stream is None else _stream(stream))
 
 
 class PrefixAttention:

@@ -2,7 +2,8 @@
 
 Each .cu translation unit compiles in parallel to an object under
 ``_build/``; the objects link into ``lib/libdsa_decode.so`` (CUDA runtime
-linked statically, so the library only needs the driver). Run as
+linked statically, so the library only needs the driver). The marshalling
+extension (``lib/_marshal.so``, plain C, no CUDA) is built beside it. Run as
 ``python -m swa_paged_decode_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -11,6 +12,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +24,9 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libdsa_decode.so")
 # The checking build (-DDSA_DEBUG): every global and tile access bounds-checked.
 LIB_DEBUG = os.path.join(LIBDIR, "libdsa_decode_debug.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(LIBDIR, "_marshal.so")
+_marshal_lock = threading.Lock()   # the release and the checking build run side by side
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,11 +48,25 @@ def _stale(lib: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """Build the CPython extension that marshals the cache and prefix calls."""
+    with _marshal_lock:
+        if not force and not _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "dsa_decode.h"), __file__]):
+            return MARSHAL
+        os.makedirs(LIBDIR, exist_ok=True)
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        subprocess.run(["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I",
+                        sysconfig.get_paths()["include"], "-o", tmp, MARSHAL_SRC], check=True)
+        os.replace(tmp, MARSHAL)
+        return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     """Build the release library, or with ``debug`` the checking build."""
     srcs = sources()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(INCLUDE, "dsa_decode.h"))
+    build_marshal(force)
     lib = LIB_DEBUG if debug else LIB
     bdir = os.path.join(BUILD, "debug") if debug else BUILD
     if not force and not extra_flags and not _stale(lib, srcs + headers + [__file__]):

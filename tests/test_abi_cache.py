@@ -97,3 +97,15 @@ def test_binding_refuses_host_tensors(lib):
         B.dsa_cache_write(c, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 512))
     with pytest.raises(B.DsaError):
         B.dsa_cache_read(c, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 512))
+
+
+def test_binding_takes_tensors_and_numbers(lib):
+    """Arguments of another kind raise; what is wrong first decides how."""
+    c = W.PagedCache(torch.zeros((2, 64 * 528), dtype=torch.uint8), 64, W.FMT_FP8_528)
+    for cache in (c, W.PagedCache([1, 2], 64, W.FMT_FP8_528)):
+        with pytest.raises((AttributeError, TypeError, B.DsaError)):
+            B.dsa_cache_read(cache, [0, 1, 2], torch.zeros(3, 512))
+        with pytest.raises((AttributeError, TypeError, B.DsaError)):
+            B.dsa_cache_write(cache, torch.zeros(3, dtype=torch.int32), None)
+    with pytest.raises(TypeError):
+        B.dsa_cache_write(c, torch.zeros(3, dtype=torch.int32), torch.zeros(3, 512), norm_eps="small")

@@ -282,3 +282,31 @@ def test_decode_reads_what_was_written(fmt):
     kept, chk = dec.selection()
     torch.cuda.synchronize()
     compare(out, lse, kept, chk, oracle_ref(w), what=f"written fmt{fmt}")
+
+
+def test_binding_refuses_what_pointers_cannot_tell():
+    fmt, n = W.FMT_FP8_528, 8
+    cache = empty_cache(fmt, 64, 64)
+    ok = dict(slots=torch.arange(n, dtype=torch.int32, device="cuda"), rows=torch.zeros((n, 512), device="cuda"))
+    w, pos, cs = torch.ones(512, device="cuda"), torch.zeros(n, dtype=torch.int64, device="cuda"), W.rope_table(16, "cuda")
+    B.dsa_cache_write(cache, **ok, norm_weight=w, positions=pos, cos_sin=cs)
+    bad = [dict(slots=ok["slots"].long()), dict(slots=ok["slots"][::2]), dict(slots=ok["slots"].view(2, 4)),
+           dict(slots=ok["slots"].cpu()), dict(slots=None), dict(rows=ok["rows"].double()), dict(rows=ok["rows"][:, :511]),
+           dict(rows=ok["rows"][1:]), dict(rows=ok["rows"].t()), dict(rows=ok["rows"].cpu()), dict(norm_weight=w[:511]),
+           dict(norm_weight=w.to(torch.bfloat16)), dict(positions=pos.int(), cos_sin=cs), dict(positions=pos[1:], cos_sin=cs),
+           dict(positions=pos, cos_sin=cs[:, :32]), dict(positions=pos, cos_sin=cs.double()), dict(positions=pos),
+           dict(device_status=pos), dict(device_status=torch.zeros(1, dtype=torch.int32))]
+    before = cache.data.clone()
+    for kw in bad:
+        with pytest.raises(B.DsaError) as e:
+            B.dsa_cache_write(cache, **dict(ok, **kw))
+        assert e.value.status == -1
+    for c in (W.PagedCache(cache.data.to(torch.int8), 64, fmt), W.PagedCache(cache.data.t(), 64, fmt),
+              W.PagedCache(cache.data.cpu(), 64, fmt), W.PagedCache(cache.data.view(-1), 64, fmt)):
+        with pytest.raises(B.DsaError):
+            B.dsa_cache_read(c, ok["slots"], ok["rows"])
+    assert torch.equal(cache.data, before)
+    st = torch.cuda.Stream()
+    B.dsa_cache_read(cache, ok["slots"], ok["rows"], stream=st)          # a stream, or its raw handle
+    B.dsa_cache_read(cache, ok["slots"], ok["rows"], stream=st.cuda_stream)
+    torch.cuda.synchronize()

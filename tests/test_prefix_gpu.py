@@ -391,3 +391,32 @@ def test_short_wait_budget_reports_a_timeout(monkeypatch):
     assert B.dsa_decode_read_status(attn.workspace) == -6
     out, lse, _ = c.run()
     c.check(out, lse)
+
+
+def test_binding_refuses_what_pointers_cannot_tell():
+    c = Case(2, 16, 300, W.FMT_FP8_528, seed=60, rope=W.ROPE_NEOX, sink=True, tail=True)
+    want, _, attn = c.run()
+    want = want.clone()
+    ok = dict(plan=attn.plan, workspace=attn.workspace, q=c.q, cache=c.cache, slots=c.slots, length=c.length, sink=c.sink,
+              positions=c.pos, cos_sin=c.cs, rope_style=0, scale=c.scale, tail_out=c.tail_out, tail_lse=c.tail_lse,
+              out=attn.out, lse=attn.lse)
+    bad = [dict(q=c.q.float()), dict(q=c.q[:1]), dict(q=c.q[:, :8]), dict(q=c.q.transpose(1, 2)), dict(q=c.q.cpu()),
+           dict(slots=c.slots[:299]), dict(slots=c.slots.long()), dict(slots=None), dict(length=c.length.long()),
+           dict(length=c.length.repeat(2)), dict(length=None), dict(sink=c.sink[:8]), dict(sink=c.sink.double()),
+           dict(positions=c.pos.int()), dict(positions=None), dict(cos_sin=c.cs[:, :60]), dict(tail_out=c.tail_out.float()),
+           dict(tail_out=None), dict(tail_lse=c.tail_lse[:, :8]), dict(tail_lse=None), dict(out=attn.out.float()),
+           dict(out=attn.out[:, :, ::2]), dict(out=None), dict(lse=attn.lse.t()), dict(lse=attn.lse.cpu())]
+    for kw in bad:
+        with pytest.raises(B.DsaError) as e:
+            B.dsa_prefix_run(**dict(ok, **kw))
+        assert e.value.status == -1, kw
+    with pytest.raises(B.DsaError) as e:
+        B.dsa_prefix_run(**dict(ok, workspace=attn.workspace[:1024]))
+    assert e.value.status == -4
+    torch.cuda.synchronize()
+    assert torch.equal(attn.out, want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    B.dsa_prefix_run(**ok, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(attn.out, want)
