@@ -232,17 +232,18 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 // for it. Every wait is bounded as in the decode kernel.
 //
 // What bounds it: the products' shared-memory operands and the issue of a
-// chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP): 348 us with
-// gather and merge, 1579 TFLOP/s of the 1872 that a library product of 8192^3
-// reaches in a burst (380 us, 1450 TFLOP/s, back to back under the power cap,
+// chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP): 342 us with
+// gather and merge, 1605 TFLOP/s of the 1872 that a library product of 8192^3
+// reaches in a burst (371 us, 1481 TFLOP/s, back to back under the power cap,
 // against its 1706); without the copies 313 us. The steps there: N = 128 tiles
 // with a relay of the chunks' arrival 1272; arrivals released at CTA scope 914;
 // N = 256, one copy a chunk, converged issue 561; three copying warps and
 // single-test waits 438; merge and gather 413; copies that complete on the
-// leader's barrier 380; Q staging, epilogue, merge and ranges 348. Two pairs
-// that share their key copies by multicast were no faster (L2 gives 11 TB/s)
-// and leave 4 of 76 pairs without a place. Few rows are latency: 32 rows x 512
-// keys take 15 us (gather 2.3, set-up and Q 4, a unit 5, epilogue 2, merge 2).
+// leader's barrier 380; Q staging, epilogue, merge and ranges 348; tails
+// prefetched 342. Two pairs that share their key copies by multicast were no
+// faster (L2 gives 11 TB/s) and leave 4 of 76 pairs without a place. Few rows
+// are latency: 32 rows x 512 keys take 15 us (gather 2.3, set-up and Q 4, a
+// unit 5, epilogue 2, merge 2).
 constexpr int kPfThreads = 384;
 constexpr int kPfCopyWarps = 3;
 constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
