@@ -23,6 +23,7 @@
 #include <cstring>
 
 #include "dsa_host.cuh"
+#include "dsa_prefix_index.cuh"
 #include "dsa_records.cuh"
 
 namespace dsa {
@@ -939,14 +940,13 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
   const int32_t KT = prefix_tiles(p, len);
   pdl_wait_primary();
   if (gr >= p.rows) return;                      // (whole warps; a block has one row where it syncs)
-  int32_t c0 = 0, c1 = -1;                       // no parts: an empty prefix
-  int64_t late = 0;
+  RowParts parts = {0, -1, 0, (int32_t)(gr & 127)};   // no parts: an empty prefix
   if (KT > 0) {
     const int2 tl = __ldcg(p.tile + (gr >> 7));
-    c0 = tl.x >> 1;
-    c1 = tl.y;
-    late = (tl.x & 1) * 128;
-    if (c0 == c1) return;                        // written by its pair
+    parts.c0 = tl.x >> 1;
+    parts.c1 = tl.y;
+    parts.late = (tl.x & 1) * 128;
+    if (parts.c0 == parts.c1) return;            // written by its pair
   }
   float lt = -INFINITY, sk = 0.f;
   uint2 tail[kQ];
@@ -961,25 +961,19 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
     }
   }
   if (p.sink) sk = __ldg(p.sink + (uint32_t)gr % (uint32_t)p.H);
-  // Partial of pair c: its first slot when the tile is its first, else its
-  // second (only c0 can have begun before the tile). A pair without units has
-  // left -inf in its first slot.
-  const int64_t row = gr & 127;
-  auto slot = [&](int32_t c) { return (int64_t)c * 256 + (c == c0 ? late : 0) + row; };
-  const int n_all = c1 - c0 + 1;
-  auto part_lse = [&](int i) { return i < n_all ? __ldcg(p.part_lse + slot(c0 + i)) : -INFINITY; };
+  const int n_all = parts.count();
+  auto part_lse = [&](int i) { return i < n_all ? __ldcg(p.part_lse + parts.slot(i)) : -INFINITY; };
   float4 o[kIn][kQ];
   auto fetch = [&](int i0) {         // the group's parts i0, i0 + kGroups, .. (the last one again past the end)
 #pragma unroll
     for (int i = 0; i < kIn; ++i) {
-      const float4 *src =
-          reinterpret_cast<const float4 *>(p.part_o + slot(c0 + min(i0 + kGroups * i, n_all - 1)) * kD) + t;
+      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + parts.loaded(i0 + kGroups * i) * kD) + t;
 #pragma unroll
       for (int q = 0; q < kQ; ++q) o[i][q] = __ldcg(src + kTh * q);
     }
   };
   const float first = part_lse(rt);
-  fetch(g);
+  if (n_all > 0) fetch(g);
   float M = first;
   bool nan = first != first;
 #pragma unroll 1
