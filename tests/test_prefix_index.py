@@ -1,9 +1,10 @@
 """Index arithmetic of the shared-prefix kernels (csrc/dsa_prefix_index.cuh),
 compiled as plain C++: every load that the merge makes for a row lies in the
-plan's workspace. No GPU."""
+plan's workspace, and the pairs' ranges cover every unit once. No GPU."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -17,10 +18,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 def index(tmp_path_factory):
     BLD.build()
     lib = str(tmp_path_factory.mktemp("index") / "prefix_index.so")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-I", BLD.CSRC, "-o", lib,
+    # a division by zero or an overflow ends the process, on every machine
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-fsanitize=integer-divide-by-zero,signed-integer-overflow",
+                    "-fsanitize-undefined-trap-on-error", "-I", BLD.CSRC, "-o", lib,
                     os.path.join(HERE, "prefix_index_host.cpp")], check=True)
-    lib = ctypes.CDLL(lib)
-    lib.part_loaded.restype = lib.part_slot.restype = ctypes.c_int64
+    path, lib = lib, ctypes.CDLL(lib)
+    lib.path = path
+    lib.part_loaded.restype = lib.part_slot.restype = lib.schedule_begin.restype = ctypes.c_int64
     return lib
 
 
@@ -52,3 +56,20 @@ def test_parts_are_the_pairs_slots(index):
         assert index.part_slot(3, 7, 128, 9, i) == (3 + i) * 256 + 9 + (128 if i == 0 else 0)
         assert index.part_loaded(3, 7, 128, 9, i) == index.part_slot(3, 7, 128, 9, i)
     assert index.part_loaded(3, 7, 128, 9, 11) == index.part_slot(3, 7, 128, 9, 4)
+
+
+def test_no_units_without_keys(index):
+    """In a process of its own: a division by zero would end it."""
+    code = ("import ctypes, sys; f = ctypes.CDLL(sys.argv[1]).schedule_begin; f.restype = ctypes.c_int64; "
+            "print(sum(abs(f(R, 0, C, c)) for R in (1, 5, 1 << 20) for C in (1, 2, 76) for c in (0, 1, C)))")
+    r = subprocess.run([sys.executable, "-c", code, index.path], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "0", (r.returncode, r.stdout, r.stderr)
+
+
+@pytest.mark.parametrize("R,KT,C", [(1, 1, 1), (1, 2, 2), (5, 5, 14), (4, 32, 76), (16, 16, 76), (128, 64, 76), (3, 7, 20),
+                                    (1, 256, 76), (1 << 24, 1, 76), (1 << 10, 1 << 21, 76), (97, 2, 700)])
+def test_ranges_cover_every_unit_once(index, R, KT, C):
+    b = [index.schedule_begin(R, KT, C, c) for c in range(C + 1)]
+    assert b[0] == 0 and b[-1] == R * KT and all(x <= y for x, y in zip(b, b[1:]))
+    most = max(y - x for x, y in zip(b, b[1:]))
+    assert most <= -(-R * (KT + 2) // C) + 1
