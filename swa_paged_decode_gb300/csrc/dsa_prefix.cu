@@ -35,6 +35,7 @@ constexpr int kPfSpread = 5;                   // log2 spread of their magnitude
 constexpr int kPfTop = 14;                     // the largest value's exponent in the f16 tile
 constexpr int kPfRange = 48;                   // exponents of the keys' magnitudes: -48..48
 constexpr int32_t kPfNoKey = INT32_MAX;        // exponent of a key that is not kept
+constexpr int32_t kPfZeroKey = -kPfRange - 1;  // of a key of zeros: any other key's will do
 constexpr int32_t kPfMixed = INT32_MIN;        // group exponent: one per key instead
 
 struct PrefixParams {
@@ -139,15 +140,15 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   for (int i = 0; i < 4; ++i) {
     const int e = __reduce_max_sync(0xffffffffu, ok[i] ? record_exponent<FMT>(raw[i], lane) : 0);
     if (lane == 0)
-      e_s[4 * warp + i] = !ok[i] ? kPfNoKey : (e < -kPfRange ? -kPfRange : (e > kPfRange ? kPfRange : e));
+      e_s[4 * warp + i] = !ok[i] ? kPfNoKey : e == kZeroShare ? kPfZeroKey : min(max(e, -kPfRange), kPfRange);
   }
   __syncthreads();
-  const int my = e_s[lane];   // lane's key of the 32
-  const bool kept = my != kPfNoKey;
+  const int raw_e = e_s[lane], my = max(raw_e, -kPfRange);   // lane's key of the 32
+  const bool kept = raw_e != kPfNoKey;
   const int hi = __reduce_max_sync(0xffffffffu, kept ? my : -kPfRange);
-  const int lo = __reduce_min_sync(0xffffffffu, kept ? my : kPfRange);
+  const int lo = __reduce_min_sync(0xffffffffu, kept && raw_e != kPfZeroKey ? my : kPfRange);
   const uint32_t mask = __ballot_sync(0xffffffffu, kept);
-  const bool mixed = mask != 0u && hi - lo > kPfSpread;
+  const bool mixed = hi - lo > kPfSpread;   // (no key but zeros: hi = -kPfRange, lo = kPfRange)
   if (warp == 0) {
     p.key_e[key0 + lane] = (kept ? (mixed ? my : hi) : hi) - kPfTop;
     if (lane == 0) p.info[blockIdx.x] = make_int2(mixed ? kPfMixed : hi - kPfTop, (int)mask);
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   for (int i = 0; i < 4; ++i) {
     const int32_t r = key0 + 4 * warp + i;
     const int es = e_s[4 * warp + i];
-    const int E = ((mixed && es != kPfNoKey) ? es : hi) - kPfTop;
+    const int E = ((mixed && es != kPfNoKey) ? max(es, -kPfRange) : hi) - kPfTop;
     const float down = __uint_as_float((uint32_t)(127 - E) << 23);
     const int64_t tile = r >> 7;
     const int g = (r & 127) >> 3, x = r & 7;

@@ -105,20 +105,17 @@ __device__ __forceinline__ void expand_record(const RawRecord &r, int lane, floa
   }
 }
 
-// e with every value of the lane's share below 2^(e + 1), from the scale alone
-// (a block's largest code is 448 or 6) and the bf16 parts.
+// e with every value of the lane's share below 2^(e + 1): from the block's
+// scale (its largest code is 448 or 6) and the bf16 parts. kZeroShare where all
+// codes are zero: the scale says nothing then (ue8m0 blocks of zeros carry
+// 2^0, which in front of small values would cost them their low bits).
+constexpr int kZeroShare = -127;
 template <int FMT>
 __device__ __forceinline__ int record_exponent(const RawRecord &r, int lane) {
   if constexpr (FMT == DSA_REC_NVFP4_288) {   // 6 s < 2^(k + 4), s < 2^(k + 1)
     const uint32_t b = r.s & 0x7Fu;
-    return b == 0u ? -127 : (b < 8u ? -6 : (int)(b >> 3) - 7) + 3;
-  } else if constexpr (FMT == DSA_REC_FP8_528 || FMT == DSA_REC_V32_656) {   // 448 s < 2^(k + 10)
-    int e = (r.s & 0x7FFFFFFFu) == 0u ? -127 : (int)((r.s >> 23) & 0xFFu) - 127 + 9;
-    if constexpr (FMT == DSA_REC_V32_656) {
-      const uint32_t m = __vmaxu2(r.t & 0x7FFF7FFFu, 0u);
-      e = max(e, (int)(max(m & 0xFFFFu, m >> 16) >> 7) - 127);
-    }
-    return e;
+    if (((r.w[0] | r.w[1]) & 0x77777777u) == 0u || b == 0u) return kZeroShare;
+    return (b < 8u ? -6 : (int)(b >> 3) - 7) + 3;
   } else {
     if (FMT == DSA_REC_MODEL1_584 && lane >= 28) {
       uint32_t m = 0;
@@ -126,7 +123,18 @@ __device__ __forceinline__ int record_exponent(const RawRecord &r, int lane) {
       for (int k = 0; k < 8; ++k) m = __vmaxu2(m, r.w[k] & 0x7FFF7FFFu);
       return (int)(max(m & 0xFFFFu, m >> 16) >> 7) - 127;
     }
-    return (int)(r.s & 0xFFu) - 127 + 8;      // 448 * 2^k < 2^(k + 9)
+    const bool zero = ((r.w[0] | r.w[1] | r.w[2] | r.w[3]) & 0x7F7F7F7Fu) == 0u;
+    int e = kZeroShare;
+    if constexpr (FMT == DSA_REC_FP8_528 || FMT == DSA_REC_V32_656) {   // 448 s < 2^(k + 10)
+      if (!zero && (r.s & 0x7FFFFFFFu) != 0u) e = (int)((r.s >> 23) & 0xFFu) - 127 + 9;
+    } else {
+      if (!zero) e = (int)(r.s & 0xFFu) - 127 + 8;                      // 448 * 2^k < 2^(k + 9)
+    }
+    if constexpr (FMT == DSA_REC_V32_656) {
+      const uint32_t m = __vmaxu2(r.t & 0x7FFF7FFFu, 0u);
+      e = max(e, (int)(max(m & 0xFFFFu, m >> 16) >> 7) - 127);
+    }
+    return e;
   }
 }
 
