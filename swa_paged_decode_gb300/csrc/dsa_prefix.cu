@@ -33,6 +33,14 @@ constexpr int kPfTile = 256;                   // keys per tile
 constexpr int kPfGroup = 32;                   // keys that share an exponent
 constexpr int kPfSpread = 5;                   // log2 spread of their magnitudes up to which they do
 constexpr int kPfTop = 14;                     // the largest value's exponent in the f16 tile
+// The row's reference m of its weights P = 2^(score + exponent - m) in f16: the
+// largest one stands at 2^kPfLift, and m moves once one exceeds 2^kPfMove (f16
+// ends at 2^16). Lifted, weights keep 11 bits down to 2^-21 of the largest and
+// are off by 2^-32 of it below (half of f16's smallest step, 2^-25). With the
+// largest at 2^0 keys of 2^-25 of its weight counted for nothing, a million of
+// them 3 % of the row.
+constexpr int kPfLift = 7;
+constexpr int kPfMove = 15;
 constexpr int kPfRange = 48;                   // exponents of the keys' magnitudes: -48..48
 constexpr int32_t kPfNoKey = INT32_MAX;        // exponent of a key that is not kept
 constexpr int32_t kPfZeroKey = -kPfRange - 1;  // of a key of zeros: any other key's will do
@@ -692,9 +700,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         };
         wait(Cfg::kSFull + (nqk & 1u), ph_s);
         tc::tc_fence_after();
-        // Scores against the running max; where a row's exceed it by 2^8 (or
-        // it has none yet: its scores stand alone) the maxima, O and the sums
-        // of the whole CTA move.
+        // Scores against the running reference; where a row's exceed it by
+        // kPfMove (or it has none yet: its scores stand alone) the references,
+        // O and the sums of the whole CTA move.
         const bool unset = m < -1e29f;
         const float mm = unset ? 0.f : m;
         load_t(mm);
@@ -702,12 +710,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll
         for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
         top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const bool moved = sm_bar_or(top[0] > (unset ? -INFINITY : 8.0f));
+        const bool moved = sm_bar_or(top[0] > (unset ? -INFINITY : (float)kPfMove));
         if (moved) {
           red_s[part * 64 + row] = top[0];
           sm_bar();
           const float tm = fmaxf(fmaxf(red_s[row], red_s[64 + row]), fmaxf(red_s[128 + row], red_s[192 + row]));
-          const float mn = fmaxf(m, mm + tm);
+          const float mn = fmaxf(m, mm + tm - (float)kPfLift);
           const float f = tc::ex2(m - mn);   // 0 with the first kept key
           const float d = mn - mm;
           m = mn;
