@@ -412,7 +412,9 @@ enum { DSA_TYPE_BF16 = 0, DSA_TYPE_F16 = 1, DSA_TYPE_F32 = 2 };
  * Row i, x = rows[i*row_stride + 0..d-1] (d = 512, or 576 for V32_656), goes
  * to the record of slots[i]:
  *   norm_weight != NULL: dims 0..511 become x * w / sqrt(mean(x^2) + eps),
- *     norm_weight fp32 [512], 16-byte aligned, norm_eps finite and >= 0;
+ *     norm_weight fp32 [512], 16-byte aligned, norm_eps finite and >= 0
+ *     (with 0 a row of zeros gives 0 / 0, a record of NaN); rows of any
+ *     finite magnitude, also where their squares overflow or vanish in fp32;
  *   cos_sin != NULL (with positions; both NULL = no RoPE): the last 64 dims
  *     are rotated by row positions[i] of the table [cos(32) | sin(32)],
  *     pairs as rope_style says (DSA_ROPE_*, over those 64 dims);

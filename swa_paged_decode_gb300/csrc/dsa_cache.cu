@@ -236,23 +236,48 @@ __device__ __forceinline__ uint32_t e2m1x8_neg(const float (&y)[16], int o) {
 // error of 2^-23 in front of the quantization would move the codes of four
 // elements in a million. The squares are summed as a tree and the lanes' sums
 // with their rounding errors; the root's reciprocal carries a correction r1,
-// and the products theirs.
+// and the products theirs. A row whose squares leave that no room (a mean below
+// 2^-60 or a sum above 2^100, which fp32 may not hold at all) is taken again
+// times a power of two, eps with it: the quotient is the same.
 __device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps) {
-  F2 sq[4];
+  float me, ml;
+#pragma unroll 1
+  for (bool again = false;; again = true) {   // (the lanes agree)
+    F2 sq[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sq[k] = f2_fma(v[2 * k], v[2 * k], f2_mul(v[2 * k + 1], v[2 * k + 1]));
-  float s0, s1;
-  f2_get(f2_add(f2_add(sq[0], sq[1]), f2_add(sq[2], sq[3])), s0, s1);
-  float ss = s0 + s1, sl = 0.f;
+    for (int k = 0; k < 4; ++k) sq[k] = f2_fma(v[2 * k], v[2 * k], f2_mul(v[2 * k + 1], v[2 * k + 1]));
+    float s0, s1;
+    f2_get(f2_add(f2_add(sq[0], sq[1]), f2_add(sq[2], sq[3])), s0, s1);
+    float ss = s0 + s1, sl = 0.f;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, ss, off), ol = __shfl_xor_sync(0xffffffffu, sl, off);
-    const float t = ss + o, z = t - ss;          // ss + o = t + the error of t
-    sl += ol + ((ss - (t - z)) + (o - z));
-    ss = t;
+    for (int off = 16; off > 0; off >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, ss, off), ol = __shfl_xor_sync(0xffffffffu, sl, off);
+      const float t = ss + o, z = t - ss;          // ss + o = t + the error of t
+      sl += ol + ((ss - (t - z)) + (o - z));
+      ss = t;
+    }
+    const float ms = ss * (1.0f / kD);
+    me = ms + eps;
+    const float mz = me - ms;
+    ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (eps - mz));
+    if (again || (me >= 8.673617379884035e-19f && ss <= 1.2676506002282294e30f)) break;
+    uint32_t m = 0;                                // largest magnitude, as bits
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float a, b;
+      f2_get(v[k], a, b);
+      m = max(m, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m >= 0x7F800000u) break;                   // an infinity or a NaN: as it is
+    // 2^e about the larger of the row and the root of eps
+    int e = max((int)(m >> 23) - 127, -126);
+    if (eps > 0.f) e = max(e, ((int)(__float_as_uint(eps) >> 23) - 126) >> 1);
+    const float d = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+    eps = (eps * d) * d;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = f2_mul(v[k], f2(d, d));
   }
-  const float ms = ss * (1.0f / kD), me = ms + eps, mz = me - ms;
-  const float ml = fmaf(sl, 1.0f / kD, (ms - (me - mz)) + (eps - mz));
   // 1 / sqrt(me + ml) = r0 + r1: an approximation and one Newton step, its
   // residual 1 - (me + ml) r0^2 by FMAs (none where me is 0 or infinite)
   const float r0 = rsqrtf(me);
