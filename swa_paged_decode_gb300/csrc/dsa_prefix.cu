@@ -19,6 +19,7 @@
 //           an empty prefix.
 #include <cuda.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -72,7 +73,21 @@ struct PrefixParams {
   int2 *tile;                  // [R] (pair of the tile's first units, * 2, + 1 if not its first tile; of its last)
   float *part_lse;             // [C][2][128]
   float *part_o;               // [C][2][128][512]
+  // checking build: the rows that out and lse, and the partials, may be touched in
+  int64_t check_rows, check_parts;
 };
+
+// The checking build's bounds of the rows of out, lse and the tail, of the
+// partials, and of the workspace's key tiles.
+__device__ __forceinline__ bool row_ok(const PrefixParams &p, int64_t gr) {
+  return dbg_ok(p.status, gr >= 0 && gr < p.check_rows, kDbgOut);
+}
+__device__ __forceinline__ bool part_ok(const PrefixParams &p, int64_t slot) {
+  return dbg_ok(p.status, slot >= 0 && slot < p.check_parts, kDbgPartial);
+}
+__device__ __forceinline__ bool key_tile_ok(const PrefixParams &p, int64_t kt) {
+  return dbg_ok(p.status, kt >= 0 && kt < ((int64_t)p.L.width + kPfTile - 1) / kPfTile, kDbgPartial);
+}
 
 // min(len, width) of the prefix list, and its key tiles
 __device__ __forceinline__ int32_t prefix_tiles(const PrefixParams &p, int32_t &len) {
@@ -103,6 +118,7 @@ __device__ __forceinline__ RowWeights row_weights(float lse, float lt, bool sink
 // 4 dims of a row's output: o (weighted) + wt * tail (4 bf16 values), as bf16.
 // A tail that weighs nothing does not count, whatever it holds.
 __device__ __forceinline__ void store_out4(const PrefixParams &p, int64_t gr, int d, float4 o, float wt, uint2 t) {
+  if (!row_ok(p, gr)) return;
   if (wt != 0.f) {
     o.x = fmaf(wt, bf16_bits_to_f32(t.x & 0xFFFFu), o.x);
     o.y = fmaf(wt, bf16_bits_to_f32(t.x >> 16), o.y);
@@ -130,7 +146,7 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
   // the warp's 4 slots, in lanes 0..3, loaded along with the length
   int32_t slot = -1;
   if (lane < 4 && key0 + 4 * warp + lane < p.L.width) slot = __ldg(p.L.ids + key0 + 4 * warp + lane);
-  if (key0 >= tiles * kPfTile) return;
+  if (key0 >= tiles * kPfTile || !key_tile_ok(p, key0 / kPfTile)) return;   // (whole blocks)
   // 4 keys per warp, their loads in flight together and kept as loaded until
   // the 32 keys' exponent is known
   RawRecord raw[4];
@@ -331,7 +347,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       uint32_t filled = 0, fill_ph = 0;   // slots this warp has filled, and the phase of their latest fill
       const uint32_t full0 = tc::mapa(tc::smem_u32(&bars[Cfg::kFull]), 0);
       constexpr int32_t kHalf = Cfg::kDB * 32;   // map rows (512 bytes) of 128 keys; a chunk has 32
+      const int64_t map_rows = ((int64_t)p.L.width + kPfTile - 1) / kPfTile * 2 * kHalf;
       auto chunk = [&](int32_t y, bool some) {
+        if (some) dbg_ok(p.status, y >= 0 && y + 32 <= map_rows, kDbgSmemKv);   // (the map gives zeros past its end)
         if (turn == 0) {
           turn = kPfCopyWarps;
           ok = wait(Cfg::kEmpty + slot, ph);
@@ -489,6 +507,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
           : "=r"(r) : "r"((int)x) : "memory");
       return r != 0;
     };
+    // 16 bytes into the Q tile (also the epilogue's staging area)
+    auto st_q = [&](uint32_t off, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      if (dbg_ok(p.status, off + 16u <= Cfg::kP - Cfg::kQ, kDbgSmemQ)) tc::st_shared_v4(q_base + off, a, b, c, d);
+    };
     bool bad_pos = false;   // reported once the gather, which clears the status word, is done
     // Q rows of this CTA -> f16 K-major tile: RoPE in fp32, times a power of
     // two per row so that its largest unrotated magnitude lies in [1, 2) (a
@@ -506,7 +528,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       const float *cp = p.cos_sin;
       if (gl < (uint32_t)p.rows) {
         const uint32_t t = gl / (uint32_t)p.H, h = gl - t * (uint32_t)p.H;
-        qp = p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh;
+        if (dbg_ok(p.status, (int64_t)t * p.H + h < (int64_t)p.rows, kDbgQ))
+          qp = p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh;
         if (rope) {
           const int64_t pos = __ldg(p.positions + t);
           if (pos >= 0 && pos < p.cs_rows) cp += pos * 64;
@@ -530,7 +553,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
           if (rope) {
             const float4 *c = reinterpret_cast<const float4 *>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cp), i0 + i));
-            if (rl) {
+            const int64_t at = reinterpret_cast<const float *>(c) - p.cos_sin;
+            if (rl && dbg_ok(p.status, at >= 0 && at + 64 <= p.cs_rows * 64, kDbgTable)) {
               ns[i][0] = __ldg(c + f0);
               ns[i][1] = __ldg(c + f1);
               ns[i][2] = __ldg(c + 8 + f0);
@@ -602,15 +626,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
           const uint32_t ro = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
-          tc::st_shared_v4(q_base + (ca >> 3) * 8192 + ro + (((ca & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
-          tc::st_shared_v4(q_base + (cb >> 3) * 8192 + ro + (((cb & 7) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+          st_q((ca >> 3) * 8192 + ro + (((ca & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+          st_q((cb >> 3) * 8192 + ro + (((cb & 7) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
           if constexpr (kV32) {
             if (lane < 8) {
               uint32_t fc[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 fc[k] = tc::pack_f16x2(bf16_bits_to_f32(wc[k] & 0xFFFFu) * down, bf16_bits_to_f32(wc[k] >> 16) * down);
-              tc::st_shared_v4(q_base + 8 * 8192 + ro + ((lane ^ (r & 7)) << 4), fc[0], fc[1], fc[2], fc[3]);
+              st_q(8 * 8192 + ro + ((lane ^ (r & 7)) << 4), fc[0], fc[1], fc[2], fc[3]);
             }
           }
         }
@@ -620,7 +644,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       if (lane == 0) tc::mbar_arrive_remote(lead_qready);
     };
 
-    if (u0 >= u1 && tid < 64) p.part_lse[(int64_t)pair * 256 + side * 64 + tid] = -INFINITY;
+    if (u0 >= u1 && tid < 64 && part_ok(p, (int64_t)pair * 256 + side * 64 + tid))
+      p.part_lse[(int64_t)pair * 256 + side * 64 + tid] = -INFINITY;
     uint32_t ph_s = 0, nqk = 0, ph_pv = 0;
     const uint32_t prow = p_base + part * 8192 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
     bool waited = false;
@@ -652,11 +677,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
       const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
-      int4 inf = __ldcg(info + (u - qt * KT) * 4);
+      auto load_info = [&](int64_t kt) { return key_tile_ok(p, kt) ? __ldcg(info + kt * 4) : make_int4(0, 0, 0, 0); };
+      int4 inf = load_info(u - qt * KT);
       for (; u < end; ++u) {
         const int64_t kt = u - qt * KT;
         const int4 cur = inf;
-        if (u + 1 < end) inf = __ldcg(info + (kt + 1) * 4);
+        if (u + 1 < end) inf = load_info(kt + 1);
         const bool mixed = cur.x == kPfMixed || cur.z == kPfMixed;   // one exponent per key
         const bool full = ((uint32_t)cur.y & (uint32_t)cur.w) == 0xFFFFFFFFu;
         const int32_t *ke = p.key_e + kt * kPfTile + part * 64;
@@ -762,8 +788,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
           ph_pv ^= 1u;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::st_shared_v4(prow + ((k ^ (row & 7)) << 4), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = prow + ((k ^ (row & 7)) << 4);
+          if (dbg_ok(p.status, at >= p_base && at + 16u <= ring, kDbgSmemP))
+            tc::st_shared_v4(at, pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        }
         tc::fence_async_smem();
         tc::tc_fence_before();
         __syncwarp();
@@ -777,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       const bool whole = first == qt * KT && end == (qt + 1) * KT;
       const int late = qt == u0 / KT ? 0 : 1;
       const int64_t ps = (2 * (int64_t)pair + late) * 128 + side * 64;
-      if (side == 0 && tid == 0) {   // which pairs the merge finds this tile in
+      if (side == 0 && tid == 0 && dbg_ok(p.status, qt >= 0 && qt < p.R, kDbgPartial)) {   // where the merge finds this tile
         if (first == qt * KT) p.tile[qt].x = 2 * pair + late;
         if (end == (qt + 1) * KT) p.tile[qt].y = pair;
       }
@@ -791,12 +820,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (gr < p.rows) {
           if (whole) {
             const RowWeights w =
-                row_weights(lse, p.tail_lse ? p.tail_lse[gr] : -INFINITY, p.sink != nullptr,
+                row_weights(lse, p.tail_lse && row_ok(p, gr) ? p.tail_lse[gr] : -INFINITY, p.sink != nullptr,
                             p.sink ? __ldg(p.sink + (uint32_t)gr % (uint32_t)p.H) : 0.f);
             wo *= w.o;
             wt = w.tail;
-            p.lse[gr] = w.lse;
-          } else {
+            if (row_ok(p, gr)) p.lse[gr] = w.lse;
+          } else if (part_ok(p, ps + row)) {
             p.part_lse[ps + row] = lse;
           }
         }
@@ -815,7 +844,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       const float wo = roww_s[row];
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        const uint32_t dst = q_base + row * 1024, c = tl + Cfg::kColO + half * 128 + pass * 64;
+        const uint32_t dst = row * 1024, c = tl + Cfg::kColO + half * 128 + pass * 64;
         uint32_t o[4][16];
         DSA_TMEM_LD16_NOWAIT(c, o[0]);
         DSA_TMEM_LD16_NOWAIT(c + 16, o[1]);
@@ -830,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(o[g][4 * i + k]) * wo);
-            tc::st_shared_v4(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            st_q(dst + ((((half * 2 + kh) * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
           }
         sm_bar();
         // lane's two 4-dim pieces of a row of the pass
@@ -843,6 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll 2
           for (int i = 0; i < n; ++i) {
             const int r = 8 * warp + i;
+            if (!part_ok(p, ps + r)) continue;
             float *dst = p.part_o + (ps + r) * kD;
             __stcg(reinterpret_cast<float4 *>(dst + d0), piece(r, 0));
             __stcg(reinterpret_cast<float4 *>(dst + d1), piece(r, 1));
@@ -857,7 +887,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               tail[i][0] = tail[i][1] = make_uint2(0, 0);
-              if (p.tail_out && i0 + i < n) {
+              if (p.tail_out && i0 + i < n && row_ok(p, g0 + 8 * warp + i0 + i)) {
                 const __nv_bfloat16 *src = p.tail_out + (g0 + 8 * warp + i0 + i) * kD;
                 tail[i][0] = *reinterpret_cast<const uint2 *>(src + d0);
                 tail[i][1] = *reinterpret_cast<const uint2 *>(src + d1);
@@ -918,7 +948,6 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
     else __syncthreads();
   };
   const int64_t gr = (int64_t)blockIdx.x * (kBlock / kRow) + threadIdx.x / kRow;
-  const bool live = gr < p.rows;                 // (whole warps; a block has one row where it syncs)
   int32_t len;
   const int32_t KT = prefix_tiles(p, len);
   pdl_wait_primary();
@@ -935,7 +964,7 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
   uint2 tail[kQ];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) tail[q] = make_uint2(0, 0);
-  if (p.tail_lse) {
+  if (p.tail_lse && row_ok(p, gr)) {
     lt = p.tail_lse[gr];
     if (g == 0) {
 #pragma unroll
@@ -945,14 +974,18 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
   }
   if (p.sink) sk = __ldg(p.sink + (uint32_t)gr % (uint32_t)p.H);
   const int n_all = parts.count();
-  auto part_lse = [&](int i) { return i < n_all ? __ldcg(p.part_lse + parts.slot(i)) : -INFINITY; };
+  auto part_lse = [&](int i) {
+    return i < n_all && part_ok(p, parts.slot(i)) ? __ldcg(p.part_lse + parts.slot(i)) : -INFINITY;
+  };
   float4 o[kIn][kQ];
   auto fetch = [&](int i0) {         // the group's parts i0, i0 + kGroups, .. (the last one again past the end)
 #pragma unroll
     for (int i = 0; i < kIn; ++i) {
-      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + parts.loaded(i0 + kGroups * i) * kD) + t;
+      const int64_t from = parts.loaded(i0 + kGroups * i);
+      const float4 *src = reinterpret_cast<const float4 *>(p.part_o + from * kD) + t;
+      const bool ok = part_ok(p, from);
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) o[i][q] = __ldcg(src + kTh * q);
+      for (int q = 0; q < kQ; ++q) o[i][q] = ok ? __ldcg(src + kTh * q) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   const float first = part_lse(rt);
@@ -1029,7 +1062,7 @@ __global__ void __launch_bounds__(kTh *kGroups < 128 ? 128 : kTh * kGroups)
   // (out may alias the tail, which its own thread has read; lse too, which
   // every thread of the row has read before a barrier above or this one)
   if constexpr (kRow == 32) __syncwarp();
-  if (rt == 0) p.lse[gr] = w.lse;
+  if (rt == 0 && row_ok(p, gr)) p.lse[gr] = w.lse;
 #pragma unroll
   for (int q = 0; q < kQ; ++q)
     store_out4(p, gr, 4 * (t + kTh * q), make_float4(acc[q].x * wo, acc[q].y * wo, acc[q].z * wo, acc[q].w * wo),
@@ -1254,6 +1287,14 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
   p.tile = reinterpret_cast<int2 *>(w + plan->ws_tile_offset);
   p.part_lse = reinterpret_cast<float *>(w + plan->ws_part_lse_offset);
   p.part_o = reinterpret_cast<float *>(w + plan->ws_part_o_offset);
+  p.check_rows = p.rows;
+  p.check_parts = 256 * (int64_t)p.C;
+#ifdef DSA_DEBUG
+  // Checking build only, test knobs: fewer rows than there are; the accesses
+  // past them are reported and left out.
+  if (const char *v = std::getenv("DSA_DEBUG_CHECK_ROWS")) p.check_rows = std::min<int64_t>(p.check_rows, std::atoll(v));
+  if (const char *v = std::getenv("DSA_DEBUG_CHECK_PARTS")) p.check_parts = std::min<int64_t>(p.check_parts, std::atoll(v));
+#endif
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dsa::kDebug && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return DSA_ERR_CUDA;
   cudaError_t e = cudaErrorInvalidValue;
