@@ -12,6 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sysconfig
 from typing import Optional
 
 import torch
@@ -20,7 +21,7 @@ from . import workloads as W
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libdsa_decode.so")
-MARSHAL_PATH = os.path.join(_HERE, "lib", "_marshal.so")
+MARSHAL_PATH = os.path.join(_HERE, "lib", "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 DSA_OK = 0
 STATUS_NAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED",

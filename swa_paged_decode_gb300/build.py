@@ -25,7 +25,8 @@ LIB = os.path.join(LIBDIR, "libdsa_decode.so")
 # The checking build (-DDSA_DEBUG): every global and tile access bounds-checked.
 LIB_DEBUG = os.path.join(LIBDIR, "libdsa_decode_debug.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
-MARSHAL = os.path.join(LIBDIR, "_marshal.so")
+# Named with the interpreter's ABI tag: another Python never takes this one's.
+MARSHAL = os.path.join(LIBDIR, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 _marshal_lock = threading.Lock()   # the release and the checking build run side by side
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
