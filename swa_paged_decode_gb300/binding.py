@@ -3,7 +3,8 @@
 Argument marshalling only: torch tensors become device pointers, strides and
 sizes; every step of the decode runs in the library's CUDA kernels. The cache
 and shared-prefix calls go through a small C extension (csrc/marshal.c) that
-also checks the tensors. The functions keep the C names. Loading fails loudly when the library is missing
+also checks the tensors, loaded with the first of them. The functions keep the
+C names. Loading fails loudly when the library or the extension is missing
 (there is no fallback path).
 """
 from __future__ import annotations
@@ -200,9 +201,7 @@ def _load_path(path: str):
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
     lib.dsa_decode_abi_version.argtypes = []
-    m = _load_marshal()
-    lib.marshal = {n: (getattr(m, n[4:]), ctypes.cast(getattr(lib, n), vp).value)
-                   for n in ("dsa_cache_write", "dsa_cache_read", "dsa_prefix_run")}
+    lib.marshal = {}   # the calls of the marshalling extension, filled as they are used
     _libs[path] = lib
     return lib
 
@@ -364,8 +363,11 @@ def _marshalled(fn: str, check: bool, *args) -> int:
     """Call ``fn`` through the marshalling extension. A tensor of another
     device than the current one, dtype, shape or layout than the call takes
     raises DSA_ERR_INVALID_ARG before the library is called."""
-    f, address = load().marshal[fn]
-    rc = f(address, *args)
+    lib = load()
+    entry = lib.marshal.get(fn)
+    if entry is None:
+        entry = lib.marshal[fn] = (getattr(_load_marshal(), fn[4:]), ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value)
+    rc = entry[0](entry[1], *args)
     if rc == -1000:                      # BAD_TENSOR
         raise DsaError(fn, -1)
     if check and rc != DSA_OK:

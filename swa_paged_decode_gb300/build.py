@@ -3,7 +3,8 @@
 Each .cu translation unit compiles in parallel to an object under
 ``_build/``; the objects link into ``lib/libdsa_decode.so`` (CUDA runtime
 linked statically, so the library only needs the driver). The marshalling
-extension (``lib/_marshal.so``, plain C, no CUDA) is built beside it. Run as
+extension of the cache and prefix calls (``lib/_marshal.*.so``, plain C, no
+CUDA) is built beside it where Python's headers are installed. Run as
 ``python -m swa_paged_decode_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -50,14 +51,20 @@ def _stale(lib: str, deps) -> bool:
 
 
 def build_marshal(force: bool = False) -> str:
-    """Build the CPython extension that marshals the cache and prefix calls."""
+    """Build the CPython extension that marshals the cache and prefix calls
+    ("" without Python's headers: the decode does not need it)."""
     with _marshal_lock:
         if not force and not _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "dsa_decode.h"), __file__]):
             return MARSHAL
         os.makedirs(LIBDIR, exist_ok=True)
         tmp = MARSHAL + f".tmp{os.getpid()}"
-        subprocess.run(["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I",
-                        sysconfig.get_paths()["include"], "-o", tmp, MARSHAL_SRC], check=True)
+        include = sysconfig.get_paths()["include"]
+        if not os.path.exists(os.path.join(include, "Python.h")):
+            sys.stderr.write(f"{MARSHAL} not built (the Python binding's cache and prefix calls need it): "
+                             f"no Python.h in {include}\n")
+            return ""
+        subprocess.run(["gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", include,
+                        "-o", tmp, MARSHAL_SRC], check=True)
         os.replace(tmp, MARSHAL)
         return MARSHAL
 
