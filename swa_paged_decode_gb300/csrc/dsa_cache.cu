@@ -577,7 +577,8 @@ dsa_status dsa_cache_write(const dsa_cache_desc *cache, const int32_t *slots, in
   CacheParams p;
   std::memset(&p, 0, sizeof(p));
   if (rope_style != DSA_ROPE_NEOX && rope_style != DSA_ROPE_GPTJ) return DSA_ERR_INVALID_ARG;
-  if ((positions == nullptr) != (cos_sin == nullptr)) return DSA_ERR_INVALID_ARG;
+  // (no rows have no positions: an empty array may have no address)
+  if (num_rows > 0 && (positions == nullptr) != (cos_sin == nullptr)) return DSA_ERR_INVALID_ARG;
   if (cos_sin && cos_sin_rows < 1) return DSA_ERR_INVALID_ARG;
   if (norm_weight && !(std::isfinite(norm_eps) && norm_eps >= 0.f)) return DSA_ERR_INVALID_ARG;
   if ((cos_sin && (!aligned(cos_sin, 16) || !aligned(positions, 8))) ||

@@ -109,3 +109,9 @@ def test_binding_takes_tensors_and_numbers(lib):
             B.dsa_cache_write(cache, torch.zeros(3, dtype=torch.int32), None)
     with pytest.raises(TypeError):
         B.dsa_cache_write(c, torch.zeros(3, dtype=torch.int32), torch.zeros(3, 512), norm_eps="small")
+
+
+def test_no_rows_with_a_table_is_fine(lib):
+    """A step without new keys: empty arrays, whose address may be null."""
+    assert write(lib, n=0, slots=None, rows=None, pos=None, table=0x50000, table_rows=4) == 0
+    assert write(lib, n=0, slots=None, rows=None, pos=0x40000, table=0x50000, table_rows=4) == 0

@@ -310,3 +310,17 @@ def test_binding_refuses_what_pointers_cannot_tell():
     B.dsa_cache_read(cache, ok["slots"], ok["rows"], stream=st)          # a stream, or its raw handle
     B.dsa_cache_read(cache, ok["slots"], ok["rows"], stream=st.cuda_stream)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_no_rows(fmt):
+    """A step without new keys: every argument empty, the table there."""
+    cache = empty_cache(fmt, 64, 64)
+    none = dict(slots=torch.empty(0, dtype=torch.int32, device="cuda"), rows=torch.empty((0, dims(fmt)), device="cuda"))
+    w, cs = torch.ones(512, device="cuda"), W.rope_table(16, "cuda")
+    B.dsa_cache_write(cache, **none)
+    B.dsa_cache_write(cache, **none, norm_weight=w, norm_eps=1e-6, cos_sin=cs,
+                      positions=torch.empty(0, dtype=torch.int64, device="cuda"))
+    B.dsa_cache_read(cache, **none)
+    torch.cuda.synchronize()
+    assert bool((cache.data == 0xA5).all())
