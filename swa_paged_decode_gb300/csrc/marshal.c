@@ -81,6 +81,15 @@ typedef struct {
   int bad, err;
 } call;
 
+/* A number that the library takes as int32; another one is not cut to one. */
+static int32_t as_i32(call *c, PyObject *o) {
+  int over = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (PyErr_Occurred()) c->err = 1;
+  if (over || v < INT32_MIN || v > INT32_MAX) c->bad = 1;
+  return c->err || c->bad ? 0 : (int32_t)v;
+}
+
 static int read_tensor(call *c, PyObject *o, tensor *t) {
   if (c->bad || c->err) return 0;
   const int rc = get(o, t);
@@ -122,7 +131,7 @@ static void *vec(call *c, PyObject *o, int opt, PyObject *dtype, Py_ssize_t nd, 
   return t.ptr;
 }
 
-static int record_bytes(long fmt) {
+static int record_bytes(int32_t fmt) {
   switch (fmt) {
     case DSA_REC_FP8_528: case DSA_REC_FP8_528_UE8M0: return 528;
     case DSA_REC_NVFP4_288: return 288;
@@ -134,11 +143,7 @@ static int record_bytes(long fmt) {
 
 static void cache(call *c, PyObject *data, PyObject *page, PyObject *fmt, dsa_cache_desc *d) {
   tensor t;
-  const long pg = PyLong_AsLong(page), f = PyLong_AsLong(fmt);
-  if (PyErr_Occurred()) {
-    c->err = 1;
-    return;
-  }
+  const int32_t pg = as_i32(c, page), f = as_i32(c, fmt);
   if (!read_tensor(c, data, &t)) return;
   if (t.dtype != t_u8 || t.nd != 2 || t.stride[1] != 1 || t.shape[1] < (long long)pg * record_bytes(f)) {
     c->bad = 1;
@@ -147,8 +152,8 @@ static void cache(call *c, PyObject *data, PyObject *page, PyObject *fmt, dsa_ca
   d->base = t.ptr;
   d->num_pages = t.shape[0];
   d->page_stride_bytes = t.stride[0];
-  d->page_size = (int32_t)pg;
-  d->format = (int32_t)f;
+  d->page_size = pg;
+  d->format = f;
 }
 
 /* Dense rows [n, dims of the format]. */
@@ -221,7 +226,7 @@ static PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t na) 
   if (want_args(na, 13)) return NULL;
   write_fn f = (write_fn)PyLong_AsVoidPtr(a[0]);
   const float eps = (float)PyFloat_AsDouble(a[7]);
-  const long style = PyLong_AsLong(a[10]);
+  const int32_t style = as_i32(&c, a[10]);
   if (PyErr_Occurred()) return NULL;
   cache(&c, a[1], a[2], a[3], &d);
   const int32_t *slots = vec(&c, a[4], 0, t_i32, 1, -1, -1, -1, &n);
@@ -231,7 +236,7 @@ static PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t na) 
   const float *cs = vec(&c, a[9], 1, t_f32, 2, -1, 64, -1, &table);
   int32_t *status = vec(&c, a[11], 1, t_i32, 1, 1, -1, -1, NULL);
   dsa_stream_t st = stream_of(&c, a[12]);
-  DSA_CALL(rc, f(&d, slots, n, r, stride, type, w, eps, pos, cs, table, (int32_t)style, status, st));
+  DSA_CALL(rc, f(&d, slots, n, r, stride, type, w, eps, pos, cs, table, style, status, st));
   return PyLong_FromLong(rc);
 }
 
@@ -265,7 +270,7 @@ static PyObject *prefix_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   if (want_args(na, 19)) return NULL;
   prefix_fn f = (prefix_fn)PyLong_AsVoidPtr(a[0]);
   const dsa_prefix_plan_t *plan = PyLong_AsVoidPtr(a[1]);
-  const long style = PyLong_AsLong(a[12]);
+  const int32_t style = as_i32(&c, a[12]);
   const float scale = (float)PyFloat_AsDouble(a[13]);
   if (PyErr_Occurred()) return NULL;
   const long long T = plan->num_tokens, H = plan->num_heads, D = plan->d_qk;
@@ -286,7 +291,7 @@ static PyObject *prefix_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   float *lse = vec(&c, a[17], 0, t_f32, 2, T, H, -1, NULL);
   dsa_stream_t st = stream_of(&c, a[18]);
   const long long sh = H > 1 ? q.stride[1] : D, sq = T > 1 ? q.stride[0] : H * sh;
-  DSA_CALL(rc, f(plan, ws, (size_t)ws_bytes, q.ptr, sq, sh, &d, slots, length, sink, pos, cs, table, (int32_t)style,
+  DSA_CALL(rc, f(plan, ws, (size_t)ws_bytes, q.ptr, sq, sh, &d, slots, length, sink, pos, cs, table, style,
                  scale, tail, tail_lse, out, lse, st));
   return PyLong_FromLong(rc);
 }
