@@ -239,7 +239,10 @@ __device__ __forceinline__ uint32_t e2m1x8_neg(const float (&y)[16], int o) {
 // and the products theirs. A row whose squares leave that no room (a mean below
 // 2^-60 or a sum above 2^100, which fp32 may not hold at all) is taken again
 // times a power of two, eps with it: the quotient is the same.
-__device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps) {
+// With kStage `stage` receives lanes 28..31's 64 results and behind them what
+// their rounding left off, for the rotation.
+template <bool kStage>
+__device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps, int lane, float *stage) {
   float me, ml;
 #pragma unroll 1
   for (bool again = false;; again = true) {   // (the lanes agree)
@@ -283,19 +286,54 @@ __device__ __forceinline__ void norm_row(F2 (&v)[8], const F2 (&w)[8], float eps
   const float r0 = rsqrtf(me);
   const float h = me * r0, hl = fmaf(me, r0, -h) + ml * r0;
   const float r1 = h == h ? 0.5f * r0 * fmaf(-hl, r0, fmaf(-h, r0, 1.0f)) : 0.f;
-  const F2 a = f2(r0, r0), b = f2(r1, r1), minus = f2(-1.f, -1.f);
+  const F2 a = f2(r0, r0), b = f2(r1, r1), na = f2(-r0, -r0), minus = f2(-1.f, -1.f);
+  F2 lo[2];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {   // x w = q + ql
     const F2 q = f2_mul(v[k], w[k]), ql = f2_fma(v[k], w[k], f2_mul(q, minus));
-    v[k] = f2_fma(q, a, f2_fma(ql, a, f2_mul(q, b)));
+    const F2 c = f2_fma(ql, a, f2_mul(q, b));
+    v[k] = f2_fma(q, a, c);
+    if constexpr (kStage) {
+      lo[k & 1] = f2_fma(f2_fma(q, na, v[k]), minus, c);
+      if ((k & 1) && lane >= 28) {
+        ulonglong2 *d = reinterpret_cast<ulonglong2 *>(stage + 16 * (lane - 28) + 2 * k - 2);
+        d[0] = make_ulonglong2(v[k - 1].v, v[k].v);
+        d[16] = make_ulonglong2(lo[0].v, lo[1].v);
+      }
+    }
   }
+}
+
+// ------------------------------------------------------------ rotation
+// (a, b) and its low part turned by (c, s): (a c - b s, b c + a s), nearly
+// always the exact values rounded to fp32: the products' and the sums' rounding
+// errors are added at the end (Dekker, "A floating-point technique for extending
+// the available precision", 1971, with the products' errors by FMAs). In plain
+// fp32 one bf16 value in 80000 behind it fell on the other side of a tie. Zeros
+// keep their sign, infinities stay.
+__device__ __forceinline__ void turn(float &a, float &b, F2 low, float c, float s) {
+  float al, bl, t0, t1, d0, d1;
+  f2_get(low, al, bl);
+  const F2 x = f2(a, b), y = f2(b, a), yl = f2(bl, al), c2 = f2(c, c), s2 = f2(-s, s), minus = f2(-1.f, -1.f);
+  const F2 p = f2_mul(x, c2), q = f2_mul(y, s2), t = f2_add(p, q);
+  const F2 z = f2_fma(p, minus, t), u = f2_fma(z, minus, t);                          // t - p, t - (t - p)
+  const F2 e = f2_add(f2_fma(u, minus, p), f2_fma(z, minus, q));                      // p + q - t
+  const F2 ep = f2_fma(x, c2, f2_mul(p, minus)), eq = f2_fma(y, s2, f2_mul(q, minus));
+  f2_get(f2_fma(low, c2, f2_fma(yl, s2, f2_add(e, f2_add(ep, eq)))), d0, d1);
+  f2_get(t, t0, t1);
+  a = d0 != 0.f && fabsf(t0) < INFINITY ? t0 + d0 : t0;
+  b = d1 != 0.f && fabsf(t1) < INFINITY ? t1 + d1 : t1;
 }
 
 // ------------------------------------------------------------ write
 // x -> (norm) -> (rotation) -> codes and scales, all in fp32 from the loaded
 // values to the codes: nothing is rounded to 16 bits in between. A warp's next
-// row is loaded before its present one is worked on.
-template <int FMT, int TY>
+// row is loaded before its present one is worked on. The rotation takes a pair
+// per lane, through shared memory, so that its exact arithmetic is the work of
+// 32 lanes and not of the 4 that hold the last 64 dims: 65536 normed MODEL1 rows
+// take 35 us, 33 with a rotation in plain fp32 in those 4. Without a table none
+// of it is compiled in (65536 plain fp8 rows 17 us, 22 with it skipped).
+template <int FMT, int TY, bool kRope>
 __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheParams p) {
   constexpr bool kV32 = FMT == DSA_REC_V32_656;
   const int lane = threadIdx.x & 31;
@@ -313,13 +351,21 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
       w[2 * k + 1] = f2(x.z, x.w);
     }
   }
+  // A row's last 64 dims on their way to a pair per lane and back (V3.2 rows
+  // hold theirs so already): values, then the norm's low parts.
+  constexpr bool kStage = kRope && !kV32;
+  __shared__ __align__(16) float rot_s[kStage ? kCacheWarps : 1][128];
+  float *stage = rot_s[kStage ? threadIdx.x >> 5 : 0];
+  // the lane's pair: dims k, 32 + k (NeoX) or 2 k, 2 k + 1 (GPT-J)
+  const int pair = kV32 && !p.gptj ? (lane & 15) * 2 + (lane >> 4) : lane;
+  const int ia = p.gptj ? 2 * pair : pair, ib = p.gptj ? 2 * pair + 1 : pair + 32;
   RowRaw<TY> next;
   int32_t next_sid = -1;
   int64_t next_pos = 0;
   auto fetch = [&](int64_t i) {
     if (i >= p.n) return;
     next_sid = __ldg(p.L.ids + i);
-    if (p.cos_sin) next_pos = __ldg(p.positions + i);
+    if constexpr (kRope) next_pos = __ldg(p.positions + i);
     load_row<TY, kV32>(src + i * stride, lane, wide, next);
   };
   int64_t i = (int64_t)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
@@ -331,69 +377,59 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
     const int64_t pos = next_pos;
     fetch(i + step);
     if (sid < 0 || (int64_t)sid >= p.L.num_slots) continue;   // padding: nothing is written
-    const float4 *cs = nullptr;
-    float4 c4[2][2];             // lanes 28..31: cos, sin of the lane's pairs (NeoX: of its 16 dims, loaded below)
-    if (p.cos_sin) {
+    float co = 0.f, si = 0.f;
+    if constexpr (kRope) {
       if (pos < 0 || pos >= p.cs_rows) {   // outside the table: the row is not written
         if (p.status && lane == 0) report_status(p.status, DSA_ERR_INVALID_ARG);
         continue;
       }
-      cs = reinterpret_cast<const float4 *>(p.cos_sin + pos * 64);
-      if (!kV32 && p.gptj && lane >= 28) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          c4[0][k] = __ldg(cs + 2 * (lane - 28) + k);
-          c4[1][k] = __ldg(cs + 8 + 2 * (lane - 28) + k);
-        }
-      }
+      const float *cs = p.cos_sin + pos * 64;
+      co = __ldg(cs + pair);
+      si = __ldg(cs + 32 + pair);
     }
     F2 v[8];
     float t0 = 0.f, t1 = 0.f;
     unpack_row<TY, kV32>(raw, v, t0, t1);
-    if (p.norm_w) norm_row(v, w, p.eps);
+    if constexpr (kStage) __syncwarp();   // the row before has left the stage
+    if (p.norm_w) norm_row<kStage>(v, w, p.eps, lane, stage);
     // (a, b) -> (a cos - b sin, b cos + a sin) on the last 64 dims
-    if (cs) {
-      const float *cf = reinterpret_cast<const float *>(cs);
-      if constexpr (kV32) {   // dims 512 + 2 lane, + 1
-        if (p.gptj) {         // one pair
-          const float c = __ldg(cf + lane), s = __ldg(cf + 32 + lane);
-          const float a = t0, b = t1;
-          t0 = fmaf(a, c, -(b * s));
-          t1 = fmaf(b, c, a * s);
-        } else {              // the partners of two pairs sit 16 lanes away
-          const float2 c = __ldg(reinterpret_cast<const float2 *>(cf) + (lane & 15));
-          const float2 s = __ldg(reinterpret_cast<const float2 *>(cf) + 16 + (lane & 15));
-          const float o0 = __shfl_xor_sync(0xffffffffu, t0, 16), o1 = __shfl_xor_sync(0xffffffffu, t1, 16);
-          const float sg = lane < 16 ? -1.f : 1.f;
-          t0 = fmaf(t0, c.x, sg * (o0 * s.x));
-          t1 = fmaf(t1, c.y, sg * (o1 * s.y));
+    float ra = 0.f, rb = 0.f;
+    if constexpr (kRope) {
+      if constexpr (kV32) {     // dims 512 + 2 lane, + 1; NeoX partners sit 16 lanes away
+        float a = t0, b = t1;
+        if (!p.gptj) {          // lower lanes take the even pairs, upper lanes the odd ones
+          const float x = __shfl_xor_sync(0xffffffffu, lane < 16 ? t1 : t0, 16);
+          (lane < 16 ? b : a) = x;
         }
-      } else if (p.gptj) {    // lanes 28..31, pairs within a lane
-        if (lane >= 28) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 c = c4[0][k >> 2], s4 = c4[1][k >> 2];
-            const float co = (k & 3) == 0 ? c.x : (k & 3) == 1 ? c.y : (k & 3) == 2 ? c.z : c.w;
-            const float si = (k & 3) == 0 ? s4.x : (k & 3) == 1 ? s4.y : (k & 3) == 2 ? s4.z : s4.w;
-            float a, b;
-            f2_get(v[k], a, b);
-            v[k] = f2(fmaf(a, co, -(b * si)), fmaf(b, co, a * si));
-          }
+        turn(a, b, f2(0.f, 0.f), co, si);
+        t0 = a;
+        t1 = b;
+        if (!p.gptj) {
+          const float x = __shfl_xor_sync(0xffffffffu, lane < 16 ? t1 : t0, 16);
+          (lane < 16 ? t1 : t0) = x;
         }
-      } else {                // partners two lanes away: (28, 30), (29, 31)
-        const float sg = lane < 30 ? -1.f : 1.f;
-        const int f = 4 * (lane & 1);
+      } else {
+        if (!p.norm_w && lane >= 28) {
+          ulonglong2 *d = reinterpret_cast<ulonglong2 *>(stage + 16 * (lane - 28));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a, b, c, d;
-          f2_get(v[2 * k], a, b);
-          f2_get(v[2 * k + 1], c, d);
-          const float oa = __shfl_xor_sync(0xffffffffu, a, 2), ob = __shfl_xor_sync(0xffffffffu, b, 2);
-          const float oc = __shfl_xor_sync(0xffffffffu, c, 2), od = __shfl_xor_sync(0xffffffffu, d, 2);
+          for (int k = 0; k < 4; ++k) d[k] = make_ulonglong2(v[2 * k].v, v[2 * k + 1].v);
+        }
+        __syncwarp();
+        ra = stage[ia];
+        rb = stage[ib];
+        turn(ra, rb, p.norm_w ? f2(stage[64 + ia], stage[64 + ib]) : f2(0.f, 0.f), co, si);
+        if constexpr (FMT != DSA_REC_MODEL1_584) {
+          stage[ia] = ra;
+          stage[ib] = rb;
+          __syncwarp();
           if (lane >= 28) {
-            const float4 co = __ldg(cs + f + k), si = __ldg(cs + 8 + f + k);
-            v[2 * k] = f2(fmaf(a, co.x, sg * (oa * si.x)), fmaf(b, co.y, sg * (ob * si.y)));
-            v[2 * k + 1] = f2(fmaf(c, co.z, sg * (oc * si.z)), fmaf(d, co.w, sg * (od * si.w)));
+            const ulonglong2 *d = reinterpret_cast<const ulonglong2 *>(stage + 16 * (lane - 28));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const ulonglong2 x = d[k];
+              v[2 * k].v = x.x;
+              v[2 * k + 1].v = x.y;
+            }
           }
         }
       }
@@ -428,13 +464,22 @@ __global__ void __launch_bounds__(32 * kCacheWarps, 5) cache_write_kernel(CacheP
         d[0] = make_uint2(c.x, c.y);
         d[1] = make_uint2(c.z, c.w);
         if ((lane & 3) == 0) rec[576 + (lane >> 2)] = (uint8_t)e;
-      } else {                 // the bf16 part, and the unused byte
+      } else if constexpr (!kRope) {   // the bf16 part
         uint2 *d = reinterpret_cast<uint2 *>(rec + 448 + 32 * (lane - 28));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           d[k] = make_uint2(bf16x2_bits(x[4 * k], x[4 * k + 1]), bf16x2_bits(x[4 * k + 2], x[4 * k + 3]));
-        if (lane == 28) rec[583] = 0;
       }
+      if constexpr (kRope) {   // the bf16 part, a pair per lane
+        const uint32_t r = bf16x2_bits(ra, rb);
+        if (p.gptj) {
+          *reinterpret_cast<uint32_t *>(rec + 448 + 4 * lane) = r;
+        } else {
+          *reinterpret_cast<uint16_t *>(rec + 448 + 2 * lane) = (uint16_t)r;
+          *reinterpret_cast<uint16_t *>(rec + 512 + 2 * lane) = (uint16_t)(r >> 16);
+        }
+      }
+      if (lane == 28) rec[583] = 0;   // the unused byte
     } else {                   // NVFP4: a block is one lane's 16 dims
       const uint32_t m = block_amax<1>(x);
       const float a6 = fminf(__fdiv_rn(__uint_as_float(m), 6.0f), 448.0f);
@@ -520,7 +565,8 @@ cudaError_t launch(const CacheParams &p, int32_t type, bool write, cudaStream_t 
   constexpr int kT = 32 * kCacheWarps;
 #define DSA_CACHE_CASE(TY)                                        \
   case TY:                                                        \
-    if (write) cache_write_kernel<FMT, TY><<<grid, kT, 0, st>>>(p); \
+    if (write && p.cos_sin) cache_write_kernel<FMT, TY, true><<<grid, kT, 0, st>>>(p); \
+    else if (write) cache_write_kernel<FMT, TY, false><<<grid, kT, 0, st>>>(p); \
     else cache_read_kernel<FMT, TY><<<grid, kT, 0, st>>>(p);        \
     break;
   switch (type) {
