@@ -424,7 +424,10 @@ enum { DSA_TYPE_BF16 = 0, DSA_TYPE_F16 = 1, DSA_TYPE_F32 = 2 };
  *     MODEL1_584 the smallest power of two >= a / 448 (exponent in
  *     [-127, 127]; 2^0 for a block of zeros); NVFP4_288 a / 6 rounded to
  *     e4m3, at most 448. bf16 parts are rounded to nearest even.
- * All of it is computed in fp32 from the row's values to the codes. A block
+ * All of it is computed in fp32 from the row's values to the codes, the
+ * rounding errors of the norm and of the rotation carried: a code or bf16
+ * value differs from that of the 64-bit formula only next to a tie (about one
+ * in a million behind a norm). A block
  * that holds a NaN reads back as NaN throughout (for FP8_528 and V32_656 one
  * that holds an infinity too; the other scales saturate).
  * rows: row_type DSA_TYPE_*, 16-byte aligned, row_stride (elements) >= d and
@@ -508,7 +511,8 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
  *   workspace: plan->workspace_bytes, 256-byte aligned; calls that share one
  *     must be ordered. Its first word is the device status
  *     (dsa_decode_read_status; a position outside the table sets
- *     DSA_ERR_INVALID_ARG and uses row 0).
+ *     DSA_ERR_INVALID_ARG and uses row 0; positions of a call whose length
+ *     is 0 are not read).
  * Precision: as dsa_decode_run, f16 products with fp32 sums; keys whose
  * largest magnitude lies in 2^-48 .. 2^48 keep f16 precision relative to it; a
  * key's weight in out is off by at most 2^-11 of itself or 2^-32 of the row's

@@ -17,6 +17,15 @@
 //           of (row tile, key tile) units per pair;
 //   merge   the rows whose key tiles were split over pairs, and the rows of
 //           an empty prefix.
+//
+// Roundings to 16 bits, as in the decode kernel: keys, queries and weights are
+// f16 operands of the tensor core (11 bits; bf16 has 8, and tf32 runs at half
+// the rate with operands twice the size), each with a power of two of its own
+// (a key or 32 of them, a query row, a row's weights) so that f16's range is no
+// limit. Codes times a power of two or an e4m3 scale are exact in them, and
+// unrotated queries but for elements below 2^-17 of the row's largest; codes
+// times an fp32 scale are off by 2^-11, which shows as 1 to 2e-6 of lse. Scores,
+// sums, partials and lse are fp32. The tail is the bf16 output of the decode.
 #include <cuda.h>
 
 #include <algorithm>
@@ -232,10 +241,11 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 // for it. Every wait is bounded as in the decode kernel.
 //
 // What bounds it: the products' shared-memory operands and the issue of a
-// chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP): 342 us with
-// gather and merge, 1605 TFLOP/s of the 1872 that a library product of 8192^3
-// reaches in a burst (371 us, 1481 TFLOP/s, back to back under the power cap,
-// against its 1706); without the copies 313 us. The steps there: N = 128 tiles
+// chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP), gather and merge
+// included: 367 us a call in a loop under the power cap (1498 TFLOP/s, a library
+// product of 8192^3 reaches 1706 there), 339 to 351 us for one call alone, by
+// the box (1566 to 1622 of 1872); 313 us without the copies, measured at 342.
+// The steps there, calls alone: N = 128 tiles
 // with a relay of the chunks' arrival 1272; arrivals released at CTA scope 914;
 // N = 256, one copy a chunk, converged issue 561; three copying warps and
 // single-test waits 438; merge and gather 413; copies that complete on the
