@@ -4,7 +4,6 @@
 #pragma once
 
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -306,7 +305,7 @@ __device__ inline float e2m1_to_f32(uint32_t nib) {
 // (V4.1 options), 24-26 (exact-budget waits), 28-30 and 32-34 (MODEL1 records),
 // 36-37 (V3.2 records), 40-42 (head groups sharing tiles), 46 and 50
 // (producers staging Q, with and without shared tiles), SIMT kernels 8-11,
-// combine 16-18, prefix attention 56-57.
+// combine 16-18.
 cudaError_t dsa_configure_once(int bit, cudaError_t (*f)(void *), void *arg);
 
 // Programmatic dependent launch: the decode kernels let the combine grid be

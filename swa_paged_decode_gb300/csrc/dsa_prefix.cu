@@ -1091,6 +1091,7 @@ cudaError_t attend_setup(void *) {
   return cudaFuncSetAttribute(dsa::prefix_attend_kernel<V32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)dsa::PfCfg<V32>::kSmem);
 }
+// (bits 56 and 57 of dsa_configure_once; the other kernels' stand at its declaration)
 template <bool V32>
 cudaError_t attend_ready() {
   return dsa::dsa_configure_once(V32 ? 57 : 56, &attend_setup<V32>, nullptr);

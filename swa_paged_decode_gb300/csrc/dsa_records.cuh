@@ -2,8 +2,10 @@
 // holds dims 16 l .. 16 l + 15 (and of a V3.2 record dims 512 + 2 l, + 1).
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "dsa_internal.cuh"
-#include "tc_ptx.cuh"
+#include "pair_ptx.cuh"
 
 namespace dsa {
 

@@ -97,3 +97,14 @@ def test_parity_record_passes_on_oracle_output_and_catches_errors():
     lb = lse.clone()
     lb[2, 0] += 2e-3
     assert not bench.parity_record(_FakeStep(w, _FakeDec(out, lb, kept, chk)), ref, False)["pass"]
+
+
+def test_traffic_record_is_keyed_by_the_decode_alone():
+    """The captured traffic holds while the decode kernel's sources are those of
+    the capture: nothing that only other kernels use stands in them."""
+    for f in bench.KERNEL_SOURCES:
+        src = open(f"{bench.ROOT}/{f}").read()
+        for other in ("cta_group::2", "prefix_", "cache_write", "stg_v8"):
+            assert other not in src, (f, other)
+    if bench.sources_hash() == bench.NCU_TRAFFIC["sources"]:
+        assert bench.ncu_traffic(bench.NCU_TRAFFIC["rows_per_launch"]) == bench.NCU_TRAFFIC["bytes_per_launch"]
