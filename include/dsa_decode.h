@@ -515,8 +515,8 @@ dsa_status dsa_prefix_plan(int32_t num_tokens, int32_t num_heads, int32_t width,
  *     is 0 are not read).
  * Precision: as dsa_decode_run, f16 products with fp32 sums; keys whose
  * largest magnitude lies in 2^-48 .. 2^48 keep f16 precision relative to it; a
- * key's weight in out is off by at most 2^-11 of itself or 2^-32 of the row's
- * largest (in lse its sum is fp32).
+ * key's share of out (its weight times its magnitude) is off by at most 2^-11 of
+ * itself or 2^-32 of the row's largest share (the sums in lse are fp32).
  * Three launches on `stream`; allocates nothing, never synchronizes. */
 dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t workspace_bytes,
                           const void *q, int64_t q_stride_t, int64_t q_stride_h,
