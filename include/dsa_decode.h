@@ -526,6 +526,78 @@ dsa_status dsa_prefix_run(const dsa_prefix_plan_t *plan, void *workspace, size_t
                           const void *tail_out, const float *tail_lse, void *out, float *lse,
                           dsa_stream_t stream);
 
+/* Plan of a chunk call (dsa_chunk_plan). Plain data: copy it freely; callers
+ * must not edit the fields. */
+typedef struct {
+  int32_t magic;
+  int32_t abi_version;
+  int32_t num_tokens;      /* T                                              */
+  int32_t num_seqs;        /* B                                              */
+  int32_t num_heads;       /* H                                              */
+  int32_t width;           /* entries of every list                          */
+  int32_t d_qk;            /* 512, or 576 for V3.2 records                   */
+  int32_t num_sms;
+  int32_t pairs;           /* CTA pairs that the work is cut for             */
+  int32_t row_tiles;       /* most 128-row tiles of query rows               */
+  int32_t seq_halves;      /* 128-key halves kept for a sequence             */
+  int32_t reserved0;
+  int64_t ws_info_offset;  /* workspace byte offsets                         */
+  int64_t ws_key_e_offset;
+  int64_t ws_image_offset;
+  int64_t ws_row_tile_offset;
+  int64_t ws_seq_tile_offset;
+  int64_t ws_begin_offset;
+  int64_t ws_tile_offset;
+  int64_t ws_part_lse_offset;
+  int64_t ws_part_o_offset;
+  int64_t workspace_bytes;
+  int64_t wait_budget_cycles; /* as in dsa_decode_plan_t                     */
+  int64_t reserved[4];
+} dsa_chunk_plan_t;
+
+/* Plan the attention of chunks of new tokens (the pages decode single tokens;
+ * they have no counterpart of this call): num_tokens tokens in all (T >= 0) of
+ * num_seqs sequences (B >= 0), any num_heads >= 1, lists of up to width
+ * entries (>= 1; starts and lengths are read on the device), d_qk 512 or 576
+ * (V3.2 records). num_sms as for dsa_prefix_plan. Fills *plan and
+ * *workspace_bytes: about 1040 bytes (1170 with d_qk = 576) per entry of all
+ * lists, of which a call touches what its sequences attend, and the partials.
+ * DSA_ERR_UNSUPPORTED beyond 2^31 - 129 query rows or 9.5e8 entries. Host
+ * only; launches nothing. */
+dsa_status dsa_chunk_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_heads, int32_t width,
+                          int32_t num_sms, int32_t d_qk, dsa_chunk_plan_t *plan,
+                          size_t *workspace_bytes);
+
+/* Attention of new tokens over paged lists (no counterpart on the pages): a
+ * prompt's chunk, single tokens, or both in one call.
+ * Sequence b brings the tokens starts[b] .. starts[b + 1] - 1, n of them, in
+ * order. Its list is slots[b * slots_stride + 0 .. L - 1], L = clamp(lengths[b],
+ * 0, width), and its last n entries are the records of those tokens, written
+ * before this call (dsa_cache_write). Token i of them sits at list position p =
+ * L - n + i and attends the entries max(0, p - window + 1) .. p (window = 0: 0
+ * .. p) whose slots lie inside the cache; at p < 0 it attends none. lse, out,
+ * the tail state and the sink as for dsa_prefix_run, each per query row.
+ *   q: bf16 [T, H, d_qk], strides and alignment as for dsa_decode_run;
+ *     positions int64 [T] and the table as there (rows of the table, not list
+ *     positions: a list that lost entries to dsa_evict keeps its order only).
+ *   starts: int32 [B + 1], ascending within [0, T]. Starts that are not leave
+ *     everything as it was and set the status to DSA_ERR_INVALID_ARG.
+ *   slots: int32, slots_stride >= width; lengths: int32 [B].
+ *   out bf16 [T, H, 512], lse fp32 [T, H], contiguous; out may be tail_out and
+ *     lse may be tail_lse. Tokens before starts[0] and from starts[B] on are
+ *     left as they were. A row that attends nothing (and has no tail) gives
+ *     zeros and -inf.
+ *   workspace, status, precision: as for dsa_prefix_run. Lists may share slots.
+ * Three launches on `stream`; allocates nothing, never synchronizes. */
+dsa_status dsa_chunk_run(const dsa_chunk_plan_t *plan, void *workspace, size_t workspace_bytes,
+                         const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                         const dsa_cache_desc *cache, const int32_t *slots, int64_t slots_stride,
+                         const int32_t *lengths, const int32_t *starts, int32_t window,
+                         const float *sink, const int64_t *positions, const float *cos_sin,
+                         int64_t cos_sin_rows, int32_t rope_style, float scale,
+                         const void *tail_out, const float *tail_lse, void *out, float *lse,
+                         dsa_stream_t stream);
+
 /* Static description of a status code (no counterpart on the pages). */
 const char *dsa_decode_status_string(dsa_status s);
 

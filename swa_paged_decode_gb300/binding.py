@@ -33,6 +33,7 @@ EXPORTED = ("dsa_decode_plan", "dsa_decode_plan_qk", "dsa_decode_run", "dsa_deco
             "dsa_decode_run_noalloc", "dsa_decode_run_v41", "dsa_decode_combine_v41")
 EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
 EXPORTED_PREFIX = ("dsa_prefix_plan", "dsa_prefix_run")
+EXPORTED_CHUNK = ("dsa_chunk_plan", "dsa_chunk_run")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
 _current_device = torch._C._cuda_getDevice
@@ -71,6 +72,17 @@ class PrefixPlan(ctypes.Structure):
         [(n, ctypes.c_int64) for n in (
             "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_tile_offset",
             "ws_part_lse_offset", "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
+        [("reserved", ctypes.c_int64 * 4)]
+
+
+class ChunkPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "magic", "abi_version", "num_tokens", "num_seqs", "num_heads", "width", "d_qk", "num_sms",
+        "pairs", "row_tiles", "seq_halves", "reserved0")] + \
+        [(n, ctypes.c_int64) for n in (
+            "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_row_tile_offset",
+            "ws_seq_tile_offset", "ws_begin_offset", "ws_tile_offset", "ws_part_lse_offset",
+            "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
         [("reserved", ctypes.c_int64 * 4)]
 
 
@@ -197,6 +209,13 @@ def _load_path(path: str):
     lib.dsa_prefix_run.argtypes = [ctypes.POINTER(PrefixPlan), vp, ctypes.c_size_t, vp, i64, i64,
                                    ctypes.POINTER(CacheDesc), vp, vp, vp, vp, vp, i64, i32,
                                    ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.dsa_chunk_plan.restype = ctypes.c_int
+    lib.dsa_chunk_plan.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(ChunkPlan),
+                                   ctypes.POINTER(ctypes.c_size_t)]
+    lib.dsa_chunk_run.restype = ctypes.c_int
+    lib.dsa_chunk_run.argtypes = [ctypes.POINTER(ChunkPlan), vp, ctypes.c_size_t, vp, i64, i64,
+                                  ctypes.POINTER(CacheDesc), vp, i64, vp, vp, i32, vp, vp, vp, i64, i32,
+                                  ctypes.c_float, vp, vp, vp, vp, vp]
     lib.dsa_decode_status_string.restype = ctypes.c_char_p
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
@@ -442,6 +461,54 @@ class PrefixAttention:
                  tail_lse: Optional[torch.Tensor] = None, stream=None):
         dsa_prefix_run(self.plan, self.workspace, q, cache, slots, length, sink, positions, cos_sin,
                        rope_style, scale, tail_out, tail_lse, self.out, self.lse, stream)
+        return self.out, self.lse
+
+
+def dsa_chunk_plan(num_tokens: int, num_seqs: int, num_heads: int, width: int, num_sms: int = 0,
+                   d_qk: int = 512):
+    """-> (ChunkPlan, workspace_bytes)."""
+    plan = ChunkPlan()
+    ws = ctypes.c_size_t(0)
+    _check("dsa_chunk_plan", load().dsa_chunk_plan(num_tokens, num_seqs, num_heads, width, num_sms, d_qk,
+                                                   ctypes.byref(plan), ctypes.byref(ws)))
+    return plan, int(ws.value)
+
+
+def dsa_chunk_run(plan: ChunkPlan, workspace: torch.Tensor, q: torch.Tensor, cache: W.PagedCache,
+                  slots: torch.Tensor, lengths: torch.Tensor, starts: torch.Tensor, window: int,
+                  sink: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                  cos_sin: Optional[torch.Tensor], rope_style: int, scale: float,
+                  tail_out: Optional[torch.Tensor], tail_lse: Optional[torch.Tensor],
+                  out: torch.Tensor, lse: torch.Tensor, stream=None, check: bool = True) -> int:
+    """Causal attention of the new tokens of every sequence b (``starts``
+    [B + 1] int32) over its list ``slots[b]`` [B, width] int32 of
+    ``lengths[b]`` records, the new tokens' own last; ``window`` > 0: over the
+    last that many of them."""
+    return _marshalled("dsa_chunk_run", check, ctypes.addressof(plan), workspace, q, cache.data,
+                       cache.page_size, cache.fmt, slots, lengths, starts, window, sink, positions,
+                       cos_sin, rope_style, scale, tail_out, tail_lse, out, lse,
+                       None if stream is None else _stream(stream))
+
+
+class ChunkAttention:
+    """Plan + workspace for up to T new tokens of ``num_seqs`` sequences whose
+    lists have up to ``width`` records; ``__call__`` runs on the current stream
+    and returns (``self.out``, ``self.lse``). ``q`` has T tokens; those outside
+    every sequence are left as they were."""
+
+    def __init__(self, T: int, num_seqs: int, H: int, width: int, device, d_qk: int = 512, num_sms: int = 0):
+        self.plan, nbytes = dsa_chunk_plan(T, num_seqs, H, width, num_sms, d_qk)
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        self.out = torch.empty((T, H, W.HEAD_DIM), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((T, H), dtype=torch.float32, device=device)
+
+    def __call__(self, q: torch.Tensor, cache: W.PagedCache, slots: torch.Tensor, lengths: torch.Tensor,
+                 starts: torch.Tensor, scale: float, window: int = 0, sink: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+                 rope_style: int = DSA_ROPE_NEOX, tail_out: Optional[torch.Tensor] = None,
+                 tail_lse: Optional[torch.Tensor] = None, stream=None):
+        dsa_chunk_run(self.plan, self.workspace, q, cache, slots, lengths, starts, window, sink, positions,
+                      cos_sin, rope_style, scale, tail_out, tail_lse, self.out, self.lse, stream)
         return self.out, self.lse
 
 

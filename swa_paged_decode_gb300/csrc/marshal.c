@@ -215,6 +215,11 @@ typedef dsa_status (*prefix_fn)(const dsa_prefix_plan_t *, void *, size_t, const
                                 const int64_t *, const float *, int64_t, int32_t, float, const void *, const float *,
                                 void *, float *, dsa_stream_t);
 
+typedef dsa_status (*chunk_fn)(const dsa_chunk_plan_t *, void *, size_t, const void *, int64_t, int64_t,
+                               const dsa_cache_desc *, const int32_t *, int64_t, const int32_t *, const int32_t *,
+                               int32_t, const float *, const int64_t *, const float *, int64_t, int32_t, float,
+                               const void *, const float *, void *, float *, dsa_stream_t);
+
 /* (address, data, page_size, fmt, slots, rows, norm_weight, norm_eps,
  *  positions, cos_sin, rope_style, device_status, stream) */
 static PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t na) {
@@ -296,6 +301,67 @@ static PyObject *prefix_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   return PyLong_FromLong(rc);
 }
 
+/* Queries [T, H, D] of a dtype, any token and head strides. */
+static void *queries(call *c, PyObject *o, PyObject *dtype, long long T, long long H, long long D, long long *st,
+                     long long *sh) {
+  tensor t;
+  if (!read_tensor(c, o, &t)) return NULL;
+  if ((dtype && t.dtype != dtype) || t.nd != 3 || t.shape[0] != T || t.shape[1] != H || t.shape[2] != D ||
+      (T > 0 && t.stride[2] != 1)) {
+    c->bad = 1;
+    return NULL;
+  }
+  *sh = H > 1 ? t.stride[1] : D;
+  *st = T > 1 ? t.stride[0] : H * *sh;
+  return t.ptr;
+}
+
+/* Lists [B, width] of a dtype, any list stride. */
+static void *lists(call *c, PyObject *o, PyObject *dtype, long long B, long long width, long long *stride) {
+  tensor t;
+  if (!read_tensor(c, o, &t)) return NULL;
+  if (t.dtype != dtype || t.nd != 2 || t.shape[0] != B || t.shape[1] != width || (B > 0 && width > 1 && t.stride[1] != 1)) {
+    c->bad = 1;
+    return NULL;
+  }
+  *stride = B > 1 ? t.stride[0] : width;
+  return t.ptr;
+}
+
+/* (address, plan address, workspace, q, data, page_size, fmt, slots, lengths,
+ *  starts, window, sink, positions, cos_sin, rope_style, scale, tail_out,
+ *  tail_lse, out, lse, stream) */
+static PyObject *chunk_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  call c = {-1, 0, 0};
+  dsa_cache_desc d = {0};
+  long long ws_bytes = 0, table = 0, st = 0, sh = 0, ls = 0;
+  dsa_status rc;
+  if (want_args(na, 21)) return NULL;
+  chunk_fn f = (chunk_fn)PyLong_AsVoidPtr(a[0]);
+  const dsa_chunk_plan_t *plan = PyLong_AsVoidPtr(a[1]);
+  const int32_t window = as_i32(&c, a[10]), style = as_i32(&c, a[14]);
+  const float scale = (float)PyFloat_AsDouble(a[15]);
+  if (PyErr_Occurred()) return NULL;
+  const long long T = plan->num_tokens, B = plan->num_seqs, H = plan->num_heads;
+  void *ws = vec(&c, a[2], 0, t_u8, 1, -1, -1, -1, &ws_bytes);
+  const void *q = queries(&c, a[3], t_bf16, T, H, plan->d_qk, &st, &sh);
+  cache(&c, a[4], a[5], a[6], &d);
+  const int32_t *slots = lists(&c, a[7], t_i32, B, plan->width, &ls);
+  const int32_t *lengths = vec(&c, a[8], 0, t_i32, 1, B, -1, -1, NULL);
+  const int32_t *starts = vec(&c, a[9], 0, t_i32, 1, B + 1, -1, -1, NULL);
+  const float *sink = vec(&c, a[11], 1, t_f32, 1, H, -1, -1, NULL);
+  const int64_t *pos = vec(&c, a[12], 1, t_i64, 1, T, -1, -1, NULL);
+  const float *cs = vec(&c, a[13], 1, t_f32, 2, -1, 64, -1, &table);
+  const void *tail = vec(&c, a[16], 1, t_bf16, 3, T, H, 512, NULL);
+  const float *tail_lse = vec(&c, a[17], 1, t_f32, 2, T, H, -1, NULL);
+  void *out = vec(&c, a[18], 0, t_bf16, 3, T, H, 512, NULL);
+  float *lse = vec(&c, a[19], 0, t_f32, 2, T, H, -1, NULL);
+  dsa_stream_t stream = stream_of(&c, a[20]);
+  DSA_CALL(rc, f(plan, ws, (size_t)ws_bytes, q, st, sh, &d, slots, ls, lengths, starts, window, sink, pos, cs, table,
+                 style, scale, tail, tail_lse, out, lse, stream));
+  return PyLong_FromLong(rc);
+}
+
 /* setup(uint8, int32, int64, bfloat16, float16, float32, current device, raw stream) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   PyObject **to[8] = {&t_u8, &t_i32, &t_i64, &t_bf16, &t_f16, &t_f32, &f_device, &f_stream};
@@ -312,6 +378,7 @@ static PyMethodDef methods[] = {
     {"cache_write", (PyCFunction)(void (*)(void))cache_write, METH_FASTCALL, NULL},
     {"cache_read", (PyCFunction)(void (*)(void))cache_read, METH_FASTCALL, NULL},
     {"prefix_run", (PyCFunction)(void (*)(void))prefix_run, METH_FASTCALL, NULL},
+    {"chunk_run", (PyCFunction)(void (*)(void))chunk_run, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
