@@ -598,6 +598,62 @@ dsa_status dsa_chunk_run(const dsa_chunk_plan_t *plan, void *workspace, size_t w
                          const void *tail_out, const float *tail_lse, void *out, float *lse,
                          dsa_stream_t stream);
 
+/* Prepare a step's queries and keys (the pages take both as given, but for
+ * the rotation of the queries inside the decode; no counterpart of this call):
+ * every query head normed and rotated into bf16 rows, and every token's key
+ * likewise into its record of the cache, in one launch.
+ *   q: row_type DSA_TYPE_*, element (t, h, d) at q + t*q_stride_t + h*q_stride_h
+ *     + d; dims 512, or 576 (V3.2). q_weight != NULL: dims 0..511 of each head
+ *     become x * w / sqrt(mean(x^2) + eps), w fp32 [512] at q_weight +
+ *     h*q_weight_stride_h (0: one for all heads), rows of any finite magnitude;
+ *     NULL: no norm.
+ *   cos_sin != NULL (with positions int64 [T]): the last 64 dims are rotated
+ *     as in dsa_cache_write. Queries so prepared go to the attention calls
+ *     without a table.
+ *   out: bf16, strides of its own; may be q when row_type is bf16 and the
+ *     strides are the same, must not overlap it otherwise. Computed in fp32,
+ *     rounded once.
+ *   keys != NULL (with cache and slots): row t of keys (row_type, key_stride)
+ *     becomes the record of slots[t], as dsa_cache_write(cache, slots, keys,
+ *     key_weight, eps, positions, cos_sin, ...) writes it, with its rules;
+ *     keys, key_weight, cache, slots all NULL: queries alone. dims = 576 goes
+ *     with V32_656 caches and only with them.
+ * Strides and pointers 16-byte aligned, weights too. A token whose position lies
+ * outside the table is not written, neither its queries nor its key, and sets
+ * *device_status (optional, int32 device word, set to 0 by the caller) to
+ * DSA_ERR_INVALID_ARG. Asynchronous, one launch, no workspace. */
+dsa_status dsa_qk_norm(int32_t num_tokens, int32_t num_heads, int32_t dims, int32_t row_type,
+                       const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                       const float *q_weight, int64_t q_weight_stride_h, void *out,
+                       int64_t out_stride_t, int64_t out_stride_h, const void *keys,
+                       int64_t key_stride, const float *key_weight, const dsa_cache_desc *cache,
+                       const int32_t *slots, float eps, const int64_t *positions,
+                       const float *cos_sin, int64_t cos_sin_rows, int32_t rope_style,
+                       int32_t *device_status, dsa_stream_t stream);
+
+/* Cut lists to a budget of records by their scores (no counterpart on the
+ * pages; dsa_weights_run gives the scores). List b is slots[b * slots_stride +
+ * 0 .. n - 1], n = clamp(lengths[b], 0, width), with scores alike.
+ *   n <= budget: all of it stays. Else budget entries do: the first
+ *   min(keep_first, budget), the last min(keep_last, what is left), and of the
+ *   entries between those the ones with the largest scores; of equal scores the
+ *   first; a NaN ranks below all numbers, -0 as 0.
+ *   kept_slots, kept_scores: the entries that stay, in their order, rows of
+ *     strides >= min(budget, width); kept_lengths[b] of them. freed (or NULL,
+ *     with freed_counts): the other entries' slots in their order, freed_counts[b]
+ *     of them, stride >= width - min(budget, width). What lies behind is left
+ *     as it was.
+ * budget >= 1, keep_first, keep_last >= 0. Outputs must not overlap the inputs.
+ * Records are not moved: the caller gives the freed slots back to its allocator.
+ * Asynchronous, one launch, no workspace; the result does not depend on
+ * timing. */
+dsa_status dsa_evict(int32_t num_seqs, int32_t width, const int32_t *slots, int64_t slots_stride,
+                     const int32_t *lengths, const float *scores, int64_t scores_stride,
+                     int32_t budget, int32_t keep_first, int32_t keep_last, int32_t *kept_slots,
+                     int64_t kept_slots_stride, float *kept_scores, int64_t kept_scores_stride,
+                     int32_t *kept_lengths, int32_t *freed, int64_t freed_stride,
+                     int32_t *freed_counts, dsa_stream_t stream);
+
 /* Static description of a status code (no counterpart on the pages). */
 const char *dsa_decode_status_string(dsa_status s);
 

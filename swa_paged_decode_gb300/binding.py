@@ -34,6 +34,7 @@ EXPORTED = ("dsa_decode_plan", "dsa_decode_plan_qk", "dsa_decode_run", "dsa_deco
 EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
 EXPORTED_PREFIX = ("dsa_prefix_plan", "dsa_prefix_run")
 EXPORTED_CHUNK = ("dsa_chunk_plan", "dsa_chunk_run")
+EXPORTED_STEP = ("dsa_qk_norm", "dsa_evict")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
 _current_device = torch._C._cuda_getDevice
@@ -216,6 +217,11 @@ def _load_path(path: str):
     lib.dsa_chunk_run.argtypes = [ctypes.POINTER(ChunkPlan), vp, ctypes.c_size_t, vp, i64, i64,
                                   ctypes.POINTER(CacheDesc), vp, i64, vp, vp, i32, vp, vp, vp, i64, i32,
                                   ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.dsa_qk_norm.restype = ctypes.c_int
+    lib.dsa_qk_norm.argtypes = [i32, i32, i32, i32, vp, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp,
+                                ctypes.POINTER(CacheDesc), vp, ctypes.c_float, vp, vp, i64, i32, vp, vp]
+    lib.dsa_evict.restype = ctypes.c_int
+    lib.dsa_evict.argtypes = [i32, i32, vp, i64, vp, vp, i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, i64, vp, vp]
     lib.dsa_decode_status_string.restype = ctypes.c_char_p
     lib.dsa_decode_status_string.argtypes = [ctypes.c_int]
     lib.dsa_decode_abi_version.restype = ctypes.c_int32
@@ -510,6 +516,35 @@ class ChunkAttention:
         dsa_chunk_run(self.plan, self.workspace, q, cache, slots, lengths, starts, window, sink, positions,
                       cos_sin, rope_style, scale, tail_out, tail_lse, self.out, self.lse, stream)
         return self.out, self.lse
+
+
+def dsa_qk_norm(q: torch.Tensor, out: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                keys: Optional[torch.Tensor] = None, key_weight: Optional[torch.Tensor] = None,
+                cache: Optional[W.PagedCache] = None, slots: Optional[torch.Tensor] = None,
+                eps: float = 0.0, positions: Optional[torch.Tensor] = None,
+                cos_sin: Optional[torch.Tensor] = None, rope_style: int = DSA_ROPE_NEOX,
+                device_status: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> int:
+    """Queries [T, H, 512] (576 for V3.2; bf16, f16 or fp32, any token and head
+    strides) normed per head (weight fp32 [512], or [H, 512]) and rotated into
+    ``out`` bf16 (which may be ``q``), and with ``cache`` the tokens' keys [T,
+    512] of the same type into the records of ``slots`` [T] int32, as
+    ``dsa_cache_write`` does."""
+    data, page, fmt = (None, 0, 0) if cache is None else (cache.data, cache.page_size, cache.fmt)
+    return _marshalled("dsa_qk_norm", check, q, out, q_weight, keys, key_weight, data, page, fmt, slots, eps,
+                       positions, cos_sin, rope_style, device_status, None if stream is None else _stream(stream))
+
+
+def dsa_evict(slots: torch.Tensor, lengths: torch.Tensor, scores: torch.Tensor, budget: int,
+              kept_slots: torch.Tensor, kept_scores: torch.Tensor, kept_lengths: torch.Tensor,
+              freed: Optional[torch.Tensor] = None, freed_counts: Optional[torch.Tensor] = None,
+              keep_first: int = 0, keep_last: int = 0, stream=None, check: bool = True) -> int:
+    """Lists ``slots`` [B, width] int32 of ``lengths`` [B] entries cut to
+    ``budget`` each: the first ``keep_first``, the last ``keep_last`` and of the
+    rest those with the largest ``scores`` [B, width] fp32, in order, into
+    ``kept_slots`` and ``kept_scores`` [B, >= budget]; the others' slots into
+    ``freed`` [B, >= width - budget]."""
+    return _marshalled("dsa_evict", check, slots, lengths, scores, budget, keep_first, keep_last, kept_slots,
+                       kept_scores, kept_lengths, freed, freed_counts, None if stream is None else _stream(stream))
 
 
 class Decoder:

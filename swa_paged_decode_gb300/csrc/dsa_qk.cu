@@ -1,0 +1,376 @@
+// dsa_qk.cu -- what stands between a layer's projections and its attention
+// (dsa_qk_norm): every query head and every token's key normed over their first
+// 512 dims,
+//
+//   y = x w / sqrt(mean x^2 + eps),
+//
+// and their last 64 dims rotated; queries leave as bf16 rows, keys as records of
+// the cache (the arithmetic of dsa_cache_write, whose rows these are).
+//
+// One pass over memory, a warp per row: of a query row lane l < 28 holds dims
+// 16 l .. 16 l + 15 and lane 28 + j the dims 448 + 8 j .. and 480 + 8 j .., so
+// that both pairings of the rotation find their partner in the same lane
+// without an exchange. The next row is on its way while one is worked on. The
+// first blocks take the keys, which cost about two query rows each.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "dsa_host.cuh"
+#include "dsa_rows.cuh"
+
+namespace dsa {
+
+struct QkParams {
+  CacheParams k;             // the keys (k.n = 0: none); eps, positions, table and status are the queries' too
+  int32_t key_blocks;
+  const void *q;
+  int64_t q_st, q_sh;        // elements
+  __nv_bfloat16 *out;
+  int64_t o_st, o_sh;
+  const float *w;            // [512], or one per head; null: no norm
+  int64_t w_sh;              // elements between heads' weights, 0: shared
+  int32_t T, H;
+};
+
+// 8 values, 16 or 32 bytes.
+template <int TY>
+struct Chunk {
+  uint4 q[TY == DSA_TYPE_F32 ? 2 : 1];
+};
+template <int TY>
+__device__ __forceinline__ void unpack_chunk(const Chunk<TY> &c, F2 (&v)[8], int at) {
+#pragma unroll
+  for (int i = 0; i < (TY == DSA_TYPE_F32 ? 2 : 1); ++i) {
+    const uint32_t w[4] = {c.q[i].x, c.q[i].y, c.q[i].z, c.q[i].w};
+    if constexpr (TY == DSA_TYPE_F32) {
+      v[at + 2 * i] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      v[at + 2 * i + 1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[at + k] = unpack2<TY>(w[k]);
+    }
+  }
+}
+template <int TY>
+__device__ __forceinline__ float one_value(const void *p) {
+  if constexpr (TY == DSA_TYPE_F32) return __ldg(static_cast<const float *>(p));
+  else if constexpr (TY == DSA_TYPE_F16) return __half2float(__ldg(static_cast<const __half *>(p)));
+  else return __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(p)));
+}
+// A query row as loaded: chunk a and chunk b of the lane, and of a 576-dim row
+// the lane's pair of the last 64 dims.
+template <int TY>
+struct QueryRaw {
+  Chunk<TY> a, b;
+  float t0, t1;
+};
+
+// r with r ~ 1 / sqrt(mean of the row's 512 squares + eps), and v scaled
+// alongside where the squares leave fp32 no room (as norm_row: the quotient is the
+// same). The outputs are bf16, so the plain fp32 sum (2^-21 of it at most) only
+// counts next to a tie.
+__device__ __forceinline__ float norm_factor(F2 (&v)[8], float eps) {
+  float me;
+#pragma unroll 1
+  for (bool again = false;; again = true) {   // (the lanes agree)
+    F2 sq[2] = {f2_mul(v[0], v[0]), f2_mul(v[1], v[1])};
+#pragma unroll
+    for (int k = 2; k < 8; ++k) sq[k & 1] = f2_fma(v[k], v[k], sq[k & 1]);
+    float s0, s1;
+    f2_get(f2_add(sq[0], sq[1]), s0, s1);
+    float ss = s0 + s1;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    me = fmaf(ss, 1.0f / kD, eps);
+    if (again || (me >= 8.673617379884035e-19f && ss <= 1.2676506002282294e30f)) break;
+    uint32_t m = 0;                                // largest magnitude, as bits
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float a, b;
+      f2_get(v[k], a, b);
+      m = max(m, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m >= 0x7F800000u) break;                   // an infinity or a NaN: as it is
+    int e = max((int)(m >> 23) - 127, -126);
+    if (eps > 0.f) e = max(e, ((int)(__float_as_uint(eps) >> 23) - 126) >> 1);
+    const float d = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+    eps = (eps * d) * d;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = f2_mul(v[k], f2(d, d));
+  }
+  return rsqrtf(me);
+}
+
+template <int TY, bool kV32, bool kRope>
+__device__ __forceinline__ void query_rows(const QkParams &p, int64_t block, int64_t blocks) {
+  const int lane = threadIdx.x & 31;
+  const bool rl = lane >= 28;
+  const int da = rl ? 448 + 8 * (lane - 28) : 16 * lane, db = rl ? da + 32 : da + 8;   // first dims of the lane's chunks
+  const bool gptj = p.k.gptj;
+  // a 576-dim row's pair of dims 512 ..
+  const int ta = kD + (gptj ? 2 * lane : lane), tb = kD + (gptj ? 2 * lane + 1 : lane + 32);
+  const int64_t step = blocks * kCacheWarps, first = block * kCacheWarps + (threadIdx.x >> 5), rows = (int64_t)p.T * p.H;
+  const uint32_t dt = (uint32_t)(step / p.H), dh = (uint32_t)(step % p.H);
+  uint32_t t = (uint32_t)(first / p.H), h = (uint32_t)(first % p.H);
+  const char *src = static_cast<const char *>(p.q);
+  const bool wide_in = (((uintptr_t)src | (uintptr_t)(p.q_st * kTypeBytes<TY>) | (uintptr_t)(p.q_sh * kTypeBytes<TY>)) & 31u) == 0;
+  const bool wide_out = (((uintptr_t)p.out | (uintptr_t)(p.o_st * 2) | (uintptr_t)(p.o_sh * 2)) & 31u) == 0;
+  F2 w[8];
+  auto weights = [&](const float *from) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float4 *w4 = reinterpret_cast<const float4 *>(from + (c ? db : da));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 x = __ldg(w4 + k);
+        w[4 * c + 2 * k] = f2(x.x, x.y);
+        w[4 * c + 2 * k + 1] = f2(x.z, x.w);
+      }
+    }
+  };
+  if (p.w && p.w_sh == 0) weights(p.w);
+  QueryRaw<TY> next;
+  auto fetch = [&](uint32_t ft, uint32_t fh) {
+    const char *row = src + ((int64_t)ft * p.q_st + (int64_t)fh * p.q_sh) * kTypeBytes<TY>;
+    const char *pa = row + da * kTypeBytes<TY>, *pb = row + db * kTypeBytes<TY>;
+    if constexpr (TY == DSA_TYPE_F32) {
+      if (wide_in) {
+        tc::ldg_nc_v8(pa, next.a.q[0], next.a.q[1]);
+        tc::ldg_nc_v8(pb, next.b.q[0], next.b.q[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          next.a.q[k] = ld_row(pa + 16 * k);
+          next.b.q[k] = ld_row(pb + 16 * k);
+        }
+      }
+    } else if (wide_in && !rl) {
+      tc::ldg_nc_v8(pa, next.a.q[0], next.b.q[0]);
+    } else {
+      next.a.q[0] = ld_row(pa);
+      next.b.q[0] = ld_row(pb);
+    }
+    if constexpr (kV32) {
+      next.t0 = one_value<TY>(row + ta * kTypeBytes<TY>);
+      next.t1 = one_value<TY>(row + tb * kTypeBytes<TY>);
+    }
+  };
+  if (first < rows) fetch(t, h);
+#pragma unroll 1
+  for (int64_t i = first; i < rows; i += step) {   // whole warps
+    const QueryRaw<TY> raw = next;
+    const uint32_t ct = t, ch = h;
+    t += dt;
+    h += dh;
+    if (h >= (uint32_t)p.H) {
+      h -= p.H;
+      ++t;
+    }
+    if (i + step < rows) fetch(t, h);
+    float4 cs[4];
+    float co = 0.f, si = 0.f;
+    if constexpr (kRope) {
+      const int64_t pos = __ldg(p.k.positions + ct);
+      if (pos < 0 || pos >= p.k.cs_rows) {   // outside the table: the token is not written
+        if (p.k.status && lane == 0) report_status(p.k.status, DSA_ERR_INVALID_ARG);
+        continue;
+      }
+      const float *row = p.k.cos_sin + pos * 64;
+      if constexpr (kV32) {
+        co = __ldg(row + lane);
+        si = __ldg(row + 32 + lane);
+      } else if (rl) {
+        const float4 *r4 = reinterpret_cast<const float4 *>(row);
+        const int j = lane - 28, f0 = gptj ? j : 2 * j, f1 = gptj ? j + 4 : 2 * j + 1;
+        cs[0] = __ldg(r4 + f0);
+        cs[1] = __ldg(r4 + f1);
+        cs[2] = __ldg(r4 + 8 + f0);
+        cs[3] = __ldg(r4 + 8 + f1);
+      }
+    }
+    F2 v[8];
+    unpack_chunk<TY>(raw.a, v, 0);
+    unpack_chunk<TY>(raw.b, v, 4);
+    if (p.w) {
+      if (p.w_sh != 0) weights(p.w + (int64_t)ch * p.w_sh);
+      const float r = norm_factor(v, p.k.eps);
+      const F2 r2 = f2(r, r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = f2_mul(f2_mul(v[k], r2), w[k]);
+    }
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f2_get(v[k], x[2 * k], x[2 * k + 1]);
+    float t0 = raw.t0, t1 = raw.t1;
+    if constexpr (kRope) {
+      if constexpr (kV32) {
+        const float a = t0, b = t1;
+        t0 = fmaf(a, co, -(b * si));
+        t1 = fmaf(b, co, a * si);
+      } else if (rl) {
+        const float c8[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
+        const float s8[8] = {cs[2].x, cs[2].y, cs[2].z, cs[2].w, cs[3].x, cs[3].y, cs[3].z, cs[3].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {   // pairs (2k, 2k + 1) of the lane's values, or (k, 8 + k)
+          const float a = gptj ? x[2 * k] : x[k], b = gptj ? x[2 * k + 1] : x[8 + k];
+          const float ra = fmaf(a, c8[k], -(b * s8[k])), rb = fmaf(b, c8[k], a * s8[k]);
+          v[k] = f2(ra, rb);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float a, b;
+          f2_get(v[k], a, b);
+          if (gptj) {
+            x[2 * k] = a;
+            x[2 * k + 1] = b;
+          } else {
+            x[k] = a;
+            x[8 + k] = b;
+          }
+        }
+      }
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = bf16x2_bits(x[2 * k], x[2 * k + 1]);
+    __nv_bfloat16 *dst = p.out + (int64_t)ct * p.o_st + (int64_t)ch * p.o_sh;
+    const uint4 oa = make_uint4(o[0], o[1], o[2], o[3]), ob = make_uint4(o[4], o[5], o[6], o[7]);
+    if (wide_out && !rl) {
+      tc::stg_v8(dst + da, oa, ob);
+    } else {
+      *reinterpret_cast<uint4 *>(dst + da) = oa;
+      *reinterpret_cast<uint4 *>(dst + db) = ob;
+    }
+    if constexpr (kV32) {
+      if (gptj) {
+        *reinterpret_cast<uint32_t *>(dst + ta) = bf16x2_bits(t0, t1);
+      } else {
+        dst[ta] = __float2bfloat16_rn(t0);
+        dst[tb] = __float2bfloat16_rn(t1);
+      }
+    }
+  }
+}
+
+template <int FMT, int TY, bool kRope>
+__global__ void __launch_bounds__(32 * kCacheWarps, 5) qk_norm_kernel(const __grid_constant__ QkParams p) {
+  if ((int32_t)blockIdx.x < p.key_blocks) write_rows<FMT, TY, kRope>(p.k, blockIdx.x, p.key_blocks);
+  else query_rows<TY, FMT == DSA_REC_V32_656, kRope>(p, blockIdx.x - p.key_blocks, gridDim.x - p.key_blocks);
+}
+
+}  // namespace dsa
+
+namespace {
+
+using dsa::aligned;
+using dsa::QkParams;
+
+template <int FMT>
+cudaError_t launch(QkParams &p, int32_t type, cudaStream_t st) {
+  using namespace dsa;
+  // A warp per row while all blocks are resident; past that the resident ones,
+  // divided as the work is, a key counting as two query rows.
+  const int64_t kb = (p.k.n + kCacheWarps - 1) / kCacheWarps, qb = ((int64_t)p.T * p.H + kCacheWarps - 1) / kCacheWarps;
+  int64_t keys = kb, blocks = kb + qb;
+  if (blocks > kCacheBlocks) {
+    blocks = kCacheBlocks;
+    keys = kb == 0 ? 0 : std::min<int64_t>(kb, std::max<int64_t>(1, kCacheBlocks * 2 * kb / (2 * kb + qb)));
+  }
+  p.key_blocks = (int32_t)keys;
+  const unsigned grid = (unsigned)blocks;
+  constexpr int kT = 32 * kCacheWarps;
+#define DSA_QK_CASE(TY)                                                      \
+  case TY:                                                                   \
+    if (p.k.cos_sin) qk_norm_kernel<FMT, TY, true><<<grid, kT, 0, st>>>(p);  \
+    else qk_norm_kernel<FMT, TY, false><<<grid, kT, 0, st>>>(p);             \
+    break;
+  switch (type) {
+    DSA_QK_CASE(DSA_TYPE_BF16)
+    DSA_QK_CASE(DSA_TYPE_F16)
+    DSA_QK_CASE(DSA_TYPE_F32)
+  }
+#undef DSA_QK_CASE
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status dsa_qk_norm(int32_t num_tokens, int32_t num_heads, int32_t dims, int32_t row_type, const void *q,
+                       int64_t q_stride_t, int64_t q_stride_h, const float *q_weight, int64_t q_weight_stride_h,
+                       void *out, int64_t out_stride_t, int64_t out_stride_h, const void *keys, int64_t key_stride,
+                       const float *key_weight, const dsa_cache_desc *cache, const int32_t *slots, float eps,
+                       const int64_t *positions, const float *cos_sin, int64_t cos_sin_rows, int32_t rope_style,
+                       int32_t *device_status, dsa_stream_t stream) {
+  dsa::NvtxRange range("dsa_qk_norm");
+  if (num_tokens < 0 || num_heads < 1 || (dims != 512 && dims != 576)) return DSA_ERR_INVALID_ARG;
+  if (row_type != DSA_TYPE_BF16 && row_type != DSA_TYPE_F16 && row_type != DSA_TYPE_F32) return DSA_ERR_UNSUPPORTED;
+  if (rope_style != DSA_ROPE_NEOX && rope_style != DSA_ROPE_GPTJ) return DSA_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return DSA_ERR_INVALID_ARG;
+  if ((int64_t)num_tokens * num_heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  QkParams p;
+  std::memset(static_cast<void *>(&p), 0, sizeof(p));
+  int32_t fmt = dims == 576 ? DSA_REC_V32_656 : DSA_REC_FP8_528;
+  if (keys || cache || slots || key_weight) {
+    const dsa_status s = dsa::fill_cache(cache, p.k.L);
+    if (s != DSA_OK) return s;
+    fmt = cache->format;
+    if ((fmt == DSA_REC_V32_656) != (dims == 576)) return DSA_ERR_UNSUPPORTED;
+    if (num_tokens > 0 && (!keys || !slots)) return DSA_ERR_INVALID_ARG;
+    p.k.n = num_tokens;
+  }
+  if (num_tokens == 0) return DSA_OK;
+  if (!q || !out) return DSA_ERR_INVALID_ARG;
+  if ((positions == nullptr) != (cos_sin == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (cos_sin && cos_sin_rows < 1) return DSA_ERR_INVALID_ARG;
+  const int64_t H = num_heads;
+  if (q_stride_h < dims || q_stride_t < (H - 1) * q_stride_h + dims || out_stride_h < dims ||
+      out_stride_t < (H - 1) * out_stride_h + dims || (p.k.n && key_stride < dims) ||
+      (q_weight && q_weight_stride_h != 0 && q_weight_stride_h < 512))
+    return DSA_ERR_INVALID_ARG;
+  const int64_t per = row_type == DSA_TYPE_F32 ? 4 : 8;   // elements in 16 bytes
+  if (!aligned(q, 16) || q_stride_t % per != 0 || q_stride_h % per != 0 || !aligned(out, 16) || out_stride_t % 8 != 0 ||
+      out_stride_h % 8 != 0 || (q_weight && (!aligned(q_weight, 16) || q_weight_stride_h % 4 != 0)) ||
+      (p.k.n && (!aligned(keys, 16) || key_stride % per != 0 || !aligned(slots, 4))) ||
+      (key_weight && !aligned(key_weight, 16)) || (cos_sin && (!aligned(cos_sin, 16) || !aligned(positions, 8))) ||
+      (device_status && !aligned(device_status, 4)))
+    return DSA_ERR_ALIGNMENT;
+  // In place only row for row: the queries' own type and strides.
+  if (out == q && (row_type != DSA_TYPE_BF16 || out_stride_t != q_stride_t || out_stride_h != q_stride_h))
+    return DSA_ERR_INVALID_ARG;
+  p.k.L.ids = slots;
+  p.k.src = keys;
+  p.k.stride = key_stride;
+  p.k.norm_w = key_weight;
+  p.k.eps = eps;
+  p.k.positions = positions;
+  p.k.cos_sin = cos_sin;
+  p.k.cs_rows = cos_sin_rows;
+  p.k.gptj = rope_style == DSA_ROPE_GPTJ ? 1 : 0;
+  p.k.status = device_status;
+  p.q = q;
+  p.q_st = q_stride_t;
+  p.q_sh = q_stride_h;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.o_st = out_stride_t;
+  p.o_sh = out_stride_h;
+  p.w = q_weight;
+  p.w_sh = q_weight_stride_h;
+  p.T = num_tokens;
+  p.H = num_heads;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (fmt) {
+    case DSA_REC_FP8_528: e = launch<DSA_REC_FP8_528>(p, row_type, st); break;
+    case DSA_REC_NVFP4_288: e = launch<DSA_REC_NVFP4_288>(p, row_type, st); break;
+    case DSA_REC_FP8_528_UE8M0: e = launch<DSA_REC_FP8_528_UE8M0>(p, row_type, st); break;
+    case DSA_REC_MODEL1_584: e = launch<DSA_REC_MODEL1_584>(p, row_type, st); break;
+    case DSA_REC_V32_656: e = launch<DSA_REC_V32_656>(p, row_type, st); break;
+  }
+  return dsa::cuda_status(e);
+}
+
+}  // extern "C"

@@ -220,6 +220,14 @@ typedef dsa_status (*chunk_fn)(const dsa_chunk_plan_t *, void *, size_t, const v
                                int32_t, const float *, const int64_t *, const float *, int64_t, int32_t, float,
                                const void *, const float *, void *, float *, dsa_stream_t);
 
+typedef dsa_status (*qk_fn)(int32_t, int32_t, int32_t, int32_t, const void *, int64_t, int64_t, const float *, int64_t,
+                            void *, int64_t, int64_t, const void *, int64_t, const float *, const dsa_cache_desc *,
+                            const int32_t *, float, const int64_t *, const float *, int64_t, int32_t, int32_t *,
+                            dsa_stream_t);
+typedef dsa_status (*evict_fn)(int32_t, int32_t, const int32_t *, int64_t, const int32_t *, const float *, int64_t,
+                               int32_t, int32_t, int32_t, int32_t *, int64_t, float *, int64_t, int32_t *, int32_t *,
+                               int64_t, int32_t *, dsa_stream_t);
+
 /* (address, data, page_size, fmt, slots, rows, norm_weight, norm_eps,
  *  positions, cos_sin, rope_style, device_status, stream) */
 static PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t na) {
@@ -301,11 +309,17 @@ static PyObject *prefix_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   return PyLong_FromLong(rc);
 }
 
+/* read_tensor, None being no tensor. */
+static int given(call *c, PyObject *o, tensor *t) {
+  if (o == Py_None) c->bad = 1;
+  return read_tensor(c, o, t);
+}
+
 /* Queries [T, H, D] of a dtype, any token and head strides. */
 static void *queries(call *c, PyObject *o, PyObject *dtype, long long T, long long H, long long D, long long *st,
                      long long *sh) {
   tensor t;
-  if (!read_tensor(c, o, &t)) return NULL;
+  if (!given(c, o, &t)) return NULL;
   if ((dtype && t.dtype != dtype) || t.nd != 3 || t.shape[0] != T || t.shape[1] != H || t.shape[2] != D ||
       (T > 0 && t.stride[2] != 1)) {
     c->bad = 1;
@@ -316,16 +330,21 @@ static void *queries(call *c, PyObject *o, PyObject *dtype, long long T, long lo
   return t.ptr;
 }
 
-/* Lists [B, width] of a dtype, any list stride. */
-static void *lists(call *c, PyObject *o, PyObject *dtype, long long B, long long width, long long *stride) {
+/* Lists [B, width] of a dtype (`exact`: else of width or more), any list
+ * stride. */
+static void *lists_of(call *c, PyObject *o, PyObject *dtype, long long B, long long width, int exact, long long *stride) {
   tensor t;
-  if (!read_tensor(c, o, &t)) return NULL;
-  if (t.dtype != dtype || t.nd != 2 || t.shape[0] != B || t.shape[1] != width || (B > 0 && width > 1 && t.stride[1] != 1)) {
+  if (!given(c, o, &t)) return NULL;
+  if (t.dtype != dtype || t.nd != 2 || t.shape[0] != B || (exact ? t.shape[1] != width : t.shape[1] < width) ||
+      (B > 0 && t.shape[1] > 1 && t.stride[1] != 1)) {
     c->bad = 1;
     return NULL;
   }
-  *stride = B > 1 ? t.stride[0] : width;
+  *stride = B > 1 ? t.stride[0] : t.shape[1];
   return t.ptr;
+}
+static void *lists(call *c, PyObject *o, PyObject *dtype, long long B, long long width, long long *stride) {
+  return lists_of(c, o, dtype, B, width, 1, stride);
 }
 
 /* (address, plan address, workspace, q, data, page_size, fmt, slots, lengths,
@@ -362,6 +381,99 @@ static PyObject *chunk_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   return PyLong_FromLong(rc);
 }
 
+/* (address, q, out, q_weight, keys, key_weight, data, page_size, fmt, slots,
+ *  eps, positions, cos_sin, rope_style, device_status, stream); data None: no
+ *  keys */
+static PyObject *qk_norm(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  call c = {-1, 0, 0};
+  dsa_cache_desc d = {0};
+  tensor q, w;
+  long long st = 0, sh = 0, ot = 0, oh = 0, wh = 0, ks = 0, table = 0, T = 0, H = 0, D = 0;
+  int32_t type = -1, ktype = -1;
+  dsa_status rc;
+  if (want_args(na, 16)) return NULL;
+  qk_fn f = (qk_fn)PyLong_AsVoidPtr(a[0]);
+  const float eps = (float)PyFloat_AsDouble(a[10]);
+  const int32_t style = as_i32(&c, a[13]);
+  if (PyErr_Occurred()) return NULL;
+  const int with_keys = a[6] != Py_None;
+  void *out = NULL, *k = NULL;
+  const float *qw = NULL, *kw = NULL;
+  const int32_t *slots = NULL;
+  if (given(&c, a[1], &q)) {
+    type = q.dtype == t_bf16 ? DSA_TYPE_BF16 : q.dtype == t_f16 ? DSA_TYPE_F16 : q.dtype == t_f32 ? DSA_TYPE_F32 : -1;
+    if (type < 0 || q.nd != 3 || q.shape[0] > INT32_MAX || q.shape[1] > INT32_MAX || (q.shape[2] != 512 && q.shape[2] != 576) ||
+        (q.shape[0] > 0 && q.stride[2] != 1)) {
+      c.bad = 1;
+    } else {
+      T = q.shape[0];
+      H = q.shape[1];
+      D = q.shape[2];
+      sh = H > 1 ? q.stride[1] : D;
+      st = T > 1 ? q.stride[0] : H * sh;
+    }
+  }
+  if (!c.bad && !c.err) out = queries(&c, a[2], t_bf16, T, H, D, &ot, &oh);
+  if (a[3] != Py_None && read_tensor(&c, a[3], &w)) { /* [512], or [H, 512] */
+    if (w.dtype != t_f32 || w.nd < 1 || w.nd > 2 || w.shape[w.nd - 1] != 512 || w.stride[w.nd - 1] != 1 ||
+        (w.nd == 2 && w.shape[0] != H)) {
+      c.bad = 1;
+    } else {
+      qw = w.ptr;
+      wh = w.nd == 2 ? (H > 1 ? w.stride[0] : 512) : 0;
+    }
+  }
+  if (with_keys) {
+    cache(&c, a[6], a[7], a[8], &d);
+    slots = vec(&c, a[9], 0, t_i32, 1, T, -1, -1, NULL);
+    if (a[4] == Py_None) c.bad = 1;
+    k = rows(&c, a[4], T, &d, &ks, &ktype);
+    kw = vec(&c, a[5], 1, t_f32, 1, 512, -1, -1, NULL);
+    if (!c.bad && (ktype != type || (d.format == DSA_REC_V32_656) != (D == 576))) c.bad = 1;
+  } else if (a[4] != Py_None || a[5] != Py_None || a[9] != Py_None) {
+    c.bad = 1;
+  }
+  const int64_t *pos = vec(&c, a[11], 1, t_i64, 1, T, -1, -1, NULL);
+  const float *cs = vec(&c, a[12], 1, t_f32, 2, -1, 64, -1, &table);
+  int32_t *status = vec(&c, a[14], 1, t_i32, 1, 1, -1, -1, NULL);
+  dsa_stream_t stream = stream_of(&c, a[15]);
+  DSA_CALL(rc, f((int32_t)T, (int32_t)H, (int32_t)D, type, q.ptr, st, sh, qw, wh, out, ot, oh, k, ks, kw,
+                 with_keys ? &d : NULL, slots, eps, pos, cs, table, style, status, stream));
+  return PyLong_FromLong(rc);
+}
+
+/* (address, slots, lengths, scores, budget, keep_first, keep_last, kept_slots,
+ *  kept_scores, kept_lengths, freed, freed_counts, stream) */
+static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  call c = {-1, 0, 0};
+  tensor t;
+  long long B = 0, width = 0, s1 = 0, s2 = 0, s3 = 0, s4 = 0, s5 = 0;
+  dsa_status rc;
+  if (want_args(na, 13)) return NULL;
+  evict_fn f = (evict_fn)PyLong_AsVoidPtr(a[0]);
+  const int32_t budget = as_i32(&c, a[4]), first = as_i32(&c, a[5]), last = as_i32(&c, a[6]);
+  if (PyErr_Occurred()) return NULL;
+  if (given(&c, a[1], &t)) {
+    if (t.nd != 2 || t.shape[0] > INT32_MAX || t.shape[1] > INT32_MAX) c.bad = 1;
+    else B = t.shape[0], width = t.shape[1];
+  }
+  const long long most = budget < width ? budget : width;
+  const int32_t *slots = lists(&c, a[1], t_i32, B, width, &s1);
+  const int32_t *lengths = vec(&c, a[2], 0, t_i32, 1, B, -1, -1, NULL);
+  const float *scores = lists(&c, a[3], t_f32, B, width, &s2);
+  int32_t *kept = lists_of(&c, a[7], t_i32, B, most, 0, &s3);
+  float *kept_scores = lists_of(&c, a[8], t_f32, B, most, 0, &s4);
+  int32_t *kept_lengths = vec(&c, a[9], 0, t_i32, 1, B, -1, -1, NULL), *freed = NULL, *counts = NULL;
+  if (a[10] != Py_None || a[11] != Py_None) {
+    freed = lists_of(&c, a[10], t_i32, B, width - most, 0, &s5);
+    counts = vec(&c, a[11], 0, t_i32, 1, B, -1, -1, NULL);
+  }
+  dsa_stream_t stream = stream_of(&c, a[12]);
+  DSA_CALL(rc, f((int32_t)B, (int32_t)width, slots, s1, lengths, scores, s2, budget, first, last, kept, s3, kept_scores,
+                 s4, kept_lengths, freed, s5, counts, stream));
+  return PyLong_FromLong(rc);
+}
+
 /* setup(uint8, int32, int64, bfloat16, float16, float32, current device, raw stream) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   PyObject **to[8] = {&t_u8, &t_i32, &t_i64, &t_bf16, &t_f16, &t_f32, &f_device, &f_stream};
@@ -379,6 +491,8 @@ static PyMethodDef methods[] = {
     {"cache_read", (PyCFunction)(void (*)(void))cache_read, METH_FASTCALL, NULL},
     {"prefix_run", (PyCFunction)(void (*)(void))prefix_run, METH_FASTCALL, NULL},
     {"chunk_run", (PyCFunction)(void (*)(void))chunk_run, METH_FASTCALL, NULL},
+    {"qk_norm", (PyCFunction)(void (*)(void))qk_norm, METH_FASTCALL, NULL},
+    {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
