@@ -631,6 +631,69 @@ dsa_status dsa_qk_norm(int32_t num_tokens, int32_t num_heads, int32_t dims, int3
                        const float *cos_sin, int64_t cos_sin_rows, int32_t rope_style,
                        int32_t *device_status, dsa_stream_t stream);
 
+/* Plan of dsa_weights_run. Plain data: copy it freely; callers must not edit
+ * the fields. */
+typedef struct {
+  int32_t magic;
+  int32_t abi_version;
+  int32_t num_tokens;      /* T                                              */
+  int32_t num_seqs;        /* B                                              */
+  int32_t num_heads;       /* H                                              */
+  int32_t width;           /* entries of every list                          */
+  int32_t d_qk;            /* 512, or 576 for V3.2 records                   */
+  int32_t num_sms;
+  int32_t pairs;           /* CTA pairs that run                             */
+  int32_t splits;          /* parts that the rows of 128 keys are cut into   */
+  int32_t tiles;           /* 128-row tiles kept of the queries              */
+  int32_t reserved0;
+  int64_t ws_item_offset;  /* workspace byte offsets                         */
+  int64_t ws_image_offset;
+  int64_t ws_row_offset;
+  int64_t ws_part_offset;
+  int64_t workspace_bytes;
+  int64_t wait_budget_cycles; /* as in dsa_decode_plan_t                     */
+  int64_t reserved[4];
+} dsa_weights_plan_t;
+
+/* Plan the attention weights of cached records (no counterpart on the pages);
+ * arguments as for dsa_chunk_plan (num_seqs up to 65535). The workspace holds
+ * the queries once more in 16 bits, not the keys. Host only; launches nothing. */
+dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_heads, int32_t width,
+                            int32_t num_sms, int32_t d_qk, dsa_weights_plan_t *plan,
+                            size_t *workspace_bytes);
+
+/* The attention weight that records receive from the new tokens, added to what
+ * they had (no counterpart on the pages): for entry j of list b, over the
+ * tokens t of sequence b that attend it (as dsa_chunk_run with the same lists,
+ * lengths, starts and window) and all heads h,
+ *   scores_out[b][j] = scores_in[b][j]
+ *                      + sum_{t,h} e^{s_j} / (e^{lse[t][h]} + e^{sink[h]}).
+ *   q: as for dsa_chunk_run, rotated already (dsa_qk_norm): there is no table
+ *     here. lse: fp32 [T, H], as the attention of these tokens left it; a row
+ *     whose lse is -inf has no weights. sink: fp32 [H] or NULL.
+ *   scores_in: fp32 rows of in_stride >= width, NULL for zeros; scores_out:
+ *     rows of out_stride >= width; the same array or one that does not overlap
+ *     it. Entries below the list's length are written (those that no token
+ *     attends, and unused slots, with scores_in), the ones behind are not, and
+ *     lists of sequences without tokens are written too.
+ *   starts that do not ascend within [0, T]: nothing is written, the status
+ *     word is DSA_ERR_INVALID_ARG.
+ * Single tokens behind dsa_decode_run: starts 0, 1, 2, ...; their own lists and
+ * lse. Precision: sums of fp32 weights, each good to a few 2^-22 relative
+ * (16-bit operands of the products are exact for queries whose elements lie
+ * within 2^-14 of their row's largest and for keys as dsa_decode.h's record
+ * formats say; fp32 block scales are applied in fp32). A record with a NaN or
+ * an infinity spoils its own score only. Reproducible bit for bit.
+ * Two launches, three when few keys meet many rows; allocates nothing, never
+ * synchronizes. workspace and status as for dsa_prefix_run. */
+dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size_t workspace_bytes,
+                           const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                           const dsa_cache_desc *cache, const int32_t *slots, int64_t slots_stride,
+                           const int32_t *lengths, const int32_t *starts, int32_t window,
+                           float scale, const float *sink, const float *lse,
+                           const float *scores_in, int64_t in_stride, float *scores_out,
+                           int64_t out_stride, dsa_stream_t stream);
+
 /* Cut lists to a budget of records by their scores (no counterpart on the
  * pages; dsa_weights_run gives the scores). List b is slots[b * slots_stride +
  * 0 .. n - 1], n = clamp(lengths[b], 0, width), with scores alike.

@@ -34,6 +34,7 @@ EXPORTED = ("dsa_decode_plan", "dsa_decode_plan_qk", "dsa_decode_run", "dsa_deco
 EXPORTED_CACHE = ("dsa_cache_write", "dsa_cache_read")
 EXPORTED_PREFIX = ("dsa_prefix_plan", "dsa_prefix_run")
 EXPORTED_CHUNK = ("dsa_chunk_plan", "dsa_chunk_run")
+EXPORTED_WEIGHTS = ("dsa_weights_plan", "dsa_weights_run")
 EXPORTED_STEP = ("dsa_qk_norm", "dsa_evict")
 DSA_ROPE_NEOX = 0
 DSA_ROPE_GPTJ = 1
@@ -84,6 +85,16 @@ class ChunkPlan(ctypes.Structure):
             "ws_info_offset", "ws_key_e_offset", "ws_image_offset", "ws_row_tile_offset",
             "ws_seq_tile_offset", "ws_begin_offset", "ws_tile_offset", "ws_part_lse_offset",
             "ws_part_o_offset", "workspace_bytes", "wait_budget_cycles")] + \
+        [("reserved", ctypes.c_int64 * 4)]
+
+
+class WeightsPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "magic", "abi_version", "num_tokens", "num_seqs", "num_heads", "width", "d_qk", "num_sms",
+        "pairs", "splits", "tiles", "reserved0")] + \
+        [(n, ctypes.c_int64) for n in (
+            "ws_item_offset", "ws_image_offset", "ws_row_offset", "ws_part_offset",
+            "workspace_bytes", "wait_budget_cycles")] + \
         [("reserved", ctypes.c_int64 * 4)]
 
 
@@ -217,6 +228,13 @@ def _load_path(path: str):
     lib.dsa_chunk_run.argtypes = [ctypes.POINTER(ChunkPlan), vp, ctypes.c_size_t, vp, i64, i64,
                                   ctypes.POINTER(CacheDesc), vp, i64, vp, vp, i32, vp, vp, vp, i64, i32,
                                   ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.dsa_weights_plan.restype = ctypes.c_int
+    lib.dsa_weights_plan.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(WeightsPlan),
+                                     ctypes.POINTER(ctypes.c_size_t)]
+    lib.dsa_weights_run.restype = ctypes.c_int
+    lib.dsa_weights_run.argtypes = [ctypes.POINTER(WeightsPlan), vp, ctypes.c_size_t, vp, i64, i64,
+                                    ctypes.POINTER(CacheDesc), vp, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64,
+                                    vp, i64, vp]
     lib.dsa_qk_norm.restype = ctypes.c_int
     lib.dsa_qk_norm.argtypes = [i32, i32, i32, i32, vp, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp,
                                 ctypes.POINTER(CacheDesc), vp, ctypes.c_float, vp, vp, i64, i32, vp, vp]
@@ -532,6 +550,47 @@ def dsa_qk_norm(q: torch.Tensor, out: torch.Tensor, q_weight: Optional[torch.Ten
     data, page, fmt = (None, 0, 0) if cache is None else (cache.data, cache.page_size, cache.fmt)
     return _marshalled("dsa_qk_norm", check, q, out, q_weight, keys, key_weight, data, page, fmt, slots, eps,
                        positions, cos_sin, rope_style, device_status, None if stream is None else _stream(stream))
+
+
+def dsa_weights_plan(num_tokens: int, num_seqs: int, num_heads: int, width: int, num_sms: int = 0,
+                     d_qk: int = 512):
+    """-> (WeightsPlan, workspace_bytes)."""
+    plan = WeightsPlan()
+    ws = ctypes.c_size_t(0)
+    _check("dsa_weights_plan", load().dsa_weights_plan(num_tokens, num_seqs, num_heads, width, num_sms, d_qk,
+                                                       ctypes.byref(plan), ctypes.byref(ws)))
+    return plan, int(ws.value)
+
+
+def dsa_weights_run(plan: WeightsPlan, workspace: torch.Tensor, q: torch.Tensor, cache: W.PagedCache,
+                    slots: torch.Tensor, lengths: torch.Tensor, starts: torch.Tensor, window: int, scale: float,
+                    sink: Optional[torch.Tensor], lse: torch.Tensor, scores_in: Optional[torch.Tensor],
+                    scores_out: torch.Tensor, stream=None, check: bool = True) -> int:
+    """``scores_out`` [B, width] fp32 = ``scores_in`` + the attention weight
+    that every entry of the lists received from the new tokens and all heads;
+    ``q`` rotated already, ``lse`` [T, H] as their attention left it."""
+    return _marshalled("dsa_weights_run", check, ctypes.addressof(plan), workspace, q, cache.data,
+                       cache.page_size, cache.fmt, slots, lengths, starts, window, scale, sink, lse, scores_in,
+                       scores_out, None if stream is None else _stream(stream))
+
+
+class AttentionWeights:
+    """Plan + workspace for the weights that records receive from up to T new
+    tokens of ``num_seqs`` sequences whose lists have up to ``width`` records;
+    ``__call__`` runs on the current stream and returns ``scores_out`` (which may be
+    ``scores_in``)."""
+
+    def __init__(self, T: int, num_seqs: int, H: int, width: int, device, d_qk: int = 512, num_sms: int = 0):
+        self.plan, nbytes = dsa_weights_plan(T, num_seqs, H, width, num_sms, d_qk)
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+    def __call__(self, q: torch.Tensor, cache: W.PagedCache, slots: torch.Tensor, lengths: torch.Tensor,
+                 starts: torch.Tensor, lse: torch.Tensor, scores_in: Optional[torch.Tensor],
+                 scores_out: torch.Tensor, scale: float, window: int = 0, sink: Optional[torch.Tensor] = None,
+                 stream=None):
+        dsa_weights_run(self.plan, self.workspace, q, cache, slots, lengths, starts, window, scale, sink, lse,
+                        scores_in, scores_out, stream)
+        return scores_out
 
 
 def dsa_evict(slots: torch.Tensor, lengths: torch.Tensor, scores: torch.Tensor, budget: int,

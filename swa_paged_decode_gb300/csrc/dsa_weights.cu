@@ -1,0 +1,883 @@
+// dsa_weights.cu -- the attention weight that cached records receive from new
+// tokens (dsa_weights_plan / dsa_weights_run): for every sequence b and entry j
+// of its list
+//
+//   out[b][j] = in[b][j] + sum_r e^{s_rj} / (e^{lse_r} + e^{z}),  s_rj = scale q_r . k_j,
+//
+// over the query rows r (token, head) that see the entry (dsa_chunk.cu says
+// which), lse_r as their attention left it and z the head's sink.
+//
+// The product is taken with the keys as rows, D[key, query row] = K . Q^T, so
+// that a thread holds one key and runs along the queries: the sum over r is a sum
+// in its own registers and needs no exchange, and a query row's constants are the
+// same for the whole warp. A weight is one exponential of (D factor_key)
+// factor_row - lse_row.
+//
+// Precision. The results are fp32 and a weight is off by what its score is off,
+// so no operand is rounded: queries are bf16 (8 bits) in f16 (11), with a power
+// of two per row; NVFP4, ue8m0 and MODEL1 values are exact in f16 with one per
+// key; the e4m3 codes of records with fp32 scales (FP8_528, V3.2) enter without
+// their scales, one accumulator per 128-dim block, and the scales are applied in
+// fp32 to the four sums (rounding code * scale to f16 first would cost 1e-4 of a
+// weight). That halves the tensor core's rate (N = 128 for the room of four
+// accumulators) and is hidden by the records' loads at single tokens.
+//
+// Two or three launches:
+//   prepare  queries to f16 tile images (128 rows x 64 dims, 128-byte swizzle),
+//            each row's constants, the list of items: (sequence, 128 keys, a
+//            range of its row tiles);
+//   weigh    CTA pairs (cta_group::2, M = 128: 64 keys in each CTA, N up to 256
+//            query rows) take items in turn: 8 warps dequantize the next item's
+//            records into one of two key tiles while the products of the present
+//            one run; query chunks come through a ring; 8 warps take the
+//            exponentials of one step while the next one's product runs;
+//   add      where items had to share the rows of their keys (few keys, many
+//            rows): the parts in order, so that the result does not depend on
+//            timing.
+#include "dsa_attend.cuh"
+#include "dsa_chunk_index.cuh"
+
+namespace dsa {
+
+constexpr int32_t kWeightsMagic = 0x57415344;   // "DSAW"
+
+struct WeightsParams {
+  ListArgs L;                  // lists: ids, lens, width, idx_stride
+  const int32_t *starts;       // [B + 1]
+  int32_t T, B, H, window, splits, max_items, tiles;   // tiles: of the query images
+  const __nv_bfloat16 *q;
+  int64_t q_st, q_sh;
+  const float *lse, *sink;
+  float scale_log2;
+  const float *in;             // or null: zeros
+  int64_t in_st;
+  float *out;
+  int64_t out_st;
+  long long wait_budget;
+  // workspace
+  int32_t *status;
+  int32_t *n_items;
+  int4 *item;                  // [max_items][2]
+  uint8_t *image;              // [tiles][64-dim block][8-row group][1 KiB]
+  float2 *row;                 // [tiles * 128] (scale log2(e) 2^e, log2 of the denominator)
+  float *part;                 // [splits][B][width]
+};
+
+constexpr int kWtPrep = 256;
+__device__ __forceinline__ Sequence weights_sequence(const WeightsParams &p, int32_t b) {
+  const int32_t s0 = __ldg(p.starts + b), s1 = __ldg(p.starts + b + 1), len = __ldg(p.L.lens + b);
+  return {s0, s1 - s0, min(max(len, 0), p.L.width), p.window};
+}
+// First image tile of a sequence: those of any two do not meet.
+__device__ __forceinline__ int32_t image_tile(const WeightsParams &p, int32_t b, int32_t s0) {
+  return (int32_t)((int64_t)s0 * p.H >> 7) + b;
+}
+// The row tiles [lo, hi) of a sequence that see any of the 128 keys from key0.
+__device__ __forceinline__ void seeing_tiles(const WeightsParams &p, const Sequence &s, int32_t key0, int32_t &lo, int32_t &hi) {
+  const int64_t before = s.len - s.n;   // position of its first token
+  const int64_t t0 = max((int64_t)0, key0 - before);
+  int64_t t1 = s.n;
+  if (p.window > 0) t1 = min(t1, (int64_t)key0 + 127 + p.window - before);
+  lo = (int32_t)(t0 * p.H >> 7);
+  hi = t1 > t0 ? (int32_t)((t1 * p.H + 127) >> 7) : lo;
+}
+
+// ------------------------------------------------------------ prepare
+template <bool kV32>
+__global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_constant__ WeightsParams p) {
+  constexpr int kDB = kV32 ? 9 : 8;
+  __shared__ int32_t w_s[kWtPrep / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!kDebug && blockIdx.x == 0 && tid == 0) *p.status = DSA_OK;
+  pdl_launch_dependents();
+  bool bad = false;
+  for (int32_t b = tid; b < p.B; b += kWtPrep) {
+    const int32_t s0 = __ldg(p.starts + b), s1 = __ldg(p.starts + b + 1);
+    bad |= s0 < 0 || s1 < s0 || s1 > p.T;
+  }
+  if (__syncthreads_or(bad)) {   // starts that do not ascend: no work, as in a chunk call
+    if (blockIdx.x == 0 && tid == 0) {
+      *p.n_items = 0;
+      report_status(p.status, DSA_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  if (blockIdx.x == 0) {
+    // items: the 128-key halves that any token of a sequence sees, its row
+    // tiles cut in `splits`
+    int32_t n = 0;
+    for (int32_t b0 = 0; b0 < p.B; b0 += kWtPrep) {
+      const int32_t b = b0 + tid;
+      Sequence s = {0, 0, 0, 0};
+      int32_t h0 = 0, mine = 0;
+      if (b < p.B) {
+        s = weights_sequence(p, b);
+        if (s.any()) {
+          h0 = s.gather_begin();
+          mine = (((s.len - 1) >> 7) + 1 - h0) * p.splits;
+        }
+      }
+      int32_t v = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += y;
+      }
+      __syncthreads();
+      if (lane == 31) w_s[warp] = v;
+      __syncthreads();
+      int32_t sum = 0;
+      for (int k = 0; k < kWtPrep / 32; ++k) {
+        if (k < warp) v += w_s[k];
+        sum += w_s[k];
+      }
+      int32_t at = n + v - mine;
+      for (int32_t i = 0; i < mine && at < p.max_items; ++i, ++at) {
+        const int32_t u = i / p.splits, part = i - u * p.splits, key0 = (h0 + u) * 128;
+        int32_t lo, hi;
+        seeing_tiles(p, s, key0, lo, hi);
+        const int32_t t0 = lo + (int32_t)((int64_t)(hi - lo) * part / p.splits), t1 = lo + (int32_t)((int64_t)(hi - lo) * (part + 1) / p.splits);
+        p.item[2 * (int64_t)at] = make_int4(b, key0, s.len, s.n);
+        p.item[2 * (int64_t)at + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part);
+      }
+      n += sum;
+    }
+    if (tid == 0) *p.n_items = min(n, p.max_items);
+    return;
+  }
+  // entries that no token sees keep what they had
+  if (p.in != p.out) {
+    for (int32_t b = blockIdx.x - 1; b < p.B; b += gridDim.x - 1) {
+      const Sequence s = weights_sequence(p, b);
+      const int32_t end = s.any() ? min(s.gather_begin() * 128, s.len) : s.len;
+      for (int32_t j = tid; j < end; j += kWtPrep) p.out[b * p.out_st + j] = p.in ? __ldg(p.in + b * p.in_st + j) : 0.f;
+    }
+  }
+  // query images, a block per 128-row tile
+  for (int32_t tile = blockIdx.x - 1; tile < p.tiles; tile += gridDim.x - 1) {
+    int32_t b = 0, hi = p.B - 1;   // the last sequence whose tiles begin at or before this one
+    while (b < hi) {
+      const int32_t mid = (b + hi + 1) >> 1;
+      if (image_tile(p, mid, __ldg(p.starts + mid)) <= tile) b = mid; else hi = mid - 1;
+    }
+    const Sequence s = weights_sequence(p, b);
+    const int32_t i = tile - image_tile(p, b, s.s0);
+    if (i < 0 || i >= s.tiles(p.H)) continue;
+    const int32_t rows = s.tile_rows(p.H, i);
+    uint8_t *base = p.image + (int64_t)tile * (kDB * 16384);
+#pragma unroll 2
+    for (int32_t r = warp; r < rows; r += kWtPrep / 32) {
+      const uint32_t gr = (uint32_t)s.s0 * p.H + 128u * i + r, t = gr / (uint32_t)p.H, h = gr - t * (uint32_t)p.H;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
+      const uint4 qa = ld_row(src + 2 * lane), qb = ld_row(src + 2 * lane + 1);
+      uint32_t qc = 0;
+      if constexpr (kV32) qc = __ldg(reinterpret_cast<const uint32_t *>(src + 64) + lane);
+      const uint32_t w[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+      uint32_t mb = qc & 0x7FFF7FFFu;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mb = __vmaxu2(mb, w[k] & 0x7FFF7FFFu);
+      mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
+      int e = mb ? (int)(mb >> 7) - 127 : 0;
+      e = e < -126 ? -126 : (e > 126 ? 126 : e);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      auto half2 = [&](uint32_t x) { return tc::pack_f16x2(bf16_bits_to_f32(x & 0xFFFFu) * down, bf16_bits_to_f32(x >> 16) * down); };
+      uint32_t f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = half2(w[k]);
+      const int x = r & 7;
+      uint8_t *row = base + (r >> 3) * 1024 + x * 128;
+      const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), c = make_uint4(f[4], f[5], f[6], f[7]);
+      tc::stg_v8(row + (lane >> 2) * 16384 + (((2 * (lane & 3)) ^ (x & 6)) << 4), (x & 1) ? c : a, (x & 1) ? a : c);
+      if constexpr (kV32)
+        *reinterpret_cast<uint32_t *>(row + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) = half2(qc);
+      if (lane == 0) {
+        // log2(e^lse + e^z); a row that attended nothing weighs nothing
+        const float lse = __ldg(p.lse + gr);
+        float l = lse == -INFINITY ? INFINITY : lse;
+        if (p.sink && lse != -INFINITY) {
+          const float z = __ldg(p.sink + h), m = fmaxf(lse, z), d = -fabsf(lse - z);
+          l = lse != lse || z != z ? lse + z : m == INFINITY ? INFINITY : z == -INFINITY ? lse : m + log1pf(expf(d));
+        }
+        p.row[(int64_t)tile * 128 + r] = make_float2(p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23), l * kLog2e);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ weigh
+constexpr int kWtThreads = 512;   // warps 0-7 exponentials, 8 MMA, 9 copies, 10-15 records
+constexpr int kWtRecords = 6;
+
+template <int FMT>
+struct WtCfg {
+  static constexpr bool kV32 = FMT == DSA_REC_V32_656;
+  static constexpr bool kBlocks = FMT == DSA_REC_FP8_528 || kV32;   // fp32 scales: an accumulator per block
+  static constexpr int kAcc = kV32 ? 5 : kBlocks ? 4 : 1;
+  static constexpr int kDB = kV32 ? 9 : 8;
+  static constexpr int kN = kBlocks ? 128 : 256;                    // query rows of a step at most
+  static constexpr int kCols = kN / 2;                              // TMEM columns of an accumulator
+  static constexpr int kAccSlots = 512 / kCols;
+  static constexpr uint32_t kChunk = kN / 2 * 128;                  // bytes of a CTA's query chunk: kN / 2 rows x 64 dims
+  static constexpr int kSlots = 65536 / kChunk;                     // 64 KiB of them
+  static constexpr uint32_t kTile = kDB * 8192;                     // a key tile: [kDB][64 keys x 64 dims] f16
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kColS = kRing + kSlots * kChunk;        // [2][kN] (factor, log2 denominator, position, -)
+  static constexpr uint32_t kFac = kColS + 2 * kN * 16;             // [2][8][64] f32 a key's factors; the last: kept or not
+  static constexpr uint32_t kRed = kFac + 4096;                     // [4][64] f32
+  static constexpr uint32_t kMisc = kRed + 1024;
+  static constexpr int kFull = 0, kEmpty = kSlots, kAFull = 2 * kSlots, kAEmpty = kAFull + kAccSlots,
+                       kKFull = kAEmpty + kAccSlots, kKReady = kKFull + 2, kKEmpty = kKReady + 2, kDrain = kKEmpty + 2,
+                       kBars = kDrain + 1;
+  static constexpr uint32_t kAbort = 8 * kBars, kTmem = kAbort + 4;
+  static constexpr uint32_t kBytes = kMisc + 512;
+  static_assert(kTmem + 4 <= 512, "misc area");
+  static_assert(kBytes + 1024 <= 232448u, "shared memory layout exceeds 227 KiB");
+  // rows of the step that starts with `left` rows to go
+  static __device__ __forceinline__ int rows(int64_t left) { return left > 128 && kN == 256 ? 256 : left > 64 ? 128 : 64; }
+};
+
+// The items of a pair, and the steps of an item (up to kN query rows each).
+template <class Cfg>
+struct Items {
+  const WeightsParams &p;
+  int32_t at, n, step;
+  int4 a, c, na, nc;
+  int32_t tile, end;     // next row tile of the item, and the row tile past its last
+  int64_t rows;          // rows of the sequence
+  __device__ __forceinline__ Items(const WeightsParams &q, int pair, int pairs) : p(q), at(pair), step(pairs) {
+    n = __ldcg(p.n_items);
+    if (at < n) load();
+  }
+  __device__ __forceinline__ void load() {
+    na = __ldcg(p.item + 2 * (int64_t)at);
+    nc = __ldcg(p.item + 2 * (int64_t)at + 1);
+  }
+  __device__ __forceinline__ bool next() {   // the next item
+    if (at >= n) return false;
+    a = na;
+    c = nc;
+    at += step;
+    if (at < n) load();
+    tile = c.y;
+    end = c.z;
+    rows = (int64_t)a.w * p.H;
+    return true;
+  }
+  __device__ __forceinline__ bool empty() const { return c.y >= c.z; }
+  __device__ __forceinline__ int64_t left() const { return min(rows, (int64_t)end * 128) - (int64_t)tile * 128; }
+  __device__ __forceinline__ bool next_step(int &N) {   // tile is the step's until the next call
+    if (tile >= end) return false;
+    N = Cfg::rows(left());
+    return true;
+  }
+  __device__ __forceinline__ void advance(int N) { tile += N == 256 ? 2 : 1; }
+};
+
+template <int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
+    weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap map16,
+                   const __grid_constant__ CUtensorMap map4) {
+  using Cfg = WtCfg<FMT>;
+  constexpr bool kV32 = Cfg::kV32;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = tc::smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+  uint8_t *smem = smem_raw + pad;
+  const uint32_t sbase = raw_base + pad, ring = sbase + Cfg::kRing;
+  float4 *col_s = reinterpret_cast<float4 *>(smem + Cfg::kColS);
+  float *fac_s = reinterpret_cast<float *>(smem + Cfg::kFac);
+  float *red_s = reinterpret_cast<float *>(smem + Cfg::kRed);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kMisc);
+  volatile int32_t *abort_s = reinterpret_cast<volatile int32_t *>(smem + Cfg::kMisc + Cfg::kAbort);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kMisc + Cfg::kTmem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t side = tc::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (warp == 0) tc::tmem_alloc_pair(tmem_slot, 512);
+  if (tid == 32) {
+    for (int b = 0; b < Cfg::kBars; ++b) {
+      const bool a = b >= Cfg::kAEmpty && b < Cfg::kKFull, k = b >= Cfg::kKFull && b < Cfg::kKReady,
+                 r = b >= Cfg::kKReady && b < Cfg::kKEmpty, e = b >= Cfg::kKEmpty && b < Cfg::kDrain;
+      tc::mbar_init(&bars[b], a ? 16u : k ? 2u * kWtRecords : r ? kWtRecords : e ? 9u : 1u);
+    }
+    tc::fence_mbar_init();
+    *abort_s = 0;
+  }
+  pdl_wait_primary();
+  Items<Cfg> items(p, pair, pairs);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](int b, uint32_t phase) -> bool {   // bounded, as in the attend kernel
+    if (tc::mbar_test_wait(&bars[b], phase)) return true;
+    if (*abort_s) return false;
+    const long long budget = p.wait_budget > 0 ? p.wait_budget : kPfWait;
+    if (tc::mbar_wait(&bars[b], phase, budget)) return true;
+    if (!*abort_s) {
+      *abort_s = 1;
+      report_status(p.status, DSA_ERR_TIMEOUT);
+    }
+    return false;
+  };
+  auto lead = [&](int b) { return tc::mapa(tc::smem_u32(&bars[b]), 0); };
+
+  if (warp >= 10) {
+    // ======================================================== records
+    // 64 keys of an item to this CTA, in groups of 4 that the warps take in turn
+    // (two or three each), a group's loads in flight while the one before it is
+    // converted; the next item's records are on their way to L2 meanwhile.
+    const int pw = warp - 10;
+    constexpr int kRounds = (16 + kWtRecords - 1) / kWtRecords;
+    bool ok = true;
+    uint32_t turn = 0;
+    auto slot_of = [&](const int4 &a) {   // lane 4 k + i: the slot of key i of the warp's group k
+      const int r = 4 * ((lane >> 2) * kWtRecords + pw) + (lane & 3);
+      const int32_t j = a.y + 64 * (int32_t)side + r;
+      return lane < 4 * kRounds && r < 64 && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
+    };
+    int32_t ahead = items.at < items.n ? slot_of(items.na) : -1;
+    while (ok && items.next()) {
+      const int32_t mine = ahead;
+      ahead = items.at < items.n ? slot_of(items.na) : -1;
+      if (items.empty()) continue;
+      RawRecord raw[2][4];
+      bool kept[2][4];
+      auto load = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t sid = __shfl_sync(0xffffffffu, mine, 4 * k + i);
+          kept[k & 1][i] = sid >= 0 && (int64_t)sid < p.L.num_slots;
+          const uint8_t *rec = record_ptr(p.L, kept[k & 1][i] ? sid : 0);
+          if (kept[k & 1][i])
+            kept[k & 1][i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
+          if (kept[k & 1][i]) load_record<FMT>(rec, lane, raw[k & 1][i]);
+        }
+      };
+      load(0);
+      const int buf = turn & 1;
+      ok = wait(Cfg::kKEmpty + buf, ((turn >> 1) & 1u) ^ 1u);
+      ++turn;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      float *fac = fac_s + buf * 512;
+      const uint32_t tile = sbase + buf * Cfg::kTile;
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        if (k + 1 < kRounds) load(k + 1);
+        const int group = k * kWtRecords + pw;
+        if (group >= 16) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const RawRecord &rr = raw[k & 1][i];
+          const int r = 4 * group + i, x = r & 7;
+          if (lane == 0) fac[7 * 64 + r] = kept[k & 1][i] ? 1.f : 0.f;
+          if (!kept[k & 1][i]) continue;   // (what its row of the tile holds stays in its own lane)
+          uint32_t f[8];
+          if constexpr (Cfg::kBlocks) {
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2) tc::e4m3x4_to_f16x4(rr.w[k2], f[2 * k2], f[2 * k2 + 1]);
+            if ((lane & 7) == 0) fac[(lane >> 3) * 64 + r] = __uint_as_float(rr.s);
+            if constexpr (kV32) {
+              const uint32_t m = rr.t & 0x7FFF7FFFu;
+              const uint32_t mb = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+              const int E = min(max((int)(mb >> 7) - 127, -kPfRange), kPfRange) - kPfTop;
+              const float down = __uint_as_float((uint32_t)(127 - E) << 23);
+              if (lane == 0) fac[4 * 64 + r] = __uint_as_float((uint32_t)(127 + E) << 23);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + 8 * 8192 + (r >> 3) * 1024 + x * 128 +
+                                                          (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)),
+                           "r"(tc::pack_f16x2(bf16_bits_to_f32(rr.t & 0xFFFFu) * down, bf16_bits_to_f32(rr.t >> 16) * down))
+                           : "memory");
+            }
+          } else {
+            const int e = __reduce_max_sync(0xffffffffu, record_exponent<FMT>(rr, lane));
+            const int E = min(max(e, -kPfRange), kPfRange) - kPfTop;
+            const float down = __uint_as_float((uint32_t)(127 - E) << 23);
+            if (lane == 0) fac[r] = __uint_as_float((uint32_t)(127 + E) << 23);
+            float v[16], t0, t1;
+            expand_record<FMT>(rr, lane, v, t0, t1);
+#pragma unroll
+            for (int k2 = 0; k2 < 8; ++k2) f[k2] = tc::pack_f16x2(v[2 * k2] * down, v[2 * k2 + 1] * down);
+          }
+          const uint32_t row = tile + (lane >> 2) * 8192 + (r >> 3) * 1024 + x * 128;
+          tc::st_shared_v4(row + (((2 * (lane & 3)) ^ x) << 4), f[0], f[1], f[2], f[3]);
+          tc::st_shared_v4(row + (((2 * (lane & 3) + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars[Cfg::kKReady + buf]), side));
+        tc::mbar_arrive_remote(lead(Cfg::kKFull + buf));
+      }
+      if (ahead >= 0 && (int64_t)ahead < p.L.num_slots) {
+        const uint8_t *rec = record_ptr(p.L, ahead);
+#pragma unroll
+        for (int b = 0; b < 768; b += 128)
+          if (b < p.L.rec) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + b));
+      }
+    }
+    // the tiles' last releases have arrived before the pair ends
+    for (int k = 0; k < 2 && ok; ++k, ++turn) ok = wait(Cfg::kKEmpty + (turn & 1), ((turn >> 1) & 1u) ^ 1u);
+  } else if (warp == 9) {
+    // ======================================================== query chunks
+    if (lane == 0) {
+      uint32_t slot = 0, ph = 1;
+      bool ok = true;
+      uint32_t filled = 0, fill_ph = 0;
+      const uint32_t full0 = lead(Cfg::kFull);
+      while (ok && items.next()) {
+        int N;
+        while (ok && items.next_step(N)) {
+          // this CTA's N / 2 rows: of a tile of its own with N = 256
+          const int64_t tile = items.c.x + items.tile + (N == 256 ? side : 0);
+          const int32_t y0 = (int32_t)(tile * (Cfg::kDB * 32)) + (N == 256 ? 0 : (int32_t)side * (N / 8));
+          const bool in = dbg_ok(p.status, tile >= 0 && tile < p.tiles, kDbgPartial);
+          for (int c = 0; c < Cfg::kDB && ok; ++c) {
+            ok = wait(Cfg::kEmpty + slot, ph);
+            if (!ok) break;
+            if (side == 0) {
+              tc::mbar_expect_tx(&bars[Cfg::kFull + slot], (uint32_t)N * 128u);   // both CTAs' bytes
+              filled |= 1u << slot;
+              fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+            }
+            const uint32_t dst = ring + slot * Cfg::kChunk, bar = full0 + 8 * slot;
+            const int32_t y = in ? y0 + c * 32 : 0;
+            if (N == 256) {
+              tc::tma_load_pair(dst, &map16, 0, y, bar);
+            } else {
+              tc::tma_load_pair(dst, &map4, 0, y, bar);
+              if (N == 128) tc::tma_load_pair(dst + 4096, &map4, 0, y + 8, bar);
+            }
+            if (++slot == Cfg::kSlots) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+          items.advance(N);
+        }
+      }
+      // no commit reaches this CTA's barriers after its end; after a timeout no
+      // copy is in flight (as in the attend kernel)
+      for (int k = 0; k < Cfg::kSlots && ok; ++k) {
+        ok = wait(Cfg::kEmpty + slot, ph);
+        if (++slot == Cfg::kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) {
+        for (int k = 0; k < Cfg::kSlots; ++k)
+          if ((filled >> k) & 1u) tc::mbar_wait(&bars[Cfg::kFull + k], (fill_ph >> k) & 1u, kPfCopyWait);
+        const long long t0 = clock64();
+        while (clock64() - t0 < kPfCopyWait / 10) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ======================================================== MMA issue
+    if (side == 0) {
+      constexpr uint16_t kBoth = 3;
+      constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
+      const uint32_t dk0 = tc::sdesc_lo(sbase, 16), dq0 = tc::sdesc_lo(ring, 16);
+      uint32_t slot = 0, ph = 0, acc = 0, ph_a = 1, turn = 0;
+      bool ok = true, issued = false;
+      auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
+      while (ok && items.next()) {
+        if (items.empty()) continue;
+        const uint32_t buf = turn & 1u, dk = dk0 + buf * (Cfg::kTile >> 4);
+        ok = here(wait(Cfg::kKFull + buf, (turn >> 1) & 1u));
+        ++turn;
+        int N;
+        while (ok && items.next_step(N)) {
+          const uint32_t idesc = N == 256 ? tc::idesc_f16(128, 256, false, false)
+                                 : N == 128 ? tc::idesc_f16(128, 128, false, false) : tc::idesc_f16(128, 64, false, false);
+          items.advance(N);
+          const bool last = items.tile >= items.end;
+#pragma unroll
+          for (int b = 0; b < Cfg::kAcc; ++b) {
+            if (!ok) break;
+            ok = here(wait(Cfg::kAEmpty + acc, ph_a));
+            if (!ok) break;
+            tc::tc_fence_after();
+            issued = true;
+            const int c0 = Cfg::kBlocks ? 2 * b : 0, c1 = Cfg::kBlocks ? (2 * b + 2 < Cfg::kDB ? 2 * b + 2 : Cfg::kDB) : Cfg::kDB;
+#pragma unroll
+            for (int c = c0; c < c1; ++c) {
+              ok = ok && here(wait(Cfg::kFull + slot, ph));
+              if (!ok) break;
+              tc::tc_fence_after();
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  tc::mma_f16_pair(tmem + acc * Cfg::kCols, dk + ((c * 8192 + ks * 32) >> 4),
+                                   dq0 + ((slot * Cfg::kChunk + ks * 32) >> 4), kHi, idesc, (c > c0 || ks) ? 1u : 0u);
+                tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+                if (c == c1 - 1) {
+                  tc::mma_commit_to(&bars[Cfg::kAFull + acc], kBoth);
+                  if (b == Cfg::kAcc - 1 && last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
+                }
+              }
+              __syncwarp();
+              if (++slot == Cfg::kSlots) {
+                slot = 0;
+                ph ^= 1u;
+              }
+            }
+            if (++acc == Cfg::kAccSlots) {
+              acc = 0;
+              ph_a ^= 1u;
+            }
+          }
+        }
+      }
+      if (issued && !ok && tc::elect_one()) {   // MMAs issued before a timeout end before TMEM is freed
+        tc::mma_commit_one(&bars[Cfg::kDrain]);
+        tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ======================================================== exponentials
+    const int q4 = warp & 3, half = warp >> 2;
+    const int lr = 32 * q4 + lane, key = lr & 63, up = lr >> 6;   // TMEM lane; key of this CTA's 64; which half of the rows
+    const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
+    auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
+    const uint32_t aempty0 = lead(Cfg::kAEmpty), kempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kKEmpty]), side);
+    uint32_t acc = 0, ph_a = 0, turn = 0, cb = 0;
+    // constants of the query rows of a step, a row to a thread
+    auto column = [&](int N) {
+      const int64_t r = (int64_t)items.tile * 128 + tid;
+      float4 v = make_float4(0.f, INFINITY, __int_as_float(INT32_MIN), 0.f);
+      if (tid < N && r < min(items.rows, (int64_t)items.end * 128)) {
+        const float2 x = __ldcg(p.row + ((int64_t)items.c.x + items.tile) * 128 + tid);
+        v = make_float4(x.x, x.y, __int_as_float(items.a.z - items.a.w + (int32_t)((uint32_t)r / (uint32_t)p.H)), 0.f);
+      }
+      return v;
+    };
+    while (items.next()) {
+      const int32_t at = items.a.y + 64 * (int32_t)side + key;   // list position of the thread's key
+      float total = 0.f;
+      bool kept = false;
+      if (!items.empty()) {
+        const int buf = turn & 1;
+        wait(Cfg::kKReady + buf, (turn >> 1) & 1u);
+        ++turn;
+        const float *fac = fac_s + buf * 512 + key;
+        kept = fac[7 * 64] != 0.f;
+        float s[Cfg::kAcc];
+#pragma unroll
+        for (int b = 0; b < Cfg::kAcc; ++b) s[b] = kept ? fac[b * 64] : 0.f;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(kempty0 + 8 * buf);   // the factors are read
+        int N;
+        while (items.next_step(N)) {
+          if (tid < N) col_s[cb * Cfg::kN + tid] = column(N);
+          sm_bar();
+          // every row there and every key before every row's place (and after its window): no tests
+          const int64_t r0 = (int64_t)items.tile * 128;
+          const int32_t p0 = items.a.z - items.a.w + (int32_t)((uint32_t)r0 / (uint32_t)p.H);
+          const int32_t p1 = items.a.z - items.a.w + (int32_t)((uint32_t)(r0 + N - 1) / (uint32_t)p.H);
+          const bool all = items.left() >= N && p0 >= items.a.y + 127 && (p.window == 0 || p1 - p.window < items.a.y);
+          const int first = up * (N / 2) + half * (N / 4);   // the thread's rows: N / 4 of them from here
+          const float4 *col = col_s + cb * Cfg::kN + first;
+          cb ^= 1u;
+          // the step's accumulators, ring slots acc .. acc + kAcc - 1
+#pragma unroll
+          for (int k = 0; k < Cfg::kAcc; ++k) {
+            const uint32_t slot = (acc + k) % Cfg::kAccSlots;
+            wait(Cfg::kAFull + slot, ph_a ^ (acc + k >= Cfg::kAccSlots ? 1u : 0u));
+          }
+          tc::tc_fence_after();
+          // 16 (a block's accumulators together) or 32 rows at a time
+          constexpr int kGroup = Cfg::kBlocks ? 16 : 32;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int g = 0; g < N / 4; g += kGroup) {
+            const uint32_t c = tl + half * (N / 4) + g;
+            float x[kGroup];
+            if constexpr (!Cfg::kBlocks) {
+              uint32_t d[2][16];   // (16 rows of N / 4 = 16: the second half is not used)
+              DSA_TMEM_LD16_NOWAIT(c + acc * Cfg::kCols, d[0]);
+              DSA_TMEM_LD16_NOWAIT(c + acc * Cfg::kCols + (N == 64 ? 0 : 16), d[1]);
+              DSA_TMEM_WAIT32(d[0], d[1]);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(d[i / 16][i % 16]) * s[0];
+            } else {
+#pragma unroll
+              for (int k = 0; k < Cfg::kAcc; k += 2) {
+                uint32_t d[2][16];
+                DSA_TMEM_LD16_NOWAIT(c + (acc + k) % Cfg::kAccSlots * Cfg::kCols, d[0]);
+                DSA_TMEM_LD16_NOWAIT(c + (acc + (k + 1 < Cfg::kAcc ? k + 1 : k)) % Cfg::kAccSlots * Cfg::kCols, d[1]);
+                DSA_TMEM_WAIT32(d[0], d[1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float v = __uint_as_float(d[0][i]);
+                  x[i] = k == 0 ? v * s[0] : fmaf(v, s[k], x[i]);
+                  if (k + 1 < Cfg::kAcc) x[i] = fmaf(__uint_as_float(d[1][i]), s[k + 1 < Cfg::kAcc ? k + 1 : 0], x[i]);
+                }
+              }
+            }
+            if (g + kGroup >= N / 4) {   // read: the slots are free again
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane < Cfg::kAcc) tc::mbar_arrive_remote(aempty0 + 8 * ((acc + lane) % Cfg::kAccSlots));
+            }
+            const int most = min(kGroup, N / 4);
+#pragma unroll
+            for (int h = 0; h < kGroup / 16; ++h) {
+              if (16 * h >= most) break;
+              if (all) {
+#pragma unroll
+                for (int i = 16 * h; i < 16 * h + 16; ++i) {
+                  const float2 k = *reinterpret_cast<const float2 *>(col + g + i);
+                  sum[i & 3] += tc::ex2(fmaf(x[i], k.x, -k.y));
+                }
+              } else {
+#pragma unroll
+                for (int i = 16 * h; i < 16 * h + 16; ++i) {
+                  const float4 k = col[g + i];
+                  const int32_t place = __float_as_int(k.z);
+                  const bool sees = at <= place && (p.window == 0 || at > place - p.window);
+                  const float e = tc::ex2(fmaf(x[i], k.x, -k.y));
+                  sum[i & 3] += sees ? e : 0.f;
+                }
+              }
+            }
+          }
+          acc += Cfg::kAcc;
+          if (acc >= Cfg::kAccSlots) {
+            acc -= Cfg::kAccSlots;
+            ph_a ^= 1u;
+          }
+          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          items.advance(N);
+        }
+      }
+      // the four threads of a key
+      red_s[(2 * up + half) * 64 + key] = total;
+      sm_bar();
+      if (up == 0 && half == 0 && at < items.a.z) {
+        const float t = kept ? (red_s[key] + red_s[64 + key]) + (red_s[128 + key] + red_s[192 + key]) : 0.f;
+        const int64_t b = items.a.x;
+        if (p.splits > 1) {
+          __stcg(p.part + ((int64_t)items.c.w * p.B + b) * p.L.width + at, t);
+        } else {
+          p.out[b * p.out_st + at] = (p.in ? p.in[b * p.in_st + at] : 0.f) + t;
+        }
+      }
+      sm_bar();
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ add
+__global__ void __launch_bounds__(256) weights_add_kernel(const __grid_constant__ WeightsParams p) {
+  const int32_t b = blockIdx.y, j = (int32_t)(blockIdx.x * 256 + threadIdx.x);
+  pdl_wait_primary();
+  if (__ldcg(p.n_items) == 0) return;
+  const Sequence s = weights_sequence(p, b);
+  if (!s.any() || j >= s.len || j < s.gather_begin() * 128) return;
+  float t = 0.f;
+  for (int32_t k = 0; k < p.splits; ++k) t += __ldcg(p.part + ((int64_t)k * p.B + b) * p.L.width + j);
+  p.out[b * p.out_st + j] = (p.in ? p.in[b * p.in_st + j] : 0.f) + t;
+}
+
+}  // namespace dsa
+
+namespace {
+
+using dsa::aligned;
+using dsa::WeightsParams;
+
+template <int FMT>
+cudaError_t weights_setup(void *) {
+  return cudaFuncSetAttribute(dsa::weights_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)(dsa::WtCfg<FMT>::kBytes + 1024));
+}
+template <int FMT>
+cudaError_t weights_ready() {   // bits 51 to 55 of dsa_configure_once
+  return dsa::dsa_configure_once(51 + FMT, &weights_setup<FMT>, nullptr);
+}
+// CTA pairs that run at the same time on the current device.
+template <int FMT>
+cudaError_t weights_pairs(int *pairs) {
+  cudaError_t e = weights_ready<FMT>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = dsa::config(2, dsa::kWtThreads, dsa::WtCfg<FMT>::kBytes + 1024, nullptr);
+  return cudaOccupancyMaxActiveClusters(pairs, dsa::weights_kernel<FMT>, &c);
+}
+
+// The query images as rows of 512 bytes, `rows` of them to a box.
+bool chunk_map(void *image, int64_t bytes, uint32_t rows, CUtensorMap *map) {
+  const dsa::EncodeTiled encode = dsa::tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {256, (cuuint64_t)(bytes / 512)}, strides[1] = {512};
+  const cuuint32_t box[2] = {256, rows}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, image, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT>
+cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
+  using namespace dsa;
+  using Cfg = WtCfg<FMT>;
+  cudaError_t e = weights_ready<FMT>();
+  if (e != cudaSuccess) return e;
+  CUtensorMap map16, map4;
+  const int64_t bytes = (int64_t)p.tiles * Cfg::kDB * 16384;
+  if (!chunk_map(p.image, bytes, 32, &map16) || !chunk_map(p.image, bytes, 8, &map4)) return cudaErrorNotSupported;
+  const unsigned blocks = 1 + (unsigned)std::min(p.tiles, 8 * 152);
+  weights_prepare_kernel<Cfg::kV32><<<blocks, kWtPrep, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(config(2u * pairs, kWtThreads, Cfg::kBytes + 1024, st), weights_kernel<FMT>, p, map16, map4);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cudaLaunchConfig_t c = config((unsigned)((p.L.width + 255) / 256), 256, 0, st);
+  c.gridDim.y = (unsigned)p.B;
+  return launch_dependent(c, weights_add_kernel, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_heads, int32_t width, int32_t num_sms,
+                            int32_t d_qk, dsa_weights_plan_t *plan, size_t *workspace_bytes) {
+  if (!plan || !workspace_bytes) return DSA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_seqs < 0 || num_heads < 1 || width < 1 || num_sms < 0) return DSA_ERR_INVALID_ARG;
+  if (d_qk != 512 && d_qk != 576) return DSA_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)num_tokens * num_heads, halves = ((int64_t)width + 127) / 128;
+  // an image tile more than the sequences': the second half of the last step
+  const int64_t tiles = dsa::chunk_row_tiles(num_tokens, num_heads, num_seqs) + num_seqs + 2;
+  // (rows and images' 512-byte rows, 288 to a tile, are counted in 31 bits, the
+  // adding kernel's grid has 2^16 - 1 lists)
+  if (rows > INT32_MAX - 128 || num_seqs > 65535 || width > (1 << 29) || tiles > INT32_MAX / 288)
+    return DSA_ERR_UNSUPPORTED;
+  int most_pairs = num_sms / 2;
+  if (num_sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        (d_qk == 576 ? weights_pairs<DSA_REC_V32_656>(&most_pairs) : weights_pairs<DSA_REC_FP8_528>(&most_pairs)) != cudaSuccess)
+      return DSA_ERR_CUDA;
+  }
+  std::memset(plan, 0, sizeof(*plan));
+  plan->magic = dsa::kWeightsMagic;
+  plan->abi_version = DSA_DECODE_ABI_VERSION;
+  plan->num_tokens = num_tokens;
+  plan->num_seqs = num_seqs;
+  plan->num_heads = num_heads;
+  plan->width = width;
+  plan->d_qk = d_qk;
+  plan->num_sms = num_sms;
+  const int64_t pairs = most_pairs < 1 ? 1 : most_pairs, units = halves * num_seqs;
+  // Items for four turns of every pair, where the rows allow it: a sequence's
+  // rows in steps of 256 (of the mean sequence; more parts than steps are empty).
+  const int64_t steps = num_seqs > 0 ? (rows / num_seqs + 255) / 256 : 1;
+  int64_t splits = units > 0 ? (4 * pairs + units - 1) / units : 1;
+  splits = splits > steps ? steps : splits;
+  splits = splits < 1 ? 1 : splits;
+  if (units * splits > INT32_MAX / 2) return DSA_ERR_UNSUPPORTED;
+  plan->splits = (int32_t)splits;
+  plan->tiles = (int32_t)tiles;
+  plan->pairs = (int32_t)(units * splits < pairs ? (units < 1 ? 1 : units * splits) : pairs);
+  int64_t off = 256;
+  auto take = [&](int64_t &at, int64_t bytes) {
+    at = off;
+    off = dsa::align_up(off + bytes, 256);
+  };
+  take(plan->ws_item_offset, 32 * units * splits);
+  take(plan->ws_image_offset, tiles * 128 * d_qk * 2);
+  take(plan->ws_row_offset, tiles * 128 * 8);
+  take(plan->ws_part_offset, splits > 1 ? splits * num_seqs * (int64_t)width * 4 : 0);
+  plan->workspace_bytes = num_tokens == 0 || num_seqs == 0 ? 0 : off;
+  // Test knob, read only here, as in dsa_decode_plan.
+  if (const char *wb = std::getenv("DSA_DECODE_WAIT_BUDGET")) {
+    const long long v = std::atoll(wb);
+    if (v > 0) plan->wait_budget_cycles = v;
+  }
+  *workspace_bytes = (size_t)plan->workspace_bytes;
+  return DSA_OK;
+}
+
+dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size_t workspace_bytes, const void *q,
+                           int64_t q_stride_t, int64_t q_stride_h, const dsa_cache_desc *cache, const int32_t *slots,
+                           int64_t slots_stride, const int32_t *lengths, const int32_t *starts, int32_t window,
+                           float scale, const float *sink, const float *lse, const float *scores_in,
+                           int64_t in_stride, float *scores_out, int64_t out_stride, dsa_stream_t stream) {
+  dsa::NvtxRange range("dsa_weights_run");
+  if (!plan || plan->magic != dsa::kWeightsMagic || plan->abi_version != DSA_DECODE_ABI_VERSION) return DSA_ERR_PLAN;
+  if (plan->num_tokens == 0 || plan->num_seqs == 0) return DSA_OK;
+  if (!q || !slots || !lengths || !starts || !lse || !scores_out) return DSA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || window < 0 || slots_stride < plan->width || out_stride < plan->width ||
+      (scores_in && in_stride < plan->width) || (scores_in == scores_out && in_stride != out_stride))
+    return DSA_ERR_INVALID_ARG;
+  if (q_stride_h < plan->d_qk || q_stride_t < (int64_t)(plan->num_heads - 1) * q_stride_h + plan->d_qk)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || q_stride_t % 8 != 0 || q_stride_h % 8 != 0 || !aligned(slots, 4) || !aligned(lengths, 4) ||
+      !aligned(starts, 4) || !aligned(lse, 4) || (sink && !aligned(sink, 4)) || (scores_in && !aligned(scores_in, 4)) ||
+      !aligned(scores_out, 4))
+    return DSA_ERR_ALIGNMENT;
+  if (!workspace || (int64_t)workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256))
+    return DSA_ERR_WORKSPACE;
+  WeightsParams p;
+  std::memset(static_cast<void *>(&p), 0, sizeof(p));
+  const dsa_status s = dsa::fill_cache(cache, p.L);
+  if (s != DSA_OK) return s;
+  if ((cache->format == DSA_REC_V32_656) != (plan->d_qk == 576)) return DSA_ERR_UNSUPPORTED;
+  p.L.ids = slots;
+  p.L.idx_stride = slots_stride;
+  p.L.lens = lengths;
+  p.L.width = plan->width;
+  p.starts = starts;
+  p.T = plan->num_tokens;
+  p.B = plan->num_seqs;
+  p.H = plan->num_heads;
+  p.window = window;
+  p.splits = plan->splits;
+  p.tiles = plan->tiles;
+  p.max_items = (int32_t)(((int64_t)plan->width + 127) / 128 * plan->num_seqs * plan->splits);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.q_st = q_stride_t;
+  p.q_sh = q_stride_h;
+  p.lse = lse;
+  p.sink = sink;
+  p.scale_log2 = scale * dsa::kLog2e;
+  p.in = scores_in;
+  p.in_st = in_stride;
+  p.out = scores_out;
+  p.out_st = out_stride;
+  p.wait_budget = plan->wait_budget_cycles;
+  char *w = static_cast<char *>(workspace);
+  p.status = reinterpret_cast<int32_t *>(w);
+  p.n_items = p.status + 2;
+  p.item = reinterpret_cast<int4 *>(w + plan->ws_item_offset);
+  p.image = reinterpret_cast<uint8_t *>(w + plan->ws_image_offset);
+  p.row = reinterpret_cast<float2 *>(w + plan->ws_row_offset);
+  p.part = reinterpret_cast<float *>(w + plan->ws_part_offset);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dsa::kDebug && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return DSA_ERR_CUDA;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (cache->format) {
+    case DSA_REC_FP8_528: e = launch_weights<DSA_REC_FP8_528>(p, plan->pairs, st); break;
+    case DSA_REC_NVFP4_288: e = launch_weights<DSA_REC_NVFP4_288>(p, plan->pairs, st); break;
+    case DSA_REC_FP8_528_UE8M0: e = launch_weights<DSA_REC_FP8_528_UE8M0>(p, plan->pairs, st); break;
+    case DSA_REC_MODEL1_584: e = launch_weights<DSA_REC_MODEL1_584>(p, plan->pairs, st); break;
+    case DSA_REC_V32_656: e = launch_weights<DSA_REC_V32_656>(p, plan->pairs, st); break;
+  }
+  return dsa::cuda_status(e);
+}
+
+}  // extern "C"

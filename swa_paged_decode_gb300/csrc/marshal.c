@@ -220,6 +220,10 @@ typedef dsa_status (*chunk_fn)(const dsa_chunk_plan_t *, void *, size_t, const v
                                int32_t, const float *, const int64_t *, const float *, int64_t, int32_t, float,
                                const void *, const float *, void *, float *, dsa_stream_t);
 
+typedef dsa_status (*weights_fn)(const dsa_weights_plan_t *, void *, size_t, const void *, int64_t, int64_t,
+                                 const dsa_cache_desc *, const int32_t *, int64_t, const int32_t *, const int32_t *,
+                                 int32_t, float, const float *, const float *, const float *, int64_t, float *, int64_t,
+                                 dsa_stream_t);
 typedef dsa_status (*qk_fn)(int32_t, int32_t, int32_t, int32_t, const void *, int64_t, int64_t, const float *, int64_t,
                             void *, int64_t, int64_t, const void *, int64_t, const float *, const dsa_cache_desc *,
                             const int32_t *, float, const int64_t *, const float *, int64_t, int32_t, int32_t *,
@@ -381,6 +385,36 @@ static PyObject *chunk_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   return PyLong_FromLong(rc);
 }
 
+/* (address, plan address, workspace, q, data, page_size, fmt, slots, lengths,
+ *  starts, window, scale, sink, lse, scores_in, scores_out, stream) */
+static PyObject *weights_run(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  call c = {-1, 0, 0};
+  dsa_cache_desc d = {0};
+  long long ws_bytes = 0, st = 0, sh = 0, ls = 0, is = 0, os = 0;
+  dsa_status rc;
+  if (want_args(na, 17)) return NULL;
+  weights_fn f = (weights_fn)PyLong_AsVoidPtr(a[0]);
+  const dsa_weights_plan_t *plan = PyLong_AsVoidPtr(a[1]);
+  const int32_t window = as_i32(&c, a[10]);
+  const float scale = (float)PyFloat_AsDouble(a[11]);
+  if (PyErr_Occurred()) return NULL;
+  const long long T = plan->num_tokens, B = plan->num_seqs, H = plan->num_heads, width = plan->width;
+  void *ws = vec(&c, a[2], 0, t_u8, 1, -1, -1, -1, &ws_bytes);
+  const void *q = queries(&c, a[3], t_bf16, T, H, plan->d_qk, &st, &sh);
+  cache(&c, a[4], a[5], a[6], &d);
+  const int32_t *slots = lists(&c, a[7], t_i32, B, width, &ls);
+  const int32_t *lengths = vec(&c, a[8], 0, t_i32, 1, B, -1, -1, NULL);
+  const int32_t *starts = vec(&c, a[9], 0, t_i32, 1, B + 1, -1, -1, NULL);
+  const float *sink = vec(&c, a[12], 1, t_f32, 1, H, -1, -1, NULL);
+  const float *lse = vec(&c, a[13], 0, t_f32, 2, T, H, -1, NULL);
+  const float *in = a[14] == Py_None ? NULL : lists(&c, a[14], t_f32, B, width, &is);
+  float *out = lists(&c, a[15], t_f32, B, width, &os);
+  dsa_stream_t stream = stream_of(&c, a[16]);
+  DSA_CALL(rc, f(plan, ws, (size_t)ws_bytes, q, st, sh, &d, slots, ls, lengths, starts, window, scale, sink, lse, in, is,
+                 out, os, stream));
+  return PyLong_FromLong(rc);
+}
+
 /* (address, q, out, q_weight, keys, key_weight, data, page_size, fmt, slots,
  *  eps, positions, cos_sin, rope_style, device_status, stream); data None: no
  *  keys */
@@ -491,6 +525,7 @@ static PyMethodDef methods[] = {
     {"cache_read", (PyCFunction)(void (*)(void))cache_read, METH_FASTCALL, NULL},
     {"prefix_run", (PyCFunction)(void (*)(void))prefix_run, METH_FASTCALL, NULL},
     {"chunk_run", (PyCFunction)(void (*)(void))chunk_run, METH_FASTCALL, NULL},
+    {"weights_run", (PyCFunction)(void (*)(void))weights_run, METH_FASTCALL, NULL},
     {"qk_norm", (PyCFunction)(void (*)(void))qk_norm, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
