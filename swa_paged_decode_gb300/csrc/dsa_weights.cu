@@ -36,6 +36,7 @@
 //            timing.
 #include "dsa_attend.cuh"
 #include "dsa_chunk_index.cuh"
+#include "dsa_rows.cuh"
 
 namespace dsa {
 
@@ -86,7 +87,7 @@ __device__ __forceinline__ void seeing_tiles(const WeightsParams &p, const Seque
 template <bool kV32>
 __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_constant__ WeightsParams p) {
   constexpr int kDB = kV32 ? 9 : 8;
-  __shared__ int32_t w_s[kWtPrep / 32];
+  __shared__ int32_t w_s[kWtPrep / 32], upto_s[kWtPrep];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (!kDebug && blockIdx.x == 0 && tid == 0) *p.status = DSA_OK;
   pdl_launch_dependents();
@@ -104,18 +105,13 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
   }
   if (blockIdx.x == 0) {
     // items: the 128-key halves that any token of a sequence sees, its row
-    // tiles cut in `splits`
+    // tiles cut in `splits`; 256 sequences at a time, then an item to a thread
     int32_t n = 0;
     for (int32_t b0 = 0; b0 < p.B; b0 += kWtPrep) {
-      const int32_t b = b0 + tid;
-      Sequence s = {0, 0, 0, 0};
-      int32_t h0 = 0, mine = 0;
-      if (b < p.B) {
-        s = weights_sequence(p, b);
-        if (s.any()) {
-          h0 = s.gather_begin();
-          mine = (((s.len - 1) >> 7) + 1 - h0) * p.splits;
-        }
+      int32_t mine = 0;
+      if (b0 + tid < p.B) {
+        const Sequence s = weights_sequence(p, b0 + tid);
+        if (s.any()) mine = (((s.len - 1) >> 7) + 1 - s.gather_begin()) * p.splits;
       }
       int32_t v = mine;
 #pragma unroll
@@ -131,14 +127,22 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
         if (k < warp) v += w_s[k];
         sum += w_s[k];
       }
-      int32_t at = n + v - mine;
-      for (int32_t i = 0; i < mine && at < p.max_items; ++i, ++at) {
-        const int32_t u = i / p.splits, part = i - u * p.splits, key0 = (h0 + u) * 128;
-        int32_t lo, hi;
-        seeing_tiles(p, s, key0, lo, hi);
-        const int32_t t0 = lo + (int32_t)((int64_t)(hi - lo) * part / p.splits), t1 = lo + (int32_t)((int64_t)(hi - lo) * (part + 1) / p.splits);
-        p.item[2 * (int64_t)at] = make_int4(b, key0, s.len, s.n);
-        p.item[2 * (int64_t)at + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part);
+      upto_s[tid] = v;
+      __syncthreads();
+      for (int32_t x = tid; x < sum && n + x < p.max_items; x += kWtPrep) {
+        int lo = 0, hi = min(kWtPrep, p.B - b0) - 1;   // the sequence of item x
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (upto_s[mid] > x) hi = mid; else lo = mid + 1;
+        }
+        const int32_t b = b0 + lo, i = x - (lo > 0 ? upto_s[lo - 1] : 0);
+        const Sequence s = weights_sequence(p, b);
+        const int32_t u = i / p.splits, part = i - u * p.splits, key0 = (s.gather_begin() + u) * 128;
+        int32_t r0, r1;
+        seeing_tiles(p, s, key0, r0, r1);
+        const int32_t t0 = r0 + (int32_t)((int64_t)(r1 - r0) * part / p.splits), t1 = r0 + (int32_t)((int64_t)(r1 - r0) * (part + 1) / p.splits);
+        p.item[2 * (int64_t)(n + x)] = make_int4(b, key0, s.len, s.n);
+        p.item[2 * (int64_t)(n + x) + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part);
       }
       n += sum;
     }
@@ -216,24 +220,26 @@ struct WtCfg {
   static constexpr int kDB = kV32 ? 9 : 8;
   static constexpr int kN = kBlocks ? 128 : 256;                    // query rows of a step at most
   static constexpr int kCols = kN / 2;                              // TMEM columns of an accumulator
-  static constexpr int kAccSlots = 512 / kCols;
-  static constexpr uint32_t kChunk = kN / 2 * 128;                  // bytes of a CTA's query chunk: kN / 2 rows x 64 dims
-  static constexpr int kSlots = 65536 / kChunk;                     // 64 KiB of them
+  static constexpr int kSets = 512 / (kAcc * kCols);                // steps whose accumulators it holds
+  // Query rows wait in slots of 16 KiB: of a step of N rows one, two or four
+  // 64-dim blocks of this CTA's N / 2 (so that a step of few rows takes few waits).
+  static constexpr int kSlots = kV32 ? 4 : 5;
   static constexpr uint32_t kTile = kDB * 8192;                     // a key tile: [kDB][64 keys x 64 dims] f16
   static constexpr uint32_t kRing = 2 * kTile;
-  static constexpr uint32_t kColS = kRing + kSlots * kChunk;        // [2][kN] (factor, log2 denominator, position, -)
-  static constexpr uint32_t kFac = kColS + 2 * kN * 16;             // [2][8][64] f32 a key's factors; the last: kept or not
-  static constexpr uint32_t kRed = kFac + 4096;                     // [4][64] f32
-  static constexpr uint32_t kMisc = kRed + 1024;
-  static constexpr int kFull = 0, kEmpty = kSlots, kAFull = 2 * kSlots, kAEmpty = kAFull + kAccSlots,
-                       kKFull = kAEmpty + kAccSlots, kKReady = kKFull + 2, kKEmpty = kKReady + 2, kDrain = kKEmpty + 2,
+  static constexpr uint32_t kColS = kRing + kSlots * 16384;         // [2][3][kN] f32: factor, - log2 denominator, position
+  static constexpr uint32_t kFac = kColS + 2 * 3 * kN * 4;          // [2][8][64] f32 a key's factors; the last: kept or not
+  static constexpr uint32_t kRed = kFac + 4096;                     // [2][4][64] f32
+  static constexpr uint32_t kMisc = kRed + 2048;
+  static constexpr int kFull = 0, kEmpty = kSlots, kAFull = 2 * kSlots, kAEmpty = kAFull + kSets,
+                       kKFull = kAEmpty + kSets, kKReady = kKFull + 2, kKEmpty = kKReady + 2, kDrain = kKEmpty + 2,
                        kBars = kDrain + 1;
   static constexpr uint32_t kAbort = 8 * kBars, kTmem = kAbort + 4;
-  static constexpr uint32_t kBytes = kMisc + 512;
-  static_assert(kTmem + 4 <= 512, "misc area");
+  static constexpr uint32_t kBytes = kMisc + 256;
+  static_assert(kTmem + 4 <= 256, "misc area");
   static_assert(kBytes + 1024 <= 232448u, "shared memory layout exceeds 227 KiB");
-  // rows of the step that starts with `left` rows to go
+  // rows of the step that starts with `left` rows to go, and 64-dim blocks to a slot
   static __device__ __forceinline__ int rows(int64_t left) { return left > 128 && kN == 256 ? 256 : left > 64 ? 128 : 64; }
+  static __device__ __forceinline__ int per_slot(int N) { return 256 / N; }
 };
 
 // The items of a pair, and the steps of an item (up to kN query rows each).
@@ -276,7 +282,7 @@ struct Items {
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap map16,
-                   const __grid_constant__ CUtensorMap map4) {
+                   const __grid_constant__ CUtensorMap map8, const __grid_constant__ CUtensorMap map4) {
   using Cfg = WtCfg<FMT>;
   constexpr bool kV32 = Cfg::kV32;
   pdl_launch_dependents();
@@ -285,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
   uint8_t *smem = smem_raw + pad;
   const uint32_t sbase = raw_base + pad, ring = sbase + Cfg::kRing;
-  float4 *col_s = reinterpret_cast<float4 *>(smem + Cfg::kColS);
+  float *col_s = reinterpret_cast<float *>(smem + Cfg::kColS);
   float *fac_s = reinterpret_cast<float *>(smem + Cfg::kFac);
   float *red_s = reinterpret_cast<float *>(smem + Cfg::kRed);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kMisc);
@@ -343,20 +349,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       const int32_t mine = ahead;
       ahead = items.at < items.n ? slot_of(items.na) : -1;
       if (items.empty()) continue;
-      RawRecord raw[2][4];
-      bool kept[2][4];
+      constexpr int kDeep = FMT == DSA_REC_MODEL1_584 ? 2 : kRounds;   // groups in flight (a MODEL1 share takes 9 registers)
+      RawRecord raw[kDeep][4];
+      bool kept[kDeep][4];
       auto load = [&](int k) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int32_t sid = __shfl_sync(0xffffffffu, mine, 4 * k + i);
-          kept[k & 1][i] = sid >= 0 && (int64_t)sid < p.L.num_slots;
-          const uint8_t *rec = record_ptr(p.L, kept[k & 1][i] ? sid : 0);
-          if (kept[k & 1][i])
-            kept[k & 1][i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
-          if (kept[k & 1][i]) load_record<FMT>(rec, lane, raw[k & 1][i]);
+          kept[k % kDeep][i] = sid >= 0 && (int64_t)sid < p.L.num_slots;
+          const uint8_t *rec = record_ptr(p.L, kept[k % kDeep][i] ? sid : 0);
+          if (kept[k % kDeep][i])
+            kept[k % kDeep][i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
+          if (kept[k % kDeep][i]) load_record<FMT>(rec, lane, raw[k % kDeep][i]);
         }
       };
-      load(0);
+#pragma unroll
+      for (int k = 0; k + 1 < kDeep; ++k) load(k);
       const int buf = turn & 1;
       ok = wait(Cfg::kKEmpty + buf, ((turn >> 1) & 1u) ^ 1u);
       ++turn;
@@ -366,15 +374,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       const uint32_t tile = sbase + buf * Cfg::kTile;
 #pragma unroll
       for (int k = 0; k < kRounds; ++k) {
-        if (k + 1 < kRounds) load(k + 1);
+        if (k + kDeep - 1 < kRounds) load(k + kDeep - 1);
         const int group = k * kWtRecords + pw;
         if (group >= 16) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const RawRecord &rr = raw[k & 1][i];
+          const RawRecord &rr = raw[k % kDeep][i];
           const int r = 4 * group + i, x = r & 7;
-          if (lane == 0) fac[7 * 64 + r] = kept[k & 1][i] ? 1.f : 0.f;
-          if (!kept[k & 1][i]) continue;   // (what its row of the tile holds stays in its own lane)
+          if (lane == 0) fac[7 * 64 + r] = kept[k % kDeep][i] ? 1.f : 0.f;
+          if (!kept[k % kDeep][i]) continue;   // (what its row of the tile holds stays in its own lane)
           uint32_t f[8];
           if constexpr (Cfg::kBlocks) {
 #pragma unroll
@@ -435,22 +443,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           const int64_t tile = items.c.x + items.tile + (N == 256 ? side : 0);
           const int32_t y0 = (int32_t)(tile * (Cfg::kDB * 32)) + (N == 256 ? 0 : (int32_t)side * (N / 8));
           const bool in = dbg_ok(p.status, tile >= 0 && tile < p.tiles, kDbgPartial);
-          for (int c = 0; c < Cfg::kDB && ok; ++c) {
+          const int per = Cfg::per_slot(N);
+          const uint32_t block = (uint32_t)N * 64u;   // bytes of this CTA's rows of a 64-dim block
+          for (int c = 0; c < Cfg::kDB && ok; c += per) {
             ok = wait(Cfg::kEmpty + slot, ph);
             if (!ok) break;
+            const int n = min(per, Cfg::kDB - c);
             if (side == 0) {
-              tc::mbar_expect_tx(&bars[Cfg::kFull + slot], (uint32_t)N * 128u);   // both CTAs' bytes
+              tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 2u * n * block);   // both CTAs' bytes
               filled |= 1u << slot;
               fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
             }
-            const uint32_t dst = ring + slot * Cfg::kChunk, bar = full0 + 8 * slot;
-            const int32_t y = in ? y0 + c * 32 : 0;
-            if (N == 256) {
-              tc::tma_load_pair(dst, &map16, 0, y, bar);
-            } else {
-              tc::tma_load_pair(dst, &map4, 0, y, bar);
-              if (N == 128) tc::tma_load_pair(dst + 4096, &map4, 0, y + 8, bar);
-            }
+            const uint32_t dst = ring + slot * 16384, bar = full0 + 8 * slot;
+            const void *map = N == 256 ? &map16 : N == 128 ? &map8 : &map4;
+            for (int j = 0; j < n; ++j) tc::tma_load_pair(dst + j * block, map, 0, in ? y0 + (c + j) * 32 : 0, bar);
             if (++slot == Cfg::kSlots) {
               slot = 0;
               ph ^= 1u;
@@ -482,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       constexpr uint16_t kBoth = 3;
       constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
       const uint32_t dk0 = tc::sdesc_lo(sbase, 16), dq0 = tc::sdesc_lo(ring, 16);
-      uint32_t slot = 0, ph = 0, acc = 0, ph_a = 1, turn = 0;
+      uint32_t slot = 0, ph = 0, set = 0, ph_a = 1, turn = 0;
       bool ok = true, issued = false;
       auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
       while (ok && items.next()) {
@@ -496,40 +502,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
                                  : N == 128 ? tc::idesc_f16(128, 128, false, false) : tc::idesc_f16(128, 64, false, false);
           items.advance(N);
           const bool last = items.tile >= items.end;
-#pragma unroll
-          for (int b = 0; b < Cfg::kAcc; ++b) {
-            if (!ok) break;
-            ok = here(wait(Cfg::kAEmpty + acc, ph_a));
+          ok = here(wait(Cfg::kAEmpty + set, ph_a));
+          if (!ok) break;
+          tc::tc_fence_after();
+          issued = true;
+          const int per = Cfg::per_slot(N);
+          const uint32_t block = (uint32_t)N * 4u, d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);   // (bytes >> 4)
+#pragma unroll 1
+          for (int c0 = 0; c0 < Cfg::kDB; c0 += per) {
+            ok = here(wait(Cfg::kFull + slot, ph));
             if (!ok) break;
             tc::tc_fence_after();
-            issued = true;
-            const int c0 = Cfg::kBlocks ? 2 * b : 0, c1 = Cfg::kBlocks ? (2 * b + 2 < Cfg::kDB ? 2 * b + 2 : Cfg::kDB) : Cfg::kDB;
+            const int c1 = min(c0 + per, Cfg::kDB);
+            if (tc::elect_one()) {
+#pragma unroll 1
+              for (int c = c0; c < c1; ++c) {
+                const uint32_t d = Cfg::kBlocks ? d0 + (c >> 1) * Cfg::kCols : d0;
+                const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
+                const uint32_t a = dk + c * 512u, q = dq0 + slot * 1024u + (c - c0) * block;
 #pragma unroll
-            for (int c = c0; c < c1; ++c) {
-              ok = ok && here(wait(Cfg::kFull + slot, ph));
-              if (!ok) break;
-              tc::tc_fence_after();
-              if (tc::elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  tc::mma_f16_pair(tmem + acc * Cfg::kCols, dk + ((c * 8192 + ks * 32) >> 4),
-                                   dq0 + ((slot * Cfg::kChunk + ks * 32) >> 4), kHi, idesc, (c > c0 || ks) ? 1u : 0u);
-                tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
-                if (c == c1 - 1) {
-                  tc::mma_commit_to(&bars[Cfg::kAFull + acc], kBoth);
-                  if (b == Cfg::kAcc - 1 && last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
-                }
+                for (int ks = 0; ks < 4; ++ks) tc::mma_f16_pair(d, a + 2 * ks, q + 2 * ks, kHi, idesc, !first || ks ? 1u : 0u);
               }
-              __syncwarp();
-              if (++slot == Cfg::kSlots) {
-                slot = 0;
-                ph ^= 1u;
+              tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+              if (c1 == Cfg::kDB) {
+                tc::mma_commit_to(&bars[Cfg::kAFull + set], kBoth);
+                if (last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
               }
             }
-            if (++acc == Cfg::kAccSlots) {
-              acc = 0;
-              ph_a ^= 1u;
+            __syncwarp();
+            if (++slot == Cfg::kSlots) {
+              slot = 0;
+              ph ^= 1u;
             }
+          }
+          if (++set == Cfg::kSets) {
+            set = 0;
+            ph_a ^= 1u;
           }
         }
       }
@@ -546,20 +554,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
     const uint32_t aempty0 = lead(Cfg::kAEmpty), kempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kKEmpty]), side);
-    uint32_t acc = 0, ph_a = 0, turn = 0, cb = 0;
-    // constants of the query rows of a step, a row to a thread
-    auto column = [&](int N) {
-      const int64_t r = (int64_t)items.tile * 128 + tid;
-      float4 v = make_float4(0.f, INFINITY, __int_as_float(INT32_MIN), 0.f);
-      if (tid < N && r < min(items.rows, (int64_t)items.end * 128)) {
-        const float2 x = __ldcg(p.row + ((int64_t)items.c.x + items.tile) * 128 + tid);
-        v = make_float4(x.x, x.y, __int_as_float(items.a.z - items.a.w + (int32_t)((uint32_t)r / (uint32_t)p.H)), 0.f);
+    uint32_t set = 0, ph_a = 0, turn = 0, cb = 0, rb = 0;
+    // The constants of a step's query rows, a row to a thread: loaded one step
+    // ahead, the first ones of the next item behind the last step of this one.
+    float2 ahead = make_float2(0.f, 0.f);
+    int32_t ahead_place = INT32_MIN;
+    auto fetch = [&](const int4 &a, int32_t base, int32_t tile, int32_t end) {
+      const int64_t r = (int64_t)tile * 128 + tid;
+      ahead = make_float2(0.f, INFINITY);
+      ahead_place = INT32_MIN;      // no such row: sees nothing
+      if (tid < Cfg::kN && r < min((int64_t)a.w * p.H, (int64_t)end * 128)) {
+        ahead = __ldcg(p.row + ((int64_t)base + tile) * 128 + tid);
+        ahead_place = a.z - a.w + (int32_t)((uint32_t)r / (uint32_t)p.H);
       }
-      return v;
     };
+    if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
     while (items.next()) {
       const int32_t at = items.a.y + 64 * (int32_t)side + key;   // list position of the thread's key
-      float total = 0.f;
+      const bool writes = up == 0 && half == 0 && at < items.a.z;
+      float total = 0.f, before = 0.f;
+      if (writes && p.splits == 1 && p.in) before = p.in[(int64_t)items.a.x * p.in_st + at];
       bool kept = false;
       if (!items.empty()) {
         const int buf = turn & 1;
@@ -567,108 +581,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
         ++turn;
         const float *fac = fac_s + buf * 512 + key;
         kept = fac[7 * 64] != 0.f;
-        float s[Cfg::kAcc];
+        F2 s[Cfg::kAcc];
 #pragma unroll
-        for (int b = 0; b < Cfg::kAcc; ++b) s[b] = kept ? fac[b * 64] : 0.f;
+        for (int b = 0; b < Cfg::kAcc; ++b) {
+          const float f = kept ? fac[b * 64] : 0.f;
+          s[b] = f2(f, f);
+        }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_remote(kempty0 + 8 * buf);   // the factors are read
         int N;
         while (items.next_step(N)) {
-          if (tid < N) col_s[cb * Cfg::kN + tid] = column(N);
+          float *col = col_s + cb * (3 * Cfg::kN);
+          cb ^= 1u;
+          if (tid < Cfg::kN) {
+            col[tid] = ahead.x;
+            col[Cfg::kN + tid] = -ahead.y;
+            reinterpret_cast<int32_t *>(col)[2 * Cfg::kN + tid] = ahead_place;
+          }
           sm_bar();
           // every row there and every key before every row's place (and after its window): no tests
           const int64_t r0 = (int64_t)items.tile * 128;
           const int32_t p0 = items.a.z - items.a.w + (int32_t)((uint32_t)r0 / (uint32_t)p.H);
           const int32_t p1 = items.a.z - items.a.w + (int32_t)((uint32_t)(r0 + N - 1) / (uint32_t)p.H);
           const bool all = items.left() >= N && p0 >= items.a.y + 127 && (p.window == 0 || p1 - p.window < items.a.y);
+          items.advance(N);
+          if (items.tile < items.end) fetch(items.a, items.c.x, items.tile, items.end);
+          else if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
           const int first = up * (N / 2) + half * (N / 4);   // the thread's rows: N / 4 of them from here
-          const float4 *col = col_s + cb * Cfg::kN + first;
-          cb ^= 1u;
-          // the step's accumulators, ring slots acc .. acc + kAcc - 1
-#pragma unroll
-          for (int k = 0; k < Cfg::kAcc; ++k) {
-            const uint32_t slot = (acc + k) % Cfg::kAccSlots;
-            wait(Cfg::kAFull + slot, ph_a ^ (acc + k >= Cfg::kAccSlots ? 1u : 0u));
-          }
+          wait(Cfg::kAFull + set, ph_a);
           tc::tc_fence_after();
-          // 16 (a block's accumulators together) or 32 rows at a time
-          constexpr int kGroup = Cfg::kBlocks ? 16 : 32;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t c0 = tl + set * (Cfg::kAcc * Cfg::kCols) + half * (N / 4);
+          F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
-          for (int g = 0; g < N / 4; g += kGroup) {
-            const uint32_t c = tl + half * (N / 4) + g;
-            float x[kGroup];
-            if constexpr (!Cfg::kBlocks) {
-              uint32_t d[2][16];   // (16 rows of N / 4 = 16: the second half is not used)
-              DSA_TMEM_LD16_NOWAIT(c + acc * Cfg::kCols, d[0]);
-              DSA_TMEM_LD16_NOWAIT(c + acc * Cfg::kCols + (N == 64 ? 0 : 16), d[1]);
-              DSA_TMEM_WAIT32(d[0], d[1]);
+          for (int g = 0; g < N / 4; g += 16) {   // 16 rows at a time
+            uint32_t d[Cfg::kAcc == 1 ? 1 : 2][16];
+            F2 x[8];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(d[i / 16][i % 16]) * s[0];
-            } else {
-#pragma unroll
-              for (int k = 0; k < Cfg::kAcc; k += 2) {
-                uint32_t d[2][16];
-                DSA_TMEM_LD16_NOWAIT(c + (acc + k) % Cfg::kAccSlots * Cfg::kCols, d[0]);
-                DSA_TMEM_LD16_NOWAIT(c + (acc + (k + 1 < Cfg::kAcc ? k + 1 : k)) % Cfg::kAccSlots * Cfg::kCols, d[1]);
+            for (int k = 0; k < Cfg::kAcc; k += 2) {
+              DSA_TMEM_LD16_NOWAIT(c0 + k * Cfg::kCols + g, d[0]);
+              if constexpr (Cfg::kAcc == 1) {
+                DSA_TMEM_WAIT32(d[0], d[0]);
+              } else {
+                DSA_TMEM_LD16_NOWAIT(c0 + (k + 1 < Cfg::kAcc ? k + 1 : k) * Cfg::kCols + g, d[1]);
                 DSA_TMEM_WAIT32(d[0], d[1]);
+              }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float v = __uint_as_float(d[0][i]);
-                  x[i] = k == 0 ? v * s[0] : fmaf(v, s[k], x[i]);
-                  if (k + 1 < Cfg::kAcc) x[i] = fmaf(__uint_as_float(d[1][i]), s[k + 1 < Cfg::kAcc ? k + 1 : 0], x[i]);
-                }
+              for (int i = 0; i < 8; ++i) {
+                const F2 v = f2(__uint_as_float(d[0][2 * i]), __uint_as_float(d[0][2 * i + 1]));
+                x[i] = k == 0 ? f2_mul(v, s[0]) : f2_fma(v, s[k], x[i]);
+                if constexpr (Cfg::kAcc > 1)
+                  if (k + 1 < Cfg::kAcc)
+                    x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k + 1 < Cfg::kAcc ? k + 1 : 0], x[i]);
               }
             }
-            if (g + kGroup >= N / 4) {   // read: the slots are free again
+            if (g + 16 >= N / 4) {   // read: the accumulators are free again
               tc::tc_fence_before();
               __syncwarp();
-              if (lane < Cfg::kAcc) tc::mbar_arrive_remote(aempty0 + 8 * ((acc + lane) % Cfg::kAccSlots));
+              if (lane == 0) tc::mbar_arrive_remote(aempty0 + 8 * set);
             }
-            const int most = min(kGroup, N / 4);
+            const float4 *ca = reinterpret_cast<const float4 *>(col + first + g), *cl = ca + Cfg::kN / 4;
+            const int4 *cp = reinterpret_cast<const int4 *>(cl + Cfg::kN / 4);
 #pragma unroll
-            for (int h = 0; h < kGroup / 16; ++h) {
-              if (16 * h >= most) break;
-              if (all) {
+            for (int i = 0; i < 4; ++i) {
+              const float4 ka = ca[i], kl = cl[i];
+              const F2 y0 = f2_fma(x[2 * i], f2(ka.x, ka.y), f2(kl.x, kl.y));
+              const F2 y1 = f2_fma(x[2 * i + 1], f2(ka.z, ka.w), f2(kl.z, kl.w));
+              float e[4];
+              f2_get(y0, e[0], e[1]);
+              f2_get(y1, e[2], e[3]);
 #pragma unroll
-                for (int i = 16 * h; i < 16 * h + 16; ++i) {
-                  const float2 k = *reinterpret_cast<const float2 *>(col + g + i);
-                  sum[i & 3] += tc::ex2(fmaf(x[i], k.x, -k.y));
-                }
-              } else {
+              for (int j = 0; j < 4; ++j) e[j] = tc::ex2(e[j]);
+              if (!all) {
+                const int4 kp = cp[i];
+                const int32_t place[4] = {kp.x, kp.y, kp.z, kp.w};
 #pragma unroll
-                for (int i = 16 * h; i < 16 * h + 16; ++i) {
-                  const float4 k = col[g + i];
-                  const int32_t place = __float_as_int(k.z);
-                  const bool sees = at <= place && (p.window == 0 || at > place - p.window);
-                  const float e = tc::ex2(fmaf(x[i], k.x, -k.y));
-                  sum[i & 3] += sees ? e : 0.f;
-                }
+                for (int j = 0; j < 4; ++j)
+                  if (!(at <= place[j] && (p.window == 0 || at > place[j] - p.window))) e[j] = 0.f;
               }
+              sum[0] = f2_add(sum[0], f2(e[0], e[1]));
+              sum[1] = f2_add(sum[1], f2(e[2], e[3]));
             }
           }
-          acc += Cfg::kAcc;
-          if (acc >= Cfg::kAccSlots) {
-            acc -= Cfg::kAccSlots;
+          if (++set == Cfg::kSets) {
+            set = 0;
             ph_a ^= 1u;
           }
-          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          items.advance(N);
+          float a0, a1;
+          f2_get(f2_add(sum[0], sum[1]), a0, a1);
+          total += a0 + a1;
         }
+      } else if (items.at < items.n) {
+        fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
       }
-      // the four threads of a key
-      red_s[(2 * up + half) * 64 + key] = total;
+      // the four threads of a key (the sums of the item before have been read: a barrier ago)
+      float *red = red_s + rb * 256;
+      rb ^= 1u;
+      red[(2 * up + half) * 64 + key] = total;
       sm_bar();
-      if (up == 0 && half == 0 && at < items.a.z) {
-        const float t = kept ? (red_s[key] + red_s[64 + key]) + (red_s[128 + key] + red_s[192 + key]) : 0.f;
+      if (writes) {
+        const float t = kept ? (red[key] + red[64 + key]) + (red[128 + key] + red[192 + key]) : 0.f;
         const int64_t b = items.a.x;
-        if (p.splits > 1) {
-          __stcg(p.part + ((int64_t)items.c.w * p.B + b) * p.L.width + at, t);
-        } else {
-          p.out[b * p.out_st + at] = (p.in ? p.in[b * p.in_st + at] : 0.f) + t;
-        }
+        if (p.splits > 1) __stcg(p.part + ((int64_t)items.c.w * p.B + b) * p.L.width + at, t);
+        else p.out[b * p.out_st + at] = before + t;
       }
-      sm_bar();
     }
   }
 
@@ -735,14 +750,14 @@ cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t s
   using Cfg = WtCfg<FMT>;
   cudaError_t e = weights_ready<FMT>();
   if (e != cudaSuccess) return e;
-  CUtensorMap map16, map4;
+  CUtensorMap map16, map8, map4;
   const int64_t bytes = (int64_t)p.tiles * Cfg::kDB * 16384;
-  if (!chunk_map(p.image, bytes, 32, &map16) || !chunk_map(p.image, bytes, 8, &map4)) return cudaErrorNotSupported;
+  if (!chunk_map(p.image, bytes, 32, &map16) || !chunk_map(p.image, bytes, 16, &map8) || !chunk_map(p.image, bytes, 8, &map4)) return cudaErrorNotSupported;
   const unsigned blocks = 1 + (unsigned)std::min(p.tiles, 8 * 152);
   weights_prepare_kernel<Cfg::kV32><<<blocks, kWtPrep, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_dependent(config(2u * pairs, kWtThreads, Cfg::kBytes + 1024, st), weights_kernel<FMT>, p, map16, map4);
+  e = launch_dependent(config(2u * pairs, kWtThreads, Cfg::kBytes + 1024, st), weights_kernel<FMT>, p, map16, map8, map4);
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t c = config((unsigned)((p.L.width + 255) / 256), 256, 0, st);
   c.gridDim.y = (unsigned)p.B;
