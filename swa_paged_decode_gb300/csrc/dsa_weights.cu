@@ -142,7 +142,10 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
         seeing_tiles(p, s, key0, r0, r1);
         const int32_t t0 = r0 + (int32_t)((int64_t)(r1 - r0) * part / p.splits), t1 = r0 + (int32_t)((int64_t)(r1 - r0) * (part + 1) / p.splits);
         p.item[2 * (int64_t)(n + x)] = make_int4(b, key0, s.len, s.n);
-        p.item[2 * (int64_t)(n + x) + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part);
+        // whether every row of the range sees every key (bit 31: none need be masked)
+        const int64_t first = s.row_position(p.H, 128 * (int64_t)t0), last = s.row_position(p.H, min(128 * (int64_t)t1, (int64_t)s.n * p.H) - 1);
+        const bool all = t1 > t0 && first >= key0 + 127 && (p.window == 0 || last - p.window < key0);
+        p.item[2 * (int64_t)(n + x) + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part | (all ? INT32_MIN : 0));
       }
       n += sum;
     }
@@ -170,7 +173,12 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
     const int32_t rows = s.tile_rows(p.H, i);
     uint8_t *base = p.image + (int64_t)tile * (kDB * 16384);
 #pragma unroll 2
-    for (int32_t r = warp; r < rows; r += kWtPrep / 32) {
+    for (int32_t r = warp; r < 128; r += kWtPrep / 32) {
+      if (r >= rows) {   // behind the sequence's last row: zeros, up to what a step may take
+        uint8_t *pad = base + (r >> 3) * 1024 + (r & 7) * 128;
+        for (int c = lane; c < 8 * kDB; c += 32) *reinterpret_cast<uint4 *>(pad + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const uint32_t gr = (uint32_t)s.s0 * p.H + 128u * i + r, t = gr / (uint32_t)p.H, h = gr - t * (uint32_t)p.H;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
       const uint4 qa = ld_row(src + 2 * lane), qb = ld_row(src + 2 * lane + 1);
@@ -209,8 +217,64 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------ weigh
-constexpr int kWtThreads = 512;   // warps 0-7 exponentials, 8 MMA, 9 copies, 10-15 records
-constexpr int kWtRecords = 6;
+constexpr int kWtThreads = 640;   // warps 0-7 exponentials, 8 MMA, 9-11 copies, 12-19 records
+constexpr int kWtCopies = 3, kWtRecords = 8;
+
+// A lane's 16 values of a record with one factor 2^E per key, in f16 and exact as
+// far as the header says: codes times a power of two (or an e4m3 scale), so the
+// products are taken in f16 (a third of the instructions of the way through
+// fp32, which blocks far below the row's largest and bf16 parts take). -> E
+template <int FMT>
+__device__ __forceinline__ int key_halves(const RawRecord &r, int lane, uint32_t (&f)[8]) {
+  const int share = record_exponent<FMT>(r, lane);
+  const int E = min(max(__reduce_max_sync(0xffffffffu, share), -kPfRange), kPfRange) - kPfTop;
+  if constexpr (FMT == DSA_REC_NVFP4_288) {
+    const bool nan = (r.s & 0x7Fu) == 0x7Fu;
+    const float m = nan ? __uint_as_float(0x7FC00000u) : e4m3_to_f32(r.s) * __uint_as_float((uint32_t)(127 - E) << 23);
+    const uint32_t m2 = share == kZeroShare && !nan ? 0u : tc::pack_f16x2(m, m);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t c[4];
+      tc::e2m1x8_to_f16x8(r.w[h], c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[4 * h + k] = tc::hmul2(c[k], m2);
+    }
+  } else {
+    const bool bf16_part = FMT == DSA_REC_MODEL1_584 && lane >= 28;
+    const int k = (int)(r.s & 0xFFu) - 127 - E;   // the block's power of two, in units of 2^E
+    const bool far = !bf16_part && share != kZeroShare && k < -24;
+    if (__any_sync(0xffffffffu, far)) {
+      float v[16], t0, t1;
+      expand_record<FMT>(r, lane, v, t0, t1);
+      const float down = __uint_as_float((uint32_t)(127 - E) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = tc::pack_f16x2(v[2 * i] * down, v[2 * i + 1] * down);
+    } else if (bf16_part) {
+      const float down = __uint_as_float((uint32_t)(127 - E) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = tc::pack_f16x2(bf16_bits_to_f32(r.w[i] & 0xFFFFu) * down, __uint_as_float(r.w[i] & 0xFFFF0000u) * down);
+    } else {
+      uint32_t m = (r.s & 0xFFu) == 0xFFu ? 0x7E00u : share == kZeroShare ? 0u : k >= -14 ? (uint32_t)(min(k, 15) + 15) << 10 : 1u << (k + 24);
+      m |= m << 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        tc::e4m3x4_to_f16x4(r.w[i], lo, hi);
+        f[2 * i] = tc::hmul2(lo, m);
+        f[2 * i + 1] = tc::hmul2(hi, m);
+      }
+    }
+  }
+  return E;
+}
+
+// Waits for the warp's outstanding TMEM loads; v is tied to the wait.
+#define DSA_TMEM_WAIT16(v)                                                                                            \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                                       \
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),      \
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]) \
+               :                                                                                                      \
+               : "memory")
 
 template <int FMT>
 struct WtCfg {
@@ -330,89 +394,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   };
   auto lead = [&](int b) { return tc::mapa(tc::smem_u32(&bars[b]), 0); };
 
-  if (warp >= 10) {
+  if (warp >= 12) {
     // ======================================================== records
-    // 64 keys of an item to this CTA, in groups of 4 that the warps take in turn
-    // (two or three each), a group's loads in flight while the one before it is
-    // converted; the next item's records are on their way to L2 meanwhile.
-    const int pw = warp - 10;
-    constexpr int kRounds = (16 + kWtRecords - 1) / kWtRecords;
+    // 64 keys of an item to this CTA, 8 to a warp, their loads in flight
+    // together. What is known ahead: the item after next, the slots of the next
+    // two, and the records of the next one are on their way to L2 for a whole
+    // item's time. A warp runs one instruction in five cycles or so at best, so
+    // what 8 lanes can find for 8 keys (addresses) they do.
+    const int pw = warp - 12;
     bool ok = true;
     uint32_t turn = 0;
-    auto slot_of = [&](const int4 &a) {   // lane 4 k + i: the slot of key i of the warp's group k
-      const int r = 4 * ((lane >> 2) * kWtRecords + pw) + (lane & 3);
-      const int32_t j = a.y + 64 * (int32_t)side + r;
-      return lane < 4 * kRounds && r < 64 && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
+    auto item_at = [&](int32_t i) { return i < items.n ? __ldcg(p.item + 2 * (int64_t)i) : make_int4(0, 0, 0, 0); };
+    auto slot_of = [&](const int4 &a) {   // lane l < 8: the slot of key 8 pw + l (a list of length 0 has none)
+      const int32_t j = a.y + 64 * (int32_t)side + 8 * pw + lane;
+      return lane < 8 && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
     };
-    int32_t ahead = items.at < items.n ? slot_of(items.na) : -1;
+    // its record, and whether it is kept; one that is not reads slot 0's, which counts for nothing
+    auto record_of = [&](int32_t slot, uint32_t &kept) {
+      bool k = slot >= 0 && (int64_t)slot < p.L.num_slots;
+      const uint8_t *rec = record_ptr(p.L, k ? slot : 0);
+      if (k && !dbg_ok(p.status, rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord)) {
+        k = false;
+        rec = p.L.base;
+      }
+      kept = __ballot_sync(0xffffffffu, k);
+      return rec;
+    };
+    int32_t slot2 = slot_of(item_at(pair + pairs));
+    uint32_t kept1;
+    const uint8_t *rec1 = record_of(slot_of(item_at(pair)), kept1);
+    int4 item3 = item_at(pair + 2 * pairs);
+    int32_t i3 = pair + 3 * pairs;
+    const uint32_t lane_at = (uint32_t)(lane >> 2) * 8192u + (uint32_t)pw * 1024u;
     while (ok && items.next()) {
-      const int32_t mine = ahead;
-      ahead = items.at < items.n ? slot_of(items.na) : -1;
-      if (items.empty()) continue;
-      constexpr int kDeep = FMT == DSA_REC_MODEL1_584 ? 2 : kRounds;   // groups in flight (a MODEL1 share takes 9 registers)
-      RawRecord raw[kDeep][4];
-      bool kept[kDeep][4];
-      auto load = [&](int k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t sid = __shfl_sync(0xffffffffu, mine, 4 * k + i);
-          kept[k % kDeep][i] = sid >= 0 && (int64_t)sid < p.L.num_slots;
-          const uint8_t *rec = record_ptr(p.L, kept[k % kDeep][i] ? sid : 0);
-          if (kept[k % kDeep][i])
-            kept[k % kDeep][i] = dbg_ok(p.status, rec >= p.L.base && rec + p.L.rec <= p.L.base + p.L.extent, kDbgRecord);
-          if (kept[k % kDeep][i]) load_record<FMT>(rec, lane, raw[k % kDeep][i]);
-        }
+      const uint8_t *rec0 = rec1;
+      const uint32_t kept0 = kept1;
+      constexpr int kDeep = FMT == DSA_REC_MODEL1_584 ? 4 : 8;   // records in flight (a MODEL1 share takes 9 registers)
+      RawRecord raw[kDeep];
+      auto load = [&](int i) {
+        const uint8_t *rec = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec0), i));
+        load_record<FMT>(rec, lane, raw[i % kDeep]);
       };
+      if (!items.empty()) {
 #pragma unroll
-      for (int k = 0; k + 1 < kDeep; ++k) load(k);
+        for (int i = 0; i < kDeep; ++i) load(i);
+      }
+      rec1 = record_of(slot2, kept1);
+      slot2 = slot_of(item3);
+      item3 = item_at(i3);
+      i3 += pairs;
+      if (items.empty()) continue;
+      {   // the next records to L2, a line of 128 bytes to a lane
+        const uint8_t *rec = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec1), lane >> 2));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int line = 128 * ((lane & 3) + 4 * b);
+          if (line < p.L.rec && ((kept1 >> (lane >> 2)) & 1u)) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + line));
+        }
+      }
       const int buf = turn & 1;
       ok = wait(Cfg::kKEmpty + buf, ((turn >> 1) & 1u) ^ 1u);
       ++turn;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      float *fac = fac_s + buf * 512;
-      const uint32_t tile = sbase + buf * Cfg::kTile;
+      float *fac = fac_s + buf * 512 + 8 * pw;
+      const uint32_t tile = sbase + buf * Cfg::kTile + lane_at;
+      if (lane < 8) fac[7 * 64 + lane] = (kept0 >> lane) & 1u ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < kRounds; ++k) {
-        if (k + kDeep - 1 < kRounds) load(k + kDeep - 1);
-        const int group = k * kWtRecords + pw;
-        if (group >= 16) break;
+      for (int i = 0; i < 8; ++i) {   // key 8 pw + i: row i of the 8-row group pw
+        const RawRecord &rr = raw[i % kDeep];
+        uint32_t f[8];
+        if constexpr (Cfg::kBlocks) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const RawRecord &rr = raw[k % kDeep][i];
-          const int r = 4 * group + i, x = r & 7;
-          if (lane == 0) fac[7 * 64 + r] = kept[k % kDeep][i] ? 1.f : 0.f;
-          if (!kept[k % kDeep][i]) continue;   // (what its row of the tile holds stays in its own lane)
-          uint32_t f[8];
-          if constexpr (Cfg::kBlocks) {
-#pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) tc::e4m3x4_to_f16x4(rr.w[k2], f[2 * k2], f[2 * k2 + 1]);
-            if ((lane & 7) == 0) fac[(lane >> 3) * 64 + r] = __uint_as_float(rr.s);
-            if constexpr (kV32) {
-              const uint32_t m = rr.t & 0x7FFF7FFFu;
-              const uint32_t mb = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-              const int E = min(max((int)(mb >> 7) - 127, -kPfRange), kPfRange) - kPfTop;
-              const float down = __uint_as_float((uint32_t)(127 - E) << 23);
-              if (lane == 0) fac[4 * 64 + r] = __uint_as_float((uint32_t)(127 + E) << 23);
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + 8 * 8192 + (r >> 3) * 1024 + x * 128 +
-                                                          (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)),
-                           "r"(tc::pack_f16x2(bf16_bits_to_f32(rr.t & 0xFFFFu) * down, bf16_bits_to_f32(rr.t >> 16) * down))
-                           : "memory");
-            }
-          } else {
-            const int e = __reduce_max_sync(0xffffffffu, record_exponent<FMT>(rr, lane));
-            const int E = min(max(e, -kPfRange), kPfRange) - kPfTop;
+          for (int k = 0; k < 4; ++k) tc::e4m3x4_to_f16x4(rr.w[k], f[2 * k], f[2 * k + 1]);
+          if ((lane & 7) == 0) fac[(lane >> 3) * 64 + i] = __uint_as_float(rr.s);
+          if constexpr (kV32) {
+            const uint32_t m = rr.t & 0x7FFF7FFFu;
+            const uint32_t mb = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+            const int E = min(max((int)(mb >> 7) - 127, -kPfRange), kPfRange) - kPfTop;
             const float down = __uint_as_float((uint32_t)(127 - E) << 23);
-            if (lane == 0) fac[r] = __uint_as_float((uint32_t)(127 + E) << 23);
-            float v[16], t0, t1;
-            expand_record<FMT>(rr, lane, v, t0, t1);
-#pragma unroll
-            for (int k2 = 0; k2 < 8; ++k2) f[k2] = tc::pack_f16x2(v[2 * k2] * down, v[2 * k2 + 1] * down);
+            if (lane == 0) fac[4 * 64 + i] = __uint_as_float((uint32_t)(127 + E) << 23);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + buf * Cfg::kTile + 8 * 8192 + pw * 1024 + i * 128 +
+                                                        (((lane >> 2) ^ i) << 4) + 4 * (lane & 3)),
+                         "r"(tc::pack_f16x2(bf16_bits_to_f32(rr.t & 0xFFFFu) * down, bf16_bits_to_f32(rr.t >> 16) * down))
+                         : "memory");
           }
-          const uint32_t row = tile + (lane >> 2) * 8192 + (r >> 3) * 1024 + x * 128;
-          tc::st_shared_v4(row + (((2 * (lane & 3)) ^ x) << 4), f[0], f[1], f[2], f[3]);
-          tc::st_shared_v4(row + (((2 * (lane & 3) + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+        } else {
+          const int E = key_halves<FMT>(rr, lane, f);
+          if (lane == 0) fac[i] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
+        if (kDeep < 8 && i + kDeep < 8) load(i + kDeep);
+        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3)) ^ i) << 4), f[0], f[1], f[2], f[3]);
+        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3) + 1) ^ i) << 4), f[4], f[5], f[6], f[7]);
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -420,19 +493,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
         tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars[Cfg::kKReady + buf]), side));
         tc::mbar_arrive_remote(lead(Cfg::kKFull + buf));
       }
-      if (ahead >= 0 && (int64_t)ahead < p.L.num_slots) {
-        const uint8_t *rec = record_ptr(p.L, ahead);
-#pragma unroll
-        for (int b = 0; b < 768; b += 128)
-          if (b < p.L.rec) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + b));
-      }
     }
     // the tiles' last releases have arrived before the pair ends
     for (int k = 0; k < 2 && ok; ++k, ++turn) ok = wait(Cfg::kKEmpty + (turn & 1), ((turn >> 1) & 1u) ^ 1u);
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     // ======================================================== query chunks
     if (lane == 0) {
       uint32_t slot = 0, ph = 1;
+      int turn = warp - 9;   // 0: this warp's slot (one thread would take longer for a slot than its products do)
       bool ok = true;
       uint32_t filled = 0, fill_ph = 0;
       const uint32_t full0 = lead(Cfg::kFull);
@@ -446,17 +514,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           const int per = Cfg::per_slot(N);
           const uint32_t block = (uint32_t)N * 64u;   // bytes of this CTA's rows of a 64-dim block
           for (int c = 0; c < Cfg::kDB && ok; c += per) {
-            ok = wait(Cfg::kEmpty + slot, ph);
-            if (!ok) break;
-            const int n = min(per, Cfg::kDB - c);
-            if (side == 0) {
-              tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 2u * n * block);   // both CTAs' bytes
-              filled |= 1u << slot;
-              fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+            if (turn == 0) {
+              turn = kWtCopies;
+              ok = wait(Cfg::kEmpty + slot, ph);
+              if (!ok) break;
+              const int n = min(per, Cfg::kDB - c);
+              if (side == 0) {
+                tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 2u * n * block);   // both CTAs' bytes
+                filled |= 1u << slot;
+                fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+              }
+              const uint32_t dst = ring + slot * 16384, bar = full0 + 8 * slot;
+              const void *map = N == 256 ? &map16 : N == 128 ? &map8 : &map4;
+              for (int j = 0; j < n; ++j) tc::tma_load_pair(dst + j * block, map, 0, in ? y0 + (c + j) * 32 : 0, bar);
             }
-            const uint32_t dst = ring + slot * 16384, bar = full0 + 8 * slot;
-            const void *map = N == 256 ? &map16 : N == 128 ? &map8 : &map4;
-            for (int j = 0; j < n; ++j) tc::tma_load_pair(dst + j * block, map, 0, in ? y0 + (c + j) * 32 : 0, bar);
+            --turn;
             if (++slot == Cfg::kSlots) {
               slot = 0;
               ph ^= 1u;
@@ -498,43 +570,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
         ++turn;
         int N;
         while (ok && items.next_step(N)) {
-          const uint32_t idesc = N == 256 ? tc::idesc_f16(128, 256, false, false)
-                                 : N == 128 ? tc::idesc_f16(128, 128, false, false) : tc::idesc_f16(128, 64, false, false);
           items.advance(N);
           const bool last = items.tile >= items.end;
           ok = here(wait(Cfg::kAEmpty + set, ph_a));
           if (!ok) break;
           tc::tc_fence_after();
           issued = true;
-          const int per = Cfg::per_slot(N);
-          const uint32_t block = (uint32_t)N * 4u, d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);   // (bytes >> 4)
-#pragma unroll 1
-          for (int c0 = 0; c0 < Cfg::kDB; c0 += per) {
-            ok = here(wait(Cfg::kFull + slot, ph));
-            if (!ok) break;
-            tc::tc_fence_after();
-            const int c1 = min(c0 + per, Cfg::kDB);
-            if (tc::elect_one()) {
-#pragma unroll 1
-              for (int c = c0; c < c1; ++c) {
-                const uint32_t d = Cfg::kBlocks ? d0 + (c >> 1) * Cfg::kCols : d0;
-                const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
-                const uint32_t a = dk + c * 512u, q = dq0 + slot * 1024u + (c - c0) * block;
+          const uint32_t d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);
+          auto products = [&](auto rows) {   // unrolled for each N: a slot is to go out in less time than its products take
+            constexpr int kRows = decltype(rows)::value, kPer = 256 / kRows;
+            constexpr uint32_t kId = tc::idesc_f16(128, kRows, false, false);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) tc::mma_f16_pair(d, a + 2 * ks, q + 2 * ks, kHi, idesc, !first || ks ? 1u : 0u);
+            for (int c0 = 0; c0 < Cfg::kDB; c0 += kPer) {
+              if (!here(wait(Cfg::kFull + slot, ph))) return false;
+              tc::tc_fence_after();
+              if (tc::elect_one()) {
+                const uint32_t q = dq0 + slot * 1024u;
+#pragma unroll
+                for (int j = 0; j < kPer && c0 + j < Cfg::kDB; ++j) {
+                  const int c = c0 + j;
+                  const uint32_t d = Cfg::kBlocks ? d0 + (c >> 1) * Cfg::kCols : d0;
+                  const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
+#pragma unroll
+                  for (int ks = 0; ks < 4; ++ks)
+                    tc::mma_f16_pair(d, dk + c * 512u + 2 * ks, q + j * (kRows * 4u) + 2 * ks, kHi, kId, !first || ks ? 1u : 0u);
+                }
+                tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+                if (c0 + kPer >= Cfg::kDB) {
+                  tc::mma_commit_to(&bars[Cfg::kAFull + set], kBoth);
+                  if (last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
+                }
               }
-              tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
-              if (c1 == Cfg::kDB) {
-                tc::mma_commit_to(&bars[Cfg::kAFull + set], kBoth);
-                if (last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
+              __syncwarp();
+              if (++slot == Cfg::kSlots) {
+                slot = 0;
+                ph ^= 1u;
               }
             }
-            __syncwarp();
-            if (++slot == Cfg::kSlots) {
-              slot = 0;
-              ph ^= 1u;
-            }
-          }
+            return true;
+          };
+          if (N == 64) ok = products(std::integral_constant<int, 64>());
+          else if (Cfg::kN == 128 || N == 128) ok = products(std::integral_constant<int, 128>());
+          else ok = products(std::integral_constant<int, Cfg::kN>());
           if (++set == Cfg::kSets) {
             set = 0;
             ph_a ^= 1u;
@@ -559,21 +636,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     // ahead, the first ones of the next item behind the last step of this one.
     float2 ahead = make_float2(0.f, 0.f);
     int32_t ahead_place = INT32_MIN;
-    auto fetch = [&](const int4 &a, int32_t base, int32_t tile, int32_t end) {
-      const int64_t r = (int64_t)tile * 128 + tid;
+    auto fetch = [&](const int4 &a, int32_t base, int32_t tile, int32_t end, int32_t flags) {
+      const uint32_t r = (uint32_t)tile * 128u + tid;
       ahead = make_float2(0.f, INFINITY);
-      ahead_place = INT32_MIN;      // no such row: sees nothing
-      if (tid < Cfg::kN && r < min((int64_t)a.w * p.H, (int64_t)end * 128)) {
+      ahead_place = INT32_MIN;      // no such row: sees nothing, and weighs nothing (its image is zeros)
+      if (tid < Cfg::kN && r < min((uint32_t)a.w * (uint32_t)p.H, (uint32_t)end * 128u)) {
         ahead = __ldcg(p.row + ((int64_t)base + tile) * 128 + tid);
-        ahead_place = a.z - a.w + (int32_t)((uint32_t)r / (uint32_t)p.H);
+        if (flags >= 0) ahead_place = a.z - a.w + (int32_t)(r / (uint32_t)p.H);
       }
     };
-    if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
+    if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
     while (items.next()) {
       const int32_t at = items.a.y + 64 * (int32_t)side + key;   // list position of the thread's key
       const bool writes = up == 0 && half == 0 && at < items.a.z;
       float total = 0.f, before = 0.f;
       if (writes && p.splits == 1 && p.in) before = p.in[(int64_t)items.a.x * p.in_st + at];
+      const bool all = items.c.w < 0;                            // every row sees every key
       bool kept = false;
       if (!items.empty()) {
         const int buf = turn & 1;
@@ -599,46 +677,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
             reinterpret_cast<int32_t *>(col)[2 * Cfg::kN + tid] = ahead_place;
           }
           sm_bar();
-          // every row there and every key before every row's place (and after its window): no tests
-          const int64_t r0 = (int64_t)items.tile * 128;
-          const int32_t p0 = items.a.z - items.a.w + (int32_t)((uint32_t)r0 / (uint32_t)p.H);
-          const int32_t p1 = items.a.z - items.a.w + (int32_t)((uint32_t)(r0 + N - 1) / (uint32_t)p.H);
-          const bool all = items.left() >= N && p0 >= items.a.y + 127 && (p.window == 0 || p1 - p.window < items.a.y);
           items.advance(N);
-          if (items.tile < items.end) fetch(items.a, items.c.x, items.tile, items.end);
-          else if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
+          if (items.tile < items.end) fetch(items.a, items.c.x, items.tile, items.end, items.c.w);
+          else if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
           const int first = up * (N / 2) + half * (N / 4);   // the thread's rows: N / 4 of them from here
           wait(Cfg::kAFull + set, ph_a);
           tc::tc_fence_after();
           const uint32_t c0 = tl + set * (Cfg::kAcc * Cfg::kCols) + half * (N / 4);
           F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll 1
-          for (int g = 0; g < N / 4; g += 16) {   // 16 rows at a time
-            uint32_t d[Cfg::kAcc == 1 ? 1 : 2][16];
-            F2 x[8];
-#pragma unroll
-            for (int k = 0; k < Cfg::kAcc; k += 2) {
-              DSA_TMEM_LD16_NOWAIT(c0 + k * Cfg::kCols + g, d[0]);
-              if constexpr (Cfg::kAcc == 1) {
-                DSA_TMEM_WAIT32(d[0], d[0]);
-              } else {
-                DSA_TMEM_LD16_NOWAIT(c0 + (k + 1 < Cfg::kAcc ? k + 1 : k) * Cfg::kCols + g, d[1]);
-                DSA_TMEM_WAIT32(d[0], d[1]);
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const F2 v = f2(__uint_as_float(d[0][2 * i]), __uint_as_float(d[0][2 * i + 1]));
-                x[i] = k == 0 ? f2_mul(v, s[0]) : f2_fma(v, s[k], x[i]);
-                if constexpr (Cfg::kAcc > 1)
-                  if (k + 1 < Cfg::kAcc)
-                    x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k + 1 < Cfg::kAcc ? k + 1 : 0], x[i]);
-              }
-            }
-            if (g + 16 >= N / 4) {   // read: the accumulators are free again
-              tc::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive_remote(aempty0 + 8 * set);
-            }
+          // 16 rows, their scores x (in units of the rows' factors)
+          auto weigh = [&](const F2 (&x)[8], int g) {
             const float4 *ca = reinterpret_cast<const float4 *>(col + first + g), *cl = ca + Cfg::kN / 4;
             const int4 *cp = reinterpret_cast<const int4 *>(cl + Cfg::kN / 4);
 #pragma unroll
@@ -661,6 +709,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
               sum[0] = f2_add(sum[0], f2(e[0], e[1]));
               sum[1] = f2_add(sum[1], f2(e[2], e[3]));
             }
+          };
+          auto release = [&]() {   // the accumulators are read
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_remote(aempty0 + 8 * set);
+          };
+          if constexpr (Cfg::kAcc == 1) {   // the next 16 rows' load in flight
+            uint32_t d[2][16];
+            auto take = [&](uint32_t (&v)[16], uint32_t (&next)[16], int g) {   // false: these were the last
+              DSA_TMEM_WAIT16(v);
+              const bool more = g + 16 < N / 4;
+              if (more) DSA_TMEM_LD16_NOWAIT(c0 + g + 16, next);
+              else release();
+              F2 x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[0]);
+              weigh(x, g);
+              return more;
+            };
+            DSA_TMEM_LD16_NOWAIT(c0, d[0]);
+#pragma unroll 1
+            for (int g = 0;; g += 32)
+              if (!take(d[0], d[1], g) || !take(d[1], d[0], g + 16)) break;
+          } else {
+#pragma unroll 1
+            for (int g = 0; g < N / 4; g += 16) {
+              uint32_t d[2][16];
+              F2 x[8];
+#pragma unroll
+              for (int k = 0; k < Cfg::kAcc; k += 2) {
+                const int k1 = k + 1 < Cfg::kAcc ? k + 1 : k;
+                DSA_TMEM_LD16_NOWAIT(c0 + k * Cfg::kCols + g, d[0]);
+                DSA_TMEM_LD16_NOWAIT(c0 + k1 * Cfg::kCols + g, d[1]);
+                DSA_TMEM_WAIT32(d[0], d[1]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const F2 v = f2(__uint_as_float(d[0][2 * i]), __uint_as_float(d[0][2 * i + 1]));
+                  x[i] = k == 0 ? f2_mul(v, s[0]) : f2_fma(v, s[k], x[i]);
+                  if (k1 > k) x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k1], x[i]);
+                }
+              }
+              if (g + 16 >= N / 4) release();
+              weigh(x, g);
+            }
           }
           if (++set == Cfg::kSets) {
             set = 0;
@@ -671,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           total += a0 + a1;
         }
       } else if (items.at < items.n) {
-        fetch(items.na, items.nc.x, items.nc.y, items.nc.z);
+        fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
       }
       // the four threads of a key (the sums of the item before have been read: a barrier ago)
       float *red = red_s + rb * 256;
@@ -681,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       if (writes) {
         const float t = kept ? (red[key] + red[64 + key]) + (red[128 + key] + red[192 + key]) : 0.f;
         const int64_t b = items.a.x;
-        if (p.splits > 1) __stcg(p.part + ((int64_t)items.c.w * p.B + b) * p.L.width + at, t);
+        if (p.splits > 1) __stcg(p.part + ((int64_t)(items.c.w & INT32_MAX) * p.B + b) * p.L.width + at, t);
         else p.out[b * p.out_st + at] = before + t;
       }
     }
