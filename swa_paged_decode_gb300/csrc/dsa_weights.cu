@@ -60,7 +60,7 @@ struct WeightsParams {
   int32_t *n_items;
   int4 *item;                  // [max_items][2]
   uint8_t *image;              // [tiles][64-dim block][8-row group][1 KiB]
-  float2 *row;                 // [tiles * 128] (scale log2(e) 2^e, log2 of the denominator)
+  float *row;                  // [tiles][2][128] scale log2(e) 2^e, and - log2 of the denominator
   float *part;                 // [splits][B][width]
 };
 
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
       if (r >= rows) {   // behind the sequence's last row: zeros, up to what a step may take
         uint8_t *pad = base + (r >> 3) * 1024 + (r & 7) * 128;
         for (int c = lane; c < 8 * kDB; c += 32) *reinterpret_cast<uint4 *>(pad + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        if (lane < 2) p.row[(int64_t)tile * 256 + 128 * lane + r] = lane ? -INFINITY : 0.f;
         continue;
       }
       const uint32_t gr = (uint32_t)s.s0 * p.H + 128u * i + r, t = gr / (uint32_t)p.H, h = gr - t * (uint32_t)p.H;
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
           const float z = __ldg(p.sink + h), m = fmaxf(lse, z), d = -fabsf(lse - z);
           l = lse != lse || z != z ? lse + z : m == INFINITY ? INFINITY : z == -INFINITY ? lse : m + log1pf(expf(d));
         }
-        p.row[(int64_t)tile * 128 + r] = make_float2(p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23), l * kLog2e);
+        p.row[(int64_t)tile * 256 + r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        p.row[(int64_t)tile * 256 + 128 + r] = -l * kLog2e;
       }
     }
   }
@@ -290,44 +292,48 @@ struct WtCfg {
   static constexpr int kSlots = kV32 ? 4 : 5;
   static constexpr uint32_t kTile = kDB * 8192;                     // a key tile: [kDB][64 keys x 64 dims] f16
   static constexpr uint32_t kRing = 2 * kTile;
-  static constexpr uint32_t kColS = kRing + kSlots * 16384;         // [2][3][kN] f32: factor, - log2 denominator, position
-  static constexpr uint32_t kFac = kColS + 2 * 3 * kN * 4;          // [2][8][64] f32 a key's factors; the last: kept or not
+  static constexpr int kConst = 4;                                  // steps whose rows' constants are held
+  static constexpr uint32_t kColS = kRing + kSlots * 16384;         // [kConst][kN / 128][2][128] f32
+  static constexpr uint32_t kFac = kColS + kConst * 8 * kN;         // [2][8][64] f32 a key's factors; the last: kept or not
   static constexpr uint32_t kRed = kFac + 4096;                     // [2][4][64] f32
-  static constexpr uint32_t kMisc = kRed + 2048;
+  static constexpr uint32_t kItems = kRed + 2048;                   // [kWtHeld][2] int4
+  static constexpr uint32_t kMisc = kItems + 2048;
   static constexpr int kFull = 0, kEmpty = kSlots, kAFull = 2 * kSlots, kAEmpty = kAFull + kSets,
-                       kKFull = kAEmpty + kSets, kKReady = kKFull + 2, kKEmpty = kKReady + 2, kDrain = kKEmpty + 2,
-                       kBars = kDrain + 1;
+                       kKFull = kAEmpty + kSets, kKReady = kKFull + 2, kKEmpty = kKReady + 2, kCFull = kKEmpty + 2, kCEmpty = kCFull + kConst,
+                       kDrain = kCEmpty + kConst, kBars = kDrain + 1;
   static constexpr uint32_t kAbort = 8 * kBars, kTmem = kAbort + 4;
-  static constexpr uint32_t kBytes = kMisc + 256;
-  static_assert(kTmem + 4 <= 256, "misc area");
+  static constexpr uint32_t kBytes = kMisc + 512;
+  static_assert(kTmem + 4 <= 512, "misc area");
   static_assert(kBytes + 1024 <= 232448u, "shared memory layout exceeds 227 KiB");
   // rows of the step that starts with `left` rows to go, and 64-dim blocks to a slot
   static __device__ __forceinline__ int rows(int64_t left) { return left > 128 && kN == 256 ? 256 : left > 64 ? 128 : 64; }
   static __device__ __forceinline__ int per_slot(int N) { return 256 / N; }
 };
 
-// The items of a pair, and the steps of an item (up to kN query rows each).
+// The items of a pair (its first kWtHeld ones in shared memory: a role that went
+// to the L2 for each would wait for it), and the steps of an item (up to kN
+// query rows each).
+constexpr int kWtHeld = 64;
 template <class Cfg>
 struct Items {
   const WeightsParams &p;
-  int32_t at, n, step;
-  int4 a, c, na, nc;
+  const int4 *held;      // [kWtHeld][2]
+  int32_t i, n, pair, pairs;   // the next one, of how many of this pair
+  int4 a, c;
   int32_t tile, end;     // next row tile of the item, and the row tile past its last
   int64_t rows;          // rows of the sequence
-  __device__ __forceinline__ Items(const WeightsParams &q, int pair, int pairs) : p(q), at(pair), step(pairs) {
-    n = __ldcg(p.n_items);
-    if (at < n) load();
+  __device__ __forceinline__ Items(const WeightsParams &q, const int4 *h, int pr, int prs) : p(q), held(h), i(0), pair(pr), pairs(prs) {
+    const int32_t all = __ldcg(p.n_items);
+    n = all > pair ? (all - pair + pairs - 1) / pairs : 0;
   }
-  __device__ __forceinline__ void load() {
-    na = __ldcg(p.item + 2 * (int64_t)at);
-    nc = __ldcg(p.item + 2 * (int64_t)at + 1);
+  __device__ __forceinline__ int4 half(int32_t k, int h) const {
+    return k < kWtHeld ? held[2 * k + h] : __ldcg(p.item + 2 * ((int64_t)pair + (int64_t)k * pairs) + h);
   }
   __device__ __forceinline__ bool next() {   // the next item
-    if (at >= n) return false;
-    a = na;
-    c = nc;
-    at += step;
-    if (at < n) load();
+    if (i >= n) return false;
+    a = half(i, 0);
+    c = half(i, 1);
+    ++i;
     tile = c.y;
     end = c.z;
     rows = (int64_t)a.w * p.H;
@@ -335,7 +341,7 @@ struct Items {
   }
   __device__ __forceinline__ bool empty() const { return c.y >= c.z; }
   __device__ __forceinline__ int64_t left() const { return min(rows, (int64_t)end * 128) - (int64_t)tile * 128; }
-  __device__ __forceinline__ bool next_step(int &N) {   // tile is the step's until the next call
+  __device__ __forceinline__ bool next_step(int &N) {   // tile is the step's until advance
     if (tile >= end) return false;
     N = Cfg::rows(left());
     return true;
@@ -368,14 +374,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   if (tid == 32) {
     for (int b = 0; b < Cfg::kBars; ++b) {
       const bool a = b >= Cfg::kAEmpty && b < Cfg::kKFull, k = b >= Cfg::kKFull && b < Cfg::kKReady,
-                 r = b >= Cfg::kKReady && b < Cfg::kKEmpty, e = b >= Cfg::kKEmpty && b < Cfg::kDrain;
-      tc::mbar_init(&bars[b], a ? 16u : k ? 2u * kWtRecords : r ? kWtRecords : e ? 9u : 1u);
+                 r = b >= Cfg::kKReady && b < Cfg::kKEmpty, e = b >= Cfg::kKEmpty && b < Cfg::kCFull, c = b >= Cfg::kCEmpty && b < Cfg::kDrain;
+      tc::mbar_init(&bars[b], a ? 16u : k ? 2u * kWtRecords : r ? kWtRecords : e ? 9u : c ? 8u : 1u);
     }
     tc::fence_mbar_init();
     *abort_s = 0;
   }
   pdl_wait_primary();
-  Items<Cfg> items(p, pair, pairs);
+  int4 *held = reinterpret_cast<int4 *>(smem + Cfg::kItems);
+  Items<Cfg> items(p, held, pair, pairs);
+  if (tid < 2 * kWtHeld && (tid >> 1) < items.n) held[tid] = __ldcg(p.item + 2 * ((int64_t)pair + (int64_t)(tid >> 1) * pairs) + (tid & 1));
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();
@@ -394,17 +402,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   };
   auto lead = [&](int b) { return tc::mapa(tc::smem_u32(&bars[b]), 0); };
 
+  // 640 threads leave 96 registers each; the exponentials want more (spilled, a
+  // load on its way to a register would be waited for), the copies need fewer:
+  // 256 x 112 + 128 x 80 + 256 x 88 = 640 x 96.
   if (warp >= 12) {
+    tc::setmaxnreg_dec<88>();
     // ======================================================== records
     // 64 keys of an item to this CTA, 8 to a warp, their loads in flight
-    // together. What is known ahead: the item after next, the slots of the next
-    // two, and the records of the next one are on their way to L2 for a whole
-    // item's time. A warp runs one instruction in five cycles or so at best, so
+    // together. The slots of the next two items are known ahead, and the records
+    // of the next one are on their way to L2 for a whole item's time. A warp runs one instruction in five cycles or so at best, so
     // what 8 lanes can find for 8 keys (addresses) they do.
     const int pw = warp - 12;
     bool ok = true;
     uint32_t turn = 0;
-    auto item_at = [&](int32_t i) { return i < items.n ? __ldcg(p.item + 2 * (int64_t)i) : make_int4(0, 0, 0, 0); };
+    auto item_at = [&](int32_t i) { return i < items.n ? items.half(i, 0) : make_int4(0, 0, 0, 0); };
     auto slot_of = [&](const int4 &a) {   // lane l < 8: the slot of key 8 pw + l (a list of length 0 has none)
       const int32_t j = a.y + 64 * (int32_t)side + 8 * pw + lane;
       return lane < 8 && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
@@ -420,11 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       kept = __ballot_sync(0xffffffffu, k);
       return rec;
     };
-    int32_t slot2 = slot_of(item_at(pair + pairs));
+    int32_t slot2 = slot_of(item_at(1));
     uint32_t kept1;
-    const uint8_t *rec1 = record_of(slot_of(item_at(pair)), kept1);
-    int4 item3 = item_at(pair + 2 * pairs);
-    int32_t i3 = pair + 3 * pairs;
+    const uint8_t *rec1 = record_of(slot_of(item_at(0)), kept1);
     const uint32_t lane_at = (uint32_t)(lane >> 2) * 8192u + (uint32_t)pw * 1024u;
     while (ok && items.next()) {
       const uint8_t *rec0 = rec1;
@@ -440,9 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
         for (int i = 0; i < kDeep; ++i) load(i);
       }
       rec1 = record_of(slot2, kept1);
-      slot2 = slot_of(item3);
-      item3 = item_at(i3);
-      i3 += pairs;
+      slot2 = slot_of(item_at(items.i + 1));
       if (items.empty()) continue;
       {   // the next records to L2, a line of 128 bytes to a lane
         const uint8_t *rec = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec1), lane >> 2));
@@ -496,7 +503,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     }
     // the tiles' last releases have arrived before the pair ends
     for (int k = 0; k < 2 && ok; ++k, ++turn) ok = wait(Cfg::kKEmpty + (turn & 1), ((turn >> 1) & 1u) ^ 1u);
-  } else if (warp >= 9) {
+  } else if (warp >= 8) {
+    tc::setmaxnreg_dec<80>();
+  if (warp >= 9) {
     // ======================================================== query chunks
     if (lane == 0) {
       uint32_t slot = 0, ph = 1;
@@ -504,9 +513,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       bool ok = true;
       uint32_t filled = 0, fill_ph = 0;
       const uint32_t full0 = lead(Cfg::kFull);
+      uint32_t cs = 0, ph_c = 1;
       while (ok && items.next()) {
         int N;
         while (ok && items.next_step(N)) {
+          if (warp == 9) {   // the constants of the step's rows, to either CTA its own copy
+            ok = wait(Cfg::kCEmpty + cs, ph_c);
+            if (!ok) break;
+            const uint32_t bytes = N == 256 ? 2048u : 1024u;
+            tc::mbar_expect_tx(&bars[Cfg::kCFull + cs], bytes);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             sbase + Cfg::kColS + cs * (8 * Cfg::kN)),
+                         "l"(p.row + ((int64_t)items.c.x + items.tile) * 256), "r"(bytes), "r"(tc::smem_u32(&bars[Cfg::kCFull + cs]))
+                         : "memory");
+            if (++cs == Cfg::kConst) {
+              cs = 0;
+              ph_c ^= 1u;
+            }
+          }
           // this CTA's N / 2 rows: of a tile of its own with N = 256
           const int64_t tile = items.c.x + items.tile + (N == 256 ? side : 0);
           const int32_t y0 = (int32_t)(tile * (Cfg::kDB * 32)) + (N == 256 ? 0 : (int32_t)side * (N / 8));
@@ -554,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else {
     // ======================================================== MMA issue
     if (side == 0) {
       constexpr uint16_t kBoth = 3;
@@ -624,34 +648,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       }
     }
     __syncwarp();
+  }
   } else {
     // ======================================================== exponentials
+    tc::setmaxnreg_inc<112>();
     const int q4 = warp & 3, half = warp >> 2;
     const int lr = 32 * q4 + lane, key = lr & 63, up = lr >> 6;   // TMEM lane; key of this CTA's 64; which half of the rows
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
     const uint32_t aempty0 = lead(Cfg::kAEmpty), kempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kKEmpty]), side);
-    uint32_t set = 0, ph_a = 0, turn = 0, cb = 0, rb = 0;
-    // The constants of a step's query rows, a row to a thread: loaded one step
-    // ahead, the first ones of the next item behind the last step of this one.
-    float2 ahead = make_float2(0.f, 0.f);
-    int32_t ahead_place = INT32_MIN;
-    auto fetch = [&](const int4 &a, int32_t base, int32_t tile, int32_t end, int32_t flags) {
-      const uint32_t r = (uint32_t)tile * 128u + tid;
-      ahead = make_float2(0.f, INFINITY);
-      ahead_place = INT32_MIN;      // no such row: sees nothing, and weighs nothing (its image is zeros)
-      if (tid < Cfg::kN && r < min((uint32_t)a.w * (uint32_t)p.H, (uint32_t)end * 128u)) {
-        ahead = __ldcg(p.row + ((int64_t)base + tile) * 128 + tid);
-        if (flags >= 0) ahead_place = a.z - a.w + (int32_t)(r / (uint32_t)p.H);
-      }
-    };
-    if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
+    const uint32_t cempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kCEmpty]), side);
+    uint32_t set = 0, ph_a = 0, turn = 0, cs = 0, ph_c = 0, rb = 0;
     while (items.next()) {
       const int32_t at = items.a.y + 64 * (int32_t)side + key;   // list position of the thread's key
       const bool writes = up == 0 && half == 0 && at < items.a.z;
       float total = 0.f, before = 0.f;
       if (writes && p.splits == 1 && p.in) before = p.in[(int64_t)items.a.x * p.in_st + at];
       const bool all = items.c.w < 0;                            // every row sees every key
+      // the query rows that see the key: see0 .. see0 + seen - 1
+      const int64_t place = at - (items.a.z - items.a.w);        // of the tokens, the key's own
+      const uint32_t see0 = (uint32_t)max((int64_t)0, place) * (uint32_t)p.H;
+      const int64_t past = p.window > 0 ? min((int64_t)items.a.w, place + p.window) : items.a.w;
+      const uint32_t seen = past > 0 && (uint32_t)past * (uint32_t)p.H > see0 ? (uint32_t)past * (uint32_t)p.H - see0 : 0u;
       bool kept = false;
       if (!items.empty()) {
         const int buf = turn & 1;
@@ -669,26 +687,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
         if (lane == 0) tc::mbar_arrive_remote(kempty0 + 8 * buf);   // the factors are read
         int N;
         while (items.next_step(N)) {
-          float *col = col_s + cb * (3 * Cfg::kN);
-          cb ^= 1u;
-          if (tid < Cfg::kN) {
-            col[tid] = ahead.x;
-            col[Cfg::kN + tid] = -ahead.y;
-            reinterpret_cast<int32_t *>(col)[2 * Cfg::kN + tid] = ahead_place;
-          }
-          sm_bar();
+          // the thread's rows, N / 4 of them from here: of its half's tile with N = 256
+          const int first = N == 256 ? half * 64 : up * (N / 2) + half * (N / 4);
+          const float *col = col_s + cs * (2 * Cfg::kN) + (N == 256 ? up * 256 : 0) + first;
+          const uint32_t row0 = (uint32_t)items.tile * 128u + (N == 256 ? up * 128 : 0) + first;
           items.advance(N);
-          if (items.tile < items.end) fetch(items.a, items.c.x, items.tile, items.end, items.c.w);
-          else if (items.at < items.n) fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
-          const int first = up * (N / 2) + half * (N / 4);   // the thread's rows: N / 4 of them from here
+          wait(Cfg::kCFull + cs, ph_c);
           wait(Cfg::kAFull + set, ph_a);
           tc::tc_fence_after();
           const uint32_t c0 = tl + set * (Cfg::kAcc * Cfg::kCols) + half * (N / 4);
           F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
           // 16 rows, their scores x (in units of the rows' factors)
-          auto weigh = [&](const F2 (&x)[8], int g) {
-            const float4 *ca = reinterpret_cast<const float4 *>(col + first + g), *cl = ca + Cfg::kN / 4;
-            const int4 *cp = reinterpret_cast<const int4 *>(cl + Cfg::kN / 4);
+          auto weigh = [&](auto masked, const F2 (&x)[8], int g) {
+            const float4 *ca = reinterpret_cast<const float4 *>(col + g), *cl = ca + 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 ka = ca[i], kl = cl[i];
@@ -699,12 +710,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
               f2_get(y1, e[2], e[3]);
 #pragma unroll
               for (int j = 0; j < 4; ++j) e[j] = tc::ex2(e[j]);
-              if (!all) {
-                const int4 kp = cp[i];
-                const int32_t place[4] = {kp.x, kp.y, kp.z, kp.w};
+              if constexpr (decltype(masked)::value) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (!(at <= place[j] && (p.window == 0 || at > place[j] - p.window))) e[j] = 0.f;
+                  if (row0 + g + 4 * i + j - see0 >= seen) e[j] = 0.f;
               }
               sum[0] = f2_add(sum[0], f2(e[0], e[1]));
               sum[1] = f2_add(sum[1], f2(e[2], e[3]));
@@ -715,6 +724,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_remote(aempty0 + 8 * set);
           };
+          // (a branch for each four rows inside would keep their loads and
+          // exponentials from overlapping: 430 cycles for 16 rows)
+          auto step = [&](auto masked) {
           if constexpr (Cfg::kAcc == 1) {   // the next 16 rows' load in flight
             uint32_t d[2][16];
             auto take = [&](uint32_t (&v)[16], uint32_t (&next)[16], int g) {   // false: these were the last
@@ -725,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
               F2 x[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[0]);
-              weigh(x, g);
+              weigh(masked, x, g);
               return more;
             };
             DSA_TMEM_LD16_NOWAIT(c0, d[0]);
@@ -751,8 +763,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
                 }
               }
               if (g + 16 >= N / 4) release();
-              weigh(x, g);
+              weigh(masked, x, g);
             }
+          }
+          };
+          if (all) step(std::false_type());
+          else step(std::true_type());
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(cempty0 + 8 * cs);   // the constants are read
+          if (++cs == Cfg::kConst) {
+            cs = 0;
+            ph_c ^= 1u;
           }
           if (++set == Cfg::kSets) {
             set = 0;
@@ -762,8 +783,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           f2_get(f2_add(sum[0], sum[1]), a0, a1);
           total += a0 + a1;
         }
-      } else if (items.at < items.n) {
-        fetch(items.na, items.nc.x, items.nc.y, items.nc.z, items.nc.w);
       }
       // the four threads of a key (the sums of the item before have been read: a barrier ago)
       float *red = red_s + rb * 256;
@@ -972,7 +991,7 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
   p.n_items = p.status + 2;
   p.item = reinterpret_cast<int4 *>(w + plan->ws_item_offset);
   p.image = reinterpret_cast<uint8_t *>(w + plan->ws_image_offset);
-  p.row = reinterpret_cast<float2 *>(w + plan->ws_row_offset);
+  p.row = reinterpret_cast<float *>(w + plan->ws_row_offset);
   p.part = reinterpret_cast<float *>(w + plan->ws_part_offset);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dsa::kDebug && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return DSA_ERR_CUDA;
