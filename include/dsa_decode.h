@@ -645,7 +645,7 @@ typedef struct {
   int32_t pairs;           /* CTA pairs that run                             */
   int32_t splits;          /* parts that the rows of 128 keys are cut into   */
   int32_t tiles;           /* 128-row tiles kept of the queries              */
-  int32_t reserved0;
+  int32_t wide_splits;     /* the same with 256 keys, 0: not taken           */
   int64_t ws_item_offset;  /* workspace byte offsets                         */
   int64_t ws_image_offset;
   int64_t ws_row_offset;

@@ -91,7 +91,7 @@ class ChunkPlan(ctypes.Structure):
 class WeightsPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "magic", "abi_version", "num_tokens", "num_seqs", "num_heads", "width", "d_qk", "num_sms",
-        "pairs", "splits", "tiles", "reserved0")] + \
+        "pairs", "splits", "tiles", "wide_splits")] + \
         [(n, ctypes.c_int64) for n in (
             "ws_item_offset", "ws_image_offset", "ws_row_offset", "ws_part_offset",
             "workspace_bytes", "wait_budget_cycles")] + \

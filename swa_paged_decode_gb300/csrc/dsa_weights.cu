@@ -46,6 +46,7 @@ struct WeightsParams {
   ListArgs L;                  // lists: ids, lens, width, idx_stride
   const int32_t *starts;       // [B + 1]
   int32_t T, B, H, window, splits, max_items, tiles;   // tiles: of the query images
+  int32_t span;                // keys of an item: 128, or 256 (wide)
   const __nv_bfloat16 *q;
   int64_t q_st, q_sh;
   const float *lse, *sink;
@@ -73,12 +74,12 @@ __device__ __forceinline__ Sequence weights_sequence(const WeightsParams &p, int
 __device__ __forceinline__ int32_t image_tile(const WeightsParams &p, int32_t b, int32_t s0) {
   return (int32_t)((int64_t)s0 * p.H >> 7) + b;
 }
-// The row tiles [lo, hi) of a sequence that see any of the 128 keys from key0.
+// The row tiles [lo, hi) of a sequence that see any of an item's keys.
 __device__ __forceinline__ void seeing_tiles(const WeightsParams &p, const Sequence &s, int32_t key0, int32_t &lo, int32_t &hi) {
   const int64_t before = s.len - s.n;   // position of its first token
   const int64_t t0 = max((int64_t)0, key0 - before);
   int64_t t1 = s.n;
-  if (p.window > 0) t1 = min(t1, (int64_t)key0 + 127 + p.window - before);
+  if (p.window > 0) t1 = min(t1, (int64_t)key0 + p.span - 1 + p.window - before);
   lo = (int32_t)(t0 * p.H >> 7);
   hi = t1 > t0 ? (int32_t)((t1 * p.H + 127) >> 7) : lo;
 }
@@ -104,14 +105,14 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
     return;
   }
   if (blockIdx.x == 0) {
-    // items: the 128-key halves that any token of a sequence sees, its row
+    // items: `span` keys that any token of a sequence sees, its row
     // tiles cut in `splits`; 256 sequences at a time, then an item to a thread
     int32_t n = 0;
     for (int32_t b0 = 0; b0 < p.B; b0 += kWtPrep) {
       int32_t mine = 0;
       if (b0 + tid < p.B) {
         const Sequence s = weights_sequence(p, b0 + tid);
-        if (s.any()) mine = (((s.len - 1) >> 7) + 1 - s.gather_begin()) * p.splits;
+        if (s.any()) mine = (s.len - s.gather_begin() * 128 + p.span - 1) / p.span * p.splits;
       }
       int32_t v = mine;
 #pragma unroll
@@ -137,14 +138,15 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
         }
         const int32_t b = b0 + lo, i = x - (lo > 0 ? upto_s[lo - 1] : 0);
         const Sequence s = weights_sequence(p, b);
-        const int32_t u = i / p.splits, part = i - u * p.splits, key0 = (s.gather_begin() + u) * 128;
+        const int32_t u = i / p.splits, part = i - u * p.splits, key0 = s.gather_begin() * 128 + u * p.span;
         int32_t r0, r1;
         seeing_tiles(p, s, key0, r0, r1);
-        const int32_t t0 = r0 + (int32_t)((int64_t)(r1 - r0) * part / p.splits), t1 = r0 + (int32_t)((int64_t)(r1 - r0) * (part + 1) / p.splits);
+        const int64_t steps = (r1 - r0 + 1) >> 1;   // (cut between steps of two tiles)
+        const int32_t t0 = min(r1, r0 + 2 * (int32_t)(steps * part / p.splits)), t1 = min(r1, r0 + 2 * (int32_t)(steps * (part + 1) / p.splits));
         p.item[2 * (int64_t)(n + x)] = make_int4(b, key0, s.len, s.n);
         // whether every row of the range sees every key (bit 31: none need be masked)
         const int64_t first = s.row_position(p.H, 128 * (int64_t)t0), last = s.row_position(p.H, min(128 * (int64_t)t1, (int64_t)s.n * p.H) - 1);
-        const bool all = t1 > t0 && first >= key0 + 127 && (p.window == 0 || last - p.window < key0);
+        const bool all = t1 > t0 && first >= key0 + p.span - 1 && (p.window == 0 || last - p.window < key0);
         p.item[2 * (int64_t)(n + x) + 1] = make_int4(image_tile(p, b, s.s0), t0, t1, part | (all ? INT32_MIN : 0));
       }
       n += sum;
@@ -278,24 +280,27 @@ __device__ __forceinline__ int key_halves(const RawRecord &r, int lane, uint32_t
                :                                                                                                      \
                : "memory")
 
-template <int FMT>
+template <int FMT, bool WIDE>
 struct WtCfg {
+  static constexpr int kKeys = WIDE ? 128 : 64;                     // of an item, to a CTA
+  static constexpr int kBufs = WIDE ? 1 : 2;                        // key tiles
   static constexpr bool kV32 = FMT == DSA_REC_V32_656;
   static constexpr bool kBlocks = FMT == DSA_REC_FP8_528 || kV32;   // fp32 scales: an accumulator per block
   static constexpr int kAcc = kV32 ? 5 : kBlocks ? 4 : 1;
   static constexpr int kDB = kV32 ? 9 : 8;
   static constexpr int kN = kBlocks ? 128 : 256;                    // query rows of a step at most
-  static constexpr int kCols = kN / 2;                              // TMEM columns of an accumulator
+  static constexpr int kCols = WIDE ? kN : kN / 2;                  // TMEM columns of an accumulator
   static constexpr int kSets = 512 / (kAcc * kCols);                // steps whose accumulators it holds
   // Query rows wait in slots of 16 KiB: of a step of N rows one, two or four
   // 64-dim blocks of this CTA's N / 2 (so that a step of few rows takes few waits).
   static constexpr int kSlots = kV32 ? 4 : 5;
-  static constexpr uint32_t kTile = kDB * 8192;                     // a key tile: [kDB][64 keys x 64 dims] f16
-  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kBlock = kKeys * 128;                   // 64 dims of the CTA's keys
+  static constexpr uint32_t kTile = kDB * kBlock;                   // a key tile: [kDB][kKeys x 64 dims] f16
+  static constexpr uint32_t kRing = kBufs * kTile;
   static constexpr int kConst = 4;                                  // steps whose rows' constants are held
   static constexpr uint32_t kColS = kRing + kSlots * 16384;         // [kConst][kN / 128][2][128] f32
-  static constexpr uint32_t kFac = kColS + kConst * 8 * kN;         // [2][8][64] f32 a key's factors; the last: kept or not
-  static constexpr uint32_t kRed = kFac + 4096;                     // [2][4][64] f32
+  static constexpr uint32_t kFac = kColS + kConst * 8 * kN;         // [kBufs][8][kKeys] f32 a key's factors; the last: kept or not
+  static constexpr uint32_t kRed = kFac + 4096;                     // [2][256] f32
   static constexpr uint32_t kItems = kRed + 2048;                   // [kWtHeld][2] int4
   static constexpr uint32_t kMisc = kItems + 2048;
   static constexpr int kFull = 0, kEmpty = kSlots, kAFull = 2 * kSlots, kAEmpty = kAFull + kSets,
@@ -349,11 +354,11 @@ struct Items {
   __device__ __forceinline__ void advance(int N) { tile += N == 256 ? 2 : 1; }
 };
 
-template <int FMT>
+template <int FMT, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap map16,
                    const __grid_constant__ CUtensorMap map8, const __grid_constant__ CUtensorMap map4) {
-  using Cfg = WtCfg<FMT>;
+  using Cfg = WtCfg<FMT, WIDE>;
   constexpr bool kV32 = Cfg::kV32;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -408,17 +413,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   if (warp >= 12) {
     tc::setmaxnreg_dec<88>();
     // ======================================================== records
-    // 64 keys of an item to this CTA, 8 to a warp, their loads in flight
-    // together. The slots of the next two items are known ahead, and the records
-    // of the next one are on their way to L2 for a whole item's time. A warp runs one instruction in five cycles or so at best, so
-    // what 8 lanes can find for 8 keys (addresses) they do.
+    // kKeys keys of an item to this CTA, 8 or 16 to a warp, 8 records' loads in
+    // flight together. The slots of the next two items are known ahead, and the
+    // records of the next one are on their way to L2 for a whole item's time. A
+    // warp runs one instruction in five cycles or so at best, so what a lane per
+    // key can find (addresses) it does.
     const int pw = warp - 12;
+    constexpr int kPer = Cfg::kKeys / kWtRecords;
     bool ok = true;
     uint32_t turn = 0;
     auto item_at = [&](int32_t i) { return i < items.n ? items.half(i, 0) : make_int4(0, 0, 0, 0); };
-    auto slot_of = [&](const int4 &a) {   // lane l < 8: the slot of key 8 pw + l (a list of length 0 has none)
-      const int32_t j = a.y + 64 * (int32_t)side + 8 * pw + lane;
-      return lane < 8 && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
+    auto slot_of = [&](const int4 &a) {   // lane l < kPer: the slot of key kPer pw + l (a list of length 0 has none)
+      const int32_t j = a.y + Cfg::kKeys * (int32_t)side + kPer * pw + lane;
+      return lane < kPer && j < a.z ? __ldg(p.L.ids + (int64_t)a.x * p.L.idx_stride + j) : -1;
     };
     // its record, and whether it is kept; one that is not reads slot 0's, which counts for nothing
     auto record_of = [&](int32_t slot, uint32_t &kept) {
@@ -434,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     int32_t slot2 = slot_of(item_at(1));
     uint32_t kept1;
     const uint8_t *rec1 = record_of(slot_of(item_at(0)), kept1);
-    const uint32_t lane_at = (uint32_t)(lane >> 2) * 8192u + (uint32_t)pw * 1024u;
+    const uint32_t lane_at = (uint32_t)(lane >> 2) * Cfg::kBlock + (uint32_t)pw * (kPer * 128u);
     while (ok && items.next()) {
       const uint8_t *rec0 = rec1;
       const uint32_t kept0 = kept1;
@@ -452,37 +459,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       slot2 = slot_of(item_at(items.i + 1));
       if (items.empty()) continue;
       {   // the next records to L2, a line of 128 bytes to a lane
-        const uint8_t *rec = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec1), lane >> 2));
+        constexpr int kLanes = 32 / kPer;   // to a key
+        const int key = lane / kLanes;
+        const uint8_t *rec = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec1), key));
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int line = 128 * ((lane & 3) + 4 * b);
-          if (line < p.L.rec && ((kept1 >> (lane >> 2)) & 1u)) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + line));
+        for (int b = 0; b < 6; b += kLanes) {
+          const int line = 128 * (lane % kLanes + b);
+          if (line < p.L.rec && ((kept1 >> key) & 1u)) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + line));
         }
       }
-      const int buf = turn & 1;
-      ok = wait(Cfg::kKEmpty + buf, ((turn >> 1) & 1u) ^ 1u);
+      const int buf = turn % Cfg::kBufs;
+      ok = wait(Cfg::kKEmpty + buf, ((turn / Cfg::kBufs) & 1u) ^ 1u);
       ++turn;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      float *fac = fac_s + buf * 512 + 8 * pw;
+      float *fac = fac_s + buf * (8 * Cfg::kKeys) + kPer * pw;
       const uint32_t tile = sbase + buf * Cfg::kTile + lane_at;
-      if (lane < 8) fac[7 * 64 + lane] = (kept0 >> lane) & 1u ? 1.f : 0.f;
+      if (lane < kPer) fac[7 * Cfg::kKeys + lane] = (kept0 >> lane) & 1u ? 1.f : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {   // key 8 pw + i: row i of the 8-row group pw
+      for (int i = 0; i < kPer; ++i) {   // row i % 8 of the warp's 8-row group i / 8
         const RawRecord &rr = raw[i % kDeep];
         uint32_t f[8];
         if constexpr (Cfg::kBlocks) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) tc::e4m3x4_to_f16x4(rr.w[k], f[2 * k], f[2 * k + 1]);
-          if ((lane & 7) == 0) fac[(lane >> 3) * 64 + i] = __uint_as_float(rr.s);
+          if ((lane & 7) == 0) fac[(lane >> 3) * Cfg::kKeys + i] = __uint_as_float(rr.s);
           if constexpr (kV32) {
             const uint32_t m = rr.t & 0x7FFF7FFFu;
             const uint32_t mb = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
             const int E = min(max((int)(mb >> 7) - 127, -kPfRange), kPfRange) - kPfTop;
             const float down = __uint_as_float((uint32_t)(127 - E) << 23);
-            if (lane == 0) fac[4 * 64 + i] = __uint_as_float((uint32_t)(127 + E) << 23);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + buf * Cfg::kTile + 8 * 8192 + pw * 1024 + i * 128 +
-                                                        (((lane >> 2) ^ i) << 4) + 4 * (lane & 3)),
+            if (lane == 0) fac[4 * Cfg::kKeys + i] = __uint_as_float((uint32_t)(127 + E) << 23);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + buf * Cfg::kTile + 8 * Cfg::kBlock + pw * (kPer * 128) + i * 128 +
+                                                        (((lane >> 2) ^ (i & 7)) << 4) + 4 * (lane & 3)),
                          "r"(tc::pack_f16x2(bf16_bits_to_f32(rr.t & 0xFFFFu) * down, bf16_bits_to_f32(rr.t >> 16) * down))
                          : "memory");
           }
@@ -490,9 +499,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           const int E = key_halves<FMT>(rr, lane, f);
           if (lane == 0) fac[i] = __uint_as_float((uint32_t)(127 + E) << 23);
         }
-        if (kDeep < 8 && i + kDeep < 8) load(i + kDeep);
-        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3)) ^ i) << 4), f[0], f[1], f[2], f[3]);
-        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3) + 1) ^ i) << 4), f[4], f[5], f[6], f[7]);
+        if (i + kDeep < kPer) load(i + kDeep);
+        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3)) ^ (i & 7)) << 4), f[0], f[1], f[2], f[3]);
+        tc::st_shared_v4(tile + i * 128 + (((2 * (lane & 3) + 1) ^ (i & 7)) << 4), f[4], f[5], f[6], f[7]);
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -502,10 +511,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       }
     }
     // the tiles' last releases have arrived before the pair ends
-    for (int k = 0; k < 2 && ok; ++k, ++turn) ok = wait(Cfg::kKEmpty + (turn & 1), ((turn >> 1) & 1u) ^ 1u);
+    for (int k = 0; k < Cfg::kBufs && ok; ++k, ++turn) ok = wait(Cfg::kKEmpty + turn % Cfg::kBufs, ((turn / Cfg::kBufs) & 1u) ^ 1u);
   } else if (warp >= 8) {
     tc::setmaxnreg_dec<80>();
-  if (warp >= 9) {
+    if (warp >= 9) {
     // ======================================================== query chunks
     if (lane == 0) {
       uint32_t slot = 0, ph = 1;
@@ -589,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
       while (ok && items.next()) {
         if (items.empty()) continue;
-        const uint32_t buf = turn & 1u, dk = dk0 + buf * (Cfg::kTile >> 4);
-        ok = here(wait(Cfg::kKFull + buf, (turn >> 1) & 1u));
+        const uint32_t buf = turn % Cfg::kBufs, dk = dk0 + buf * (Cfg::kTile >> 4);
+        ok = here(wait(Cfg::kKFull + buf, (turn / Cfg::kBufs) & 1u));
         ++turn;
         int N;
         while (ok && items.next_step(N)) {
@@ -603,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           const uint32_t d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);
           auto products = [&](auto rows) {   // unrolled for each N: a slot is to go out in less time than its products take
             constexpr int kRows = decltype(rows)::value, kPer = 256 / kRows;
-            constexpr uint32_t kId = tc::idesc_f16(128, kRows, false, false);
+            constexpr uint32_t kId = tc::idesc_f16(2 * Cfg::kKeys, kRows, false, false);
 #pragma unroll
             for (int c0 = 0; c0 < Cfg::kDB; c0 += kPer) {
               if (!here(wait(Cfg::kFull + slot, ph))) return false;
@@ -617,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
                   const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
 #pragma unroll
                   for (int ks = 0; ks < 4; ++ks)
-                    tc::mma_f16_pair(d, dk + c * 512u + 2 * ks, q + j * (kRows * 4u) + 2 * ks, kHi, kId, !first || ks ? 1u : 0u);
+                    tc::mma_f16_pair(d, dk + c * (Cfg::kBlock >> 4) + 2 * ks, q + j * (kRows * 4u) + 2 * ks, kHi, kId, !first || ks ? 1u : 0u);
                 }
                 tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
                 if (c0 + kPer >= Cfg::kDB) {
@@ -653,15 +662,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     // ======================================================== exponentials
     tc::setmaxnreg_inc<112>();
     const int q4 = warp & 3, half = warp >> 2;
-    const int lr = 32 * q4 + lane, key = lr & 63, up = lr >> 6;   // TMEM lane; key of this CTA's 64; which half of the rows
+    // TMEM lane; the key of this CTA's; which part of the rows its two (wide) or
+    // four threads take: with 64 keys the upper lanes hold the upper half of N
+    const int lr = 32 * q4 + lane, key = lr % Cfg::kKeys, part = WIDE ? half : 2 * (lr >> 6) + half;
+    constexpr int kParts = WIDE ? 2 : 4;
     const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
     auto sm_bar = [&]() { asm volatile("barrier.sync 1, 256;" ::: "memory"); };
     const uint32_t aempty0 = lead(Cfg::kAEmpty), kempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kKEmpty]), side);
     const uint32_t cempty0 = tc::mapa(tc::smem_u32(&bars[Cfg::kCEmpty]), side);
     uint32_t set = 0, ph_a = 0, turn = 0, cs = 0, ph_c = 0, rb = 0;
     while (items.next()) {
-      const int32_t at = items.a.y + 64 * (int32_t)side + key;   // list position of the thread's key
-      const bool writes = up == 0 && half == 0 && at < items.a.z;
+      const int32_t at = items.a.y + Cfg::kKeys * (int32_t)side + key;   // list position of the thread's key
+      const bool writes = part == 0 && at < items.a.z;
       float total = 0.f, before = 0.f;
       if (writes && p.splits == 1 && p.in) before = p.in[(int64_t)items.a.x * p.in_st + at];
       const bool all = items.c.w < 0;                            // every row sees every key
@@ -672,30 +684,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       const uint32_t seen = past > 0 && (uint32_t)past * (uint32_t)p.H > see0 ? (uint32_t)past * (uint32_t)p.H - see0 : 0u;
       bool kept = false;
       if (!items.empty()) {
-        const int buf = turn & 1;
-        wait(Cfg::kKReady + buf, (turn >> 1) & 1u);
+        const int buf = turn % Cfg::kBufs;
+        wait(Cfg::kKReady + buf, (turn / Cfg::kBufs) & 1u);
         ++turn;
-        const float *fac = fac_s + buf * 512 + key;
-        kept = fac[7 * 64] != 0.f;
+        const float *fac = fac_s + buf * (8 * Cfg::kKeys) + key;
+        kept = fac[7 * Cfg::kKeys] != 0.f;
         F2 s[Cfg::kAcc];
 #pragma unroll
         for (int b = 0; b < Cfg::kAcc; ++b) {
-          const float f = kept ? fac[b * 64] : 0.f;
+          const float f = kept ? fac[b * Cfg::kKeys] : 0.f;
           s[b] = f2(f, f);
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_remote(kempty0 + 8 * buf);   // the factors are read
         int N;
         while (items.next_step(N)) {
-          // the thread's rows, N / 4 of them from here: of its half's tile with N = 256
-          const int first = N == 256 ? half * 64 : up * (N / 2) + half * (N / 4);
-          const float *col = col_s + cs * (2 * Cfg::kN) + (N == 256 ? up * 256 : 0) + first;
-          const uint32_t row0 = (uint32_t)items.tile * 128u + (N == 256 ? up * 128 : 0) + first;
+          // the thread's rows, `mine` of them from `first` (128 and up: in the second tile)
+          const int mine = N / kParts, first = part * mine;
+          const float *col = col_s + cs * (2 * Cfg::kN) + (first >> 7) * 256 + (first & 127);
+          const uint32_t row0 = (uint32_t)items.tile * 128u + first;
           items.advance(N);
           wait(Cfg::kCFull + cs, ph_c);
           wait(Cfg::kAFull + set, ph_a);
           tc::tc_fence_after();
-          const uint32_t c0 = tl + set * (Cfg::kAcc * Cfg::kCols) + half * (N / 4);
+          const uint32_t c0 = tl + set * (Cfg::kAcc * Cfg::kCols) + half * mine;
           F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
           // 16 rows, their scores x (in units of the rows' factors)
           auto weigh = [&](auto masked, const F2 (&x)[8], int g) {
@@ -731,7 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
             uint32_t d[2][16];
             auto take = [&](uint32_t (&v)[16], uint32_t (&next)[16], int g) {   // false: these were the last
               DSA_TMEM_WAIT16(v);
-              const bool more = g + 16 < N / 4;
+              const bool more = g + 16 < mine;
               if (more) DSA_TMEM_LD16_NOWAIT(c0 + g + 16, next);
               else release();
               F2 x[8];
@@ -746,7 +758,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
               if (!take(d[0], d[1], g) || !take(d[1], d[0], g + 16)) break;
           } else {
 #pragma unroll 1
-            for (int g = 0; g < N / 4; g += 16) {
+            for (int g = 0; g < mine; g += 16) {
               uint32_t d[2][16];
               F2 x[8];
 #pragma unroll
@@ -762,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
                   if (k1 > k) x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k1], x[i]);
                 }
               }
-              if (g + 16 >= N / 4) release();
+              if (g + 16 >= mine) release();
               weigh(masked, x, g);
             }
           }
@@ -784,13 +796,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           total += a0 + a1;
         }
       }
-      // the four threads of a key (the sums of the item before have been read: a barrier ago)
+      // the threads of a key (the sums of the item before have been read: a barrier ago)
       float *red = red_s + rb * 256;
       rb ^= 1u;
-      red[(2 * up + half) * 64 + key] = total;
+      red[part * Cfg::kKeys + key] = total;
       sm_bar();
       if (writes) {
-        const float t = kept ? (red[key] + red[64 + key]) + (red[128 + key] + red[192 + key]) : 0.f;
+        float t = red[key];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) t += red[k * Cfg::kKeys + key];
+        t = kept ? t : 0.f;
         const int64_t b = items.a.x;
         if (p.splits > 1) __stcg(p.part + ((int64_t)(items.c.w & INT32_MAX) * p.B + b) * p.L.width + at, t);
         else p.out[b * p.out_st + at] = before + t;
@@ -826,22 +841,22 @@ namespace {
 using dsa::aligned;
 using dsa::WeightsParams;
 
-template <int FMT>
+template <int FMT, bool WIDE>
 cudaError_t weights_setup(void *) {
-  return cudaFuncSetAttribute(dsa::weights_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)(dsa::WtCfg<FMT>::kBytes + 1024));
+  return cudaFuncSetAttribute(dsa::weights_kernel<FMT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)(dsa::WtCfg<FMT, WIDE>::kBytes + 1024));
 }
-template <int FMT>
-cudaError_t weights_ready() {   // bits 51 to 55 of dsa_configure_once
-  return dsa::dsa_configure_once(51 + FMT, &weights_setup<FMT>, nullptr);
+template <int FMT, bool WIDE>
+cudaError_t weights_ready() {   // bits 51 to 55 and 61 to 63 of dsa_configure_once
+  return dsa::dsa_configure_once(WIDE ? 60 + FMT : 51 + FMT, &weights_setup<FMT, WIDE>, nullptr);
 }
 // CTA pairs that run at the same time on the current device.
 template <int FMT>
 cudaError_t weights_pairs(int *pairs) {
-  cudaError_t e = weights_ready<FMT>();
+  cudaError_t e = weights_ready<FMT, false>();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = dsa::config(2, dsa::kWtThreads, dsa::WtCfg<FMT>::kBytes + 1024, nullptr);
-  return cudaOccupancyMaxActiveClusters(pairs, dsa::weights_kernel<FMT>, &c);
+  cudaLaunchConfig_t c = dsa::config(2, dsa::kWtThreads, dsa::WtCfg<FMT, false>::kBytes + 1024, nullptr);
+  return cudaOccupancyMaxActiveClusters(pairs, dsa::weights_kernel<FMT, false>, &c);
 }
 
 // The query images as rows of 512 bytes, `rows` of them to a box.
@@ -855,20 +870,28 @@ bool chunk_map(void *image, int64_t bytes, uint32_t rows, CUtensorMap *map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT>
-cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
+template <int FMT, bool WIDE>
+cudaError_t launch_weigh(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
   using namespace dsa;
-  using Cfg = WtCfg<FMT>;
-  cudaError_t e = weights_ready<FMT>();
+  using Cfg = WtCfg<FMT, WIDE>;
+  cudaError_t e = weights_ready<FMT, WIDE>();
   if (e != cudaSuccess) return e;
   CUtensorMap map16, map8, map4;
   const int64_t bytes = (int64_t)p.tiles * Cfg::kDB * 16384;
-  if (!chunk_map(p.image, bytes, 32, &map16) || !chunk_map(p.image, bytes, 16, &map8) || !chunk_map(p.image, bytes, 8, &map4)) return cudaErrorNotSupported;
+  if (!chunk_map(p.image, bytes, 32, &map16) || !chunk_map(p.image, bytes, 16, &map8) || !chunk_map(p.image, bytes, 8, &map4))
+    return cudaErrorNotSupported;
+  return launch_dependent(config(2u * pairs, kWtThreads, Cfg::kBytes + 1024, st), weights_kernel<FMT, WIDE>, p, map16, map8, map4);
+}
+
+template <int FMT>
+cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
+  using namespace dsa;
   const unsigned blocks = 1 + (unsigned)std::min(p.tiles, 8 * 152);
-  weights_prepare_kernel<Cfg::kV32><<<blocks, kWtPrep, 0, st>>>(p);
-  e = cudaGetLastError();
+  weights_prepare_kernel<FMT == DSA_REC_V32_656><<<blocks, kWtPrep, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_dependent(config(2u * pairs, kWtThreads, Cfg::kBytes + 1024, st), weights_kernel<FMT>, p, map16, map8, map4);
+  constexpr bool kCanWiden = !WtCfg<FMT, false>::kBlocks;
+  e = p.span == 256 ? launch_weigh<FMT, kCanWiden>(p, pairs, st) : launch_weigh<FMT, false>(p, pairs, st);
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t c = config((unsigned)((p.L.width + 255) / 256), 256, 0, st);
   c.gridDim.y = (unsigned)p.B;
@@ -908,15 +931,30 @@ dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_he
   plan->width = width;
   plan->d_qk = d_qk;
   plan->num_sms = num_sms;
+  // How to cut the work, by what it takes about: a pair's items one after the
+  // other, an item a set-up (its records) and its steps of 256 rows, of the mean
+  // sequence. In microseconds: 3.5 and 1.6 for 128 keys, 8 and 2.2 for 256
+  // (wide), 3 to add parts up. Measured (ue8m0, 8 lists of 8192): 1024 rows 76.9
+  // narrow, 74.2 wide, 88.1 with two parts; 4096 rows 211, 180, 221; a list of
+  // 32768 and 4096 rows 126, 107 wide in two parts.
+  const int64_t steps = num_seqs > 0 ? std::max<int64_t>(1, (rows / num_seqs + 255) / 256) : 1;
   const int64_t pairs = most_pairs < 1 ? 1 : most_pairs, units = halves * num_seqs;
-  // Items for four turns of every pair, where the rows allow it: a sequence's
-  // rows in steps of 256 (of the mean sequence; more parts than steps are empty).
-  const int64_t steps = num_seqs > 0 ? (rows / num_seqs + 255) / 256 : 1;
-  int64_t splits = units > 0 ? (4 * pairs + units - 1) / units : 1;
-  splits = splits > steps ? steps : splits;
-  splits = splits < 1 ? 1 : splits;
+  auto cut = [&](int64_t items, double setup, double step, int32_t &splits) {
+    double best = 0;
+    for (int64_t n = 1; n <= std::min<int64_t>(steps, 16); ++n) {
+      const double t = (double)((items * n + pairs - 1) / pairs) * (setup + step * (double)((steps + n - 1) / n)) + (n > 1 ? 3.0 : 0.0);
+      if (n == 1 || t < best) {
+        best = t;
+        splits = (int32_t)n;
+      }
+    }
+    return best;
+  };
+  int32_t wide_splits = 1;
+  const double narrow = cut(units, 3.5, 1.6, plan->splits);
+  if (cut((halves + 1) / 2 * num_seqs, 8.0, 2.2, wide_splits) < narrow) plan->wide_splits = wide_splits;
+  const int64_t splits = std::max(plan->splits, plan->wide_splits);
   if (units * splits > INT32_MAX / 2) return DSA_ERR_UNSUPPORTED;
-  plan->splits = (int32_t)splits;
   plan->tiles = (int32_t)tiles;
   plan->pairs = (int32_t)(units * splits < pairs ? (units < 1 ? 1 : units * splits) : pairs);
   int64_t off = 256;
@@ -972,9 +1010,12 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
   p.B = plan->num_seqs;
   p.H = plan->num_heads;
   p.window = window;
-  p.splits = plan->splits;
   p.tiles = plan->tiles;
-  p.max_items = (int32_t)(((int64_t)plan->width + 127) / 128 * plan->num_seqs * plan->splits);
+  // (records with fp32 scales take products half as fast: the queries' way from L2 keeps up)
+  const bool wide = plan->wide_splits > 0 && cache->format != DSA_REC_FP8_528 && cache->format != DSA_REC_V32_656;
+  p.span = wide ? 256 : 128;
+  p.splits = wide ? plan->wide_splits : plan->splits;
+  p.max_items = (int32_t)(((int64_t)plan->width + 127) / 128 * plan->num_seqs * p.splits);
   p.q = static_cast<const __nv_bfloat16 *>(q);
   p.q_st = q_stride_t;
   p.q_sh = q_stride_h;

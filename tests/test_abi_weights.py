@@ -52,10 +52,11 @@ def test_plan_needs_somewhere_to_put_it(lib):
 def test_plan_layout(lib, T, S, H, width, sms, d):
     p, nbytes = B.dsa_weights_plan(T, S, H, width, sms, d)
     units = -(-width // 128) * S
-    assert p.splits == max(1, min(-(-4 * max(1, sms // 2) // units), -(-(T * H // S) // 256)))
+    steps, splits = max(1, -(-(T * H // S) // 256)), max(p.splits, p.wide_splits)
+    assert 1 <= p.splits <= min(steps, 16) and 0 <= p.wide_splits <= min(steps, 16)
     assert 1 <= p.pairs <= max(1, sms // 2)
-    spans = [(0, 256), (p.ws_item_offset, 32 * units * p.splits), (p.ws_image_offset, 2 * d * 128 * p.tiles),
-             (p.ws_row_offset, 8 * 128 * p.tiles), (p.ws_part_offset, 4 * p.splits * S * width if p.splits > 1 else 0)]
+    spans = [(0, 256), (p.ws_item_offset, 32 * units * splits), (p.ws_image_offset, 2 * d * 128 * p.tiles),
+             (p.ws_row_offset, 8 * 128 * p.tiles), (p.ws_part_offset, 4 * splits * S * width if splits > 1 else 0)]
     for (a, n), (b, _) in zip(spans, spans[1:] + [(nbytes, 0)]):
         assert a % 256 == 0 and a + n <= b
     # every sequence's tiles, however the tokens are split, and one more

@@ -130,15 +130,21 @@ def test_lengths(length, window):
 def test_rows_shared_by_several_items(sms, fmt, window):
     c = Case([(90, 400), (1, 130), (40, 333)], 64, fmt, seed=sms, sink=True, window=window)
     out, attn = c.run(sms)
-    assert attn.plan.splits == max(1, min(-(-4 * (sms // 2) // 12), -(-131 * 64 // 3 // 256)))
+    assert {2: attn.plan.splits == 1, 152: attn.plan.splits > 1}.get(sms, 1 <= attn.plan.splits <= 11)
     c.check(out)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_many_rows_per_key(fmt):
-    c = Case([(100, 260)], 128, fmt, seed=21, sink=True)
-    for sms in (2, 0):
-        c.check(c.run(sms)[0])
+@pytest.mark.parametrize("sizes,window", [([(100, 260)], 0), ([(100, 2300), (77, 1500)], 0), ([(150, 1200), (120, 120)], 100)])
+def test_many_rows_per_key(fmt, sizes, window):
+    """128 and 256 keys to an item, whole and in parts."""
+    c = Case(sizes, 128, fmt, seed=21, sink=True, window=window, invalid=0.05)
+    kinds = set()
+    for sms in (2, 8, 0):
+        out, attn = c.run(sms)
+        c.check(out)
+        kinds.add((attn.plan.splits > 1, attn.plan.wide_splits))
+    assert len(kinds) > 1
 
 
 def test_many_sequences_and_items():
