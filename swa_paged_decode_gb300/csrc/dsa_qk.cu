@@ -7,10 +7,10 @@
 // and their last 64 dims rotated; queries leave as bf16 rows, keys as records of
 // the cache (the arithmetic of dsa_cache_write, whose rows these are).
 //
-// One pass over memory, a warp per row: of a query row lane l < 28 holds dims
-// 16 l .. 16 l + 15 and lane 28 + j the dims 448 + 8 j .. and 480 + 8 j .., so
-// that both pairings of the rotation find their partner in the same lane
-// without an exchange. The next row is on its way while one is worked on. The
+// One pass over memory, a warp per row, lane l on dims 16 l .. 16 l + 15, the
+// next row on its way while one is worked on. What bounds it is instructions: the
+// rotation takes a pair per lane, through shared memory, as in the cache write
+// (in the four lanes that hold the last 64 dims it was a third of them). The
 // first blocks take the keys, which cost about two query rows each.
 #include <algorithm>
 #include <cmath>
@@ -33,36 +33,16 @@ struct QkParams {
   int32_t T, H;
 };
 
-// 8 values, 16 or 32 bytes.
-template <int TY>
-struct Chunk {
-  uint4 q[TY == DSA_TYPE_F32 ? 2 : 1];
-};
-template <int TY>
-__device__ __forceinline__ void unpack_chunk(const Chunk<TY> &c, F2 (&v)[8], int at) {
-#pragma unroll
-  for (int i = 0; i < (TY == DSA_TYPE_F32 ? 2 : 1); ++i) {
-    const uint32_t w[4] = {c.q[i].x, c.q[i].y, c.q[i].z, c.q[i].w};
-    if constexpr (TY == DSA_TYPE_F32) {
-      v[at + 2 * i] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-      v[at + 2 * i + 1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[at + k] = unpack2<TY>(w[k]);
-    }
-  }
-}
 template <int TY>
 __device__ __forceinline__ float one_value(const void *p) {
   if constexpr (TY == DSA_TYPE_F32) return __ldg(static_cast<const float *>(p));
   else if constexpr (TY == DSA_TYPE_F16) return __half2float(__ldg(static_cast<const __half *>(p)));
   else return __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(p)));
 }
-// A query row as loaded: chunk a and chunk b of the lane, and of a 576-dim row
-// the lane's pair of the last 64 dims.
+// A query row as loaded, and of a 576-dim row the lane's pair of the last 64 dims.
 template <int TY>
 struct QueryRaw {
-  Chunk<TY> a, b;
+  RowRaw<TY> r;
   float t0, t1;
 };
 
@@ -106,70 +86,50 @@ __device__ __forceinline__ float norm_factor(F2 (&v)[8], float eps) {
 template <int TY, bool kV32, bool kRope>
 __device__ __forceinline__ void query_rows(const QkParams &p, int64_t block, int64_t blocks) {
   const int lane = threadIdx.x & 31;
-  const bool rl = lane >= 28;
-  const int da = rl ? 448 + 8 * (lane - 28) : 16 * lane, db = rl ? da + 32 : da + 8;   // first dims of the lane's chunks
   const bool gptj = p.k.gptj;
-  // a 576-dim row's pair of dims 512 ..
-  const int ta = kD + (gptj ? 2 * lane : lane), tb = kD + (gptj ? 2 * lane + 1 : lane + 32);
-  const int64_t step = blocks * kCacheWarps, first = block * kCacheWarps + (threadIdx.x >> 5), rows = (int64_t)p.T * p.H;
-  const uint32_t dt = (uint32_t)(step / p.H), dh = (uint32_t)(step % p.H);
+  // the lane's pair of the last 64 dims
+  const int ia = gptj ? 2 * lane : lane, ib = gptj ? 2 * lane + 1 : lane + 32;
+  constexpr bool kStage = kRope && !kV32;
+  __shared__ __align__(16) float last_s[kStage ? kCacheWarps : 1][64];
+  float *last = last_s[kStage ? threadIdx.x >> 5 : 0];
+  // A run of rows to a warp: the heads of a token find its position and table row
+  // in L1 (rows strided over the grid each waited for theirs: 418 us).
+  const int64_t rows = (int64_t)p.T * p.H, warps = blocks * kCacheWarps, per = (rows + warps - 1) / warps;
+  const int64_t first = (block * kCacheWarps + (threadIdx.x >> 5)) * per, end = min(rows, first + per);
   uint32_t t = (uint32_t)(first / p.H), h = (uint32_t)(first % p.H);
   const char *src = static_cast<const char *>(p.q);
   const bool wide_in = (((uintptr_t)src | (uintptr_t)(p.q_st * kTypeBytes<TY>) | (uintptr_t)(p.q_sh * kTypeBytes<TY>)) & 31u) == 0;
   const bool wide_out = (((uintptr_t)p.out | (uintptr_t)(p.o_st * 2) | (uintptr_t)(p.o_sh * 2)) & 31u) == 0;
   F2 w[8];
   auto weights = [&](const float *from) {
+    const float4 *w4 = reinterpret_cast<const float4 *>(from) + 4 * lane;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float4 *w4 = reinterpret_cast<const float4 *>(from + (c ? db : da));
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 x = __ldg(w4 + k);
-        w[4 * c + 2 * k] = f2(x.x, x.y);
-        w[4 * c + 2 * k + 1] = f2(x.z, x.w);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float4 x = __ldg(w4 + k);
+      w[2 * k] = f2(x.x, x.y);
+      w[2 * k + 1] = f2(x.z, x.w);
     }
   };
   if (p.w && p.w_sh == 0) weights(p.w);
   QueryRaw<TY> next;
   auto fetch = [&](uint32_t ft, uint32_t fh) {
     const char *row = src + ((int64_t)ft * p.q_st + (int64_t)fh * p.q_sh) * kTypeBytes<TY>;
-    const char *pa = row + da * kTypeBytes<TY>, *pb = row + db * kTypeBytes<TY>;
-    if constexpr (TY == DSA_TYPE_F32) {
-      if (wide_in) {
-        tc::ldg_nc_v8(pa, next.a.q[0], next.a.q[1]);
-        tc::ldg_nc_v8(pb, next.b.q[0], next.b.q[1]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          next.a.q[k] = ld_row(pa + 16 * k);
-          next.b.q[k] = ld_row(pb + 16 * k);
-        }
-      }
-    } else if (wide_in && !rl) {
-      tc::ldg_nc_v8(pa, next.a.q[0], next.b.q[0]);
-    } else {
-      next.a.q[0] = ld_row(pa);
-      next.b.q[0] = ld_row(pb);
-    }
+    load_row<TY, false>(row, lane, wide_in, next.r);
     if constexpr (kV32) {
-      next.t0 = one_value<TY>(row + ta * kTypeBytes<TY>);
-      next.t1 = one_value<TY>(row + tb * kTypeBytes<TY>);
+      next.t0 = one_value<TY>(row + (kD + ia) * kTypeBytes<TY>);
+      next.t1 = one_value<TY>(row + (kD + ib) * kTypeBytes<TY>);
     }
   };
-  if (first < rows) fetch(t, h);
+  if (first < end) fetch(t, h);
 #pragma unroll 1
-  for (int64_t i = first; i < rows; i += step) {   // whole warps
+  for (int64_t i = first; i < end; ++i) {   // whole warps
     const QueryRaw<TY> raw = next;
     const uint32_t ct = t, ch = h;
-    t += dt;
-    h += dh;
-    if (h >= (uint32_t)p.H) {
-      h -= p.H;
+    if (++h == (uint32_t)p.H) {
+      h = 0;
       ++t;
     }
-    if (i + step < rows) fetch(t, h);
-    float4 cs[4];
+    if (i + 1 < end) fetch(t, h);
     float co = 0.f, si = 0.f;
     if constexpr (kRope) {
       const int64_t pos = __ldg(p.k.positions + ct);
@@ -177,22 +137,12 @@ __device__ __forceinline__ void query_rows(const QkParams &p, int64_t block, int
         if (p.k.status && lane == 0) report_status(p.k.status, DSA_ERR_INVALID_ARG);
         continue;
       }
-      const float *row = p.k.cos_sin + pos * 64;
-      if constexpr (kV32) {
-        co = __ldg(row + lane);
-        si = __ldg(row + 32 + lane);
-      } else if (rl) {
-        const float4 *r4 = reinterpret_cast<const float4 *>(row);
-        const int j = lane - 28, f0 = gptj ? j : 2 * j, f1 = gptj ? j + 4 : 2 * j + 1;
-        cs[0] = __ldg(r4 + f0);
-        cs[1] = __ldg(r4 + f1);
-        cs[2] = __ldg(r4 + 8 + f0);
-        cs[3] = __ldg(r4 + 8 + f1);
-      }
+      co = __ldg(p.k.cos_sin + pos * 64 + lane);
+      si = __ldg(p.k.cos_sin + pos * 64 + 32 + lane);
     }
     F2 v[8];
-    unpack_chunk<TY>(raw.a, v, 0);
-    unpack_chunk<TY>(raw.b, v, 4);
+    float u0, u1;
+    unpack_row<TY, false>(raw.r, v, u0, u1);
     if (p.w) {
       if (p.w_sh != 0) weights(p.w + (int64_t)ch * p.w_sh);
       const float r = norm_factor(v, p.k.eps);
@@ -200,56 +150,47 @@ __device__ __forceinline__ void query_rows(const QkParams &p, int64_t block, int
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = f2_mul(f2_mul(v[k], r2), w[k]);
     }
-    float x[16];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f2_get(v[k], x[2 * k], x[2 * k + 1]);
-    float t0 = raw.t0, t1 = raw.t1;
-    if constexpr (kRope) {
-      if constexpr (kV32) {
-        const float a = t0, b = t1;
-        t0 = fmaf(a, co, -(b * si));
-        t1 = fmaf(b, co, a * si);
-      } else if (rl) {
-        const float c8[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
-        const float s8[8] = {cs[2].x, cs[2].y, cs[2].z, cs[2].w, cs[3].x, cs[3].y, cs[3].z, cs[3].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {   // pairs (2k, 2k + 1) of the lane's values, or (k, 8 + k)
-          const float a = gptj ? x[2 * k] : x[k], b = gptj ? x[2 * k + 1] : x[8 + k];
-          const float ra = fmaf(a, c8[k], -(b * s8[k])), rb = fmaf(b, c8[k], a * s8[k]);
-          v[k] = f2(ra, rb);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float a, b;
-          f2_get(v[k], a, b);
-          if (gptj) {
-            x[2 * k] = a;
-            x[2 * k + 1] = b;
-          } else {
-            x[k] = a;
-            x[8 + k] = b;
-          }
-        }
-      }
-    }
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = bf16x2_bits(x[2 * k], x[2 * k + 1]);
     __nv_bfloat16 *dst = p.out + (int64_t)ct * p.o_st + (int64_t)ch * p.o_sh;
-    const uint4 oa = make_uint4(o[0], o[1], o[2], o[3]), ob = make_uint4(o[4], o[5], o[6], o[7]);
-    if (wide_out && !rl) {
-      tc::stg_v8(dst + da, oa, ob);
+    if (kStage && lane >= 28) {   // on their way to a pair per lane
+      ulonglong2 *d = reinterpret_cast<ulonglong2 *>(last + 16 * (lane - 28));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = make_ulonglong2(v[2 * k].v, v[2 * k + 1].v);
     } else {
-      *reinterpret_cast<uint4 *>(dst + da) = oa;
-      *reinterpret_cast<uint4 *>(dst + db) = ob;
-    }
-    if constexpr (kV32) {
-      if (gptj) {
-        *reinterpret_cast<uint32_t *>(dst + ta) = bf16x2_bits(t0, t1);
-      } else {
-        dst[ta] = __float2bfloat16_rn(t0);
-        dst[tb] = __float2bfloat16_rn(t1);
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float a, b;
+        f2_get(v[k], a, b);
+        o[k] = bf16x2_bits(a, b);
       }
+      const uint4 oa = make_uint4(o[0], o[1], o[2], o[3]), ob = make_uint4(o[4], o[5], o[6], o[7]);
+      if (wide_out) {
+        tc::stg_v8(dst + 16 * lane, oa, ob);
+      } else {
+        *reinterpret_cast<uint4 *>(dst + 16 * lane) = oa;
+        *reinterpret_cast<uint4 *>(dst + 16 * lane + 8) = ob;
+      }
+    }
+    if constexpr (kStage || kV32) {
+      float a = raw.t0, b = raw.t1;
+      if constexpr (kStage) {
+        __syncwarp();
+        a = last[ia];
+        b = last[ib];
+      }
+      if constexpr (kRope) {
+        const float ra = fmaf(a, co, -(b * si)), rb = fmaf(b, co, a * si);
+        a = ra;
+        b = rb;
+      }
+      __nv_bfloat16 *tail = dst + (kV32 ? kD : kD - 64);
+      if (gptj) {
+        *reinterpret_cast<uint32_t *>(tail + ia) = bf16x2_bits(a, b);
+      } else {
+        tail[ia] = __float2bfloat16_rn(a);
+        tail[ib] = __float2bfloat16_rn(b);
+      }
+      if constexpr (kStage) __syncwarp();   // the stage is free again
     }
   }
 }
