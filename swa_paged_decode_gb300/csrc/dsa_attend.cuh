@@ -657,9 +657,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     // found once, by a lane of its own: this code runs once per 128 rows, so
     // its size is its time (8 rows unrolled took 9700 cycles, 700 a row).
     auto stage_q = [&](int64_t g0, int32_t rows) {
-      const bool rl = lane >= 28, rope = p.cos_sin != nullptr;
-      const int ca = rl ? 56 + (lane - 28) : 2 * lane, cb = rl ? 60 + (lane - 28) : 2 * lane + 1;
-      const int f0 = p.gptj ? lane - 28 : 2 * (lane - 28), f1 = p.gptj ? lane - 24 : 2 * (lane - 28) + 1;
+      const bool rope = p.cos_sin != nullptr;
+      // The rotation takes a pair per lane, through the P tile, which no product
+      // reads now (in the four lanes that hold the last 64 dims it was a third of
+      // the instructions).
+      const int ia = p.gptj ? 2 * lane : lane, ib = p.gptj ? 2 * lane + 1 : lane + 32;
+      float *turn_s = reinterpret_cast<float *>(smem + Cfg::kP) + 128 * warp;   // [2 rows][64]
       // row lane % 8 of the warp's: its queries, its table row
       const uint32_t in = side * 64u + 8u * warp + (lane & 7), gl = (uint32_t)g0 + in;
       const __nv_bfloat16 *qp = nullptr;
@@ -675,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         }
       }
       uint4 na[2], nb[2], nc[2];
-      float4 ns[2][4];
+      float nco[2], nsi[2];
       auto fetch = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -683,20 +686,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(qp), i0 + i));
           na[i] = nb[i] = nc[i] = make_uint4(0, 0, 0, 0);
           if (r) {
-            na[i] = __ldg(r + ca);
-            nb[i] = __ldg(r + cb);
+            na[i] = __ldg(r + 2 * lane);
+            nb[i] = __ldg(r + 2 * lane + 1);
             if constexpr (kV32)
               if (lane < 8) nc[i] = __ldg(r + 64 + lane);   // dims 512 + 8 lane ..
           }
           if (rope) {
-            const float4 *c = reinterpret_cast<const float4 *>(
+            const float *c = reinterpret_cast<const float *>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cp), i0 + i));
-            const int64_t at = reinterpret_cast<const float *>(c) - p.cos_sin;
-            if (rl && dbg_ok(p.status, at >= 0 && at + 64 <= p.cs_rows * 64, kDbgTable)) {
-              ns[i][0] = __ldg(c + f0);
-              ns[i][1] = __ldg(c + f1);
-              ns[i][2] = __ldg(c + 8 + f0);
-              ns[i][3] = __ldg(c + 8 + f1);
+            const int64_t at = c - p.cos_sin;
+            if (dbg_ok(p.status, at >= 0 && at + 64 <= p.cs_rows * 64, kDbgTable)) {
+              nco[i] = __ldg(c + lane);
+              nsi[i] = __ldg(c + 32 + lane);
             }
           }
         }
@@ -705,14 +706,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll 1
       for (int i0 = 0; i0 < 8; i0 += 2) {
         uint4 qa[2], qb[2], qc[2];
-        float4 cs[2][4];
+        float co[2], si[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           qa[i] = na[i];
           qb[i] = nb[i];
           qc[i] = nc[i];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) cs[i][k] = ns[i][k];
+          co[i] = nco[i];
+          si[i] = nsi[i];
         }
         if (i0 < 6) fetch(i0 + 2);
 #pragma unroll
@@ -737,35 +738,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu) * down;
-            v[2 * k + 1] = bf16_bits_to_f32(w[k] >> 16) * down;
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * down;
           }
-          if (rope && rl) {
-            const float c8[8] = {cs[i][0].x, cs[i][0].y, cs[i][0].z, cs[i][0].w,
-                                 cs[i][1].x, cs[i][1].y, cs[i][1].z, cs[i][1].w};
-            const float s8[8] = {cs[i][2].x, cs[i][2].y, cs[i][2].z, cs[i][2].w,
-                                 cs[i][3].x, cs[i][3].y, cs[i][3].z, cs[i][3].w};
-            if (p.gptj) {   // pairs (2k, 2k + 1)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float x1 = v[2 * k], x2 = v[2 * k + 1];
-                v[2 * k] = fmaf(x1, c8[k], -(x2 * s8[k]));
-                v[2 * k + 1] = fmaf(x2, c8[k], x1 * s8[k]);
-              }
-            } else {        // pairs (k, 8 + k)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float x1 = v[k], x2 = v[8 + k];
-                v[k] = fmaf(x1, c8[k], -(x2 * s8[k]));
-                v[8 + k] = fmaf(x2, c8[k], x1 * s8[k]);
-              }
-            }
-          }
-          uint32_t f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
           const uint32_t ro = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
-          st_q((ca >> 3) * 8192 + ro + (((ca & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
-          st_q((cb >> 3) * 8192 + ro + (((cb & 7) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+          if (rope && lane >= 28) {
+            float4 *d = reinterpret_cast<float4 *>(turn_s + 64 * i + 16 * (lane - 28));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          } else {
+            uint32_t f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
+            const uint32_t at = (uint32_t)(lane >> 2) * 8192u + ro, c = 2 * (lane & 3);
+            st_q(at + ((c ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+            st_q(at + (((c + 1) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+          }
           if constexpr (kV32) {
             if (lane < 8) {
               uint32_t fc[4];
@@ -775,6 +762,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
               st_q(8 * 8192 + ro + ((lane ^ (r & 7)) << 4), fc[0], fc[1], fc[2], fc[3]);
             }
           }
+        }
+        if (rope) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * warp + i0 + i;
+            const float x1 = turn_s[64 * i + ia], x2 = turn_s[64 * i + ib];
+            const uint32_t f = tc::pack_f16x2(fmaf(x1, co[i], -(x2 * si[i])), fmaf(x2, co[i], x1 * si[i]));
+            uint8_t *q = smem + Cfg::kQ + 7 * 8192 + (r >> 3) * 1024 + (r & 7) * 128;
+            uint8_t *qa = q + (((ia >> 3) ^ (r & 7)) << 4) + 2 * (ia & 7);
+            if (p.gptj) {
+              *reinterpret_cast<uint32_t *>(qa) = f;
+            } else {
+              *reinterpret_cast<uint16_t *>(qa) = (uint16_t)f;
+              *reinterpret_cast<uint16_t *>(q + (((ib >> 3) ^ (r & 7)) << 4) + 2 * (ib & 7)) = (uint16_t)(f >> 16);
+            }
+          }
+          __syncwarp();   // the stage is free again
         }
       }
       tc::fence_async_smem();
@@ -789,8 +794,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     TileRun seg;
     for (bool begun = false; walk.next(seg); begun = true) {
       const int32_t late = begun ? 1 : 0;   // (a later tile than the pair's first)
+      const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
+      auto load_info = [&](int64_t half) { return halves_ok(p, half) ? __ldcg(info + half * 2) : make_int4(0, 0, 0, 0); };
+      int4 inf = make_int4(0, 0, 0, 0);
+      if (kChunk || begun) inf = load_info(seg.half);
       stage_q(seg.g0, seg.n);
-      if (!kChunk && !begun) pdl_wait_primary();   // group records of the gather
+      if (!kChunk && !begun) {
+        pdl_wait_primary();   // group records of the gather
+        inf = load_info(seg.half);
+      }
       if (bad_pos) report_status(p.status, DSA_ERR_INVALID_ARG);
       sm_bar();   // headf_s
       int64_t next_g0;
@@ -814,9 +826,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       }
       const float hf = headf_s[row];
       float m = -1e30f, l = 0.f;
-      const int4 *info = reinterpret_cast<const int4 *>(p.info) + part;   // (exponent, mask) of two groups
-      auto load_info = [&](int64_t half) { return halves_ok(p, half) ? __ldcg(info + half * 2) : make_int4(0, 0, 0, 0); };
-      int4 inf = load_info(seg.half);
       // chunk: the row's own place among the keys of this thread, moved on with the units
       int32_t place = 0;
       if constexpr (kChunk) place = (int32_t)((uint32_t)(seg.g0 + side * 64 + row) / (uint32_t)p.H) + seg.shift - seg.key0 - 64 * part;
@@ -997,6 +1006,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       // from the threads, 16 bytes to a row at a time, an epilogue took 11000
       // cycles.)
       const float wo = roww_s[row];
+      if (whole && !p.tail_out) {
+        // Nothing to add: the tile fits as bf16, in one pass; whole rows leave in
+        // 32 bytes a lane (5000 cycles with the two passes of fp32 below).
+        const uint32_t dst = row * 1024, c = tl + Cfg::kColO + half * 128;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t o[2][16];
+          DSA_TMEM_LD16_NOWAIT(c + 32 * g, o[0]);
+          DSA_TMEM_LD16_NOWAIT(c + 32 * g + 16, o[1]);
+          DSA_TMEM_WAIT32(o[0], o[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 8 * (i & 1) + 2 * k;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[i >> 1][e]) * wo, __uint_as_float(o[i >> 1][e + 1]) * wo);
+              w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            st_q(dst + (((half * 32 + kh * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+          }
+        }
+        sm_bar();
+        const int n = min(8, rows_here - 8 * warp);   // the warp's rows that exist
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const int r = 8 * warp + i;
+          if (!row_ok(p, g0 + r)) continue;
+          const uint8_t *src = smem + Cfg::kQ + r * 1024;
+          const uint4 a = *reinterpret_cast<const uint4 *>(src + (((2 * lane) ^ (r & 7)) << 4));
+          const uint4 b = *reinterpret_cast<const uint4 *>(src + (((2 * lane + 1) ^ (r & 7)) << 4));
+          __nv_bfloat16 *to = p.out + (g0 + r) * kD + 16 * lane;
+          if (wide) {
+            tc::stg_v8(to, a, b);
+          } else {
+            reinterpret_cast<uint4 *>(to)[0] = a;
+            reinterpret_cast<uint4 *>(to)[1] = b;
+          }
+        }
+        sm_bar();   // the tile is free again
+        tc::tc_fence_before();   // O read before the next product
+        continue;
+      }
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         const uint32_t dst = row * 1024, c = tl + Cfg::kColO + half * 128 + pass * 64;
