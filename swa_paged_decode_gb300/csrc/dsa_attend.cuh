@@ -650,38 +650,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       if (dbg_ok(p.status, off + 16u <= Cfg::kP - Cfg::kQ, kDbgSmemQ)) tc::st_shared_v4(q_base + off, a, b, c, d);
     };
     bool bad_pos = false;   // reported once the gather, which clears the status word, is done
+    // Row lane % 8 of the warp's 8 of a tile: its queries, its table row (found
+    // before the epilogue of the tile before: its position is a load of its own).
+    const __nv_bfloat16 *qp = nullptr;
+    const float *cp = p.cos_sin;
+    auto find_rows = [&](int64_t g0, int32_t rows) {
+      const uint32_t in = side * 64u + 8u * warp + (lane & 7), gl = (uint32_t)g0 + in;
+      qp = nullptr;
+      cp = p.cos_sin;
+      if ((int32_t)in < rows) {
+        const uint32_t t = gl / (uint32_t)p.H, h = gl - t * (uint32_t)p.H;
+        if (dbg_ok(p.status, (int64_t)t * p.H + h < (int64_t)p.rows, kDbgQ))
+          qp = p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh;
+        if (cp) {
+          const int64_t pos = __ldg(p.positions + t);
+          if (pos >= 0 && pos < p.cs_rows) cp += pos * 64;
+          else bad_pos = true;   // outside the table: flag, row 0
+        }
+      }
+    };
+    bool leaving = false;   // rows of the tile before are on their way out of the Q tile
     // Q rows of this CTA -> f16 K-major tile: RoPE in fp32, times a power of
     // two per row so that its largest unrotated magnitude lies in [1, 2) (a
     // rotation adds half a bit at most). A warp takes 8 rows, 2 at a time
     // with the next 2 in flight; the loop stays rolled and a row's address is
     // found once, by a lane of its own: this code runs once per 128 rows, so
     // its size is its time (8 rows unrolled took 9700 cycles, 700 a row).
-    auto stage_q = [&](int64_t g0, int32_t rows) {
+    auto stage_q = [&]() {
       const bool rope = p.cos_sin != nullptr;
       // The rotation takes a pair per lane, through the P tile, which no product
       // reads now (in the four lanes that hold the last 64 dims it was a third of
       // the instructions).
       const int ia = p.gptj ? 2 * lane : lane, ib = p.gptj ? 2 * lane + 1 : lane + 32;
-      float *turn_s = reinterpret_cast<float *>(smem + Cfg::kP) + 128 * warp;   // [2 rows][64]
-      // row lane % 8 of the warp's: its queries, its table row
-      const uint32_t in = side * 64u + 8u * warp + (lane & 7), gl = (uint32_t)g0 + in;
-      const __nv_bfloat16 *qp = nullptr;
-      const float *cp = p.cos_sin;
-      if ((int32_t)in < rows) {
-        const uint32_t t = gl / (uint32_t)p.H, h = gl - t * (uint32_t)p.H;
-        if (dbg_ok(p.status, (int64_t)t * p.H + h < (int64_t)p.rows, kDbgQ))
-          qp = p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh;
-        if (rope) {
-          const int64_t pos = __ldg(p.positions + t);
-          if (pos >= 0 && pos < p.cs_rows) cp += pos * 64;
-          else bad_pos = true;   // outside the table: flag, row 0
-        }
-      }
-      uint4 na[2], nb[2], nc[2];
-      float nco[2], nsi[2];
+      float *turn_s = reinterpret_cast<float *>(smem + Cfg::kP) + 256 * warp;   // [rows at a time][64]
+      constexpr int kIn = kChunk ? 4 : 2;   // rows at a time (chunks: many short tiles)
+      uint4 na[kIn], nb[kIn], nc[kIn];
+      float nco[kIn], nsi[kIn];
       auto fetch = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kIn; ++i) {
           const uint4 *r = reinterpret_cast<const uint4 *>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(qp), i0 + i));
           na[i] = nb[i] = nc[i] = make_uint4(0, 0, 0, 0);
@@ -703,21 +710,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         }
       };
       fetch(0);
+      if (leaving) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        sm_bar();
+        leaving = false;
+      }
 #pragma unroll 1
-      for (int i0 = 0; i0 < 8; i0 += 2) {
-        uint4 qa[2], qb[2], qc[2];
-        float co[2], si[2];
+      for (int i0 = 0; i0 < 8; i0 += kIn) {
+        uint4 qa[kIn], qb[kIn], qc[kIn];
+        float co[kIn], si[kIn];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kIn; ++i) {
           qa[i] = na[i];
           qb[i] = nb[i];
           qc[i] = nc[i];
           co[i] = nco[i];
           si[i] = nsi[i];
         }
-        if (i0 < 6) fetch(i0 + 2);
+        if (i0 + kIn < 8) fetch(i0 + kIn);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kIn; ++i) {
           const int r = 8 * warp + i0 + i;
           const uint32_t w[8] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w, qb[i].x, qb[i].y, qb[i].z, qb[i].w};
           const uint32_t wc[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
@@ -766,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (rope) {
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < kIn; ++i) {
             const int r = 8 * warp + i0 + i;
             const float x1 = turn_s[64 * i + ia], x2 = turn_s[64 * i + ib];
             const uint32_t f = tc::pack_f16x2(fmaf(x1, co[i], -(x2 * si[i])), fmaf(x2, co[i], x1 * si[i]));
@@ -798,7 +810,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       auto load_info = [&](int64_t half) { return halves_ok(p, half) ? __ldcg(info + half * 2) : make_int4(0, 0, 0, 0); };
       int4 inf = make_int4(0, 0, 0, 0);
       if (kChunk || begun) inf = load_info(seg.half);
-      stage_q(seg.g0, seg.n);
+      if (!begun) find_rows(seg.g0, seg.n);
+      stage_q();
       if (!kChunk && !begun) {
         pdl_wait_primary();   // group records of the gather
         inf = load_info(seg.half);
@@ -966,6 +979,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if ((nqk & 1u) == 0) ph_s ^= 1u;
       }
       // ---- epilogue
+      {   // (the next tile's rows, while the last products run)
+        int64_t g;
+        const int32_t n = walk.peek(seg, g);
+        if (n) find_rows(g, n);
+      }
       red_s[part * 64 + row] = l;
       const int64_t g0 = seg.g0 + side * 64;       // this CTA's first row
       const int32_t rows_here = seg.n - side * 64; // and how many it has of the tile's (none: <= 0)
@@ -1007,9 +1025,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
       // cycles.)
       const float wo = roww_s[row];
       if (whole && !p.tail_out) {
-        // Nothing to add: the tile fits as bf16, in one pass; whole rows leave in
-        // 32 bytes a lane (5000 cycles with the two passes of fp32 below).
-        const uint32_t dst = row * 1024, c = tl + Cfg::kColO + half * 128;
+        // Nothing to add: the tile fits as bf16, in one pass, and its rows leave
+        // by bulk copies, 1 KiB each, that the next tile's queries wait for
+        // (5000 cycles with the two passes of fp32 below). Rows lie 1040 bytes
+        // apart, the last ones in the P tile: 8 rows' pieces in 8 bank groups.
+        constexpr uint32_t kPitch = 1040;
+        const uint32_t dst = q_base + row * kPitch + (half * 32 + kh * 16) * 16, c = tl + Cfg::kColO + half * 128;
+        static_assert(Cfg::kQ + 64 * kPitch <= Cfg::kRing, "rows on their way out");
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t o[2][16];
@@ -1025,29 +1047,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
               const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[i >> 1][e]) * wo, __uint_as_float(o[i >> 1][e + 1]) * wo);
               w[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            st_q(dst + (((half * 32 + kh * 16 + 4 * g + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            tc::st_shared_v4(dst + (4 * g + i) * 16, w[0], w[1], w[2], w[3]);
           }
         }
-        sm_bar();
-        const int n = min(8, rows_here - 8 * warp);   // the warp's rows that exist
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const int r = 8 * warp + i;
-          if (!row_ok(p, g0 + r)) continue;
-          const uint8_t *src = smem + Cfg::kQ + r * 1024;
-          const uint4 a = *reinterpret_cast<const uint4 *>(src + (((2 * lane) ^ (r & 7)) << 4));
-          const uint4 b = *reinterpret_cast<const uint4 *>(src + (((2 * lane + 1) ^ (r & 7)) << 4));
-          __nv_bfloat16 *to = p.out + (g0 + r) * kD + 16 * lane;
-          if (wide) {
-            tc::stg_v8(to, a, b);
-          } else {
-            reinterpret_cast<uint4 *>(to)[0] = a;
-            reinterpret_cast<uint4 *>(to)[1] = b;
-          }
-        }
-        sm_bar();   // the tile is free again
+        tc::fence_async_smem();
         tc::tc_fence_before();   // O read before the next product
+        sm_bar();
+        const int r = 8 * warp + lane;
+        if (lane < 8 && r < rows_here && row_ok(p, g0 + r)) {
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 1024;" ::"l"(p.out + (g0 + r) * kD),
+                       "r"(q_base + r * kPitch)
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        leaving = true;
         continue;
       }
 #pragma unroll 1
@@ -1117,6 +1130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     }
   }
 
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // (rows that left by bulk copies have arrived)
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();   // no MMA, commit or arrive of the other CTA reaches this one any more
