@@ -17,7 +17,8 @@
 //   attend  units start at the half tile of the tile's first key; the keys that
 //           a row may not see are masked like unused slots, by two words per
 //           thread and unit;
-//   merge   by (row tile, row).
+//   merge   the rows of tiles that pairs share and of tiles without keys, from a
+//           list that block 0 leaves too.
 #include "dsa_attend.cuh"
 #include "dsa_chunk_index.cuh"
 
@@ -66,6 +67,8 @@ __device__ void lay_out(const ChunkParams &p, bool ok) {
   __shared__ int64_t w_s[kChThreads / 32];
   const int tid = threadIdx.x;
   int64_t tiles = 0;
+  if (tid == 0) *p.n_merge = 0;
+  __syncthreads();
   if (ok) {
     for (int32_t b0 = 0; b0 < p.B; b0 += kChThreads) {
       const int32_t b = b0 + tid;
@@ -117,14 +120,21 @@ __device__ void lay_out(const ChunkParams &p, bool ok) {
   each([&](int32_t t, int32_t b, const Sequence &s, int32_t i, int32_t half, int32_t u) {
     p.row_tile[2 * (int64_t)t] = make_int4(s.s0 * p.H + 128 * i, s.tile_rows(p.H, i), u, 0);
     p.row_tile[2 * (int64_t)t + 1] = make_int4(b * p.seq_halves + half, half * 128, s.len - s.n - s.s0, 0);
-    if (u == 0) return;
+    if (u == 0) {
+      p.merge[atomicAdd(p.n_merge, 1)] = t;
+      return;
+    }
     const int64_t cost = u + tile_cost, next = at + cost;
+    bool shared = false;   // (the list's order does not matter)
     // pairs c with at <= total c / C < next
     for (int64_t c = (at * p.C + total - 1) / total; c < p.C; ++c) {
       const int64_t x = total * c / p.C;
       if (x >= next) break;
-      p.begin[c] = make_int2(t, (int32_t)max(x - at - tile_cost, (int64_t)0));
+      const int32_t w = (int32_t)max(x - at - tile_cost, (int64_t)0);
+      p.begin[c] = make_int2(t, w);
+      shared |= w > 0;
     }
+    if (shared) p.merge[atomicAdd(p.n_merge, 1)] = t;
     at = next;
   });
   if (total == 0)
@@ -204,8 +214,9 @@ cudaError_t launch_chunk(const ChunkParams &p, int32_t num_sms, cudaStream_t st)
   e = launch_dependent(config(2u * p.C, kPfThreads, PfCfg<kV32>::kSmem, st), prefix_attend_kernel<kV32, true>, p, map);
   if (e != cudaSuccess) return e;
   // as for a prefix: few parts to a row by a warp, many by a block
-  if (p.C < 8 * p.R) return launch_dependent(config(32u * p.R, 128, 0, st), prefix_merge_kernel<32, 1, true>, p);
-  return launch_dependent(config(128u * p.R, 256, 0, st), prefix_merge_kernel<128, 2, true>, p);
+  const unsigned most = (unsigned)std::min(p.R, p.C);
+  if (p.C < 8 * p.R) return launch_dependent(config(32u * most, 128, 0, st), prefix_merge_kernel<32, 1, true>, p);
+  return launch_dependent(config(128u * most, 256, 0, st), prefix_merge_kernel<128, 2, true>, p);
 }
 
 }  // namespace
@@ -262,7 +273,7 @@ dsa_status dsa_chunk_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_head
   take(plan->ws_row_tile_offset, 32 * row_tiles);
   take(plan->ws_seq_tile_offset, 4 * (int64_t)num_seqs);
   take(plan->ws_begin_offset, 8 * ((int64_t)plan->pairs + 1));
-  take(plan->ws_tile_offset, 8 * row_tiles);
+  take(plan->ws_tile_offset, 12 * row_tiles);   // (and the list of tiles to merge)
   take(plan->ws_part_lse_offset, 4 * slots);
   take(plan->ws_part_o_offset, 4 * slots * dsa::kD);
   plan->workspace_bytes = num_tokens == 0 || num_seqs == 0 ? 0 : off;
@@ -343,6 +354,8 @@ dsa_status dsa_chunk_run(const dsa_chunk_plan_t *plan, void *workspace, size_t w
   p.seq_tile = reinterpret_cast<int32_t *>(w + plan->ws_seq_tile_offset);
   p.begin = reinterpret_cast<int2 *>(w + plan->ws_begin_offset);
   p.tile = reinterpret_cast<int2 *>(w + plan->ws_tile_offset);
+  p.merge = reinterpret_cast<int32_t *>(p.tile + p.R);
+  p.n_merge = p.status + 2;
   p.part_lse = reinterpret_cast<float *>(w + plan->ws_part_lse_offset);
   p.part_o = reinterpret_cast<float *>(w + plan->ws_part_o_offset);
   p.check_rows = p.rows;

@@ -56,7 +56,7 @@ def test_plan_layout(lib, T, S, H, width, sms, d):
     keys, parts = 128 * p.seq_halves * S, 2 * p.pairs * 128
     spans = [(0, 256), (p.ws_info_offset, 8 * keys // 32), (p.ws_key_e_offset, 4 * keys), (p.ws_image_offset, 2 * d * keys),
              (p.ws_row_tile_offset, 32 * p.row_tiles), (p.ws_seq_tile_offset, 4 * S), (p.ws_begin_offset, 8 * (p.pairs + 1)),
-             (p.ws_tile_offset, 8 * p.row_tiles), (p.ws_part_lse_offset, 4 * parts), (p.ws_part_o_offset, 2048 * parts)]
+             (p.ws_tile_offset, 12 * p.row_tiles), (p.ws_part_lse_offset, 4 * parts), (p.ws_part_o_offset, 2048 * parts)]
     for (a, n), (b, _) in zip(spans, spans[1:] + [(nbytes, 0)]):
         assert a % 256 == 0 and a + n <= b
     assert p.workspace_bytes == nbytes and p.wait_budget_cycles == 0
