@@ -24,16 +24,30 @@
 //
 // Two or three launches:
 //   prepare  queries to f16 tile images (128 rows x 64 dims, 128-byte swizzle),
-//            each row's constants, the list of items: (sequence, 128 keys, a
-//            range of its row tiles);
-//   weigh    CTA pairs (cta_group::2, M = 128: 64 keys in each CTA, N up to 256
-//            query rows) take items in turn: 8 warps dequantize the next item's
-//            records into one of two key tiles while the products of the present
-//            one run; query chunks come through a ring; 8 warps take the
-//            exponentials of one step while the next one's product runs;
+//            each row's constants, the list of items: (sequence, 128 or 256 keys,
+//            a range of its row tiles);
+//   weigh    CTA pairs (cta_group::2) take items in turn: 8 warps dequantize the
+//            next item's records into one of two key tiles while the products of
+//            the present one run; query chunks come through a ring, three warps
+//            copying; 8 warps take the exponentials of one step (up to 256 query
+//            rows) while the next one's product runs;
 //   add      where items had to share the rows of their keys (few keys, many
 //            rows): the parts in order, so that the result does not depend on
 //            timing.
+//
+// What bounds it. Many rows: the queries' way from L2. With 64 keys in each CTA
+// (M = 128) a step's 256 KiB feed 2048 cycles of products, more than L2's 12 TB/s:
+// leaving out half of the products or all exponentials changed nothing (64 tokens
+// x 128 heads over 65536 MODEL1 records 408 us). With 128 keys in each (WIDE, M =
+// 256, one key tile in place of two) the same bytes feed twice the work: 314 us,
+// 1749 TFLOP/s, 0.91 of the measured peak; an item's set-up then stands alone, so
+// few rows keep to 64 (dsa_weights_plan). Single tokens: latency, four roles of
+// 2000 to 4000 cycles per 128 keys behind one another (32 tokens x 64 heads over
+// 98000 records 33 us, 1.6 TB/s). The steps there: block-wide staging of the rows'
+// constants and one warp per key's loads 60 and 653 us; constants a step ahead,
+// packed arithmetic 48, 528; records converted in f16 by 8 warps, addresses found a
+// lane per key, products unrolled 44, 452; items in shared memory 34; constants
+// by bulk copies and no barrier per step 33, 408.
 #include "dsa_attend.cuh"
 #include "dsa_chunk_index.cuh"
 #include "dsa_rows.cuh"
@@ -515,149 +529,149 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
   } else if (warp >= 8) {
     tc::setmaxnreg_dec<80>();
     if (warp >= 9) {
-    // ======================================================== query chunks
-    if (lane == 0) {
-      uint32_t slot = 0, ph = 1;
-      int turn = warp - 9;   // 0: this warp's slot (one thread would take longer for a slot than its products do)
-      bool ok = true;
-      uint32_t filled = 0, fill_ph = 0;
-      const uint32_t full0 = lead(Cfg::kFull);
-      uint32_t cs = 0, ph_c = 1;
-      while (ok && items.next()) {
-        int N;
-        while (ok && items.next_step(N)) {
-          if (warp == 9) {   // the constants of the step's rows, to either CTA its own copy
-            ok = wait(Cfg::kCEmpty + cs, ph_c);
-            if (!ok) break;
-            const uint32_t bytes = N == 256 ? 2048u : 1024u;
-            tc::mbar_expect_tx(&bars[Cfg::kCFull + cs], bytes);
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             sbase + Cfg::kColS + cs * (8 * Cfg::kN)),
-                         "l"(p.row + ((int64_t)items.c.x + items.tile) * 256), "r"(bytes), "r"(tc::smem_u32(&bars[Cfg::kCFull + cs]))
-                         : "memory");
-            if (++cs == Cfg::kConst) {
-              cs = 0;
-              ph_c ^= 1u;
-            }
-          }
-          // this CTA's N / 2 rows: of a tile of its own with N = 256
-          const int64_t tile = items.c.x + items.tile + (N == 256 ? side : 0);
-          const int32_t y0 = (int32_t)(tile * (Cfg::kDB * 32)) + (N == 256 ? 0 : (int32_t)side * (N / 8));
-          const bool in = dbg_ok(p.status, tile >= 0 && tile < p.tiles, kDbgPartial);
-          const int per = Cfg::per_slot(N);
-          const uint32_t block = (uint32_t)N * 64u;   // bytes of this CTA's rows of a 64-dim block
-          for (int c = 0; c < Cfg::kDB && ok; c += per) {
-            if (turn == 0) {
-              turn = kWtCopies;
-              ok = wait(Cfg::kEmpty + slot, ph);
+      // ======================================================== query chunks
+      if (lane == 0) {
+        uint32_t slot = 0, ph = 1;
+        int turn = warp - 9;   // 0: this warp's slot (one thread would take longer for a slot than its products do)
+        bool ok = true;
+        uint32_t filled = 0, fill_ph = 0;
+        const uint32_t full0 = lead(Cfg::kFull);
+        uint32_t cs = 0, ph_c = 1;
+        while (ok && items.next()) {
+          int N;
+          while (ok && items.next_step(N)) {
+            if (warp == 9) {   // the constants of the step's rows, to either CTA its own copy
+              ok = wait(Cfg::kCEmpty + cs, ph_c);
               if (!ok) break;
-              const int n = min(per, Cfg::kDB - c);
-              if (side == 0) {
-                tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 2u * n * block);   // both CTAs' bytes
-                filled |= 1u << slot;
-                fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
+              const uint32_t bytes = N == 256 ? 2048u : 1024u;
+              tc::mbar_expect_tx(&bars[Cfg::kCFull + cs], bytes);
+              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                               sbase + Cfg::kColS + cs * (8 * Cfg::kN)),
+                           "l"(p.row + ((int64_t)items.c.x + items.tile) * 256), "r"(bytes), "r"(tc::smem_u32(&bars[Cfg::kCFull + cs]))
+                           : "memory");
+              if (++cs == Cfg::kConst) {
+                cs = 0;
+                ph_c ^= 1u;
               }
-              const uint32_t dst = ring + slot * 16384, bar = full0 + 8 * slot;
-              const void *map = N == 256 ? &map16 : N == 128 ? &map8 : &map4;
-              for (int j = 0; j < n; ++j) tc::tma_load_pair(dst + j * block, map, 0, in ? y0 + (c + j) * 32 : 0, bar);
             }
-            --turn;
-            if (++slot == Cfg::kSlots) {
-              slot = 0;
-              ph ^= 1u;
-            }
-          }
-          items.advance(N);
-        }
-      }
-      // no commit reaches this CTA's barriers after its end; after a timeout no
-      // copy is in flight (as in the attend kernel)
-      for (int k = 0; k < Cfg::kSlots && ok; ++k) {
-        ok = wait(Cfg::kEmpty + slot, ph);
-        if (++slot == Cfg::kSlots) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      }
-      if (!ok) {
-        for (int k = 0; k < Cfg::kSlots; ++k)
-          if ((filled >> k) & 1u) tc::mbar_wait(&bars[Cfg::kFull + k], (fill_ph >> k) & 1u, kPfCopyWait);
-        const long long t0 = clock64();
-        while (clock64() - t0 < kPfCopyWait / 10) __nanosleep(1000);
-      }
-    }
-    __syncwarp();
-  } else {
-    // ======================================================== MMA issue
-    if (side == 0) {
-      constexpr uint16_t kBoth = 3;
-      constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
-      const uint32_t dk0 = tc::sdesc_lo(sbase, 16), dq0 = tc::sdesc_lo(ring, 16);
-      uint32_t slot = 0, ph = 0, set = 0, ph_a = 1, turn = 0;
-      bool ok = true, issued = false;
-      auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
-      while (ok && items.next()) {
-        if (items.empty()) continue;
-        const uint32_t buf = turn % Cfg::kBufs, dk = dk0 + buf * (Cfg::kTile >> 4);
-        ok = here(wait(Cfg::kKFull + buf, (turn / Cfg::kBufs) & 1u));
-        ++turn;
-        int N;
-        while (ok && items.next_step(N)) {
-          items.advance(N);
-          const bool last = items.tile >= items.end;
-          ok = here(wait(Cfg::kAEmpty + set, ph_a));
-          if (!ok) break;
-          tc::tc_fence_after();
-          issued = true;
-          const uint32_t d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);
-          auto products = [&](auto rows) {   // unrolled for each N: a slot is to go out in less time than its products take
-            constexpr int kRows = decltype(rows)::value, kPer = 256 / kRows;
-            constexpr uint32_t kId = tc::idesc_f16(2 * Cfg::kKeys, kRows, false, false);
-#pragma unroll
-            for (int c0 = 0; c0 < Cfg::kDB; c0 += kPer) {
-              if (!here(wait(Cfg::kFull + slot, ph))) return false;
-              tc::tc_fence_after();
-              if (tc::elect_one()) {
-                const uint32_t q = dq0 + slot * 1024u;
-#pragma unroll
-                for (int j = 0; j < kPer && c0 + j < Cfg::kDB; ++j) {
-                  const int c = c0 + j;
-                  const uint32_t d = Cfg::kBlocks ? d0 + (c >> 1) * Cfg::kCols : d0;
-                  const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
-#pragma unroll
-                  for (int ks = 0; ks < 4; ++ks)
-                    tc::mma_f16_pair(d, dk + c * (Cfg::kBlock >> 4) + 2 * ks, q + j * (kRows * 4u) + 2 * ks, kHi, kId, !first || ks ? 1u : 0u);
+            // this CTA's N / 2 rows: of a tile of its own with N = 256
+            const int64_t tile = items.c.x + items.tile + (N == 256 ? side : 0);
+            const int32_t y0 = (int32_t)(tile * (Cfg::kDB * 32)) + (N == 256 ? 0 : (int32_t)side * (N / 8));
+            const bool in = dbg_ok(p.status, tile >= 0 && tile < p.tiles, kDbgPartial);
+            const int per = Cfg::per_slot(N);
+            const uint32_t block = (uint32_t)N * 64u;   // bytes of this CTA's rows of a 64-dim block
+            for (int c = 0; c < Cfg::kDB && ok; c += per) {
+              if (turn == 0) {
+                turn = kWtCopies;
+                ok = wait(Cfg::kEmpty + slot, ph);
+                if (!ok) break;
+                const int n = min(per, Cfg::kDB - c);
+                if (side == 0) {
+                  tc::mbar_expect_tx(&bars[Cfg::kFull + slot], 2u * n * block);   // both CTAs' bytes
+                  filled |= 1u << slot;
+                  fill_ph = (fill_ph & ~(1u << slot)) | ((ph ^ 1u) << slot);
                 }
-                tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
-                if (c0 + kPer >= Cfg::kDB) {
-                  tc::mma_commit_to(&bars[Cfg::kAFull + set], kBoth);
-                  if (last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
-                }
+                const uint32_t dst = ring + slot * 16384, bar = full0 + 8 * slot;
+                const void *map = N == 256 ? &map16 : N == 128 ? &map8 : &map4;
+                for (int j = 0; j < n; ++j) tc::tma_load_pair(dst + j * block, map, 0, in ? y0 + (c + j) * 32 : 0, bar);
               }
-              __syncwarp();
+              --turn;
               if (++slot == Cfg::kSlots) {
                 slot = 0;
                 ph ^= 1u;
               }
             }
-            return true;
-          };
-          if (N == 64) ok = products(std::integral_constant<int, 64>());
-          else if (Cfg::kN == 128 || N == 128) ok = products(std::integral_constant<int, 128>());
-          else ok = products(std::integral_constant<int, Cfg::kN>());
-          if (++set == Cfg::kSets) {
-            set = 0;
-            ph_a ^= 1u;
+            items.advance(N);
           }
         }
+        // no commit reaches this CTA's barriers after its end; after a timeout no
+        // copy is in flight (as in the attend kernel)
+        for (int k = 0; k < Cfg::kSlots && ok; ++k) {
+          ok = wait(Cfg::kEmpty + slot, ph);
+          if (++slot == Cfg::kSlots) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) {
+          for (int k = 0; k < Cfg::kSlots; ++k)
+            if ((filled >> k) & 1u) tc::mbar_wait(&bars[Cfg::kFull + k], (fill_ph >> k) & 1u, kPfCopyWait);
+          const long long t0 = clock64();
+          while (clock64() - t0 < kPfCopyWait / 10) __nanosleep(1000);
+        }
       }
-      if (issued && !ok && tc::elect_one()) {   // MMAs issued before a timeout end before TMEM is freed
-        tc::mma_commit_one(&bars[Cfg::kDrain]);
-        tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
+      __syncwarp();
+    } else {
+      // ======================================================== MMA issue
+      if (side == 0) {
+        constexpr uint16_t kBoth = 3;
+        constexpr uint32_t kHi = tc::sdesc_hi(1024, tc::kSwz128);
+        const uint32_t dk0 = tc::sdesc_lo(sbase, 16), dq0 = tc::sdesc_lo(ring, 16);
+        uint32_t slot = 0, ph = 0, set = 0, ph_a = 1, turn = 0;
+        bool ok = true, issued = false;
+        auto here = [&](bool x) { return __all_sync(0xffffffffu, x); };
+        while (ok && items.next()) {
+          if (items.empty()) continue;
+          const uint32_t buf = turn % Cfg::kBufs, dk = dk0 + buf * (Cfg::kTile >> 4);
+          ok = here(wait(Cfg::kKFull + buf, (turn / Cfg::kBufs) & 1u));
+          ++turn;
+          int N;
+          while (ok && items.next_step(N)) {
+            items.advance(N);
+            const bool last = items.tile >= items.end;
+            ok = here(wait(Cfg::kAEmpty + set, ph_a));
+            if (!ok) break;
+            tc::tc_fence_after();
+            issued = true;
+            const uint32_t d0 = tmem + set * (Cfg::kAcc * Cfg::kCols);
+            auto products = [&](auto rows) {   // unrolled for each N: a slot is to go out in less time than its products take
+              constexpr int kRows = decltype(rows)::value, kPer = 256 / kRows;
+              constexpr uint32_t kId = tc::idesc_f16(2 * Cfg::kKeys, kRows, false, false);
+#pragma unroll
+              for (int c0 = 0; c0 < Cfg::kDB; c0 += kPer) {
+                if (!here(wait(Cfg::kFull + slot, ph))) return false;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+                  const uint32_t q = dq0 + slot * 1024u;
+#pragma unroll
+                  for (int j = 0; j < kPer && c0 + j < Cfg::kDB; ++j) {
+                    const int c = c0 + j;
+                    const uint32_t d = Cfg::kBlocks ? d0 + (c >> 1) * Cfg::kCols : d0;
+                    const bool first = Cfg::kBlocks ? (c & 1) == 0 : c == 0;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                      tc::mma_f16_pair(d, dk + c * (Cfg::kBlock >> 4) + 2 * ks, q + j * (kRows * 4u) + 2 * ks, kHi, kId, !first || ks ? 1u : 0u);
+                  }
+                  tc::mma_commit_to(&bars[Cfg::kEmpty + slot], kBoth);
+                  if (c0 + kPer >= Cfg::kDB) {
+                    tc::mma_commit_to(&bars[Cfg::kAFull + set], kBoth);
+                    if (last) tc::mma_commit_to(&bars[Cfg::kKEmpty + buf], kBoth);
+                  }
+                }
+                __syncwarp();
+                if (++slot == Cfg::kSlots) {
+                  slot = 0;
+                  ph ^= 1u;
+                }
+              }
+              return true;
+            };
+            if (N == 64) ok = products(std::integral_constant<int, 64>());
+            else if (Cfg::kN == 128 || N == 128) ok = products(std::integral_constant<int, 128>());
+            else ok = products(std::integral_constant<int, Cfg::kN>());
+            if (++set == Cfg::kSets) {
+              set = 0;
+              ph_a ^= 1u;
+            }
+          }
+        }
+        if (issued && !ok && tc::elect_one()) {   // MMAs issued before a timeout end before TMEM is freed
+          tc::mma_commit_one(&bars[Cfg::kDrain]);
+          tc::mbar_wait(&bars[Cfg::kDrain], 0u, kPfWait);
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ======================================================== exponentials
     tc::setmaxnreg_inc<112>();
@@ -739,45 +753,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
           // (a branch for each four rows inside would keep their loads and
           // exponentials from overlapping: 430 cycles for 16 rows)
           auto step = [&](auto masked) {
-          if constexpr (Cfg::kAcc == 1) {   // the next 16 rows' load in flight
-            uint32_t d[2][16];
-            auto take = [&](uint32_t (&v)[16], uint32_t (&next)[16], int g) {   // false: these were the last
-              DSA_TMEM_WAIT16(v);
-              const bool more = g + 16 < mine;
-              if (more) DSA_TMEM_LD16_NOWAIT(c0 + g + 16, next);
-              else release();
-              F2 x[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[0]);
-              weigh(masked, x, g);
-              return more;
-            };
-            DSA_TMEM_LD16_NOWAIT(c0, d[0]);
-#pragma unroll 1
-            for (int g = 0;; g += 32)
-              if (!take(d[0], d[1], g) || !take(d[1], d[0], g + 16)) break;
-          } else {
-#pragma unroll 1
-            for (int g = 0; g < mine; g += 16) {
+            if constexpr (Cfg::kAcc == 1) {   // the next 16 rows' load in flight
               uint32_t d[2][16];
-              F2 x[8];
+              auto take = [&](uint32_t (&v)[16], uint32_t (&next)[16], int g) {   // false: these were the last
+                DSA_TMEM_WAIT16(v);
+                const bool more = g + 16 < mine;
+                if (more) DSA_TMEM_LD16_NOWAIT(c0 + g + 16, next);
+                else release();
+                F2 x[8];
 #pragma unroll
-              for (int k = 0; k < Cfg::kAcc; k += 2) {
-                const int k1 = k + 1 < Cfg::kAcc ? k + 1 : k;
-                DSA_TMEM_LD16_NOWAIT(c0 + k * Cfg::kCols + g, d[0]);
-                DSA_TMEM_LD16_NOWAIT(c0 + k1 * Cfg::kCols + g, d[1]);
-                DSA_TMEM_WAIT32(d[0], d[1]);
+                for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[0]);
+                weigh(masked, x, g);
+                return more;
+              };
+              DSA_TMEM_LD16_NOWAIT(c0, d[0]);
+#pragma unroll 1
+              for (int g = 0;; g += 32)
+                if (!take(d[0], d[1], g) || !take(d[1], d[0], g + 16)) break;
+            } else {
+#pragma unroll 1
+              for (int g = 0; g < mine; g += 16) {
+                uint32_t d[2][16];
+                F2 x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const F2 v = f2(__uint_as_float(d[0][2 * i]), __uint_as_float(d[0][2 * i + 1]));
-                  x[i] = k == 0 ? f2_mul(v, s[0]) : f2_fma(v, s[k], x[i]);
-                  if (k1 > k) x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k1], x[i]);
+                for (int k = 0; k < Cfg::kAcc; k += 2) {
+                  const int k1 = k + 1 < Cfg::kAcc ? k + 1 : k;
+                  DSA_TMEM_LD16_NOWAIT(c0 + k * Cfg::kCols + g, d[0]);
+                  DSA_TMEM_LD16_NOWAIT(c0 + k1 * Cfg::kCols + g, d[1]);
+                  DSA_TMEM_WAIT32(d[0], d[1]);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const F2 v = f2(__uint_as_float(d[0][2 * i]), __uint_as_float(d[0][2 * i + 1]));
+                    x[i] = k == 0 ? f2_mul(v, s[0]) : f2_fma(v, s[k], x[i]);
+                    if (k1 > k) x[i] = f2_fma(f2(__uint_as_float(d[1][2 * i]), __uint_as_float(d[1][2 * i + 1])), s[k1], x[i]);
+                  }
                 }
+                if (g + 16 >= mine) release();
+                weigh(masked, x, g);
               }
-              if (g + 16 >= mine) release();
-              weigh(masked, x, g);
             }
-          }
           };
           if (all) step(std::false_type());
           else step(std::true_type());

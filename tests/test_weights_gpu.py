@@ -153,9 +153,11 @@ def test_many_sequences_and_items():
     c.check(c.run()[0])
 
 
-def test_long_list():
+@pytest.mark.parametrize("sms", [0, 2])
+def test_long_list(sms):
+    """Also more items to a pair than it holds in shared memory."""
     c = Case([(1, 70001)], 16, W.FMT_FP8_528, seed=13, num_slots=4096)
-    c.check(c.run()[0])
+    c.check(c.run(sms)[0])
 
 
 @pytest.mark.parametrize("fmt", [W.FMT_FP8_528, W.FMT_MODEL1_584, W.FMT_V32_656])
