@@ -133,6 +133,15 @@ def test_splits(sms, tail):
     check(c, out, lse)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("sms", [2, 6])
+def test_whole_tiles_with_rows_that_end_inside_a_warp(fmt, tail, sms):
+    """Several tiles to a pair, whole and shared, whose last rows are not 32."""
+    c = Batch([(17, 300), (1, 40), (20, 500), (9, 9)], 20, fmt, seed=sms, sink=True, tail=tail, window=0 if sms == 2 else 150)
+    check(c, *run(c, sms)[:2])
+
+
 def test_no_slot_kept():
     c = Batch([(3, 300), (4, 200)], 16, W.FMT_FP8_528, seed=6, tail=True)
     c.slots[0] = -1
