@@ -171,6 +171,40 @@ def test_many_row_tiles():
     check(c, *run(c)[:2])
 
 
+@pytest.mark.parametrize("H", [1, 7, 200, 300])
+def test_any_head_count(H):
+    """Row tiles that begin and end inside a token's heads."""
+    c = Batch([(5, 300), (1, 40), (9, 150)], H, W.FMT_FP8_528_UE8M0, seed=H, sink=True, window=100)
+    for sms in (4, 0):
+        check(c, *run(c, sms)[:2])
+
+
+def test_outputs_on_16_byte_boundaries():
+    c = Batch([(30, 300), (9, 150)], 64, W.FMT_NVFP4_288, seed=3, sink=True)
+    for tail in (False, True):
+        if tail:
+            c.tail_out, c.tail_lse = 0.1 * torch.ones((c.T, 64, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((c.T, 64), device="cuda")
+        for sms in (2, 0):
+            attn = attention(c, sms)
+            room = torch.full((c.T * 64 * 512 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+            attn.out = room[8:-8].view(c.T, 64, 512)
+            assert attn.out.data_ptr() % 32 == 16
+            check(c, *run(c, attn=attn)[:2])
+            assert bool((room[:8] == 7).all()) and bool((room[-8:] == 7).all())
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+def test_negative_and_zero_scale(scale):
+    c = Batch([(20, 300)], 16, W.FMT_NVFP4_288, seed=33)
+    c.scale = scale
+    check(c, *run(c)[:2])
+
+
+def test_no_tokens_in_any_sequence():
+    c = Batch([(0, 30), (0, 0)], 16, W.FMT_FP8_528, seed=4, behind=5)
+    check(c, *run(c)[:2])
+
+
 def test_long_list_of_few_tokens():
     c = Batch([(2, 70000)], 16, W.FMT_NVFP4_288, seed=13, num_slots=4096)
     check(c, *run(c)[:2])

@@ -190,6 +190,18 @@ def test_in_place_strided_and_accumulated():
         assert float((view[b, :n] - twice[b, :n]).abs().max()) <= 1e-5
 
 
+def test_negative_scale_and_no_tokens():
+    c = Case([(20, 300), (1, 64)], 16, W.FMT_FP8_528, seed=33)
+    c.c.scale = -0.03
+    for b, t, at, k, x, mass in c.c.scores():
+        c.lse[t:t + x.shape[0]] = torch.logsumexp(x, 2).float()
+    c.check(c.run()[0])
+    c = Case([(0, 30), (0, 0), (0, 200)], 16, W.FMT_FP8_528, seed=4, behind=5)
+    out, _ = c.run()
+    c.check(out)
+    assert torch.equal(out[0, :30], c.before[0, :30]) and torch.equal(out[2, :200], c.before[2, :200])
+
+
 def test_sums_of_all_weights():
     """Every query row's weights add up to one."""
     c = Case([(30, 500), (1, 300)], 64, W.FMT_FP8_528_UE8M0, seed=30, base=False)
