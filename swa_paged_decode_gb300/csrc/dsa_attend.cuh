@@ -276,15 +276,14 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 //
 // What bounds it: the products' shared-memory operands and the issue of a
 // chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP), gather and merge
-// included: 367 us a call in a loop under the power cap (1498 TFLOP/s, a library
-// product of 8192^3 reaches 1706 there), 339 to 351 us for one call alone, by
-// the box (1566 to 1622 of 1872); 313 us without the copies, measured at 342.
+// included: 330 to 340 us for one call alone, by the box (1620 to 1670 TFLOP/s of
+// 1918); 313 us without the copies, measured at 342.
 // The steps there, calls alone: N = 128 tiles
 // with a relay of the chunks' arrival 1272; arrivals released at CTA scope 914;
 // N = 256, one copy a chunk, converged issue 561; three copying warps and
 // single-test waits 438; merge and gather 413; copies that complete on the
 // leader's barrier 380; Q staging, epilogue, merge and ranges 348; tails
-// prefetched 342. Two pairs that share their key copies by multicast were no
+// prefetched 342; the rotation a pair per lane, rows out by bulk copies 335. Two pairs that share their key copies by multicast were no
 // faster (L2 gives 11 TB/s) and leave 4 of 76 pairs without a place. Few rows
 // are latency: 32 rows x 512 keys take 15 us (gather 2.3, set-up and Q 4, a
 // unit 5, epilogue 2, merge 2).

@@ -9,8 +9,11 @@
 // 10 of them: three histograms, each added up over the cluster in the shared memory
 // of its first CTA), then every warp walks its own run of entries with ballots,
 // knowing from the counts before it where its entries go: no CTA waits for another
-// one there, and the order does not depend on timing. Small lists are latency: a
-// launch, three histograms and two walks.
+// one there, and the order does not depend on timing. All of it is latency: a
+// launch, three histograms and two walks for 32 lists of 2048 (8.8 us), eight
+// cluster barriers and 512 entries to a warp for 16 of 65521 (23 us; 51 with
+// scores compared as floats, every CTA reading the sums and slots loaded 32 at a
+// time).
 #include <cooperative_groups.h>
 
 #include <algorithm>

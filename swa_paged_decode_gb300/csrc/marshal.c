@@ -1,5 +1,5 @@
 /*
- * marshal.c -- the argument marshalling of the cache and shared-prefix calls
+ * marshal.c -- the argument marshalling of the cache, shared-prefix and prompt calls
  * as a CPython extension (swa_paged_decode_gb300._marshal): a tensor's own
  * properties (device, dtype, extents, strides), which its pointer cannot
  * carry, are read and checked here, and the library's function is called
