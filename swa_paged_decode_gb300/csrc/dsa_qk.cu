@@ -9,11 +9,12 @@
 //
 // One pass over memory, a warp per row, lane l on dims 16 l .. 16 l + 15, the
 // next row on its way while one is worked on. What bounds it is memory and issue
-// together (49 % of the issue slots, 214 instructions a row): the rotation takes a pair per lane, through shared memory, as in the cache write
-// (in the four lanes that hold the last 64 dims it was a third of them). The
-// first blocks take the keys, which cost about two query rows each. 8192 tokens x
-// 128 heads: 375 us, 5.8 TB/s, 0.85 of the measured copy rate (418 us with rows
-// strided over the grid and the rotation in four lanes).
+// together (49 % of the issue slots, 214 instructions a row): the rotation takes
+// a pair per lane, through shared memory, as in the cache write (in the four lanes
+// that hold the last 64 dims it was a third of the instructions). The first blocks
+// take the keys, which cost about two query rows each. 8192 tokens x 128 heads: 375
+// us, 5.8 TB/s, 0.85 of the measured copy rate (418 us with rows strided over the
+// grid and the rotation in four lanes).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
