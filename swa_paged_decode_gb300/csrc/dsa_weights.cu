@@ -39,15 +39,17 @@
 // (M = 128) a step's 256 KiB feed 2048 cycles of products, more than L2's 12 TB/s:
 // leaving out half of the products or all exponentials changed nothing (64 tokens
 // x 128 heads over 65536 MODEL1 records 408 us). With 128 keys in each (WIDE, M =
-// 256, one key tile in place of two) the same bytes feed twice the work: 314 us,
-// 1749 TFLOP/s, 0.91 of the measured peak; an item's set-up then stands alone, so
-// few rows keep to 64 (dsa_weights_plan). Single tokens: latency, four roles of
-// 2000 to 4000 cycles per 128 keys behind one another (32 tokens x 64 heads over
-// 98000 records 33 us, 1.6 TB/s). The steps there: block-wide staging of the rows'
-// constants and one warp per key's loads 60 and 653 us; constants a step ahead,
-// packed arithmetic 48, 528; records converted in f16 by 8 warps, addresses found a
-// lane per key, products unrolled 44, 452; items in shared memory 34; constants
-// by bulk copies and no barrier per step 33, 408.
+// 256, one key tile in place of two) the same bytes feed twice the work: 304 us,
+// 1810 TFLOP/s, 0.94 of the measured peak; an item's set-up then stands alone, so
+// few rows keep to 64 (dsa_weights_plan). Single tokens: latency, 5 us to prepare,
+// then roles of 3000 cycles per 128 keys beside one another (32 tokens x 64 heads
+// over 98000 records 26 us, 2.0 TB/s). The steps there: block-wide staging of the
+// rows' constants and one warp per key's loads 60 and 653 us; constants a step
+// ahead, packed arithmetic 48, 528; records converted in f16 by 8 warps, addresses
+// found a lane per key, products unrolled 44, 452; items in shared memory 34;
+// constants by bulk copies and no barrier per step 33, 408; images by blocks of 32
+// rows, the pairs set up before they wait for them 26, 304 (wide). Records of the
+// next item loaded as those of this one are converted: no faster.
 #include "dsa_attend.cuh"
 #include "dsa_chunk_index.cuh"
 #include "dsa_rows.cuh"
@@ -176,8 +178,11 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
       for (int32_t j = tid; j < end; j += kWtPrep) p.out[b * p.out_st + j] = p.in ? __ldg(p.in + b * p.in_st + j) : 0.f;
     }
   }
-  // query images, a block per 128-row tile
-  for (int32_t tile = blockIdx.x - 1; tile < p.tiles; tile += gridDim.x - 1) {
+  // query images, a block per 32 rows of a 128-row tile, 4 to a warp with their
+  // loads in flight together (a block per tile, a row after the other, took 8 us
+  // longer)
+  for (int32_t unit = blockIdx.x - 1; unit < 4 * p.tiles; unit += gridDim.x - 1) {
+    const int32_t tile = unit >> 2;
     int32_t b = 0, hi = p.B - 1;   // the last sequence whose tiles begin at or before this one
     while (b < hi) {
       const int32_t mid = (b + hi + 1) >> 1;
@@ -186,25 +191,34 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
     const Sequence s = weights_sequence(p, b);
     const int32_t i = tile - image_tile(p, b, s.s0);
     if (i < 0 || i >= s.tiles(p.H)) continue;
-    const int32_t rows = s.tile_rows(p.H, i);
+    const int32_t rows = s.tile_rows(p.H, i), first = 32 * (unit & 3) + warp;
+    if (i == 0 && rows <= 64 && first >= 64) continue;   // (a sequence of one step of 64 rows)
     uint8_t *base = p.image + (int64_t)tile * (kDB * 16384);
-#pragma unroll 2
-    for (int32_t r = warp; r < 128; r += kWtPrep / 32) {
-      if (r >= rows) {   // behind the sequence's last row: zeros, up to what a step may take
-        uint8_t *pad = base + (r >> 3) * 1024 + (r & 7) * 128;
-        for (int c = lane; c < 8 * kDB; c += 32) *reinterpret_cast<uint4 *>(pad + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        if (lane < 2) p.row[(int64_t)tile * 256 + 128 * lane + r] = lane ? -INFINITY : 0.f;
-        continue;
-      }
+    uint4 qa[4], qb[4];
+    uint32_t qc[4];
+    float lse[4], sink[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t r = first + 8 * k;
+      qa[k] = qb[k] = make_uint4(0, 0, 0, 0);
+      qc[k] = 0;
+      lse[k] = sink[k] = 0.f;
+      if (r >= rows) continue;
       const uint32_t gr = (uint32_t)s.s0 * p.H + 128u * i + r, t = gr / (uint32_t)p.H, h = gr - t * (uint32_t)p.H;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_st + (int64_t)h * p.q_sh);
-      const uint4 qa = ld_row(src + 2 * lane), qb = ld_row(src + 2 * lane + 1);
-      uint32_t qc = 0;
-      if constexpr (kV32) qc = __ldg(reinterpret_cast<const uint32_t *>(src + 64) + lane);
-      const uint32_t w[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-      uint32_t mb = qc & 0x7FFF7FFFu;
+      qa[k] = ld_row(src + 2 * lane);
+      qb[k] = ld_row(src + 2 * lane + 1);
+      if constexpr (kV32) qc[k] = __ldg(reinterpret_cast<const uint32_t *>(src + 64) + lane);
+      lse[k] = __ldg(p.lse + gr);
+      if (p.sink) sink[k] = __ldg(p.sink + h);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mb = __vmaxu2(mb, w[k] & 0x7FFF7FFFu);
+    for (int k = 0; k < 4; ++k) {
+      const int32_t r = first + 8 * k;
+      const uint32_t w[8] = {qa[k].x, qa[k].y, qa[k].z, qa[k].w, qb[k].x, qb[k].y, qb[k].z, qb[k].w};
+      uint32_t mb = qc[k] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mb = __vmaxu2(mb, w[j] & 0x7FFF7FFFu);
       mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
       int e = mb ? (int)(mb >> 7) - 127 : 0;
       e = e < -126 ? -126 : (e > 126 ? 126 : e);
@@ -212,23 +226,24 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
       auto half2 = [&](uint32_t x) { return tc::pack_f16x2(bf16_bits_to_f32(x & 0xFFFFu) * down, bf16_bits_to_f32(x >> 16) * down); };
       uint32_t f[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = half2(w[k]);
+      for (int j = 0; j < 8; ++j) f[j] = half2(w[j]);
       const int x = r & 7;
       uint8_t *row = base + (r >> 3) * 1024 + x * 128;
-      const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), c = make_uint4(f[4], f[5], f[6], f[7]);
-      tc::stg_v8(row + (lane >> 2) * 16384 + (((2 * (lane & 3)) ^ (x & 6)) << 4), (x & 1) ? c : a, (x & 1) ? a : c);
+      const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), up = make_uint4(f[4], f[5], f[6], f[7]);
+      tc::stg_v8(row + (lane >> 2) * 16384 + (((2 * (lane & 3)) ^ (x & 6)) << 4), (x & 1) ? up : lo, (x & 1) ? lo : up);
       if constexpr (kV32)
-        *reinterpret_cast<uint32_t *>(row + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) = half2(qc);
+        *reinterpret_cast<uint32_t *>(row + 8 * 16384 + (((lane >> 2) ^ x) << 4) + 4 * (lane & 3)) = half2(qc[k]);
       if (lane == 0) {
-        // log2(e^lse + e^z); a row that attended nothing weighs nothing
-        const float lse = __ldg(p.lse + gr);
-        float l = lse == -INFINITY ? INFINITY : lse;
-        if (p.sink && lse != -INFINITY) {
-          const float z = __ldg(p.sink + h), m = fmaxf(lse, z), d = -fabsf(lse - z);
-          l = lse != lse || z != z ? lse + z : m == INFINITY ? INFINITY : z == -INFINITY ? lse : m + log1pf(expf(d));
+        // log2(e^lse + e^z); a row that attended nothing weighs nothing, nor do the
+        // zeros behind the sequence's last row
+        float l = lse[k] == -INFINITY ? INFINITY : lse[k];
+        if (p.sink && lse[k] != -INFINITY) {
+          const float z = sink[k], m = fmaxf(lse[k], z), d = -fabsf(lse[k] - z);
+          l = lse[k] != lse[k] || z != z ? lse[k] + z : m == INFINITY ? INFINITY : z == -INFINITY ? lse[k] : m + log1pf(expf(d));
         }
-        p.row[(int64_t)tile * 256 + r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        p.row[(int64_t)tile * 256 + 128 + r] = -l * kLog2e;
+        const bool in = r < rows;
+        p.row[(int64_t)tile * 256 + r] = in ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
+        p.row[(int64_t)tile * 256 + 128 + r] = in ? -l * kLog2e : -INFINITY;
       }
     }
   }
@@ -399,15 +414,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
     tc::fence_mbar_init();
     *abort_s = 0;
   }
-  pdl_wait_primary();
-  int4 *held = reinterpret_cast<int4 *>(smem + Cfg::kItems);
-  Items<Cfg> items(p, held, pair, pairs);
-  if (tid < 2 * kWtHeld && (tid >> 1) < items.n) held[tid] = __ldcg(p.item + 2 * ((int64_t)pair + (int64_t)(tid >> 1) * pairs) + (tid & 1));
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait_primary();
+  int4 *held = reinterpret_cast<int4 *>(smem + Cfg::kItems);
+  if (tid < 2 * kWtHeld) {   // (past the last item: not looked at)
+    const int64_t at = (int64_t)pair + (int64_t)(tid >> 1) * pairs;
+    if (at < p.max_items) held[tid] = __ldcg(p.item + 2 * at + (tid & 1));
+  }
+  Items<Cfg> items(p, held, pair, pairs);
+  __syncthreads();
   auto wait = [&](int b, uint32_t phase) -> bool {   // bounded, as in the attend kernel
     if (tc::mbar_test_wait(&bars[b], phase)) return true;
     if (*abort_s) return false;
@@ -900,7 +919,7 @@ cudaError_t launch_weigh(const WeightsParams &p, int32_t pairs, cudaStream_t st)
 template <int FMT>
 cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
   using namespace dsa;
-  const unsigned blocks = 1 + (unsigned)std::min(p.tiles, 8 * 152);
+  const unsigned blocks = 1 + (unsigned)std::min(4 * (int64_t)p.tiles, (int64_t)8 * 152);
   weights_prepare_kernel<FMT == DSA_REC_V32_656><<<blocks, kWtPrep, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
