@@ -3,9 +3,9 @@
 Argument marshalling only: torch tensors become device pointers, strides and
 sizes; every step of the decode runs in the library's CUDA kernels. The calls
 beyond the decode (cache, shared prefix, prompt) go through a small C extension
-(csrc/marshal.c) that also checks the tensors, loaded with the first of them. The functions keep the
-C names. Loading fails loudly when the library or the extension is missing
-(there is no fallback path).
+(csrc/marshal.c) that also checks the tensors, loaded with the first of them. The
+functions keep the C names. Loading fails loudly when the library or the
+extension is missing (there is no fallback path).
 """
 from __future__ import annotations
 

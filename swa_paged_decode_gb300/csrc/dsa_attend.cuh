@@ -276,17 +276,18 @@ __global__ void __launch_bounds__(256) prefix_gather_kernel(PrefixParams p) {
 //
 // What bounds it: the products' shared-memory operands and the issue of a
 // chunk every 270 cycles. 16384 rows x 16384 keys (550 GFLOP), gather and merge
-// included: 330 to 340 us for one call alone, by the box (1620 to 1670 TFLOP/s of
+// included: 326 to 335 us for one call alone, by the box (1640 to 1690 TFLOP/s of
 // 1918); 313 us without the copies, measured at 342.
-// The steps there, calls alone: N = 128 tiles
-// with a relay of the chunks' arrival 1272; arrivals released at CTA scope 914;
+// The steps there, calls alone: N = 128 tiles with a relay of the chunks' arrival
+// 1272; arrivals released at CTA scope 914;
 // N = 256, one copy a chunk, converged issue 561; three copying warps and
 // single-test waits 438; merge and gather 413; copies that complete on the
 // leader's barrier 380; Q staging, epilogue, merge and ranges 348; tails
-// prefetched 342; the rotation a pair per lane, rows out by bulk copies 335. Two pairs that share their key copies by multicast were no
-// faster (L2 gives 11 TB/s) and leave 4 of 76 pairs without a place. Few rows
-// are latency: 32 rows x 512 keys take 15 us (gather 2.3, set-up and Q 4, a
-// unit 5, epilogue 2, merge 2).
+// prefetched 342; the rotation a pair per lane, rows out by bulk copies 335;
+// queries' pieces over all banks 328. Two pairs that share their key copies by
+// multicast were no faster (L2 gives 11 TB/s) and leave 4 of 76 pairs without a
+// place. Few rows are latency: 32 rows x 512 keys take 15 us (gather 2.3, set-up
+// and Q 4, a unit 5, epilogue 2, merge 2).
 constexpr int kPfThreads = 384;
 constexpr int kPfCopyWarps = 3;
 constexpr long long kPfWait = 4000000000ll;   // SM cycles (~2 s) per wait
@@ -447,13 +448,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     tc::fence_mbar_init();
     *abort_s = 0;
   }
-  if constexpr (kChunk) pdl_wait_primary();   // (the pairs' ranges)
-  Walk<kChunk> walk(p, pair);
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kChunk) pdl_wait_primary();   // (the pairs' ranges)
+  Walk<kChunk> walk(p, pair);
 
   // Bounded wait on a phase, after any timeout of the CTA a mere test; false:
   // given up. What is there already passes in one test: at a chunk every 270
@@ -672,10 +673,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     bool leaving = false;   // rows of the tile before are on their way out of the Q tile
     // Q rows of this CTA -> f16 K-major tile: RoPE in fp32, times a power of
     // two per row so that its largest unrotated magnitude lies in [1, 2) (a
-    // rotation adds half a bit at most). A warp takes 8 rows, 2 at a time
-    // with the next 2 in flight; the loop stays rolled and a row's address is
+    // rotation adds half a bit at most). A warp takes 8 rows, 2 or 4 at a time
+    // with the next ones in flight; the loop stays rolled and a row's address is
     // found once, by a lane of its own: this code runs once per 128 rows, so
-    // its size is its time (8 rows unrolled took 9700 cycles, 700 a row).
+    // its size is its time (8 rows unrolled took 9700 cycles, 700 a row). A lane
+    // takes the 16-byte pieces l and 32 + l: 8 lanes fill the 128 bytes of a row of
+    // the image, all banks (with pieces 2 l and 2 l + 1 half of them twice: 5400
+    // cycles a tile against 4500).
     auto stage_q = [&]() {
       const bool rope = p.cos_sin != nullptr;
       // The rotation takes a pair per lane, through the P tile, which no product
@@ -693,8 +697,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(qp), i0 + i));
           na[i] = nb[i] = nc[i] = make_uint4(0, 0, 0, 0);
           if (r) {
-            na[i] = __ldg(r + 2 * lane);
-            nb[i] = __ldg(r + 2 * lane + 1);
+            na[i] = __ldg(r + lane);
+            nb[i] = __ldg(r + 32 + lane);
             if constexpr (kV32)
               if (lane < 8) nc[i] = __ldg(r + 64 + lane);   // dims 512 + 8 lane ..
           }
@@ -753,17 +757,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * down;
           }
           const uint32_t ro = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
-          if (rope && lane >= 28) {
-            float4 *d = reinterpret_cast<float4 *>(turn_s + 64 * i + 16 * (lane - 28));
+          const uint32_t at = (uint32_t)(lane >> 3) * 8192u + ro + (((lane & 7) ^ (r & 7)) << 4);
+          uint32_t f[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
+          st_q(at, f[0], f[1], f[2], f[3]);
+          if (rope && lane >= 24) {
+            float4 *d = reinterpret_cast<float4 *>(turn_s + 64 * i + 8 * (lane - 24));
+            d[0] = make_float4(v[8], v[9], v[10], v[11]);
+            d[1] = make_float4(v[12], v[13], v[14], v[15]);
           } else {
-            uint32_t f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = tc::pack_f16x2(v[2 * k], v[2 * k + 1]);
-            const uint32_t at = (uint32_t)(lane >> 2) * 8192u + ro, c = 2 * (lane & 3);
-            st_q(at + ((c ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
-            st_q(at + (((c + 1) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+            st_q(at + 4 * 8192u, f[4], f[5], f[6], f[7]);
           }
           if constexpr (kV32) {
             if (lane < 8) {
