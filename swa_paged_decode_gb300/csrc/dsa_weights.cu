@@ -967,9 +967,10 @@ dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_he
   // How to cut the work, by what it takes about: a pair's items one after the
   // other, an item a set-up (its records) and its steps of 256 rows, of the mean
   // sequence. In microseconds: 3.5 and 1.6 for 128 keys, 8 and 2.2 for 256
-  // (wide), 3 to add parts up. Measured (ue8m0, 8 lists of 8192): 1024 rows 76.9
-  // narrow, 74.2 wide, 88.1 with two parts; 4096 rows 211, 180, 221; a list of
-  // 32768 and 4096 rows 126, 107 wide in two parts.
+  // (wide), 3 to add parts up. Measured (ue8m0, 8 lists of 8192): 1024 rows 63.8
+  // narrow, 61.6 wide, 71.3 wide in two parts; 4096 rows 203, 171, 169; a list of
+  // 32768 and 4096 rows 115, 85.5, 95.9; 4 lists of 6000 and 2048 rows 51.7, 51.9,
+  // 50.1.
   const int64_t steps = num_seqs > 0 ? std::max<int64_t>(1, (rows / num_seqs + 255) / 256) : 1;
   const int64_t pairs = most_pairs < 1 ? 1 : most_pairs, units = halves * num_seqs;
   auto cut = [&](int64_t items, double setup, double step, int32_t &splits) {
