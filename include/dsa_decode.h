@@ -706,7 +706,8 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
  *     with freed_counts): the other entries' slots in their order, freed_counts[b]
  *     of them, stride >= width - min(budget, width). What lies behind is left
  *     as it was.
- * budget >= 1, keep_first, keep_last >= 0. Outputs must not overlap the inputs.
+ * budget >= 1, keep_first, keep_last >= 0. Outputs must not overlap the inputs
+ * (the lengths neither) or one another.
  * Records are not moved: the caller gives the freed slots back to its allocator.
  * Asynchronous, one launch, no workspace; the result does not depend on
  * timing. */

@@ -263,7 +263,9 @@ extern "C" dsa_status dsa_evict(int32_t num_seqs, int32_t width, const int32_t *
   if (slots_stride < width || scores_stride < width || kept_slots_stride < most || kept_scores_stride < most ||
       (freed && freed_stride < width - most))
     return DSA_ERR_INVALID_ARG;
-  if (kept_slots == slots || kept_scores == scores || (freed && freed == slots)) return DSA_ERR_INVALID_ARG;
+  if (kept_slots == slots || kept_scores == scores || kept_lengths == lengths || freed_counts == lengths ||
+      freed_counts == kept_lengths || (freed && (freed == slots || freed == kept_slots)))
+    return DSA_ERR_INVALID_ARG;
   if (!aligned(slots, 4) || !aligned(lengths, 4) || !aligned(scores, 4) || !aligned(kept_slots, 4) ||
       !aligned(kept_scores, 4) || !aligned(kept_lengths, 4) || (freed && (!aligned(freed, 4) || !aligned(freed_counts, 4))))
     return DSA_ERR_ALIGNMENT;

@@ -89,6 +89,12 @@ def test_evict_refusals(lib, kw, expect):
     assert evict(lib, **kw) == expect
 
 
+@pytest.mark.parametrize("kw", [dict(klen=0x20000), dict(counts=0x20000), dict(counts=0x60000), dict(freed=0x40000)])
+def test_evict_refuses_outputs_in_place_of_lengths_or_one_another(lib, kw):
+    """Every CTA of a list reads its length while the first one writes the new one."""
+    assert evict(lib, **kw) == INVALID
+
+
 def test_evict_of_no_lists(lib):
     assert evict(lib, n=0, slots=None) == 0
 
