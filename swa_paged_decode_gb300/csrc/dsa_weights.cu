@@ -340,7 +340,7 @@ struct WtCfg {
   static_assert(kTmem + 4 <= 512, "misc area");
   static_assert(kBytes + 1024 <= 232448u, "shared memory layout exceeds 227 KiB");
   // rows of the step that starts with `left` rows to go, and 64-dim blocks to a slot
-  static __device__ __forceinline__ int rows(int64_t left) { return left > 128 && kN == 256 ? 256 : left > 64 ? 128 : 64; }
+  static __device__ __forceinline__ int rows(int32_t left) { return left > 128 && kN == 256 ? 256 : left > 64 ? 128 : 64; }
   static __device__ __forceinline__ int per_slot(int N) { return 256 / N; }
 };
 
@@ -355,7 +355,7 @@ struct Items {
   int32_t i, n, pair, pairs;   // the next one, of how many of this pair
   int4 a, c;
   int32_t tile, end;     // next row tile of the item, and the row tile past its last
-  int64_t rows;          // rows of the sequence
+  int32_t past;          // the row past its last (rows are counted in 31 bits less 128)
   __device__ __forceinline__ Items(const WeightsParams &q, const int4 *h, int pr, int prs) : p(q), held(h), i(0), pair(pr), pairs(prs) {
     const int32_t all = __ldcg(p.n_items);
     n = all > pair ? (all - pair + pairs - 1) / pairs : 0;
@@ -370,11 +370,11 @@ struct Items {
     ++i;
     tile = c.y;
     end = c.z;
-    rows = (int64_t)a.w * p.H;
+    past = min(a.w * p.H, end * 128);
     return true;
   }
   __device__ __forceinline__ bool empty() const { return c.y >= c.z; }
-  __device__ __forceinline__ int64_t left() const { return min(rows, (int64_t)end * 128) - (int64_t)tile * 128; }
+  __device__ __forceinline__ int32_t left() const { return past - tile * 128; }
   __device__ __forceinline__ bool next_step(int &N) {   // tile is the step's until advance
     if (tile >= end) return false;
     N = Cfg::rows(left());
@@ -711,10 +711,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWtThreads, 1)
       if (writes && p.splits == 1 && p.in) before = p.in[(int64_t)items.a.x * p.in_st + at];
       const bool all = items.c.w < 0;                            // every row sees every key
       // the query rows that see the key: see0 .. see0 + seen - 1
-      const int64_t place = at - (items.a.z - items.a.w);        // of the tokens, the key's own
-      const uint32_t see0 = (uint32_t)max((int64_t)0, place) * (uint32_t)p.H;
-      const int64_t past = p.window > 0 ? min((int64_t)items.a.w, place + p.window) : items.a.w;
-      const uint32_t seen = past > 0 && (uint32_t)past * (uint32_t)p.H > see0 ? (uint32_t)past * (uint32_t)p.H - see0 : 0u;
+      uint32_t see0 = 0, seen = 0xFFFFFFFFu;
+      if (!all) {
+        const int32_t place = at - (items.a.z - items.a.w);      // of the tokens, the key's own
+        const int32_t past = p.window > 0 && p.window < items.a.z - at ? max(place + p.window, 0) : items.a.w;
+        see0 = (uint32_t)max(0, place) * (uint32_t)p.H;
+        seen = (uint32_t)max(past - max(0, place), 0) * (uint32_t)p.H;
+      }
       bool kept = false;
       if (!items.empty()) {
         const int buf = turn % Cfg::kBufs;
