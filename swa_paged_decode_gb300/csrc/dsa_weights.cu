@@ -39,8 +39,8 @@
 // (M = 128) a step's 256 KiB feed 2048 cycles of products, more than L2's 12 TB/s:
 // leaving out half of the products or all exponentials changed nothing (64 tokens
 // x 128 heads over 65536 MODEL1 records 408 us). With 128 keys in each (WIDE, M =
-// 256, one key tile in place of two) the same bytes feed twice the work: 304 us,
-// 1810 TFLOP/s, 0.94 of the measured peak; an item's set-up then stands alone, so
+// 256, one key tile in place of two) the same bytes feed twice the work: 296 us,
+// 1855 TFLOP/s, 0.97 of the measured peak; an item's set-up then stands alone, so
 // few rows keep to 64 (dsa_weights_plan). Single tokens: latency, 5 us to prepare,
 // then roles of 3000 cycles per 128 keys beside one another (32 tokens x 64 heads
 // over 98000 records 26 us, 2.0 TB/s). The steps there: block-wide staging of the
@@ -48,8 +48,9 @@
 // ahead, packed arithmetic 48, 528; records converted in f16 by 8 warps, addresses
 // found a lane per key, products unrolled 44, 452; items in shared memory 34;
 // constants by bulk copies and no barrier per step 33, 408; images by blocks of 32
-// rows, the pairs set up before they wait for them 26, 304 (wide). Records of the
-// next item loaded as those of this one are converted: no faster.
+// rows, the pairs set up before they wait for them 26, 304 (wide); items counted in
+// 32 bits 26, 296. Records of the next item loaded as those of this one are
+// converted: no faster.
 #include "dsa_attend.cuh"
 #include "dsa_chunk_index.cuh"
 #include "dsa_rows.cuh"
