@@ -205,6 +205,16 @@ def test_no_tokens_in_any_sequence():
     check(c, *run(c)[:2])
 
 
+@pytest.mark.parametrize("window", [0, 50])
+def test_what_the_workspace_held_does_not_count(window):
+    """Images of keys that no record fills are zeros wherever a product takes them."""
+    c = Batch([(3, 300), (1, 17), (20, 450), (1, 1)], 20, W.FMT_FP8_528, seed=2, invalid=0.1, window=window)
+    attn = attention(c)
+    for byte in (0xFF, 0x7C):   # NaN, and large numbers and infinities
+        attn.workspace.fill_(byte)
+        check(c, *run(c, attn=attn)[:2])
+
+
 def test_long_list_of_few_tokens():
     c = Batch([(2, 70000)], 16, W.FMT_NVFP4_288, seed=13, num_slots=4096)
     check(c, *run(c)[:2])

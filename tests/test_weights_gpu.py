@@ -202,6 +202,17 @@ def test_negative_scale_and_no_tokens():
     assert torch.equal(out[0, :30], c.before[0, :30]) and torch.equal(out[2, :200], c.before[2, :200])
 
 
+@pytest.mark.parametrize("H", [1, 20, 64, 65, 100])
+@pytest.mark.parametrize("fmt", [W.FMT_FP8_528, W.FMT_NVFP4_288, W.FMT_V32_656])
+def test_what_the_workspace_held_does_not_count(H, fmt):
+    """Image rows behind a sequence's last one: zeros, or never taken."""
+    c = Case([(1, 300), (2, 200), (3, 130), (1, 1), (4, 500)], H, fmt, seed=H, sink=True)
+    attn = B.AttentionWeights(c.c.T, c.c.B, H, c.c.width, "cuda", c.c.d)
+    for byte in (0xFF, 0x7C):   # NaN, and large numbers and infinities
+        attn.workspace.fill_(byte)
+        c.check(c.run(attn=attn)[0])
+
+
 def test_sums_of_all_weights():
     """Every query row's weights add up to one."""
     c = Case([(30, 500), (1, 300)], 64, W.FMT_FP8_528_UE8M0, seed=30, base=False)
