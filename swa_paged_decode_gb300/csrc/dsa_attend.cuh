@@ -12,8 +12,8 @@
 #include <cstring>
 #include <type_traits>
 
+#include "dsa_chunk_index.cuh"
 #include "dsa_host.cuh"
-#include "dsa_prefix_index.cuh"
 #include "dsa_records.cuh"
 
 namespace dsa {
@@ -319,17 +319,6 @@ struct PfCfg {
   static_assert(kBytes <= 232448u, "shared memory layout exceeds 227 KiB");
 };
 
-// A run of units of one row tile that a pair works on.
-struct TileRun {
-  int32_t qt;         // row tile
-  int64_t g0;         // its first row
-  int32_t n;          // its rows, 1..128
-  int64_t half;       // image half at which the first unit starts
-  int32_t units;
-  bool head, tail;    // begins, ends with the tile
-  int32_t key0;       // chunk: list position of the first unit's first key,
-  int32_t shift;      // and of a row g's token less g / H
-};
 // The segments of a pair's range, in order.
 template <bool kChunk>
 struct Walk;
@@ -365,55 +354,19 @@ struct Walk<false> {
     return u < u1 ? (int32_t)min((int64_t)128, rows - g0) : 0;
   }
 };
-template <>
-struct Walk<true> {
+struct LoadRowTile {
   const int4 *tiles;
-  int32_t t, w, t1, w1;
-  int4 a, b;                      // row tile t, loaded ahead
-  __device__ __forceinline__ void load() {
-    if (t < t1 || (t == t1 && w1 > 0)) {
-      a = __ldcg(tiles + 2 * (int64_t)t);
-      b = __ldcg(tiles + 2 * (int64_t)t + 1);
-    }
+  __device__ __forceinline__ void operator()(int32_t t, RowTile &r) const {
+    const int4 a = __ldcg(tiles + 2 * (int64_t)t), b = __ldcg(tiles + 2 * (int64_t)t + 1);
+    r = {a.x, a.y, a.z, b.x, b.y, b.z};
   }
-  __device__ __forceinline__ Walk(const ChunkParams &p, int pair) : tiles(p.row_tile) {
-    const int2 x = __ldcg(p.begin + pair), y = __ldcg(p.begin + pair + 1);
-    t = x.x;
-    w = x.y;
-    t1 = y.x;
-    w1 = y.y;
-    load();
-  }
-  __device__ __forceinline__ bool empty() const { return t > t1 || (t == t1 && w >= w1); }
-  __device__ __forceinline__ bool next(TileRun &s) {
-    while (!empty()) {
-      const int32_t end = t == t1 ? w1 : a.z;
-      if (w >= end) {             // (a tile without keys)
-        ++t;
-        w = 0;
-        load();
-        continue;
-      }
-      s.qt = t;
-      s.g0 = a.x;
-      s.n = a.y;
-      s.half = b.x + 2 * w;
-      s.key0 = b.y + kPfTile * w;
-      s.shift = b.z;
-      s.units = end - w;
-      s.head = w == 0;
-      s.tail = end == a.z;
-      ++t;
-      w = 0;
-      load();
-      return true;
-    }
-    return false;
-  }
-  __device__ __forceinline__ int32_t peek(const TileRun &, int64_t &g0) const {
-    g0 = a.x;
-    return empty() ? 0 : a.y;
-  }
+};
+template <>
+struct Walk<true> : TileWalk<LoadRowTile> {
+  __device__ __forceinline__ Walk(const ChunkParams &p, int pair)
+      : Walk(p, __ldcg(p.begin + pair), __ldcg(p.begin + pair + 1)) {}
+  __device__ __forceinline__ Walk(const ChunkParams &p, int2 from, int2 to)
+      : TileWalk<LoadRowTile>({p.row_tile}, from.x, from.y, to.x, to.y) {}
 };
 
 template <bool kV32, bool kChunk>

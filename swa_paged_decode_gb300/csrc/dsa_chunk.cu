@@ -27,7 +27,6 @@
 // us; 361 with the output through fp32 in shared memory, the rotation in four
 // lanes and a merge over all rows). Few tokens: three dependent kernels (22.6 us).
 #include "dsa_attend.cuh"
-#include "dsa_chunk_index.cuh"
 
 namespace dsa {
 
@@ -131,18 +130,13 @@ __device__ void lay_out(const ChunkParams &p, bool ok) {
       p.merge[atomicAdd(p.n_merge, 1)] = t;
       return;
     }
-    const int64_t cost = u + tile_cost, next = at + cost;
     bool shared = false;   // (the list's order does not matter)
-    // pairs c with at <= total c / C < next
-    for (int64_t c = (at * p.C + total - 1) / total; c < p.C; ++c) {
-      const int64_t x = total * c / p.C;
-      if (x >= next) break;
-      const int32_t w = (int32_t)max(x - at - tile_cost, (int64_t)0);
+    pairs_in_tile(at, u, tile_cost, total, p.C, [&](int32_t c, int32_t w) {
       p.begin[c] = make_int2(t, w);
       shared |= w > 0;
-    }
+    });
     if (shared) p.merge[atomicAdd(p.n_merge, 1)] = t;
-    at = next;
+    at += u + tile_cost;
   });
   if (total == 0)
     for (int32_t c = tid; c < p.C; c += kChThreads) p.begin[c] = make_int2(R, 0);

@@ -42,6 +42,67 @@ struct Sequence {
   }
 };
 
+// What the lay-out leaves of a row tile; without units none of its rows has a key.
+struct RowTile {
+  int32_t g0, rows, units;     // first row, rows
+  int32_t half, key0, shift;   // as in TileRun, of the tile's first unit
+};
+
+// The pairs whose ranges begin in a tile of `units` > 0 units: of C equal shares
+// of `total` those that begin within the tile's cost, units + tile_cost from `at`
+// on. f(pair, unit) for each of them, in order.
+template <class F>
+DSA_KERNEL void pairs_in_tile(int64_t at, int32_t units, int64_t tile_cost, int64_t total, int32_t C, F f) {
+  const int64_t next = at + units + tile_cost;
+  for (int64_t c = (at * C + total - 1) / total; c < C; ++c) {   // the first with at <= total c / C
+    const int64_t x = total * c / C, unit = x - at - tile_cost;
+    if (x >= next) break;
+    f((int32_t)c, unit > 0 ? (int32_t)unit : 0);
+  }
+}
+
+// A pair's range, from unit w of row tile t to before unit w1 of tile t1, tile
+// by tile; load(t, tile) reads a row tile. It stands on a tile with units or at
+// its end, never on a tile without: peek names the tile that next returns.
+template <class Load>
+struct TileWalk {
+  Load load;
+  int32_t t, w, t1, w1;
+  RowTile tile;   // row tile t, loaded ahead
+  DSA_KERNEL TileWalk(Load l, int32_t t_, int32_t w_, int32_t t1_, int32_t w1_) : load(l), t(t_), w(w_), t1(t1_), w1(w1_), tile() {
+    settle();
+  }
+  DSA_KERNEL bool empty() const { return t > t1 || (t == t1 && w >= w1); }
+  DSA_KERNEL int32_t end() const { return t == t1 ? w1 : tile.units; }
+  DSA_KERNEL void settle() {
+    for (; !empty(); ++t, w = 0) {
+      load(t, tile);
+      if (w < end()) return;
+    }
+  }
+  DSA_KERNEL bool next(TileRun &s) {
+    if (empty()) return false;
+    s.qt = t;
+    s.g0 = tile.g0;
+    s.n = tile.rows;
+    s.half = tile.half + 2 * (int64_t)w;
+    s.key0 = tile.key0 + 256 * w;
+    s.shift = tile.shift;
+    s.units = end() - w;
+    s.head = w == 0;
+    s.tail = end() == tile.units;
+    ++t;
+    w = 0;
+    settle();
+    return true;
+  }
+  // rows of the next segment's tile (0: none)
+  DSA_KERNEL int32_t peek(const TileRun &, int64_t &g0) const {
+    g0 = tile.g0;
+    return empty() ? 0 : tile.rows;
+  }
+};
+
 // Row tiles and image halves that a call can need at most.
 DSA_HD int64_t chunk_row_tiles(int64_t T, int64_t H, int64_t B) { return T * H / 128 + (B < T ? B : T); }
 DSA_HD int64_t chunk_seq_halves(int64_t width) { return (width + 127) / 128 + 1; }

@@ -7,8 +7,10 @@
 
 #ifdef __CUDACC__
 #define DSA_HD __host__ __device__ __forceinline__
+#define DSA_KERNEL __device__ __forceinline__   // (calls back into code of the device only)
 #else
 #define DSA_HD inline
+#define DSA_KERNEL inline
 #endif
 
 namespace dsa {
@@ -40,6 +42,17 @@ DSA_HD Schedule make_schedule(int32_t R, int32_t KT, int32_t C) {
   return {R, KT, C, (int64_t)R * KT >= 2 * (int64_t)C ? 2 : 0};
 }
 
+// A run of units of one row tile that a pair works on.
+struct TileRun {
+  int32_t qt;         // row tile
+  int64_t g0;         // its first row
+  int32_t n;          // its rows, 1..128
+  int64_t half;       // image half at which the first unit starts
+  int32_t units;
+  bool head, tail;    // begins, ends with the tile
+  int32_t key0;       // chunk: list position of the first unit's first key,
+  int32_t shift;      // and of a row g's token less g / H
+};
 // The parts of a query row: the pairs c0..c1 whose ranges meet its row tile
 // (none: c1 < c0, an empty prefix). The partial of pair c lies in the pair's
 // first 128 rows when the tile is its first, else in its second 128 (`late`:

@@ -52,7 +52,6 @@
 // 32 bits 26, 296. Records of the next item loaded as those of this one are
 // converted: no faster.
 #include "dsa_attend.cuh"
-#include "dsa_chunk_index.cuh"
 #include "dsa_rows.cuh"
 
 namespace dsa {
