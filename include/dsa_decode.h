@@ -675,7 +675,10 @@ dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_he
  *     rows of out_stride >= width; the same array or one that does not overlap
  *     it. Entries below the list's length are written (those that no token
  *     attends, and unused slots, with scores_in), the ones behind are not, and
- *     lists of sequences without tokens are written too.
+ *     lists of sequences without tokens are written too. A plan of no tokens at
+ *     all asks for no workspace: a call that brings one of 256 bytes (for the
+ *     status) writes them like any other, one that does not returns DSA_OK and
+ *     writes nothing.
  *   starts that do not ascend within [0, T]: nothing is written, the status
  *     word is DSA_ERR_INVALID_ARG.
  * Single tokens behind dsa_decode_run: starts 0, 1, 2, ...; their own lists and

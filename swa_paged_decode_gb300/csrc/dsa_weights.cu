@@ -922,10 +922,10 @@ cudaError_t launch_weigh(const WeightsParams &p, int32_t pairs, cudaStream_t st)
 template <int FMT>
 cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
   using namespace dsa;
-  const unsigned blocks = 1 + (unsigned)std::min(4 * (int64_t)p.tiles, (int64_t)8 * 152);
+  const unsigned blocks = 1 + (unsigned)std::min(std::max(4 * (int64_t)p.tiles, (int64_t)p.B), (int64_t)8 * 152);
   weights_prepare_kernel<FMT == DSA_REC_V32_656><<<blocks, kWtPrep, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.T == 0) return e;   // (no tokens: the scores are copied, nothing is weighed)
   constexpr bool kCanWiden = !WtCfg<FMT, false>::kBlocks;
   e = p.span == 256 ? launch_weigh<FMT, kCanWiden>(p, pairs, st) : launch_weigh<FMT, false>(p, pairs, st);
   if (e != cudaSuccess || p.splits == 1) return e;
@@ -1020,15 +1020,18 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
                            int64_t in_stride, float *scores_out, int64_t out_stride, dsa_stream_t stream) {
   dsa::NvtxRange range("dsa_weights_run");
   if (!plan || plan->magic != dsa::kWeightsMagic || plan->abi_version != DSA_DECODE_ABI_VERSION) return DSA_ERR_PLAN;
-  if (plan->num_tokens == 0 || plan->num_seqs == 0) return DSA_OK;
-  if (!q || !slots || !lengths || !starts || !lse || !scores_out) return DSA_ERR_INVALID_ARG;
+  // A step without tokens still copies the scores; a plan of one asks for no
+  // workspace, without which there is no status word to report to.
+  const bool tokens = plan->num_tokens > 0;
+  if (plan->num_seqs == 0 || (!tokens && (!workspace || workspace_bytes < 256))) return DSA_OK;
+  if (!slots || !lengths || !starts || !scores_out || (tokens && (!q || !lse))) return DSA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || window < 0 || slots_stride < plan->width || out_stride < plan->width ||
       (scores_in && in_stride < plan->width) || (scores_in == scores_out && in_stride != out_stride))
     return DSA_ERR_INVALID_ARG;
-  if (q_stride_h < plan->d_qk || q_stride_t < (int64_t)(plan->num_heads - 1) * q_stride_h + plan->d_qk)
+  if (tokens && (q_stride_h < plan->d_qk || q_stride_t < (int64_t)(plan->num_heads - 1) * q_stride_h + plan->d_qk))
     return DSA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || q_stride_t % 8 != 0 || q_stride_h % 8 != 0 || !aligned(slots, 4) || !aligned(lengths, 4) ||
-      !aligned(starts, 4) || !aligned(lse, 4) || (sink && !aligned(sink, 4)) || (scores_in && !aligned(scores_in, 4)) ||
+  if ((tokens && (!aligned(q, 16) || q_stride_t % 8 != 0 || q_stride_h % 8 != 0 || !aligned(lse, 4))) ||
+      !aligned(slots, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || (sink && !aligned(sink, 4)) || (scores_in && !aligned(scores_in, 4)) ||
       !aligned(scores_out, 4))
     return DSA_ERR_ALIGNMENT;
   if (!workspace || (int64_t)workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256))
@@ -1047,7 +1050,7 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
   p.B = plan->num_seqs;
   p.H = plan->num_heads;
   p.window = window;
-  p.tiles = plan->tiles;
+  p.tiles = tokens ? plan->tiles : 0;
   // (records with fp32 scales take products half as fast: the queries' way from L2 keeps up)
   const bool wide = plan->wide_splits > 0 && cache->format != DSA_REC_FP8_528 && cache->format != DSA_REC_V32_656;
   p.span = wide ? 256 : 128;
