@@ -587,7 +587,9 @@ dsa_status dsa_chunk_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_head
  *     lse may be tail_lse. Tokens before starts[0] and from starts[B] on are
  *     left as they were. A row that attends nothing (and has no tail) gives
  *     zeros and -inf.
- *   workspace, status, precision: as for dsa_prefix_run. Lists may share slots.
+ *   workspace, status, precision: as for dsa_prefix_run. A key with a NaN, an
+ *     infinity or an element of 2^49 or more has NaN for its scores: it spoils
+ *     the rows that attend it and no others. Lists may share slots.
  * Three launches on `stream`; allocates nothing, never synchronizes. */
 dsa_status dsa_chunk_run(const dsa_chunk_plan_t *plan, void *workspace, size_t workspace_bytes,
                          const void *q, int64_t q_stride_t, int64_t q_stride_h,

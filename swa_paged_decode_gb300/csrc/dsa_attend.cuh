@@ -34,9 +34,10 @@ constexpr int kPfRange = 48;                   // exponents of the keys' magnitu
 constexpr int32_t kPfNoKey = INT32_MAX;        // exponent of a key that is not kept
 constexpr int32_t kPfZeroKey = -kPfRange - 1;  // of a key of zeros: any other key's will do
 constexpr int32_t kPfMixed = INT32_MIN;        // group exponent: one per key instead
-// Chunk: exponent of a key with an infinity, a NaN or a magnitude past the range.
-// Its image holds zeros and its scores are NaN, so that rows that may not see it
-// do not meet it as 0 * NaN. A multiple of 2^9: as an exponent field it reads 2^0.
+// Chunk: exponent of a key with an infinity, a NaN or an element of 2^49 or more
+// (with the range's largest exponent f16 ends at 2^50). Its image holds zeros and
+// its scores are NaN, so that rows that may not see it do not meet it as 0 * NaN. A
+// multiple of 2^9: as an exponent field it reads 2^0.
 constexpr int32_t kPfNanKey = 1 << 20;
 
 struct PrefixParams {
@@ -186,8 +187,18 @@ __device__ __forceinline__ void gather_group(const PrefixParams &p, int32_t slot
   for (int i = 0; i < 4; ++i) {
     const int e = __reduce_max_sync(0xffffffffu, ok[i] ? record_exponent<FMT>(raw[i], lane) : 0);
     int share = !ok[i] ? kPfNoKey : e == kZeroShare ? kPfZeroKey : min(max(e, -kPfRange), kPfRange);
-    if constexpr (kChunk)
-      if (__any_sync(0xffffffffu, ok[i] && (e > kPfRange || share_not_finite<FMT>(raw[i], lane)))) share = kPfNanKey;
+    if constexpr (kChunk) {
+      bool bad = ok[i] && share_not_finite<FMT>(raw[i], lane);
+      if (ok[i] && e > kPfRange) {   // by its scale; its codes may be small (the warp agrees)
+        float v[16], t0 = 0.f, t1 = 0.f;
+        expand_record<FMT>(raw[i], lane, v, t0, t1);
+        float most = fmaxf(fabsf(t0), fabsf(t1));
+#pragma unroll
+        for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(v[k]));
+        bad |= most >= 562949953421312.f;   // 2^49
+      }
+      if (__any_sync(0xffffffffu, bad)) share = kPfNanKey;
+    }
     if (lane == 0) e_s[4 * warp + i] = share;
   }
   __syncthreads();
