@@ -687,8 +687,9 @@ dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_he
  * lse. Precision: sums of fp32 weights, each good to a few 2^-22 relative
  * (16-bit operands of the products are exact for queries whose elements lie
  * within 2^-14 of their row's largest and for keys as dsa_decode.h's record
- * formats say; fp32 block scales are applied in fp32). A record with a NaN or
- * an infinity spoils its own score only. Reproducible bit for bit.
+ * formats say, with magnitudes of 2^-48 .. 2^48; fp32 block scales are applied in
+ * fp32). A record with a NaN or an infinity spoils its own score only, and one
+ * with an element of 2^50 or more may count as one. Reproducible bit for bit.
  * Two launches, three when few keys meet many rows; allocates nothing, never
  * synchronizes. workspace and status as for dsa_prefix_run. */
 dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size_t workspace_bytes,

@@ -256,7 +256,8 @@ constexpr int kWtCopies = 3, kWtRecords = 8;
 // A lane's 16 values of a record with one factor 2^E per key, in f16 and exact as
 // far as the header says: codes times a power of two (or an e4m3 scale), so the
 // products are taken in f16 (a third of the instructions of the way through
-// fp32, which blocks far below the row's largest and bf16 parts take). -> E
+// fp32, which bf16 parts take, and blocks whose scale is no f16 in units of 2^E:
+// far below the row's largest, or with small codes above the range of E). -> E
 template <int FMT>
 __device__ __forceinline__ int key_halves(const RawRecord &r, int lane, uint32_t (&f)[8]) {
   const int share = record_exponent<FMT>(r, lane);
@@ -275,7 +276,7 @@ __device__ __forceinline__ int key_halves(const RawRecord &r, int lane, uint32_t
   } else {
     const bool bf16_part = FMT == DSA_REC_MODEL1_584 && lane >= 28;
     const int k = (int)(r.s & 0xFFu) - 127 - E;   // the block's power of two, in units of 2^E
-    const bool far = !bf16_part && share != kZeroShare && k < -24;
+    const bool far = !bf16_part && share != kZeroShare && (k < -24 || k > 15);
     if (__any_sync(0xffffffffu, far)) {
       float v[16], t0, t1;
       expand_record<FMT>(r, lane, v, t0, t1);
@@ -287,7 +288,7 @@ __device__ __forceinline__ int key_halves(const RawRecord &r, int lane, uint32_t
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = tc::pack_f16x2(bf16_bits_to_f32(r.w[i] & 0xFFFFu) * down, __uint_as_float(r.w[i] & 0xFFFF0000u) * down);
     } else {
-      uint32_t m = (r.s & 0xFFu) == 0xFFu ? 0x7E00u : share == kZeroShare ? 0u : k >= -14 ? (uint32_t)(min(k, 15) + 15) << 10 : 1u << (k + 24);
+      uint32_t m = (r.s & 0xFFu) == 0xFFu ? 0x7E00u : share == kZeroShare ? 0u : k >= -14 ? (uint32_t)(k + 15) << 10 : 1u << (k + 24);
       m |= m << 16;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

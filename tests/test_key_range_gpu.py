@@ -1,6 +1,7 @@
 """Finite keys of any scale: records whose scales are large and whose codes are
 small stay within the range that the calls state (largest magnitude up to 2^48),
-against the formulas in 64 bits and the tolerances of test_chunk_gpu."""
+against the formulas in 64 bits and the tolerances of test_chunk_gpu and
+test_weights_gpu."""
 import pytest
 import torch
 
@@ -8,6 +9,7 @@ from swa_paged_decode_gb300 import binding as B
 from swa_paged_decode_gb300 import build as BLD
 from swa_paged_decode_gb300 import workloads as W
 from tests import test_chunk_gpu as CH
+from tests import test_weights_gpu as WT
 from tests._serve_ref import Batch
 
 pytestmark = pytest.mark.gpu
@@ -56,6 +58,18 @@ def batch(fmt, k, every=1):
 def test_chunk(fmt, k):
     c = batch(fmt, k)
     CH.check(c, *CH.run(c)[:2])
+
+
+@pytest.mark.parametrize("fmt", SCALED)
+@pytest.mark.parametrize("k", [30, 41, 54])
+def test_weights(fmt, k):
+    case = WT.Case.__new__(WT.Case)
+    case.c = c = batch(fmt, k)
+    case.lse = torch.full((c.T, c.H), -float("inf"), dtype=torch.float64, device="cuda")
+    for b, t, at, key, x, mass in c.scores():
+        case.lse[t:t + x.shape[0]] = torch.logsumexp(x, 2)
+    case.lse, case.before = case.lse.float(), None
+    case.check(case.run()[0])
 
 
 @pytest.mark.parametrize("fmt", SCALED)
