@@ -170,12 +170,17 @@ __global__ void __launch_bounds__(kWtPrep) weights_prepare_kernel(const __grid_c
     if (tid == 0) *p.n_items = min(n, p.max_items);
     return;
   }
-  // entries that no token sees keep what they had
+  // entries that no token sees keep what they had: a list's share of the blocks
+  // takes 256 of them in turn
   if (p.in != p.out) {
-    for (int32_t b = blockIdx.x - 1; b < p.B; b += gridDim.x - 1) {
+    const int32_t blocks = gridDim.x - 1, share = max(1, blocks / p.B);
+    for (int32_t u = blockIdx.x - 1; u < p.B * share; u += blocks) {
+      const int32_t b = u / share;
       const Sequence s = weights_sequence(p, b);
       const int32_t end = s.any() ? min(s.gather_begin() * 128, s.len) : s.len;
-      for (int32_t j = tid; j < end; j += kWtPrep) p.out[b * p.out_st + j] = p.in ? __ldg(p.in + b * p.in_st + j) : 0.f;
+#pragma unroll 4
+      for (int32_t j = (u - b * share) * kWtPrep + tid; j < end; j += share * kWtPrep)
+        p.out[b * p.out_st + j] = p.in ? __ldg(p.in + b * p.in_st + j) : 0.f;
     }
   }
   // query images, a block per 32 rows of a 128-row tile, 4 to a warp with their
@@ -921,9 +926,11 @@ cudaError_t launch_weigh(const WeightsParams &p, int32_t pairs, cudaStream_t st)
 }
 
 template <int FMT>
-cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, cudaStream_t st) {
+cudaError_t launch_weights(const WeightsParams &p, int32_t pairs, int32_t num_sms, cudaStream_t st) {
   using namespace dsa;
-  const unsigned blocks = 1 + (unsigned)std::min(std::max(4 * (int64_t)p.tiles, (int64_t)p.B), (int64_t)8 * 152);
+  // a block to 32 rows of queries, or to 4096 entries to copy where those are more
+  const int64_t copies = p.in != p.out ? p.B * (((int64_t)p.L.width + 4095) / 4096) : 1;
+  const unsigned blocks = 1 + (unsigned)std::min(std::max(4 * (int64_t)p.tiles, copies), 8 * (int64_t)num_sms);
   weights_prepare_kernel<FMT == DSA_REC_V32_656><<<blocks, kWtPrep, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.T == 0) return e;   // (no tokens: the scores are copied, nothing is weighed)
@@ -1079,11 +1086,11 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
   if (dsa::kDebug && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return DSA_ERR_CUDA;
   cudaError_t e = cudaErrorInvalidValue;
   switch (cache->format) {
-    case DSA_REC_FP8_528: e = launch_weights<DSA_REC_FP8_528>(p, plan->pairs, st); break;
-    case DSA_REC_NVFP4_288: e = launch_weights<DSA_REC_NVFP4_288>(p, plan->pairs, st); break;
-    case DSA_REC_FP8_528_UE8M0: e = launch_weights<DSA_REC_FP8_528_UE8M0>(p, plan->pairs, st); break;
-    case DSA_REC_MODEL1_584: e = launch_weights<DSA_REC_MODEL1_584>(p, plan->pairs, st); break;
-    case DSA_REC_V32_656: e = launch_weights<DSA_REC_V32_656>(p, plan->pairs, st); break;
+    case DSA_REC_FP8_528: e = launch_weights<DSA_REC_FP8_528>(p, plan->pairs, plan->num_sms, st); break;
+    case DSA_REC_NVFP4_288: e = launch_weights<DSA_REC_NVFP4_288>(p, plan->pairs, plan->num_sms, st); break;
+    case DSA_REC_FP8_528_UE8M0: e = launch_weights<DSA_REC_FP8_528_UE8M0>(p, plan->pairs, plan->num_sms, st); break;
+    case DSA_REC_MODEL1_584: e = launch_weights<DSA_REC_MODEL1_584>(p, plan->pairs, plan->num_sms, st); break;
+    case DSA_REC_V32_656: e = launch_weights<DSA_REC_V32_656>(p, plan->pairs, plan->num_sms, st); break;
   }
   return dsa::cuda_status(e);
 }
