@@ -1292,10 +1292,9 @@ cudaError_t attend_setup(void *) {
   return cudaFuncSetAttribute(prefix_attend_kernel<V32, kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)PfCfg<V32>::kSmem);
 }
-// (bits 56 to 59 of dsa_configure_once; the other kernels' stand at its declaration)
 template <bool V32, bool kChunk>
 cudaError_t attend_ready() {
-  return dsa_configure_once((kChunk ? 58 : 56) + (V32 ? 1 : 0), &attend_setup<V32, kChunk>, nullptr);
+  return dsa_configure_once((kChunk ? kOnceChunk : kOncePrefix) + (V32 ? 1 : 0), &attend_setup<V32, kChunk>, nullptr);
 }
 
 inline cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t st) {

@@ -278,7 +278,7 @@ extern "C" dsa_status dsa_evict(int32_t num_seqs, int32_t width, const int32_t *
                    freed_counts};
   const int64_t run = ((int64_t)width + cluster - 1) / cluster;
   const bool held = run <= dsa::kEvCached;
-  cudaError_t e = dsa::dsa_configure_once(60, &evict_setup, nullptr);
+  cudaError_t e = dsa::dsa_configure_once(dsa::kOnceEvict, &evict_setup, nullptr);
   if (e != cudaSuccess) return dsa::cuda_status(e);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)num_seqs * cluster);

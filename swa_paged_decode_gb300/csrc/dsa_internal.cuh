@@ -301,12 +301,21 @@ __device__ inline float e2m1_to_f32(uint32_t nib) {
 // One-time per-device kernel set-up (function attributes): `f` runs on the
 // first launch of kernel variant `bit` on the current device, later launches
 // skip it (they may be captured into a CUDA graph, where no set-up call is
-// wanted). Thread-safe. Bits in use: tensor-core kernels 0-2 (plain), 20-22
+// wanted). Thread-safe. A bit past 63 would run `f` on every call. Bits in use:
+// tensor-core kernels 0-2 (plain), 20-22
 // (V4.1 options), 24-26 (exact-budget waits), 28-30 and 32-34 (MODEL1 records),
 // 36-37 (V3.2 records), 40-42 (head groups sharing tiles), 46 and 50
 // (producers staging Q, with and without shared tiles), SIMT kernels 8-11,
-// combine 16-18.
+// combine 16-18, and from 51 on those below.
 cudaError_t dsa_configure_once(int bit, cudaError_t (*f)(void *), void *arg);
+constexpr int kOnceWeights = 51;       // + record format: 51-55
+constexpr int kOncePrefix = 56;        // + 1 with V3.2 records: 56-57
+constexpr int kOnceChunk = 58;         // likewise: 58-59
+constexpr int kOnceEvict = 60;
+constexpr int kOnceWeightsWide = 61;   // + record format - 1, of the three with power-of-two scales: 61-63
+static_assert(kOnceWeights + DSA_REC_V32_656 < kOncePrefix && kOncePrefix + 1 < kOnceChunk && kOnceChunk + 1 < kOnceEvict &&
+                  kOnceEvict < kOnceWeightsWide && kOnceWeightsWide + DSA_REC_MODEL1_584 - 1 < 64,
+              "every kernel variant has a bit of its own");
 
 // Programmatic dependent launch: the decode kernels let the combine grid be
 // scheduled early; the combine kernel waits for their completion (and

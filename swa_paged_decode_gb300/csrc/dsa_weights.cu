@@ -889,8 +889,10 @@ cudaError_t weights_setup(void *) {
                               (int)(dsa::WtCfg<FMT, WIDE>::kBytes + 1024));
 }
 template <int FMT, bool WIDE>
-cudaError_t weights_ready() {   // bits 51 to 55 and 61 to 63 of dsa_configure_once
-  return dsa::dsa_configure_once(WIDE ? 60 + FMT : 51 + FMT, &weights_setup<FMT, WIDE>, nullptr);
+cudaError_t weights_ready() {
+  static_assert(!WIDE || (FMT >= DSA_REC_NVFP4_288 && FMT <= DSA_REC_MODEL1_584), "a wide kernel without a bit of its own");
+  constexpr int bit = WIDE ? dsa::kOnceWeightsWide + FMT - 1 : dsa::kOnceWeights + FMT;
+  return dsa::dsa_configure_once(bit, &weights_setup<FMT, WIDE>, nullptr);
 }
 // CTA pairs that run at the same time on the current device.
 template <int FMT>
