@@ -684,11 +684,12 @@ dsa_status dsa_weights_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_he
  *   starts that do not ascend within [0, T]: nothing is written, the status
  *     word is DSA_ERR_INVALID_ARG.
  * Single tokens behind dsa_decode_run: starts 0, 1, 2, ...; their own lists and
- * lse. Precision: sums of fp32 weights, each good to a few 2^-22 relative
- * (16-bit operands of the products are exact for queries whose elements lie
- * within 2^-14 of their row's largest and for keys as dsa_decode.h's record
- * formats say, with magnitudes of 2^-48 .. 2^48; fp32 block scales are applied in
- * fp32). A record with a NaN or an infinity spoils its own score only, and one
+ * lse. Precision: fp32 sums of weights. A weight is off by a factor e^d, |d| <=
+ * 2^-16 A + 2^-22 (1 + |s| + |lse|), A = |scale| sum_d |q_d k_d|: the products'
+ * sum, and what fp32 holds of score and lse (16-bit operands of the products are
+ * exact for queries whose elements lie within 2^-14 of their row's largest and
+ * for keys as the record formats say, with magnitudes of 2^-48 .. 2^48; fp32
+ * block scales are applied in fp32). A record with a NaN or an infinity spoils its own score only, and one
  * with an element of 2^50 or more may count as one. Reproducible bit for bit.
  * Two launches, three when few keys meet many rows; allocates nothing, never
  * synchronizes. workspace and status as for dsa_prefix_run. */
