@@ -716,6 +716,10 @@ dsa_status dsa_weights_run(const dsa_weights_plan_t *plan, void *workspace, size
  * budget >= 1, keep_first, keep_last >= 0. Outputs must not overlap the inputs
  * (the lengths neither) or one another.
  * Records are not moved: the caller gives the freed slots back to its allocator.
+ * Slots are not looked at: an unused entry (-1, or another slot outside the cache)
+ * competes by its score like any other and comes out as it stands, in freed too;
+ * nor are duplicates, which a list's other entry may still hold. What is no
+ * record to give back is for the caller to leave out.
  * Asynchronous, one launch, no workspace; the result does not depend on
  * timing. */
 dsa_status dsa_evict(int32_t num_seqs, int32_t width, const int32_t *slots, int64_t slots_stride,
