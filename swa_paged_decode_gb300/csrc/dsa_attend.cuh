@@ -94,7 +94,7 @@ struct ChunkParams : PrefixParams {
   int4 *row_tile;              // [R][2] of each row tile: (first row, rows, units, -), (first unit's half, its first
                                // key's list position, list position of row g's token - g / H, -)
   int32_t *seq_tile;           // [B] first row tile of every sequence
-  int2 *begin;                 // [C + 1] (row tile, unit of it) at which a pair begins; the last: (row tiles, 0)
+  int2 *begin;                 // [C + 1] (row tile, unit of it) at which a pair begins; the last: (row tiles with units, 0)
   int32_t *n_merge, *merge;    // [R] the row tiles that pairs share, or that have no keys
 };
 template <bool kChunk>

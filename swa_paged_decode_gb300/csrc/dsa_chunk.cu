@@ -67,8 +67,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *w, int64_t &to
   return v;
 }
 
-// Row tiles, their units, and the pairs' ranges: block 0 of the gather. A
-// unit costs 1 and a tile with any `tile_cost` more (dsa_prefix_index.cuh).
+// Row tiles (those with keys first), their units, and the pairs' ranges: block 0
+// of the gather. A unit costs 1 and a tile with any `tile_cost` more
+// (dsa_prefix_index.cuh).
 __device__ void lay_out(const ChunkParams &p, bool ok) {
   __shared__ int64_t w_s[kChThreads / 32];
   const int tid = threadIdx.x;
@@ -122,25 +123,27 @@ __device__ void lay_out(const ChunkParams &p, bool ok) {
   const int64_t before_u = block_scan(units, w_s, all_units) - units;
   const int64_t before_l = block_scan(live, w_s, all_live) - live;
   const int64_t tile_cost = all_units >= 2 * (int64_t)p.C ? 2 : 0, total = all_units + tile_cost * all_live;
-  int64_t at = before_u + tile_cost * before_l;
+  int64_t at = before_u + tile_cost * before_l, l = before_l;
   each([&](int32_t t, int32_t b, const Sequence &s, int32_t i, int32_t half, int32_t u) {
-    p.row_tile[2 * (int64_t)t] = make_int4(s.s0 * p.H + 128 * i, s.tile_rows(p.H, i), u, 0);
-    p.row_tile[2 * (int64_t)t + 1] = make_int4(b * p.seq_halves + half, half * 128, s.len - s.n - s.s0, 0);
+    const int32_t to = tile_place(t, u, l, all_live);
+    p.row_tile[2 * (int64_t)to] = make_int4(s.s0 * p.H + 128 * i, s.tile_rows(p.H, i), u, 0);
+    p.row_tile[2 * (int64_t)to + 1] = make_int4(b * p.seq_halves + half, half * 128, s.len - s.n - s.s0, 0);
     if (u == 0) {
-      p.merge[atomicAdd(p.n_merge, 1)] = t;
+      p.merge[atomicAdd(p.n_merge, 1)] = to;
       return;
     }
+    ++l;
     bool shared = false;   // (the list's order does not matter)
     pairs_in_tile(at, u, tile_cost, total, p.C, [&](int32_t c, int32_t w) {
-      p.begin[c] = make_int2(t, w);
+      p.begin[c] = make_int2(to, w);
       shared |= w > 0;
     });
-    if (shared) p.merge[atomicAdd(p.n_merge, 1)] = t;
+    if (shared) p.merge[atomicAdd(p.n_merge, 1)] = to;
     at += u + tile_cost;
   });
   if (total == 0)
-    for (int32_t c = tid; c < p.C; c += kChThreads) p.begin[c] = make_int2(R, 0);
-  if (tid == 0) p.begin[p.C] = make_int2(R, 0);
+    for (int32_t c = tid; c < p.C; c += kChThreads) p.begin[c] = make_int2(0, 0);
+  if (tid == 0) p.begin[p.C] = make_int2((int32_t)all_live, 0);
 }
 
 template <int FMT>

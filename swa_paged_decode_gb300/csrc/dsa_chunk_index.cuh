@@ -47,6 +47,13 @@ struct RowTile {
   int32_t g0, rows, units;     // first row, rows
   int32_t half, key0, shift;   // as in TileRun, of the tile's first unit
 };
+// Its place: those with units first, in order, so that the pairs' ranges meet no
+// other one (a pair that looked for the next tile with units waited for its
+// record: 240 us against 235 for a window of 128); `live`: tiles with units,
+// live_before: of them before tile t.
+DSA_HD int32_t tile_place(int32_t t, int32_t units, int64_t live_before, int64_t live) {
+  return (int32_t)(units > 0 ? live_before : live + (t - live_before));
+}
 
 // The pairs whose ranges begin in a tile of `units` > 0 units: of C equal shares
 // of `total` those that begin within the tile's cost, units + tile_cost from `at`
@@ -62,38 +69,35 @@ DSA_KERNEL void pairs_in_tile(int64_t at, int32_t units, int64_t tile_cost, int6
 }
 
 // A pair's range, from unit w of row tile t to before unit w1 of tile t1, tile
-// by tile; load(t, tile) reads a row tile. It stands on a tile with units or at
-// its end, never on a tile without: peek names the tile that next returns.
+// by tile, all of them with units; load(t, tile) reads a row tile. peek names the
+// tile that next returns.
 template <class Load>
 struct TileWalk {
   Load load;
   int32_t t, w, t1, w1;
   RowTile tile;   // row tile t, loaded ahead
   DSA_KERNEL TileWalk(Load l, int32_t t_, int32_t w_, int32_t t1_, int32_t w1_) : load(l), t(t_), w(w_), t1(t1_), w1(w1_), tile() {
-    settle();
+    ahead();
   }
   DSA_KERNEL bool empty() const { return t > t1 || (t == t1 && w >= w1); }
-  DSA_KERNEL int32_t end() const { return t == t1 ? w1 : tile.units; }
-  DSA_KERNEL void settle() {
-    for (; !empty(); ++t, w = 0) {
-      load(t, tile);
-      if (w < end()) return;
-    }
+  DSA_KERNEL void ahead() {   // (loaded, not looked at: a role would wait for it)
+    if (t < t1 || (t == t1 && w1 > 0)) load(t, tile);
   }
   DSA_KERNEL bool next(TileRun &s) {
     if (empty()) return false;
+    const int32_t end = t == t1 ? w1 : tile.units;
     s.qt = t;
     s.g0 = tile.g0;
     s.n = tile.rows;
-    s.half = tile.half + 2 * (int64_t)w;
+    s.half = tile.half + 2 * w;
     s.key0 = tile.key0 + 256 * w;
     s.shift = tile.shift;
-    s.units = end() - w;
+    s.units = end - w;
     s.head = w == 0;
-    s.tail = end() == tile.units;
+    s.tail = end == tile.units;
     ++t;
     w = 0;
-    settle();
+    ahead();
     return true;
   }
   // rows of the next segment's tile (0: none)

@@ -9,9 +9,10 @@ using namespace dsa;
 // -> 0, or what is wrong: 1 a segment that peek did not name before, 2 a segment
 // outside its tile or without units, 3 a unit of a tile that not exactly one pair
 // takes, 4 head or tail marks that do not meet the segment's ends, 5 a walk that
-// does not end, 6 units for a tile's keyless rows alone.
+// does not end, 6 units for a tile's keyless rows alone, 7 two tiles in one
+// place.
 extern "C" int walk_batch(int B, const int *n, const int *len, int window, int H, int C) {
-  std::vector<RowTile> tiles;
+  std::vector<RowTile> all;
   int32_t s0 = 0;
   const int32_t seq_halves = 1 << 16;
   for (int b = 0; b < B; ++b) {
@@ -21,26 +22,33 @@ extern "C" int walk_batch(int B, const int *n, const int *len, int window, int H
       const int32_t units = s.tile_units(H, i, half);
       const int32_t last = s.row_position(H, 128 * (int64_t)i + s.tile_rows(H, i) - 1);
       if ((units > 0) != (last >= 0)) return 6;
-      tiles.push_back({s0 * H + 128 * i, s.tile_rows(H, i), units, b * seq_halves + half, half * 128, s.len - s.n - s0});
+      all.push_back({s0 * H + 128 * i, s.tile_rows(H, i), units, b * seq_halves + half, half * 128, s.len - s.n - s0});
     }
     s0 += n[b];
   }
   int64_t units = 0, live = 0;
-  for (const RowTile &t : tiles) {
+  for (const RowTile &t : all) {
     units += t.units;
     live += t.units > 0;
   }
   const int64_t tile_cost = units >= 2 * (int64_t)C ? 2 : 0, total = units + tile_cost * live;
-  const int32_t R = (int32_t)tiles.size();
-  std::vector<int32_t> from(C + 1, R), at_unit(C + 1, 0);
-  int64_t at = 0;
+  const int32_t R = (int32_t)all.size();
+  std::vector<RowTile> tiles(R);
+  std::vector<int> filled(R, 0);
+  std::vector<int32_t> from(C + 1, 0), at_unit(C + 1, 0);
+  from[C] = (int32_t)live;
+  int64_t at = 0, before = 0;
   for (int32_t t = 0; t < R; ++t) {
-    if (tiles[t].units == 0) continue;
-    pairs_in_tile(at, tiles[t].units, tile_cost, total, C, [&](int32_t c, int32_t unit) {
-      from[c] = t;
+    const int32_t to = tile_place(t, all[t].units, before, live);
+    if (to < 0 || to >= R || filled[to]++) return 7;
+    tiles[to] = all[t];
+    if (all[t].units == 0) continue;
+    ++before;
+    pairs_in_tile(at, all[t].units, tile_cost, total, C, [&](int32_t c, int32_t unit) {
+      from[c] = to;
       at_unit[c] = unit;
     });
-    at += tiles[t].units + tile_cost;
+    at += all[t].units + tile_cost;
   }
   std::vector<std::vector<int>> taken(R);
   for (int32_t t = 0; t < R; ++t) taken[t].assign(tiles[t].units, 0);
