@@ -587,7 +587,11 @@ dsa_status dsa_chunk_plan(int32_t num_tokens, int32_t num_seqs, int32_t num_head
  *     lse may be tail_lse. Tokens before starts[0] and from starts[B] on are
  *     left as they were. A row that attends nothing (and has no tail) gives
  *     zeros and -inf.
- *   workspace, status, precision: as for dsa_prefix_run. A key with a NaN, an
+ *   workspace, status, precision: as for dsa_prefix_run (positions of tokens
+ *     that attend nothing may not be looked at). lse is off by 1 to 3e-6 where
+ *     queries are rotated here or records have fp32 scales, whose products are
+ *     rounded to f16; queries rotated by dsa_qk_norm over records of the other
+ *     formats are exact operands. A key with a NaN, an
  *     infinity or an element of 2^49 or more has NaN for its scores: it spoils
  *     the rows that attend it and no others. Lists may share slots.
  * Three launches on `stream`; allocates nothing, never synchronizes. */

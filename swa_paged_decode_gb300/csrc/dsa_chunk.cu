@@ -23,9 +23,9 @@
 // What bounds it. Long lists: as the shared prefix, the products (1024 tokens x 128
 // heads over 16384 records 2.37 ms alone, 1800 TFLOP/s, 0.94 of the measured
 // peak). Windows: the chain of one tile after the other on a pair, 17000 cycles for
-// 2 tokens x 64 heads and 128 keys, of which the products are 4500 (3400 tokens 236
+// 2 tokens x 64 heads and 128 keys, of which the products are 4500 (3400 tokens 235
 // us; 361 with the output through fp32 in shared memory, the rotation in four
-// lanes and a merge over all rows). Few tokens: three dependent kernels (22.6 us).
+// lanes and a merge over all rows). Few tokens: three dependent kernels (21.1 us).
 #include "dsa_attend.cuh"
 
 namespace dsa {
